@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libgdn.so")
 (GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_LAUNCH, GDN_ERR_CUDA,
  GDN_ERR_TOO_LARGE) = range(6)
 PREFILL_STATIC_SCRATCH_BYTES = 16 << 20
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_E4M3 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 DEVSTAT_BAD_INDEX, DEVSTAT_BAD_SEQLEN, DEVSTAT_TIMEOUT = 0x1, 0x2, 0x4
 
 # Every symbol the header declares (checked by the tests against the .so).
@@ -32,7 +33,7 @@ EXPORTS = (
     "gdn_decode_recurrent_gated", "gdn_decode_step_fused", "gdn_mixed_batch",
     "gdn_debug_set_wait_limit", "gdn_prefill_chunked_gated", "gdn_mtp_step_fused",
     "gdn_decode_step_workspace_size", "gdn_prefill_layer", "gdn_prefill_layer_workspace_size",
-    "gdn_prefill_layer_gated",
+    "gdn_prefill_layer_gated", "gdn_add_rmsnorm", "gdn_gated_rmsnorm_quant", "gdn_linear",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -64,6 +65,11 @@ _SIGS = {
     "gdn_decode_step_fused": [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                               _f32, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp, _vp],
     "gdn_gated_rmsnorm": [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _i32, _vp],
+    "gdn_add_rmsnorm": [_vp, _i64, _vp, _i64, _vp, _f32, _i64, _i32, _f32, _vp, _i64, _vp, _i64, _vp,
+                        _i32, _i32, _vp],
+    "gdn_gated_rmsnorm_quant": [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _i32, _vp],
+    "gdn_linear": [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp,
+                   _i64, _i32, _i32, _vp],
     "gdn_decode_recurrent_gated": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp, _vp, _vp, _i64,
                                    _vp, _f32, _vp, _i32, _vp],
@@ -682,6 +688,141 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-6, y=None):
     _need(y.is_contiguous() and y.shape == o.shape and y.dtype == o.dtype, "y: like o")
     _check(_lib.gdn_gated_rmsnorm(_ptr(o), _ptr(z), zs, _ptr(weight), T, hv, dv, float(eps),
                                   _ptr(y), _dtype_code(o), _stream(o.device)), "gdn_gated_rmsnorm")
+    return y
+
+
+def _same_device(first, *ts):
+    """Every tensor on the CUDA device of the first one; returns its index."""
+    _need(first.is_cuda, "all tensors must be on a CUDA device")
+    dev = first.get_device()
+    for t in ts:
+        if t is not None:
+            _need(t.get_device() == dev, "all tensors must be on one CUDA device")
+    return dev
+
+
+def _call(fn, name, dev, *args):
+    """fn on the current stream of device `dev`, which becomes the current one for the call."""
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+
+
+def _rows(t, T, n, name):
+    """t is [T, n] with unit column stride; returns its row stride (n where T = 1)."""
+    _need(t.dim() == 2 and t.shape[0] == T and t.shape[1] == n, f"{name}: [{T}, {n}]")
+    _need(n == 1 or t.stride(1) == 1, f"{name}: unit column stride")
+    st = t.stride(0)
+    if T <= 1:
+        return max(n, st)
+    _need(st >= n, f"{name}: rows must not overlap")
+    return st
+
+
+def _f32_vec(t, n, name):
+    _need(t.dtype == torch.float32 and t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1),
+          f"{name}: [{n}] fp32, contiguous")
+    return t.data_ptr()
+
+
+def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, y_dtype=None,
+                    residual_out=None, y=None, y_scale=None):
+    """s = x + residual; y = s / sqrt(mean(s^2) + eps) * (weight_offset + weight)
+    per token row.  x, residual [T, H] (views with a free row stride), fp32 or
+    bf16; weight [H] fp32.  y_dtype: x's dtype (default) or
+    torch.float8_e4m3fn, then with one fp32 scale per token, y * y_scale[:, None]
+    being the norm.  Returns (y, y_scale or None, residual_out or None), where
+    residual_out [T, H] is s in x's dtype, made when a residual is given (pass
+    residual_out=residual to update the stream in place)."""
+    dev = _same_device(x, weight, residual, residual_out, y, y_scale)
+    _need(x.dim() == 2, "x: [T, H]")
+    T, H = x.shape
+    xs, dt = _rows(x, T, H, "x"), _dtype_code(x)
+    wp = _f32_vec(weight, H, "weight")
+    rs = ros = 0
+    if residual is not None:
+        _need(residual.dtype == x.dtype, "residual: x's dtype")
+        rs = _rows(residual, T, H, "residual")
+        if residual_out is None:
+            residual_out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    if residual_out is not None:
+        _need(residual_out.dtype == x.dtype, "residual_out: x's dtype")
+        ros = _rows(residual_out, T, H, "residual_out")
+    if y is None:
+        y = torch.empty((T, H), dtype=x.dtype if y_dtype is None else y_dtype, device=x.device)
+    _need(y_dtype is None or y.dtype == y_dtype, "y: y_dtype")
+    quant = y.dtype == torch.float8_e4m3fn
+    _need(quant or y.dtype == x.dtype, "y: x's dtype or float8_e4m3fn")
+    ys = _rows(y, T, H, "y")
+    if quant:
+        y_scale = torch.empty(T, dtype=torch.float32, device=x.device) if y_scale is None else y_scale
+        sp = _f32_vec(y_scale, T, "y_scale")
+    else:
+        _need(y_scale is None, "y_scale: only with an 8-bit y")
+        sp = None
+    _call(_lib.gdn_add_rmsnorm, "gdn_add_rmsnorm", dev, x.data_ptr(), xs,
+          None if residual is None else residual.data_ptr(), rs, wp, weight_offset, T, H, eps,
+          None if residual_out is None else residual_out.data_ptr(), ros, y.data_ptr(), ys, sp, dt,
+          GDN_E4M3 if quant else dt)
+    return y, y_scale, residual_out
+
+
+def gdn_gated_rmsnorm_quant(o, z, weight, eps=1e-6, y=None, y_scale=None):
+    """gdn_gated_rmsnorm with an 8-bit output: returns y [T, hv, dv]
+    float8_e4m3fn and y_scale [T] fp32 (one scale per token), y * y_scale being
+    the gated norm.  o [T, hv, dv] contiguous; z [T, hv, dv] or [T, hv*dv] (a
+    view with a free row stride); weight [dv] fp32.  y viewed as [T, hv*dv] is
+    gdn_linear's 8-bit x."""
+    dev = _same_device(o, z, weight, y, y_scale)
+    _need(o.dim() == 3 and o.is_contiguous(), "o: [T, hv, dv] contiguous")
+    T, hv, dv = o.shape
+    zs = _heads_view(z, hv, dv, "z")
+    zs = max(zs, hv * dv) if T <= 1 else zs
+    _need(z.shape[0] == T and z.dtype == o.dtype, "z: rows and dtype of o")
+    wp = _f32_vec(weight, dv, "weight")
+    y = torch.empty((T, hv, dv), dtype=torch.float8_e4m3fn, device=o.device) if y is None else y
+    _need(y.dtype == torch.float8_e4m3fn and y.shape == o.shape and y.is_contiguous(),
+          "y: [T, hv, dv] float8_e4m3fn, contiguous")
+    y_scale = torch.empty(T, dtype=torch.float32, device=o.device) if y_scale is None else y_scale
+    _call(_lib.gdn_gated_rmsnorm_quant, "gdn_gated_rmsnorm_quant", dev, o.data_ptr(), z.data_ptr(),
+          zs, wp, T, hv, dv, eps, y.data_ptr(), _f32_vec(y_scale, T, "y_scale"), _dtype_code(o))
+    return y, y_scale
+
+
+def gdn_linear(x, weight, x_scale=None, weight_scale=None, bias=None, act="none", residual=None,
+               y_dtype=None, y=None):
+    """y = act(x_scale weight_scale (x @ weight.T) + bias) + residual.
+    x [T, K], weight [N, K]: both bf16, or both float8_e4m3fn with x_scale [T]
+    and weight_scale [N] fp32 (None = 1); unit column stride, rows on 16-byte
+    boundaries (K itself may be odd).  bias [N] fp32; act "none", "silu" or
+    "gelu"; residual [T, N] in y's dtype.  y [T, N] bf16 (default) or fp32,
+    columns of a wider buffer if wanted; y may be residual.  Returns y."""
+    dev = _same_device(x, weight, x_scale, weight_scale, bias, residual, y)
+    _need(x.dim() == 2 and weight.dim() == 2, "x: [T, K], weight: [N, K]")
+    T, K = x.shape
+    N = weight.shape[0]
+    _need(x.dtype == weight.dtype, "x, weight: one dtype")
+    if x.dtype == torch.float8_e4m3fn:
+        dt = GDN_E4M3
+    else:
+        dt = _dtype_code(x)
+        _need(x_scale is None and weight_scale is None, "scales: only with 8-bit x and weight")
+    xs, ws = _rows(x, T, K, "x"), _rows(weight, N, K, "weight")
+    sxp = None if x_scale is None else _f32_vec(x_scale, T, "x_scale")
+    swp = None if weight_scale is None else _f32_vec(weight_scale, N, "weight_scale")
+    bp = None if bias is None else _f32_vec(bias, N, "bias")
+    _need(act in ACTIVATIONS, f"act: one of {tuple(ACTIVATIONS)}")
+    if y is None:
+        y = torch.empty((T, N), dtype=torch.bfloat16 if y_dtype is None else y_dtype, device=x.device)
+    _need(y_dtype is None or y.dtype == y_dtype, "y: y_dtype")
+    ys, rs, rp = _rows(y, T, N, "y"), 0, None
+    if residual is not None:
+        _need(residual.dtype == y.dtype, "residual: y's dtype")
+        rs, rp = _rows(residual, T, N, "residual"), residual.data_ptr()
+    _call(_lib.gdn_linear, "gdn_linear", dev, x.data_ptr(), xs, sxp, weight.data_ptr(), ws, swp, bp,
+          rp, rs, T, K, N, ACTIVATIONS[act], y.data_ptr(), ys, dt, _dtype_code(y))
     return y
 
 

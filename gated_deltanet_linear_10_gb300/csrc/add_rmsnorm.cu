@@ -1,0 +1,181 @@
+// The block's input norm: the residual's addition and the RMSNorm of the sum,
+// per token row of `hidden` elements,
+//   s = x + residual,  residual_out = s,
+//   y = s / sqrt(mean(s^2) + eps) * (weight_offset + weight),
+// with y in x's type or as e4m3 with one fp32 scale per token ("RMSNorm" and
+// "Gemma RMSNorm", the (1 + w)-scaled form, "[model] Support Qwen3next",
+// LightLLM issue 1097, Highlights; no formula is printed there).
+//
+// s stays in fp32 registers from the loads to the stores: the norm reads the
+// unrounded sum, and residual_out is its one rounding to the stream's type.
+// The maximum that the 8-bit scale needs is taken over |s (offset + w)| in the
+// same pass as the sum of squares, since 1 / rms is one factor of the row.
+//
+// One CTA works on a row at a time, kVecs vectors of 16 bytes per thread; the
+// weights stay in registers over the rows of a CTA.
+#include <algorithm>
+
+#include "quant.cuh"
+
+namespace gdn {
+
+constexpr int kRmsMaxHidden = 16384;
+
+// T: x, residual and residual_out.  O: y (T or E4m3).  N: elements per vector
+// (16 bytes of T, or 1 where a row is not on 16-byte boundaries).
+constexpr int rms_threads(int n, int vecs, size_t elem) {   // the most a launch below takes
+    return n == 1 || (vecs == 4 && elem == 4) ? 1024 : 512;
+}
+
+template <typename T, typename O, int N, int kVecs>
+__global__ void __launch_bounds__(rms_threads(N, kVecs, sizeof(T)))
+add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs,
+                                   const float *__restrict__ w, float offset, int n_rows,
+                                   int hidden, float eps, T *res_out, int64_t ros, O *y,
+                                   int64_t ys, float *__restrict__ y_scale) {
+    __shared__ float2 part[2][32];
+    constexpr bool kQuant = sizeof(O) == 1;
+    griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
+    const int tid = threadIdx.x;
+    float wv[kVecs][N];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        const int e = (tid + k * blockDim.x) * N;
+#pragma unroll
+        for (int c = 0; c < N; ++c) wv[k][c] = e < hidden ? offset + w[e + c] : 0.f;
+    }
+    int flip = 0;
+    for (int row = blockIdx.x; row < n_rows; row += gridDim.x, flip ^= 1) {
+        RawVec<T, N> a[kVecs], b[kVecs];
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int e = (tid + k * blockDim.x) * N;
+            a[k].zero();
+            b[k].zero();
+            if (e < hidden) {
+                a[k].load(x + row * xs + e);
+                if (res) b[k].load(res + row * rs + e);
+            }
+        }
+        float s[kVecs][N], ss = 0.f, mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            float r[N];
+            a[k].get(s[k]);
+            b[k].get(r);
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                s[k][c] += r[c];
+                ss = fmaf(s[k][c], s[k][c], ss);
+                if constexpr (kQuant) mx = max_nan(mx, fabsf(s[k][c] * wv[k][c]));
+            }
+            const int e = (tid + k * blockDim.x) * N;
+            if (res_out && e < hidden) store_row<N>(res_out + row * ros + e, s[k]);
+        }
+        const float2 red = block_sum_max(ss, mx, part[flip]);
+        const float inv = rsqrtf(red.x / (float)hidden + eps);
+        float q = 1.0f;
+        if constexpr (kQuant) {
+            const float scale = e4m3_scale(red.y * inv);
+            q = 1.0f / scale;
+            if (tid == 0) y_scale[row] = scale;
+        }
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int e = (tid + k * blockDim.x) * N;
+            if (e >= hidden) continue;
+            float v[N];
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                v[c] = s[k][c] * wv[k][c] * inv;
+                if constexpr (kQuant) v[c] *= q;
+            }
+            store_row<N>(y + row * ys + e, v);
+        }
+    }
+}
+
+template <typename T, typename O, int N, int kVecs>
+static cudaError_t launch_rms_n(const void *x, int64_t xs, const void *res, int64_t rs,
+                                const float *w, float offset, int n_rows, int hidden, float eps,
+                                void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
+                                cudaStream_t s) {
+    const int per = N * kVecs;
+    const int threads = (((hidden + per - 1) / per) + 31) / 32 * 32;
+    const int per_sm = std::max(1, 2048 / threads);
+    const int grid = std::min(n_rows, sm_count() * per_sm);
+    return launch_after(add_rmsnorm_kernel<T, O, N, kVecs>, dim3(grid), dim3(threads), 0, s,
+                        (const T *)x, xs, (const T *)res, rs, w, offset, n_rows, hidden, eps,
+                        (T *)res_out, ros, (O *)y, ys, y_scale);
+}
+
+// One vector per thread while that fits a CTA of 512 threads (rows of at most
+// 512 vectors), more beyond.
+template <typename T, typename O>
+static cudaError_t launch_rms(bool vec, const void *x, int64_t xs, const void *res, int64_t rs,
+                              const float *w, float offset, int n_rows, int hidden, float eps,
+                              void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
+                              cudaStream_t s) {
+    constexpr int N = 16 / sizeof(T);
+#define GDN_RMS(n, v) \
+    launch_rms_n<T, O, n, v>(x, xs, res, rs, w, offset, n_rows, hidden, eps, res_out, ros, y, ys, y_scale, s)
+    if (vec) {
+        if (hidden <= 512 * N) return GDN_RMS(N, 1);
+        if (hidden <= 1024 * N) return GDN_RMS(N, 2);
+        return GDN_RMS(N, 4);
+    }
+    if (hidden <= 4096) return GDN_RMS(1, 4);
+    return GDN_RMS(1, 16);
+#undef GDN_RMS
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *residual,
+                                      int64_t residual_row_stride, const float *weight,
+                                      float weight_offset, int64_t n_tokens, int32_t hidden,
+                                      float eps, void *residual_out,
+                                      int64_t residual_out_row_stride, void *y,
+                                      int64_t y_row_stride, float *y_scale, int32_t dtype,
+                                      int32_t y_dtype, void *stream) {
+    GDN_REQUIRE(dtype == GDN_F32 || dtype == GDN_BF16, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(y_dtype == dtype || y_dtype == GDN_E4M3, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(n_tokens >= 0 && hidden > 0 && eps >= 0.f, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(hidden <= kRmsMaxHidden && n_tokens < (1ll << 31), GDN_ERR_UNSUPPORTED);
+    if (n_tokens == 0) return GDN_OK;
+    GDN_REQUIRE(x && weight && y, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE((y_scale != nullptr) == (y_dtype == GDN_E4M3), GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(x_row_stride >= hidden && y_row_stride >= hidden, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(!residual || residual_row_stride >= hidden, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(!residual_out || residual_out_row_stride >= hidden, GDN_ERR_INVALID_ARG);
+    const uintptr_t elem = dtype == GDN_F32 ? 4 : 2, yelem = y_dtype == GDN_E4M3 ? 1 : elem;
+    GDN_REQUIRE((uintptr_t)x % elem == 0 && (uintptr_t)residual % elem == 0 &&
+                    (uintptr_t)residual_out % elem == 0 && (uintptr_t)y % yelem == 0 &&
+                    (uintptr_t)weight % 4 == 0 && (uintptr_t)y_scale % 4 == 0,
+                GDN_ERR_INVALID_ARG);
+    // 16-byte vectors of the stream (and the y elements that belong to one)
+    const int64_t n = 16 / (int64_t)elem;
+    const bool vec = hidden % n == 0 && (uintptr_t)x % 16 == 0 && x_row_stride % n == 0 &&
+                     (!residual || ((uintptr_t)residual % 16 == 0 && residual_row_stride % n == 0)) &&
+                     (!residual_out ||
+                      ((uintptr_t)residual_out % 16 == 0 && residual_out_row_stride % n == 0)) &&
+                     (uintptr_t)y % (n * yelem) == 0 && y_row_stride % n == 0;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+#define GDN_RMS(T, O)                                                                           \
+    launch_rms<T, O>(vec, x, x_row_stride, residual, residual_row_stride, weight, weight_offset, \
+                     (int)n_tokens, hidden, eps, residual_out, residual_out_row_stride, y,        \
+                     y_row_stride, y_scale, s)
+    if (dtype == GDN_BF16)
+        e = y_dtype == GDN_E4M3 ? GDN_RMS(__nv_bfloat16, E4m3) : GDN_RMS(__nv_bfloat16, __nv_bfloat16);
+    else
+        e = y_dtype == GDN_E4M3 ? GDN_RMS(float, E4m3) : GDN_RMS(float, float);
+#undef GDN_RMS
+    if (e != cudaSuccess) {
+        set_last_cuda_error(e);
+        return GDN_ERR_LAUNCH;
+    }
+    return GDN_OK;
+}

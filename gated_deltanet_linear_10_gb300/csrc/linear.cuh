@@ -1,0 +1,67 @@
+// The matrix product with its epilogue (internal header):
+//   y[t][n] = act(sx[t] sw[n] sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n]
+#pragma once
+
+#include "quant.cuh"
+#include "tc.cuh"
+
+namespace gdn {
+
+// The epilogue's inputs and the output; null pointers leave a part out.
+struct LinearEpi {
+    const float *sx, *sw, *bias;
+    const void *res;
+    int64_t rs;
+    void *y;
+    int64_t ys;
+    int n_tokens, n_out, act;
+    bool out_f32;
+};
+
+template <int kAct> __device__ __forceinline__ float linear_act(float v) {
+    if constexpr (kAct == GDN_ACT_SILU) return silu_f(v);
+    if constexpr (kAct == GDN_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118f));
+    return v;
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 accumulator (the
+// type fields of A and B are 0 for e4m3; the rest is laid out as for f16).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D(tmem) (+)= A(smem) * B(smem), 32 bytes of K: 16 bf16 or 32 e4m3.
+template <bool kE4m3>
+__device__ __forceinline__ void linear_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    if constexpr (kE4m3)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        tc::mma_ss(d, a, b, idesc, accumulate);
+}
+
+// mbar_wait for a copy or product that is in flight already when the CTA has
+// given up: it does not return at once on the abort flag, but it is bounded.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
+    volatile int give_up = 0;
+    tc::mbar_wait(bar, parity, &give_up);
+}
+
+// The product's 2-D operand: rows of `cols` elements of 2 bytes (bf16) or 1
+// (e4m3), loaded as boxes of 128 bytes x box_rows in the 128-byte swizzle.
+bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64_t rows,
+                         int64_t row_stride_elems, uint32_t box_rows, bool e4m3);
+
+struct LinearCall {
+    const void *x, *w;
+    int64_t xs, ws;
+    int n_in;
+    LinearEpi e;
+    cudaStream_t stream;
+};
+
+}  // namespace gdn

@@ -1,0 +1,127 @@
+// 8-bit outputs (e4m3) with one fp32 scale per row, and the vector accesses
+// and reductions the row kernels share (internal header).
+//
+//   scale = max(max_j |y_j| / 448, 2^-126),   q_j = rn_e4m3(y_j / scale)
+//
+// 448 is the largest e4m3 value.  The lower bound keeps 1 / scale finite, so
+// a row of zeros gives q = 0.  Nothing is hidden: a NaN among the y_j makes the
+// scale and every q_j of the row NaN, an infinite y_j makes the scale infinite.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace gdn {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinScale = 1.17549435e-38f;   // 2^-126
+
+// max(a, b), NaN when either is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float e4m3_scale(float amax) {
+    return max_nan(amax * (1.0f / kE4m3Max), kMinScale);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// One e4m3 value.
+struct E4m3 {
+    uint8_t v;
+};
+
+// N elements of T as registers: raw bytes as loaded (so that a row can be
+// requested while another is worked on), unpacked to fp32 where used.
+// N = 1: one element; otherwise N * sizeof(T) is 16 or 32 bytes, moved as
+// 16-byte accesses (or, with `half`, 8-byte ones).
+template <typename T, int N> struct RawVec {
+    uint4 r[N * sizeof(T) / 16];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void load_half(const T *p) {   // 8-byte aligned p
+        uint2 *d = reinterpret_cast<uint2 *>(r);
+#pragma unroll
+        for (int i = 0; i < (int)(N * sizeof(T) / 8); ++i) d[i] = reinterpret_cast<const uint2 *>(p)[i];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(float *out) const {
+#pragma unroll
+        for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i)
+            Vec16<T>::unpack(r[i], out + i * Vec16<T>::N);
+    }
+};
+template <typename T> struct RawVec<T, 1> {
+    T r;
+    __device__ __forceinline__ void load(const T *p) { r = *p; }
+    __device__ __forceinline__ void zero() { Io<T>::store(&r, 0.f); }
+    __device__ __forceinline__ void get(float *out) const { out[0] = Io<T>::load(&r); }
+};
+
+// Stores N fp32 values as O (N = 1, 4 or 8; vectors aligned to their size).
+template <int N> __device__ __forceinline__ void store_row(float *p, const float *v) {
+    if constexpr (N == 1) {
+        *p = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) Vec16<float>::store(p + i, v + i);
+    }
+}
+template <int N> __device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float *v) {
+    if constexpr (N == 1) {
+        *p = __float2bfloat16_rn(v[0]);
+    } else {
+        static_assert(N == 8, "bf16 vectors are 16 bytes");
+        Vec16<__nv_bfloat16>::store(p, v);
+    }
+}
+template <int N> __device__ __forceinline__ void store_row(E4m3 *p, const float *v) {
+    if constexpr (N == 1) {
+        p->v = (uint8_t)__nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<uint32_t *>(p) = pack_e4m3x4(v[0], v[1], v[2], v[3]);
+    } else {
+        static_assert(N == 8, "e4m3 vectors are 4 or 8 bytes");
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_e4m3x4(v[0], v[1], v[2], v[3]),
+                                                   pack_e4m3x4(v[4], v[5], v[6], v[7]));
+    }
+}
+
+// (sum, NaN-keeping max) over the block; every thread gets both.  `part` is
+// one of two shared arrays of 32 float2 used alternately, so that one barrier
+// per call is enough: a thread is at most one call ahead of the slowest.
+__device__ __forceinline__ float2 block_sum_max(float sum, float mx, float2 *part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    }
+    if (warps == 1) return make_float2(sum, mx);
+    if (lane == 0) part[warp] = make_float2(sum, mx);
+    __syncthreads();
+    const float2 p = lane < warps ? part[lane] : make_float2(0.f, 0.f);
+    sum = p.x;
+    mx = p.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    }
+    return make_float2(sum, mx);
+}
+
+}  // namespace gdn

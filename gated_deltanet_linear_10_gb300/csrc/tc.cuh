@@ -304,4 +304,8 @@ namespace gdn {
 bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
                          uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows,
                          bool swizzle128 = true);
+// The same for any element type, with the row pitch in bytes.
+bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+                    uint64_t rows, uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
+                    bool swizzle128);
 }  // namespace gdn

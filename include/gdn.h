@@ -35,7 +35,10 @@
  *     by the kernels: an index outside [0, n_slots) is skipped (as if < 0)
  *     and sets GDN_DEVSTAT_BAD_INDEX in the device status word.
  *   - Element counts and strides are in ELEMENTS, not bytes.
- *   - dtype: GDN_F32 = fp32 activations, GDN_BF16 = bf16 activations.
+ *   - dtype: GDN_F32 = fp32 activations, GDN_BF16 = bf16 activations,
+ *     GDN_E4M3 = 8-bit floats (4 exponent bits, 3 mantissa bits, largest value
+ *     448), each standing for itself times its row's fp32 scale; only where an
+ *     entry point names it.
  *     g, beta, A_log, dt_bias and the recurrent state pool are always fp32.
  *   - Two entries of one call naming the same slot (twice as a destination,
  *     or as the source of one and the destination of another) give an
@@ -62,8 +65,16 @@ typedef enum gdn_status {
 
 typedef enum gdn_dtype {
     GDN_F32 = 0,
-    GDN_BF16 = 1
+    GDN_BF16 = 1,
+    GDN_E4M3 = 2
 } gdn_dtype;
+
+/* Activations of gdn_linear's epilogue. */
+typedef enum gdn_act {
+    GDN_ACT_NONE = 0,
+    GDN_ACT_SILU = 1, /* v / (1 + exp(-v))             */
+    GDN_ACT_GELU = 2  /* v (1 + erf(v / sqrt(2))) / 2  */
+} gdn_act;
 
 /* Bits of the device status word (gdn_get_device_status). */
 #define GDN_DEVSTAT_BAD_INDEX 0x1u  /* a slot index >= n_slots was skipped      */
@@ -401,6 +412,84 @@ gdn_status gdn_gated_rmsnorm(const void *o, const void *z, int64_t z_row_stride,
                              const float *weight, int64_t n_tokens, int32_t hv,
                              int32_t dv, float eps, void *y, int32_t dtype,
                              void *stream);
+
+/*
+ * gdn_gated_rmsnorm with an 8-bit output and one scale per token, for an
+ * output projection whose operands are 8-bit (gdn_linear with GDN_E4M3):
+ *   v = o / sqrt(mean(o^2) + eps) * weight * SiLU(z)   per (token, V head) row
+ *   y_scale[t] = max(max over the token's hv*dv values of |v| / 448, 2^-126)
+ *   y = v / y_scale[t] rounded to e4m3
+ * A token with a NaN gets a NaN scale and NaN values; one of zeros gets zeros.
+ *   o, z, weight, eps: as gdn_gated_rmsnorm (o and z aligned to 4 elements,
+ *      z_row_stride a multiple of 4), in `dtype`.
+ *   y: [n_tokens][hv][dv] e4m3, contiguous, 8-byte aligned; y_scale:
+ *      [n_tokens] fp32.
+ * Built: dv in {16, 32, 64, 128, 256}, hv * dv <= 16384.
+ */
+gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_stride,
+                                   const float *weight, int64_t n_tokens, int32_t hv,
+                                   int32_t dv, float eps, void *y, float *y_scale,
+                                   int32_t dtype, void *stream);
+
+/*
+ * The block's input norm: the residual's addition and the RMSNorm of the sum
+ * ("RMSNorm" and the (1 + w)-scaled "Gemma RMSNorm", "[model] Support
+ * Qwen3next", LightLLM issue 1097, Highlights).  Per token row
+ *   s = x + residual                  (in fp32; s = x without a residual)
+ *   residual_out = s                  (rounded once to `dtype`)
+ *   v = s / sqrt(mean(s^2) + eps) * (weight_offset + weight)
+ *   y = v, or with y_dtype == GDN_E4M3
+ *   y_scale = max(max |v| / 448, 2^-126) and y = v / y_scale rounded to e4m3.
+ * A row with a NaN or an infinity gives NaNs in its y; one of zeros zeros
+ * (eps > 0).
+ *   x, residual, residual_out: rows of `hidden` elements in `dtype`, each with
+ *      its own row stride (>= hidden).  residual, residual_out: NULL leaves
+ *      them out.  residual_out may be residual or x (same pointer and stride).
+ *   weight: [hidden] fp32; weight_offset: 0, or 1 for the (1 + w) form.
+ *   y: rows of `hidden` elements in y_dtype (`dtype` or GDN_E4M3), row stride
+ *      y_row_stride; y may be x or residual (same pointer and stride) when
+ *      y_dtype == dtype.  y_scale: [n_tokens] fp32 with GDN_E4M3, else NULL.
+ * Any alignment of whole elements is taken; rows on 16-byte boundaries (and
+ * hidden a multiple of 16 bytes) run on vector accesses.
+ * Built: hidden <= 16384.
+ */
+gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *residual,
+                           int64_t residual_row_stride, const float *weight,
+                           float weight_offset, int64_t n_tokens, int32_t hidden,
+                           float eps, void *residual_out,
+                           int64_t residual_out_row_stride, void *y,
+                           int64_t y_row_stride, float *y_scale, int32_t dtype,
+                           int32_t y_dtype, void *stream);
+
+/*
+ * Matrix product of a projection, with its epilogue:
+ *   y[t][n] = act(x_scale[t] w_scale[n] sum_k x[t][k] w[n][k] + bias[n])
+ *             + residual[t][n]
+ * accumulated in fp32 by the tensor cores and rounded once, to y_dtype.  It
+ * makes the layer's inputs (the q|k|v stream, z, a, b) from the hidden state
+ * and the hidden state from the layer's output; x and w in 8 bits take the
+ * outputs of gdn_add_rmsnorm and gdn_gated_rmsnorm_quant with their scales.
+ *   x: [n_tokens] rows of n_in elements, w: [n_out] rows of n_in elements,
+ *      both in `dtype` (GDN_BF16 or GDN_E4M3), 16-byte aligned, row strides in
+ *      elements and multiples of 16 bytes (of any size >= n_in: n_in itself
+ *      may be odd).  What lies between n_in and the stride is not read.
+ *   x_scale [n_tokens], w_scale [n_out]: fp32, NULL = 1.
+ *   bias: [n_out] fp32 or NULL.  act: gdn_act.
+ *   residual: rows of n_out elements in y_dtype, or NULL.
+ *   y: rows of n_out elements, GDN_BF16 or GDN_F32, row stride y_row_stride
+ *      (>= n_out: y may be columns of a wider buffer).  y may be residual
+ *      (same pointer and stride); it must not overlap x or w.
+ * The result of a row does not depend on the other rows or on the call's
+ * timing; it may differ in the last fp32 bits between numbers of tokens (the
+ * order of the sum over k follows the tile that the sizes choose).
+ * Built: GDN_BF16 and GDN_E4M3 operands; n_tokens <= 16,776,960.
+ */
+gdn_status gdn_linear(const void *x, int64_t x_row_stride, const float *x_scale,
+                      const void *w, int64_t w_row_stride, const float *w_scale,
+                      const float *bias, const void *residual,
+                      int64_t residual_row_stride, int64_t n_tokens, int32_t n_in,
+                      int32_t n_out, int32_t act, void *y, int64_t y_row_stride,
+                      int32_t dtype, int32_t y_dtype, void *stream);
 
 /*
  * gdn_decode_recurrent with the gated RMSNorm above fused into its output:

@@ -295,3 +295,89 @@ def test_prefill_layer_gated_host_checks(lib):
     assert f(*bad) == 1
     bad = list(base); bad[13] = 0; bad[14] = 0   # empty: no launch
     assert f(*bad) == 0
+
+
+def test_add_rmsnorm_host_checks(lib):
+    """Bad types, sizes, strides, a scale without an 8-bit output and the
+    other way round, misaligned elements: refused on the host."""
+    f = lib.gdn_add_rmsnorm
+    f.argtypes = [V, I64, V, I64, V, F32, I64, I32, F32, V, I64, V, I64, V, I32, I32, V]
+    A = 1 << 20
+    base = [A, 64, A, 64, A, 0.0, 4, 64, 1e-6, A, 64, A, 64, None, 1, 1, None]
+
+    def rc(**at):
+        a = list(base)
+        for k, v in at.items():
+            a[int(k[1:])] = v
+        return f(*a)
+
+    assert rc(_14=2) == 1 and rc(_14=7) == 1            # an 8-bit stream, an unknown type
+    assert rc(_15=0) == 1 and rc(_15=5) == 1            # y neither the stream's type nor e4m3
+    assert rc(_6=-1) == 1 and rc(_7=0) == 1 and rc(_8=-1e-6) == 1
+    assert rc(_8=float("nan")) == 1
+    assert rc(_7=16385, _1=20000, _3=20000, _10=20000, _12=20000) == 2
+    assert rc(_6=1 << 31) == 2
+    assert rc(_0=None) == 1 and rc(_4=None) == 1 and rc(_11=None) == 1
+    assert rc(_1=63) == 1 and rc(_3=63) == 1 and rc(_10=63) == 1 and rc(_12=63) == 1
+    assert rc(_15=2) == 1 and rc(_13=A) == 1            # e4m3 without scales, scales without e4m3
+    assert rc(_0=A + 1) == 1 and rc(_2=A + 1) == 1 and rc(_9=A + 1) == 1 and rc(_4=A + 2) == 1
+    assert rc(_0=None, _6=0) == 0                       # no rows: no launch
+
+
+def test_gated_rmsnorm_quant_host_checks(lib):
+    f = lib.gdn_gated_rmsnorm_quant
+    f.argtypes = [V, V, I64, V, I64, I32, I32, F32, V, V, I32, V]
+    A = 1 << 20
+    assert f(A, A, 512, A, 4, 4, 96, 1e-6, A, A, 1, None) == 2          # dv 96 not built
+    assert f(A, A, 16640, A, 4, 65, 256, 1e-6, A, A, 1, None) == 2      # past 16384 values a token
+    assert f(A, A, 512, A, 4, 4, 128, 1e-6, A, A, 2, None) == 1         # an 8-bit input
+    assert f(A, A, 512, A, 4, 4, 128, -1.0, A, A, 1, None) == 1
+    assert f(A, A, 512, A, 4, 4, 128, float("nan"), A, A, 1, None) == 1
+    assert f(A, A, 500, A, 4, 4, 128, 1e-6, A, A, 1, None) == 1         # stride < hv * dv
+    assert f(A, A + 2, 512, A, 4, 4, 128, 1e-6, A, A, 1, None) == 1     # z not 4-element aligned
+    assert f(A, A, 514, A, 4, 4, 128, 1e-6, A, A, 1, None) == 1
+    assert f(A, A, 512, A, 4, 4, 128, 1e-6, A + 4, A, 1, None) == 1     # y not 8-byte aligned
+    assert f(A, A, 512, A, 4, 4, 128, 1e-6, A, None, 1, None) == 1      # no scales
+    assert f(A, A, 512, A, -1, 4, 128, 1e-6, A, A, 1, None) == 1
+    assert f(None, None, 512, None, 0, 4, 128, 1e-6, None, None, 1, None) == 0
+
+
+def test_linear_host_checks(lib):
+    f = lib.gdn_linear
+    f.argtypes = [V, I64, V, V, I64, V, V, V, I64, I64, I32, I32, I32, V, I64, I32, I32, V]
+    A = 1 << 20
+    base = [A, 64, None, A, 64, None, None, None, 0, 4, 64, 96, 0, A, 96, 1, 1, None]
+
+    def rc(**at):
+        a = list(base)
+        for k, v in at.items():
+            a[int(k[1:])] = v
+        return f(*a)
+
+    assert rc(_15=0) == 2                               # fp32 operands are not built
+    assert rc(_15=3) == 1 and rc(_16=2) == 1 and rc(_16=-1) == 1
+    assert rc(_12=3) == 1 and rc(_12=-1) == 1           # activation
+    assert rc(_9=-1) == 1 and rc(_10=0) == 1 and rc(_11=0) == 1
+    assert rc(_9=65535 * 256 + 1) == 2
+    assert rc(_0=None) == 1 and rc(_3=None) == 1 and rc(_13=None) == 1
+    assert rc(_1=63) == 1 and rc(_4=63) == 1 and rc(_14=95) == 1
+    assert rc(_7=A, _8=95) == 1                         # residual rows overlap
+    assert rc(_0=A + 8) == 1 and rc(_3=A + 8) == 1      # operands not on 16 bytes
+    assert rc(_1=68) == 1 and rc(_4=68) == 1            # ... nor their rows
+    assert rc(_15=2, _1=72) == 1                        # 8 bits: multiples of 16
+    assert rc(_13=A + 1) == 1 and rc(_6=A + 2) == 1 and rc(_2=A + 2) == 1 and rc(_5=A + 1) == 1
+    assert rc(_0=None, _9=0) == 0                       # no rows: no launch
+
+
+def test_block_binding_refuses_before_the_library():
+    """The Python checks of the block operators on CPU tensors: a clear error, nothing launched."""
+    import torch
+
+    import gated_deltanet_linear_10_gb300 as gdn
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(gdn.GdnError, match="CUDA"):
+        gdn.gdn_add_rmsnorm(x, torch.ones(64))
+    with pytest.raises(gdn.GdnError, match="CUDA"):
+        gdn.gdn_linear(x, x)
+    with pytest.raises(gdn.GdnError, match="CUDA"):
+        gdn.gdn_gated_rmsnorm_quant(x.view(2, 2, 32), x.view(2, 2, 32), torch.ones(32))
