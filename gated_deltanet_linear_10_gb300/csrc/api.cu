@@ -9,7 +9,8 @@ namespace gdn {
 
 GDN_DECLARE_STATUS_WORD(g_status_api)
 gdn_status read_status_norm(uint32_t *out, int clear, cudaStream_t s);   // rmsnorm.cu
-gdn_status read_status_linear(uint32_t *out, int clear, cudaStream_t s); // linear.cu
+gdn_status read_status_linear(uint32_t *out, int clear, cudaStream_t s);        // linear.cu
+gdn_status read_status_linear_wide(uint32_t *out, int clear, cudaStream_t s);   // linear_wide.cu
 GDN_STATUS_READER(read_status_api, g_status_api)
 
 static thread_local char t_last_err[256] = "";
@@ -106,6 +107,7 @@ gdn_status gdn_get_device_status(uint32_t *out, int32_t clear, void *stream) {
     if ((st = read_status_prefill_scan(out, clear, s)) != GDN_OK) return st;
     if ((st = read_status_mtp_step(out, clear, s)) != GDN_OK) return st;
     if ((st = read_status_linear(out, clear, s)) != GDN_OK) return st;
+    if ((st = read_status_linear_wide(out, clear, s)) != GDN_OK) return st;
     return GDN_OK;
 }
 

@@ -174,6 +174,7 @@ static gdn_status launch_narrow(const LinearCall &c) {
 
 template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
     const int t = c.e.n_tokens;
+    if (t >= 512) return launch_linear_wide(c, kE4m3);
     if (t <= 16) return launch_narrow<16, kE4m3>(c);
     if (t <= 32) return launch_narrow<32, kE4m3>(c);
     if (t <= 64) return launch_narrow<64, kE4m3>(c);

@@ -64,4 +64,6 @@ struct LinearCall {
     cudaStream_t stream;
 };
 
+gdn_status launch_linear_wide(const LinearCall &c, bool e4m3);   // linear_wide.cu
+
 }  // namespace gdn
