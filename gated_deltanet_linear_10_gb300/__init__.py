@@ -691,39 +691,45 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-6, y=None):
     return y
 
 
-def _same_device(first, *ts):
+def _one_device(first, *ts):
     """Every tensor on the CUDA device of the first one; returns its index."""
-    _need(first.is_cuda, "all tensors must be on a CUDA device")
     dev = first.get_device()
     for t in ts:
-        if t is not None:
-            _need(t.get_device() == dev, "all tensors must be on one CUDA device")
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise GdnError("all tensors must be on one CUDA device")
     return dev
 
 
 def _call(fn, name, dev, *args):
-    """fn on the current stream of device `dev`, which becomes the current one for the call."""
-    if dev == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+    """fn on the current stream of device `dev`, which is made the current device for the call."""
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status, name)
 
 
 def _rows(t, T, n, name):
-    """t is [T, n] with unit column stride; returns its row stride (n where T = 1)."""
-    _need(t.dim() == 2 and t.shape[0] == T and t.shape[1] == n, f"{name}: [{T}, {n}]")
-    _need(n == 1 or t.stride(1) == 1, f"{name}: unit column stride")
-    st = t.stride(0)
-    if T <= 1:
-        return max(n, st)
-    _need(st >= n, f"{name}: rows must not overlap")
+    """t is [T, n] with unit column stride; returns its row stride (at least n where T is 1)."""
+    if t.shape != (T, n):
+        raise GdnError(f"{name}: shape {tuple(t.shape)}, not [{T}, {n}]")
+    st, one = t.stride()
+    if one != 1 and n != 1:
+        raise GdnError(f"{name}: unit column stride")
+    if st < n:
+        if T > 1:
+            raise GdnError(f"{name}: rows must not overlap")
+        return n
     return st
 
 
 def _f32_vec(t, n, name):
-    _need(t.dtype == torch.float32 and t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1),
-          f"{name}: [{n}] fp32, contiguous")
+    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise GdnError(f"{name}: [{n}] fp32, contiguous")
     return t.data_ptr()
 
 
@@ -736,7 +742,7 @@ def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, y_dty
     being the norm.  Returns (y, y_scale or None, residual_out or None), where
     residual_out [T, H] is s in x's dtype, made when a residual is given (pass
     residual_out=residual to update the stream in place)."""
-    dev = _same_device(x, weight, residual, residual_out, y, y_scale)
+    dev = _one_device(x, weight, residual, residual_out, y, y_scale)
     _need(x.dim() == 2, "x: [T, H]")
     T, H = x.shape
     xs, dt = _rows(x, T, H, "x"), _dtype_code(x)
@@ -775,7 +781,7 @@ def gdn_gated_rmsnorm_quant(o, z, weight, eps=1e-6, y=None, y_scale=None):
     the gated norm.  o [T, hv, dv] contiguous; z [T, hv, dv] or [T, hv*dv] (a
     view with a free row stride); weight [dv] fp32.  y viewed as [T, hv*dv] is
     gdn_linear's 8-bit x."""
-    dev = _same_device(o, z, weight, y, y_scale)
+    dev = _one_device(o, z, weight, y, y_scale)
     _need(o.dim() == 3 and o.is_contiguous(), "o: [T, hv, dv] contiguous")
     T, hv, dv = o.shape
     zs = _heads_view(z, hv, dv, "z")
@@ -799,7 +805,7 @@ def gdn_linear(x, weight, x_scale=None, weight_scale=None, bias=None, act="none"
     boundaries (K itself may be odd).  bias [N] fp32; act "none", "silu" or
     "gelu"; residual [T, N] in y's dtype.  y [T, N] bf16 (default) or fp32,
     columns of a wider buffer if wanted; y may be residual.  Returns y."""
-    dev = _same_device(x, weight, x_scale, weight_scale, bias, residual, y)
+    dev = _one_device(x, weight, x_scale, weight_scale, bias, residual, y)
     _need(x.dim() == 2 and weight.dim() == 2, "x: [T, K], weight: [N, K]")
     T, K = x.shape
     N = weight.shape[0]
@@ -813,7 +819,7 @@ def gdn_linear(x, weight, x_scale=None, weight_scale=None, bias=None, act="none"
     sxp = None if x_scale is None else _f32_vec(x_scale, T, "x_scale")
     swp = None if weight_scale is None else _f32_vec(weight_scale, N, "weight_scale")
     bp = None if bias is None else _f32_vec(bias, N, "bias")
-    _need(act in ACTIVATIONS, f"act: one of {tuple(ACTIVATIONS)}")
+    _need(act in ACTIVATIONS, "act: none, silu or gelu")
     if y is None:
         y = torch.empty((T, N), dtype=torch.bfloat16 if y_dtype is None else y_dtype, device=x.device)
     _need(y_dtype is None or y.dtype == y_dtype, "y: y_dtype")

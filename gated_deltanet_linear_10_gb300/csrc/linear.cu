@@ -26,97 +26,141 @@ bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64
                           base, cols, rows, row_stride_elems * elem, 128 / elem, box_rows, true);
 }
 
-// BT: tokens per tile (the product's N).  One CTA per 128 x BT tile.
+// BT: tokens per tile (the product's N).  A cluster of `splits` CTAs per
+// 128 x BT tile, each on its part of k.
 template <int BT> struct NarrowCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
-    static constexpr int kStages = BT >= 256 ? 4 : BT >= 128 ? 6 : 8;
-    static constexpr uint32_t kSmem = kStages * kStage + 1024;
-    static constexpr uint32_t kCols = BT < 32 ? 32 : BT;
+    static constexpr int kStages = 4;
+    static constexpr uint32_t kSums = BT * 512;          // BT tokens x 128 channels, fp32
+    static constexpr uint32_t kSmem = kStages * kStage + kSums + 1024;
+    static_assert(kStages * kStage >= kSums, "a CTA's own sums fit its stages");
 };
+constexpr int kNarrowThreads = 192;
 
-// COLS accumulator columns of one weight row n, tokens t0 ..: scale, bias,
-// activation, residual, store.  A warp's 32 lanes are 32 consecutive n.  The
-// residual is read for all columns before the first store (y may be residual).
-template <int COLS, int kAct, typename O>
-__device__ __forceinline__ void narrow_store(const uint32_t (&r)[32], const LinearEpi &ep, int n,
-                                             int t0, float swn, float bn) {
-    O *y = reinterpret_cast<O *>(ep.y) + t0 * ep.ys + n;
-    const O *res = reinterpret_cast<const O *>(ep.res) + t0 * ep.rs + n;
-    const int cnt = min(COLS, ep.n_tokens - t0);
-    float rv[COLS];
+// Copy of this CTA's shared memory into another CTA's of the cluster, its bytes
+// counted on a barrier of that CTA (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_send(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "r"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// 8 channels n .. n + 7 of token t: scale, bias, activation, residual, one
+// rounding.  y may be residual: the 8 are read before they are written.
+template <typename O>
+__device__ __forceinline__ void narrow_out8(float (&v)[8], const LinearEpi &ep, int t, int n, const float *sw,
+                                            const float *bias) {
+    const float sx = ep.sx ? ep.sx[t] : 1.0f;
 #pragma unroll
-    for (int j = 0; j < COLS; ++j) rv[j] = ep.res && j < cnt ? Io<O>::load(res + j * ep.rs) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sx * sw[i], bias[i]);
+    if (ep.act == GDN_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < COLS; ++j) {
-        if (j < cnt) {
-            const float sc = ep.sx ? ep.sx[t0 + j] * swn : swn;
-            Io<O>::store(y + j * ep.ys, linear_act<kAct>(fmaf(__uint_as_float(r[j]), sc, bn)) + rv[j]);
+        for (int i = 0; i < 8; ++i) v[i] = linear_act<GDN_ACT_SILU>(v[i]);
+    } else if (ep.act == GDN_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = linear_act<GDN_ACT_GELU>(v[i]);
+    }
+    O *y = reinterpret_cast<O *>(ep.y) + t * ep.ys + n;
+    const O *res = reinterpret_cast<const O *>(ep.res) + t * ep.rs + n;
+    if (ep.vec8 && n + 8 <= ep.n_out) {
+        if (ep.res) {
+            RawVec<O, 8> q;
+            float r[8];
+            q.load(res);
+            q.get(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
         }
+        store_row<8>(y, v);
+    } else {
+        const int cnt = min(8, ep.n_out - n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (ep.res && i < cnt) v[i] += Io<O>::load(res + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cnt) Io<O>::store(y + i, v[i]);
     }
 }
 
-template <int COLS, typename O>
-__device__ __forceinline__ void narrow_store_act(const uint32_t (&r)[32], const LinearEpi &ep, int n,
-                                                 int t0, float swn, float bn) {
-    if (ep.act == GDN_ACT_SILU) narrow_store<COLS, GDN_ACT_SILU, O>(r, ep, n, t0, swn, bn);
-    else if (ep.act == GDN_ACT_GELU) narrow_store<COLS, GDN_ACT_GELU, O>(r, ep, n, t0, swn, bn);
-    else narrow_store<COLS, GDN_ACT_NONE, O>(r, ep, n, t0, swn, bn);
-}
-
+// grid (channel tiles * splits, token tiles); the `splits` CTAs of a tile are a
+// cluster, CTA r of it on the k blocks [r nk / splits, (r + 1) nk / splits).
+// Its sums go from tensor memory to its shared memory as rows of 128 channels.
+// With splits > 1, CTA r collects the tokens [r BT / splits, (r + 1) BT / splits)
+// of every CTA by bulk copies and adds them in the order of the CTAs, so the
+// result has one order of sums; with one, it has them all.  Then 16 threads
+// write a token's 128 channels.
+//
+// The code behind the products runs once per CTA, so it is kept short and
+// rolled: unrolled over 32 tokens with its variants it took 3 to 20 us of
+// instruction fetches and dependent loads at 256 tokens.
 template <int BT, bool kE4m3>
-__global__ void __launch_bounds__(192)
+__global__ void __launch_bounds__(kNarrowThreads)
 linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                     const __grid_constant__ LinearEpi ep, int n_in) {
+                     const __grid_constant__ LinearEpi ep, int n_in, int splits) {
     using C = NarrowCfg<BT>;
+    constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], done;
+    __shared__ uint64_t full[S], empty[S], done, arrived;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int n0 = blockIdx.x * 128, t0 = blockIdx.y * BT;
+    const int rank = splits > 1 ? (int)cta_rank() : 0;
+    const int n0 = blockIdx.x / splits * 128, t0 = blockIdx.y * BT;
     constexpr int kElems = kE4m3 ? 128 : 64;                 // k per block of 128 bytes
-    const int nk = (n_in + kElems - 1) / kElems;
+    const int blocks = (n_in + kElems - 1) / kElems;
+    const int k0 = (int)((int64_t)blocks * rank / splits);
+    const int nk = (int)((int64_t)blocks * (rank + 1) / splits) - k0;
+    volatile int *abort = &abort_flag;
+    auto load = [&](int i) {
+        const int s = i % S;
+        uint8_t *st = smem + s * C::kStage;
+        mbar_arrive_expect_tx(&full[s], C::kStage);
+        tma_load_2d(st, &mw, &full[s], (k0 + i) * kElems, n0);
+        tma_load_2d(st + C::kW, &mx, &full[s], (k0 + i) * kElems, t0);
+    };
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&mx);
         prefetch_tensormap(&mw);
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(&done, 1);
+        mbar_init(&arrived, 1);
         abort_flag = 0;
         fence_mbar_init();
+        fence_async_smem();
+        griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
+        for (int i = 0; i < min(S, nk); ++i) load(i);
     }
+    __syncwarp();
     if (warp == 1) {
-        tmem_alloc(&tmem_base, C::kCols);
+        tmem_alloc(&tmem_base, BT);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
-    volatile int *abort = &abort_flag;
+    if (splits > 1) cluster_arrive();      // waited for before the first copy to another CTA
+    griddep_wait();
 
     if (warp == 0 && lane == 0) {
-        int i = 0;
+        int i = S;
         for (; i < nk; ++i) {
-            const int s = i % C::kStages;
-            if (i >= C::kStages && !mbar_wait(&empty[s], ((i / C::kStages) - 1) & 1, abort)) break;
-            uint8_t *st = smem + s * C::kStage;
-            mbar_arrive_expect_tx(&full[s], C::kStage);
-            tma_load_2d(st, &mw, &full[s], i * kElems, n0);
-            tma_load_2d(st + C::kW, &mx, &full[s], i * kElems, t0);
+            if (!mbar_wait(&empty[i % S], ((i / S) - 1) & 1, abort)) break;
+            load(i);
         }
         if (*abort)
-            for (int j = i > C::kStages ? i - C::kStages : 0; j < i; ++j)
-                mbar_drain(&full[j % C::kStages], (j / C::kStages) & 1);
+            for (int j = i - S; j < min(i, nk); ++j) mbar_drain(&full[j % S], (j / S) & 1);
     } else if (warp == 1 && lane == 0) {
         constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
         for (int i = 0; i < nk; ++i) {
-            const int s = i % C::kStages;
-            if (!mbar_wait(&full[s], (i / C::kStages) & 1, abort)) break;
+            const int s = i % S;
+            if (!mbar_wait(&full[s], (i / S) & 1, abort)) break;
             tc_fence_after();
             const uint32_t st = smem_u32(smem + s * C::kStage);
 #pragma unroll
@@ -127,29 +171,80 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         }
         mma_commit(&done);
         mbar_drain(&done, 0);
-    } else if (warp >= 2) {
-        // lane l of the quadrant q reads accumulator lane 32 q + l: one weight row
-        const uint32_t quad = warp & 3;
-        const int n = n0 + quad * 32 + lane;
-        const bool on = n < ep.n_out;
-        const float swn = on && ep.sw ? ep.sw[n] : 1.0f;
-        const float bn = on && ep.bias ? ep.bias[n] : 0.0f;
-        if (mbar_wait(&done, 0, abort)) {
-            tc_fence_after();
-            constexpr int COLS = BT < 32 ? BT : 32;
-            for (int c = 0; c < BT && t0 + c < ep.n_tokens; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem_addr(tmem_base, quad * 32, c), r);   // at least 32 columns are allocated
-                if (!on) continue;
-                if (ep.out_f32) narrow_store_act<COLS, float>(r, ep, n, t0 + c, swn, bn);
-                else narrow_store_act<COLS, __nv_bfloat16>(r, ep, n, t0 + c, swn, bn);
-            }
+    }
+    __syncwarp();
+
+    const int per = BT / splits;                         // tokens that a CTA collects
+    const int first = t0 + rank * per, cnt = min(per, ep.n_tokens - first);   // those it writes (cnt <= 0: none)
+    float *own = reinterpret_cast<float *>(smem);        // where the operands were
+    float *got = reinterpret_cast<float *>(smem + S * C::kStage);
+    const int g = tid & 15, n = n0 + g * 8;              // this thread's channels below
+    float sw[8], bias[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool on = n + i < ep.n_out;
+        sw[i] = on && ep.sw ? ep.sw[n + i] : 1.0f;
+        bias[i] = on && ep.bias ? ep.bias[n + i] : 0.0f;
+    }
+    if (warp >= 2 && __all_sync(0xffffffffu, mbar_wait(&done, 0, abort))) {
+        // accumulator lane 32 q + l is channel n0 + 32 q + l, its columns the tokens
+        tc_fence_after();
+        const int quad = warp & 3;
+        float *col = own + quad * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < BT && t0 + c < ep.n_tokens; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tmem_addr(tmem_base, quad * 32, c), r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) col[(c + j) * 128] = __uint_as_float(r[j]);
         }
         tc_fence_before();
+        fence_async_smem();
+    }
+    if (splits > 1) {
+        __syncwarp();
+        cluster_wait();                                  // every CTA of the cluster has its barriers
     }
     __syncthreads();
+    if (splits > 1) {
+        if (tid == 0 && !*abort) {
+            if (cnt > 0) mbar_arrive_expect_tx(&arrived, (splits - 1) * cnt * 512);
+            for (int o = 1; o < splits; ++o) {           // each starts with another one
+                const int to = (rank + o) & (splits - 1);
+                const int tokens = min(per, ep.n_tokens - t0 - to * per);
+                if (tokens > 0)
+                    bulk_send(peer_smem(smem_u32(got + rank * per * 128), to), smem_u32(own + to * per * 128),
+                              tokens * 512, peer_smem(smem_u32(&arrived), to));
+            }
+        }
+        if (cnt > 0 && !mbar_wait(&arrived, 0, abort)) mbar_drain(&arrived, 0);
+        __syncwarp();
+        cluster_arrive();                                // this CTA has what was sent to it
+    }
+    if (!*abort) {
+#pragma unroll 1
+        for (int i = tid; i < cnt * 16; i += kNarrowThreads) {
+            const int tok = i >> 4;
+            float v[8] = {};
+#pragma unroll 1
+            for (int r = 0; r < splits; ++r) {
+                const float *p = (r == rank ? own : got) + (r * per + tok) * 128 + g * 8;
+                const float4 a = *reinterpret_cast<const float4 *>(p);
+                const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+            }
+            if (n < ep.n_out) {
+                if (ep.out_f32) narrow_out8<float>(v, ep, first + tok, n, sw, bias);
+                else narrow_out8<__nv_bfloat16>(v, ep, first + tok, n, sw, bias);
+            }
+        }
+    }
+    __syncwarp();
+    if (splits > 1) cluster_wait();                      // and the others what it sent
+    __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, C::kCols);
+    if (warp == 1) tmem_dealloc(tmem_base, BT);
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
@@ -160,11 +255,17 @@ static gdn_status launch_narrow(const LinearCall &c) {
     if (!encode_tmap_operand(&mx, c.x, c.n_in, c.e.n_tokens, c.xs, BT, kE4m3) ||
         !encode_tmap_operand(&mw, c.w, c.n_in, c.e.n_out, c.ws, 128, kE4m3))
         return GDN_ERR_CUDA;
+    // as many CTAs as there are SMs, by cutting k: powers of two up to the 8
+    // CTAs of a portable cluster, each with at least two k blocks
+    const int nn = (c.e.n_out + 127) / 128, nt = (c.e.n_tokens + BT - 1) / BT;
+    const int blocks = (c.n_in + (kE4m3 ? 127 : 63)) / (kE4m3 ? 128 : 64), sms = sm_count();
+    int splits = 1;
+    while (splits < 8 && (int64_t)nn * nt * splits * 2 <= sms && blocks >= splits * 4) splits *= 2;
     auto kernel = linear_narrow_kernel<BT, kE4m3>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
-        e = launch_after(kernel, dim3((c.e.n_out + 127) / 128, (c.e.n_tokens + BT - 1) / BT), dim3(192),
-                         C::kSmem, c.stream, mx, mw, c.e, c.n_in);
+        e = launch_after_cluster(kernel, splits, dim3(nn * splits, nt), dim3(kNarrowThreads), C::kSmem, c.stream, mx, mw,
+                                 c.e, c.n_in, splits);
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return GDN_ERR_LAUNCH;
@@ -175,11 +276,9 @@ static gdn_status launch_narrow(const LinearCall &c) {
 template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
     const int t = c.e.n_tokens;
     if (t >= 512) return launch_linear_wide(c, kE4m3);
-    if (t <= 16) return launch_narrow<16, kE4m3>(c);
     if (t <= 32) return launch_narrow<32, kE4m3>(c);
     if (t <= 64) return launch_narrow<64, kE4m3>(c);
-    if (t <= 128) return launch_narrow<128, kE4m3>(c);
-    return launch_narrow<256, kE4m3>(c);
+    return launch_narrow<128, kE4m3>(c);
 }
 
 }  // namespace gdn
@@ -222,6 +321,9 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     c.n_in = n_in;
     c.stream = (cudaStream_t)stream;
     c.e = {x_scale, w_scale, bias, residual, residual_row_stride, y, y_row_stride,
-           (int)n_tokens, n_out, act, y_dtype == GDN_F32};
+           (int)n_tokens, n_out, act, y_dtype == GDN_F32, false};
+    // 8 channels at a time: 16 bytes of bf16, 32 of fp32
+    c.e.vec8 = (uintptr_t)y % 16 == 0 && y_row_stride * (int64_t)ye % 16 == 0 &&
+               (!residual || ((uintptr_t)residual % 16 == 0 && residual_row_stride * (int64_t)ye % 16 == 0));
     return dtype == GDN_E4M3 ? launch_linear<true>(c) : launch_linear<false>(c);
 }

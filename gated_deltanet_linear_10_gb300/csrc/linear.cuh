@@ -16,6 +16,7 @@ struct LinearEpi {
     int64_t ys;
     int n_tokens, n_out, act;
     bool out_f32;
+    bool vec8;            // rows of y and residual on 16-byte boundaries
 };
 
 template <int kAct> __device__ __forceinline__ float linear_act(float v) {
@@ -44,6 +45,31 @@ __device__ __forceinline__ void linear_mma(uint32_t d, uint64_t a, uint64_t b, u
         tc::mma_ss(d, a, b, idesc, accumulate);
 }
 
+// ------------------------------------------------------------ clusters --
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    cluster_arrive();
+    cluster_wait();
+}
+// Address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 // mbar_wait for a copy or product that is in flight already when the CTA has
 // given up: it does not return at once on the abort flag, but it is bounded.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
@@ -55,6 +81,27 @@ __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
 // (e4m3), loaded as boxes of 128 bytes x box_rows in the 128-byte swizzle.
 bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64_t rows,
                          int64_t row_stride_elems, uint32_t box_rows, bool e4m3);
+
+// launch_after with clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_after_cluster(void (*kernel)(KArgs...), int cluster, dim3 grid, dim3 block,
+                                        size_t smem, cudaStream_t s, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 struct LinearCall {
     const void *x, *w;

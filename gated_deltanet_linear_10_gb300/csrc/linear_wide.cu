@@ -39,24 +39,6 @@ template <int BN> struct WideCfg {
     static constexpr uint32_t kCols = 2 * BN;
 };
 
-__device__ __forceinline__ uint32_t cta_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-// Address of the same shared variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
 // Tiled load into this CTA's shared memory, its bytes counted on a barrier of
 // either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar,
@@ -122,6 +104,38 @@ template <> __device__ __forceinline__ void add_chunk<float>(float *v, const uin
     Vec16<float>::unpack(q, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += f[i];
+}
+
+// 32 rows of 128 bytes between a staging buffer and memory that TMA cannot
+// address, element by element: a warp's lanes take consecutive elements, and
+// 16 rows are in flight at a time.
+template <typename O, bool kLoad>
+__device__ __forceinline__ void plain_rows(uint8_t *buf, O *p, int64_t stride, int t0, int n0,
+                                           int n_tokens, int n_out, int lane) {
+    constexpr int COLS = 128 / sizeof(O), PART = COLS / 32, ROWS = 16;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += ROWS) {
+        if (t0 + r0 >= n_tokens) break;
+        O v[ROWS][PART];
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int c = 0; c < PART; ++c) {
+                    const int col = c * 32 + lane, t = t0 + r0 + r;
+                    const bool on = t < n_tokens && n0 + col < n_out;
+                    const uint32_t off = col * sizeof(O);
+                    O *in_buf = reinterpret_cast<O *>(
+                        buf + (r0 + r) * 128 + (((off >> 4) ^ ((r0 + r) & 7)) << 4) + (off & 15));
+                    O *in_mem = p + t * stride + n0 + col;
+                    if (pass == 0) {
+                        if (on) v[r][c] = kLoad ? *in_mem : *in_buf;
+                    } else if (on) {
+                        *(kLoad ? in_buf : in_mem) = v[r][c];
+                    }
+                }
+    }
 }
 
 struct WideFlags {
@@ -301,7 +315,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             const float sx = ep.sx && t < ep.n_tokens ? ep.sx[t] : 1.0f;
             if (lane == 0) bulk_wait_read<2>();
             if (res_tma) ask(sl, n0, t0);
-            if (!mbar_wait(&acc_full[b], (u >> 1) & 1, abort)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (u >> 1) & 1, abort))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int s = 0; s < SLICES; ++s, ++sl) {
@@ -314,20 +328,11 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 if (has_res) {
                     if (res_tma) {
                         if (s + 1 < SLICES) ask(sl + 1, nc + COLS, t0);
-                        if (mbar_wait(&rbar[sl % kStagingBufs], (sl / kStagingBufs) & 1, abort)) ++seen;
+                        if (__all_sync(0xffffffffu, mbar_wait(&rbar[sl % kStagingBufs], (sl / kStagingBufs) & 1, abort)))
+                            ++seen;
                     } else {
-                        const O *res = reinterpret_cast<const O *>(ep.res);
-#pragma unroll 4
-                        for (int r = 0; r < 32; ++r)
-#pragma unroll
-                            for (int c = 0; c < COLS; c += 32) {
-                                const int col = c + lane;
-                                if (t0 + r < ep.n_tokens && nc + col < ep.n_out) {
-                                    const uint32_t off = col * sizeof(O);
-                                    *reinterpret_cast<O *>(buf + r * 128 + (((off >> 4) ^ (r & 7)) << 4) +
-                                                           (off & 15)) = res[(t0 + r) * ep.rs + nc + col];
-                                }
-                            }
+                        plain_rows<O, true>(buf, reinterpret_cast<O *>(const_cast<void *>(ep.res)), ep.rs,
+                                            t0, nc, ep.n_tokens, ep.n_out, lane);
                         __syncwarp();
                     }
                 }
@@ -353,18 +358,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     }
                 } else {
                     __syncwarp();
-                    O *y = reinterpret_cast<O *>(ep.y);
-#pragma unroll 4
-                    for (int r = 0; r < 32; ++r)
-#pragma unroll
-                        for (int c = 0; c < COLS; c += 32) {
-                            const int col = c + lane;
-                            if (t0 + r < ep.n_tokens && nc + col < ep.n_out) {
-                                const uint32_t off = col * sizeof(O);
-                                y[(t0 + r) * ep.ys + nc + col] = *reinterpret_cast<const O *>(
-                                    buf + r * 128 + (((off >> 4) ^ (r & 7)) << 4) + (off & 15));
-                            }
-                        }
+                    plain_rows<O, false>(buf, reinterpret_cast<O *>(ep.y), ep.ys, t0, nc, ep.n_tokens,
+                                         ep.n_out, lane);
                     // the next user of the buffer may be a copy of the async proxy
                     fence_async_smem();
                     __syncwarp();
