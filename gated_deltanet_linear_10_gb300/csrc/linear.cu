@@ -156,21 +156,28 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         }
         if (*abort)
             for (int j = i - S; j < min(i, nk); ++j) mbar_drain(&full[j % S], (j / S) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
+        const bool one = elect_lane();
+        const uint64_t desc = sdesc_sw128(0, 0, 1024);
         for (int i = 0; i < nk; ++i) {
             const int s = i % S;
-            if (!mbar_wait(&full[s], (i / S) & 1, abort)) break;
+            if (!mbar_wait_all(&full[s], (i / S) & 1, abort)) break;
             tc_fence_after();
-            const uint32_t st = smem_u32(smem + s * C::kStage);
+            if (one) {
+                const uint32_t st = smem_u32(smem + s * C::kStage) >> 4;
+                const uint64_t da = desc | st, db = desc | (st + (C::kW >> 4));
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                linear_mma<kE4m3>(tmem_base, sdesc_sw128(st + k * 32, 0, 1024),
-                                  sdesc_sw128(st + C::kW + k * 32, 0, 1024), idesc, i > 0 || k > 0);
-            mma_commit(&empty[s]);
+                for (int k = 0; k < 4; ++k)
+                    linear_mma<kE4m3>(tmem_base, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
+                mma_commit(&empty[s]);
+            }
+            __syncwarp();
         }
-        mma_commit(&done);
-        mbar_drain(&done, 0);
+        if (one) {
+            mma_commit(&done);
+            mbar_drain(&done, 0);
+        }
     }
     __syncwarp();
 
@@ -186,7 +193,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         sw[i] = on && ep.sw ? ep.sw[n + i] : 1.0f;
         bias[i] = on && ep.bias ? ep.bias[n + i] : 0.0f;
     }
-    if (warp >= 2 && __all_sync(0xffffffffu, mbar_wait(&done, 0, abort))) {
+    if (warp >= 2 && mbar_wait_all(&done, 0, abort)) {
         // accumulator lane 32 q + l is channel n0 + 32 q + l, its columns the tokens
         tc_fence_after();
         const int quad = warp & 3;

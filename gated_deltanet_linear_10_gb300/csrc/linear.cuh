@@ -19,9 +19,28 @@ struct LinearEpi {
     bool vec8;            // rows of y and residual on 16-byte boundaries
 };
 
+// GELU by the rational approximation of erfc of Abramowitz and Stegun, Handbook
+// of Mathematical Functions, 7.1.26: for x >= 0
+//   erfc(x) = (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-x^2) + e,
+//   t = 1 / (1 + p x), |e| <= 1.5e-7,
+// with the fast reciprocal and exponential.  |error| <= 2e-7 |v| of the result,
+// some 25 times less than what the sum over k leaves at n_in = 64, and a third
+// of erff's instructions: with erff the epilogue of 20668 x 2048 x 8192 took
+// longer than the products (470 us, this form: see linear_wide.cu).
+__device__ __forceinline__ float gelu_f(float v) {
+    const float x = fabsf(v) * 0.70710678118f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float half_erfc = 0.5f * p * t * __expf(-x * x);   // of |v| / sqrt(2)
+    return v * (v > 0.0f ? 1.0f - half_erfc : half_erfc);
+}
+
 template <int kAct> __device__ __forceinline__ float linear_act(float v) {
     if constexpr (kAct == GDN_ACT_SILU) return silu_f(v);
-    if constexpr (kAct == GDN_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118f));
+    if constexpr (kAct == GDN_ACT_GELU) return gelu_f(v);
     return v;
 }
 
@@ -70,11 +89,43 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// True in one lane of the (whole, converged) warp.  The warp that issues the
+// products stays converged and issues them under this predicate: from a branch
+// that one lane took alone (lane == 0) the same loop issued 155 cycles a
+// product, in this form it keeps up with the 128 that the tensor cores take
+// (256 x 256 x 16 by a pair of CTAs).
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+    return e != 0;
+}
+// mbar_wait by a whole warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_all(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
+}
+
 // mbar_wait for a copy or product that is in flight already when the CTA has
 // given up: it does not return at once on the abort flag, but it is bounded.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
     volatile int give_up = 0;
     tc::mbar_wait(bar, parity, &give_up);
+}
+
+// mbar_wait for a whole warp that has time: one lane looks, and sleeps between looks.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0 && !tc::mbar_try_wait(bar, parity)) {
+        const uint64_t t0 = tc::globaltimer_ns(), limit = *(volatile uint64_t *)&tc::g_wait_limit_ns;
+        while (!tc::mbar_try_wait(bar, parity)) {
+            if (*abort || tc::globaltimer_ns() - t0 > limit) {
+                *abort = 1;
+                ok = 0;
+                break;
+            }
+            __nanosleep(100);
+        }
+    }
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 // The product's 2-D operand: rows of `cols` elements of 2 bytes (bf16) or 1

@@ -1,20 +1,16 @@
 // gdn_linear for many tokens: a persistent grid of CTA pairs, each pair on one
-// tile of 256 tokens x BN channels at a time (tcgen05 cta_group::2, M = 256).
+// tile of 256 tokens x up to 256 channels at a time (tcgen05 cta_group::2,
+// M = 256).
 //
 // A CTA of a pair loads its own 128 tokens and half of the tile's weight rows,
-// so a pair reads each operand byte once from L2 and its tensor cores read
-// (128 + BN) x 128 B of shared memory per 128 bytes of k where two single CTAs
-// would read (128 + BN) x 128 B each for half the products.  The accumulator
-// (BN fp32 columns) is doubled in tensor memory: the epilogue warps turn one
-// tile into y while the next one's products run.
+// so a pair reads each operand byte once from L2.  The accumulator is doubled
+// in tensor memory: the epilogue warps turn one tile into y while the next
+// one's products run.
 //
-// Epilogue: a thread holds one token row and takes 128 bytes of y at a time
-// (64 bf16 or 32 fp32 columns): scale, bias, activation, residual, one
-// rounding, then into a 128-byte-swizzled staging row (4 KB per warp, three of
-// them), from which one TMA store writes 32 rows; the residual comes through
-// the same staging row by a TMA load, requested one slice ahead.  A y or residual that TMA cannot address
-// (rows off 16-byte boundaries) goes through the staging row to plain accesses
-// of consecutive elements.
+// What bounds it: TODO
+//
+// Only rows off 16-byte boundaries go through shared memory, turned there so
+// that a warp's lanes access consecutive elements.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -28,16 +24,14 @@ GDN_STATUS_READER(read_status_linear_wide, g_status_linear_wide)
 
 namespace {
 
-constexpr int kTokTile = 256, kTokHalf = 128, kStagesWide = 5, kEpiWarps = 4;
-constexpr int kStagingBufs = 3;
+constexpr int kTokTile = 256, kTokHalf = 128, kChTile = 256, kStagesWide = 6, kEpiWarps = 4;
+constexpr int kWideThreads = 128 + 32 * kEpiWarps;
 constexpr int kRaster = 8;     // token tiles of one raster group (below)
-
-template <int BN> struct WideCfg {
-    static constexpr uint32_t kA = kTokHalf * 128, kB = BN / 2 * 128, kStage = kA + kB;
-    static constexpr uint32_t kStaging = kEpiWarps * kStagingBufs * 4096;
-    static constexpr uint32_t kSmem = kStagesWide * kStage + kStaging + 1024;
-    static constexpr uint32_t kCols = 2 * BN;
-};
+constexpr int kTurnPitch = 33; // floats per row of a warp's 32 x 32 turning buffer
+constexpr uint32_t kStaging = 5 * 1024;   // per warp: 32 rows of 128 bytes, or the turning buffer
+constexpr uint32_t kStageA = kTokHalf * 128, kStageBytes = kStageA + kChTile / 2 * 128;
+static_assert(32 * kTurnPitch * 4 <= kStaging, "the turning buffer fits");
+constexpr uint32_t kWideSmem = kStagesWide * kStageBytes + kEpiWarps * kStaging + 1024;
 
 // Tiled load into this CTA's shared memory, its bytes counted on a barrier of
 // either CTA of the pair.
@@ -58,10 +52,6 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-// Waits until at most N of this thread's committed stores have not read their source.
-template <int N> __device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
 template <bool kE4m3>
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -79,110 +69,85 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
             : "memory");
 }
 
-// Tile order: groups of kRaster token tiles; within a group the token tile
-// runs fastest, then the channel tile.  The tiles in flight at one time then
-// share about as many token rows as weight rows.
-struct WideTiles {
-    int nt, nn;      // token and channel tiles
-    __device__ __forceinline__ void at(int tile, int &t, int &n) const {
-        const int per = kRaster * nn, g = tile / per, r = tile - g * per;
-        const int rows = min(kRaster, nt - g * kRaster);
-        n = r / rows;
-        t = g * kRaster + (r - n * rows);
-    }
-};
-
-template <typename O> __device__ __forceinline__ void add_chunk(float *v, const uint4 &q);
-template <> __device__ __forceinline__ void add_chunk<__nv_bfloat16>(float *v, const uint4 &q) {
-    float f[8];
-    Vec16<__nv_bfloat16>::unpack(q, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += f[i];
-}
-template <> __device__ __forceinline__ void add_chunk<float>(float *v, const uint4 &q) {
-    float f[4];
-    Vec16<float>::unpack(q, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += f[i];
-}
-
-// 32 rows of 128 bytes between a staging buffer and memory that TMA cannot
-// address, element by element: a warp's lanes take consecutive elements, and
-// 16 rows are in flight at a time.
-template <typename O, bool kLoad>
-__device__ __forceinline__ void plain_rows(uint8_t *buf, O *p, int64_t stride, int t0, int n0,
-                                           int n_tokens, int n_out, int lane) {
-    constexpr int COLS = 128 / sizeof(O), PART = COLS / 32, ROWS = 16;
-#pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += ROWS) {
-        if (t0 + r0 >= n_tokens) break;
-        O v[ROWS][PART];
-#pragma unroll
-        for (int pass = 0; pass < 2; ++pass)
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-                for (int c = 0; c < PART; ++c) {
-                    const int col = c * 32 + lane, t = t0 + r0 + r;
-                    const bool on = t < n_tokens && n0 + col < n_out;
-                    const uint32_t off = col * sizeof(O);
-                    O *in_buf = reinterpret_cast<O *>(
-                        buf + (r0 + r) * 128 + (((off >> 4) ^ ((r0 + r) & 7)) << 4) + (off & 15));
-                    O *in_mem = p + t * stride + n0 + col;
-                    if (pass == 0) {
-                        if (on) v[r][c] = kLoad ? *in_mem : *in_buf;
-                    } else if (on) {
-                        *(kLoad ? in_buf : in_mem) = v[r][c];
-                    }
-                }
-    }
-}
-
-struct WideFlags {
-    bool y_tma, res_tma;
-};
-
-// One staging row's worth of columns of a tile: accumulator -> y values in the
-// staging row.  cols: the columns' scales, then their biases, in shared memory.
-template <int kAct, typename O, int BN>
-__device__ __forceinline__ void wide_slice(uint32_t taddr, const float *cols, float sx, bool has_res,
-                                           uint8_t *row, int r7) {
-    constexpr int COLS = 128 / sizeof(O), PER = 16 / sizeof(O);
-#pragma unroll
-    for (int h = 0; h < COLS / 32; ++h) {
-        uint32_t r[32];
-        tmem_ld32(taddr + h * 32, r);
-#pragma unroll
-        for (int c = 0; c < 32 / PER; ++c) {
-            float v[PER];
-            const int j0 = h * 32 + c * PER;
-#pragma unroll
-            for (int i = 0; i < PER; i += 4) {
-                const float4 s = *reinterpret_cast<const float4 *>(cols + j0 + i);
-                const float4 b = *reinterpret_cast<const float4 *>(cols + BN + j0 + i);
-                const uint32_t *a = r + c * PER + i;
-                v[i] = linear_act<kAct>(fmaf(__uint_as_float(a[0]), sx * s.x, b.x));
-                v[i + 1] = linear_act<kAct>(fmaf(__uint_as_float(a[1]), sx * s.y, b.y));
-                v[i + 2] = linear_act<kAct>(fmaf(__uint_as_float(a[2]), sx * s.z, b.z));
-                v[i + 3] = linear_act<kAct>(fmaf(__uint_as_float(a[3]), sx * s.w, b.w));
-            }
-            uint4 *chunk = reinterpret_cast<uint4 *>(row + (((j0 / PER) ^ r7) << 4));
-            if (has_res) add_chunk<O>(v, *chunk);
-            Vec16<O>::store(reinterpret_cast<O *>(chunk), v);
+// The tiles: token rows [0, nt_full) in channel tiles of kChTile, the token
+// rows behind them in channel tiles of tail_w.  Order: groups of kRaster token
+// tiles; within a group the token tile runs fastest, then the channel tile, so
+// the tiles in flight at one time share about as many token rows as weight rows
+// (all token tiles in one group: 9 % slower at 20668 x 2048 x 8192).
+struct WidePlan {
+    int nt_full, nt, nn, n_full, tail_w, n_tiles;
+    __device__ __forceinline__ void at(int tile, int n_out, int &t0, int &n0, int &box, int &width) const {
+        int t, n;
+        if (tile < n_full) {
+            const int per = kRaster * nn, g = tile / per, r = tile - g * per;
+            const int rows = min(kRaster, nt_full - g * kRaster);
+            n = r / rows;
+            t = g * kRaster + (r - n * rows);
+            box = kChTile;
+        } else {
+            const int r = tile - n_full, rows = nt - nt_full;
+            n = r / rows;
+            t = nt_full + (r - n * rows);
+            box = tail_w;
         }
+        t0 = t * kTokTile;
+        n0 = n * box;
+        width = min(box, (n_out - n0 + 31) / 32 * 32);   // the product's N: no wider than the channels left
+    }
+};
+
+enum WideRows { kRows32, kRows16, kRowsPlain };   // alignment of y's and the residual's rows
+
+// 32 bytes of a row into registers.
+__device__ __forceinline__ void load32(uint32_t *r, const void *p, int rows) {
+    if (rows == kRows32) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                       "=r"(r[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+        r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+    }
+}
+// A value of O as 32 bits, so that loads stay in flight until it is used.
+template <typename O> __device__ __forceinline__ uint32_t load_bits(const O *p) {
+    if constexpr (sizeof(O) == 4) return *reinterpret_cast<const uint32_t *>(p);
+    else return *reinterpret_cast<const uint16_t *>(p);
+}
+template <typename O> __device__ __forceinline__ float bits_value(uint32_t b) {
+    return __uint_as_float(sizeof(O) == 4 ? b : b << 16);
+}
+
+// 32 accumulators of one token row -> act(sx sw acc + bias), in place.  cols:
+// the columns' scales in shared memory, their biases kChTile floats on.
+template <int kAct, bool kCols>
+__device__ __forceinline__ void wide_values(uint32_t (&r)[32], const float *cols, float sx) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        float4 s = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (kCols) {
+            s = *reinterpret_cast<const float4 *>(cols + j);
+            b = *reinterpret_cast<const float4 *>(cols + kChTile + j);
+        }
+        r[j] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j]), sx * s.x, b.x)));
+        r[j + 1] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j + 1]), sx * s.y, b.y)));
+        r[j + 2] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j + 2]), sx * s.z, b.z)));
+        r[j + 3] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j + 3]), sx * s.w, b.w)));
     }
 }
 
-template <int BN, bool kE4m3, typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
+template <bool kE4m3, typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                   const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mres,
-                   const __grid_constant__ LinearEpi ep, int n_in, WideTiles tiles, WideFlags flags) {
-    using C = WideCfg<BN>;
-    constexpr int S = kStagesWide, COLS = 128 / sizeof(O), SLICES = BN / COLS;
+                   const __grid_constant__ CUtensorMap mw_tail, const __grid_constant__ CUtensorMap my,
+                   const __grid_constant__ LinearEpi ep, int n_in, WidePlan plan, int rows) {
+    constexpr int S = kStagesWide;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[S], empty[S], acc_full[2], acc_empty[2], res_full[kEpiWarps][kStagingBufs], drained;
-    __shared__ __align__(16) float cols[2][2 * BN];
+    __shared__ uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
+    __shared__ __align__(16) float cols[2][2 * kChTile];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -190,7 +155,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     constexpr int kElems = kE4m3 ? 128 : 64;                 // k per block of 128 bytes
     const int nk = (n_in + kElems - 1) / kElems;
-    const int n_tiles = tiles.nt * tiles.nn, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&mx);
@@ -203,8 +168,6 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
-        for (int w = 0; w < kEpiWarps; ++w)
-            for (int b = 0; b < kStagingBufs; ++b) mbar_init(&res_full[w][b], 1);
         mbar_init(&drained, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -212,10 +175,11 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_base)),
-                     "r"(C::kCols)
+                     "r"(2 * kChTile)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    __syncwarp();
     tc_fence_before();
     cluster_sync_all();        // both CTAs' barriers and tensor memory are ready
     tc_fence_after();
@@ -226,21 +190,23 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         // Loads: this CTA's half of both operands, counted on the leader's barrier.
         int i = 0;
         bool ok = true;
-        for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
-            int tt, tn;
-            tiles.at(tile, tt, tn);
-            const int t0 = tt * kTokTile + (int)rank * kTokHalf, n0 = tn * BN + (int)rank * (BN / 2);
+        for (int tile = pair; tile < plan.n_tiles && ok; tile += pairs) {
+            int t0, n0, box, width;
+            plan.at(tile, ep.n_out, t0, n0, box, width);
+            const CUtensorMap *map = box == kChTile ? &mw : &mw_tail;
+            const uint32_t bytes = 2 * (kStageA + box / 2 * 128);
+            const int tr = t0 + (int)rank * kTokHalf, nr = n0 + (int)rank * (width / 2);
             for (int k = 0; k < nk; ++k, ++i) {
                 const int s = i % S;
                 if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1, abort)) {
                     ok = false;
                     break;
                 }
-                uint8_t *st = smem + s * C::kStage;
+                uint8_t *st = smem + s * kStageBytes;
                 const uint32_t bar = peer_smem(smem_u32(&full[s]), 0);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
-                tma_load_2d_pair(st, &mx, bar, k * kElems, t0);
-                tma_load_2d_pair(st + C::kA, &mw, bar, k * kElems, n0);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                tma_load_2d_pair(st, &mx, bar, k * kElems, tr);
+                tma_load_2d_pair(st + kStageA, map, bar, k * kElems, nr);
             }
         }
         if (!ok || *abort) {
@@ -255,166 +221,227 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 }
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-        constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(256, BN) : idesc_bf16(256, BN);
-        int i = 0, u = 0;
+    } else if (warp == 1 && rank == 0) {
+        const bool one = elect_lane();
+        const uint32_t first = smem_u32(smem) >> 4;       // descriptors count in 16 bytes
+        const uint64_t desc = sdesc_sw128(0, 0, 1024);
+        const uint32_t idesc0 = kE4m3 ? idesc_e4m3(256, 0) : idesc_bf16(256, 0);
+        int tile = pair, t0, n0, box, width, s = 0;
+        uint32_t phase = 0, st = first;
         bool ok = true;
-        for (int tile = pair; tile < n_tiles && ok; tile += pairs, ++u) {
+        plan.at(tile, ep.n_out, t0, n0, box, width);
+        for (int u = 0; tile < plan.n_tiles && ok; ++u) {
             const int b = u & 1;
-            if (u >= 2 && !mbar_wait(&acc_empty[b], ((u >> 1) - 1) & 1, abort)) break;
+            if (u >= 2 && !mbar_wait_all(&acc_empty[b], ((u >> 1) - 1) & 1, abort)) break;
             tc_fence_after();
-            const uint32_t d = tmem_base + b * BN;
-            for (int k = 0; k < nk; ++k, ++i) {
-                const int s = i % S;
-                if (!mbar_wait(&full[s], (i / S) & 1, abort)) {
+            const uint32_t d = tmem_base + b * kChTile, idesc = idesc0 | ((uint32_t)(width >> 3) << 17);
+#pragma unroll 1
+            for (int k = 0; k < nk; ++k) {
+                if (!mbar_wait_all(&full[s], phase, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * C::kStage);
+                if (one) {
+                    const uint64_t da = desc | st, db = desc | (st + (kStageA >> 4));
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    mma_pair<kE4m3>(d, sdesc_sw128(st + q * 32, 0, 1024),
-                                    sdesc_sw128(st + C::kA + q * 32, 0, 1024), idesc, k > 0 || q > 0);
-                mma_commit_pair(&empty[s]);
-            }
-            if (ok) mma_commit_pair(&acc_full[b]);
-        }
-        mma_commit_pair(&drained);      // every product issued is done before the pair ends
-        mbar_drain(&drained, 0);
-    } else if (warp >= 4) {
-        const int q = warp & 3, etid = tid - 128;
-        uint8_t *staging = smem + S * C::kStage + q * (kStagingBufs * 4096);
-        uint64_t *rbar = res_full[q];
-        const bool has_res = ep.res != nullptr, res_tma = has_res && flags.res_tma;
-        int u = 0, sl = 0;              // sl: slices so far; a slice's staging buffer is sl % 3
-        int asked = 0, seen = 0;        // residual slices requested and waited for
-        // Requests a slice's residual into its buffer, which the store of three
-        // slices before has read (the bulk_wait_read before each call).
-        auto ask = [&](int slice, int nc, int t0) {
-            if (lane == 0) {
-                uint64_t *bar = &rbar[slice % kStagingBufs];
-                mbar_arrive_expect_tx(bar, 4096);
-                tma_load_2d(staging + (slice % kStagingBufs) * 4096, &mres, bar, nc, t0);
-            }
-            ++asked;
-        };
-        for (int tile = pair; tile < n_tiles; tile += pairs, ++u) {
-            const int b = u & 1;
-            int tt, tn;
-            tiles.at(tile, tt, tn);
-            const int t0 = tt * kTokTile + (int)rank * kTokHalf + q * 32, n0 = tn * BN;
-            const int t = t0 + lane;
-            float *cb = cols[b];
-            for (int c = etid; c < BN; c += 128) {
-                const bool on = n0 + c < ep.n_out;
-                cb[c] = on && ep.sw ? ep.sw[n0 + c] : 1.0f;
-                cb[BN + c] = on && ep.bias ? ep.bias[n0 + c] : 0.0f;
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            const float sx = ep.sx && t < ep.n_tokens ? ep.sx[t] : 1.0f;
-            if (lane == 0) bulk_wait_read<2>();
-            if (res_tma) ask(sl, n0, t0);
-            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (u >> 1) & 1, abort))) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int s = 0; s < SLICES; ++s, ++sl) {
-                uint8_t *buf = staging + (sl % kStagingBufs) * 4096;
-                uint8_t *my_row = buf + lane * 128;
-                const int nc = n0 + s * COLS;
-                // free the next slice's buffer: the store of two slices ago has read it
-                if (lane == 0) bulk_wait_read<1>();
+                    for (int q = 0; q < 4; ++q) mma_pair<kE4m3>(d, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                    mma_commit_pair(&empty[s]);
+                }
                 __syncwarp();
-                if (has_res) {
-                    if (res_tma) {
-                        if (s + 1 < SLICES) ask(sl + 1, nc + COLS, t0);
-                        if (__all_sync(0xffffffffu, mbar_wait(&rbar[sl % kStagingBufs], (sl / kStagingBufs) & 1, abort)))
-                            ++seen;
-                    } else {
-                        plain_rows<O, true>(buf, reinterpret_cast<O *>(const_cast<void *>(ep.res)), ep.rs,
-                                            t0, nc, ep.n_tokens, ep.n_out, lane);
+                st += kStageBytes >> 4;
+                if (++s == S) {
+                    s = 0;
+                    st = first;
+                    phase ^= 1;
+                }
+                if (k == 0) {                             // the next tile, behind this one's products
+                    tile += pairs;
+                    if (tile < plan.n_tiles) plan.at(tile, ep.n_out, t0, n0, box, width);
+                }
+            }
+            if (ok && one) mma_commit_pair(&acc_full[b]);
+            __syncwarp();
+        }
+        if (one) {
+            mma_commit_pair(&drained);    // every product issued is done before the pair ends
+            mbar_drain(&drained, 0);
+        }
+    } else if (warp >= 4) {
+        // Accumulator lane 32 q + l is token row 32 q + l of this CTA's half.
+        const int q = warp & 3, etid = tid - 128;
+        uint8_t *staging = smem + S * kStageBytes + q * kStaging;
+        const bool has_cols = ep.sw || ep.bias || ep.act != GDN_ACT_NONE;
+        const O *res = reinterpret_cast<const O *>(ep.res);
+        int u = 0;
+        for (int tile = pair; tile < plan.n_tiles; tile += pairs, ++u) {
+            const int b = u & 1;
+            int t0, n0, box, width;
+            plan.at(tile, ep.n_out, t0, n0, box, width);
+            t0 += (int)rank * kTokHalf + q * 32;
+            const int t = t0 + lane;
+            if (has_cols) {
+                float *cb = cols[b];
+                for (int c = etid; c < kChTile; c += 32 * kEpiWarps) {
+                    const int n = n0 + c;
+                    cb[c] = n < ep.n_out && ep.sw ? ep.sw[n] : 1.0f;
+                    cb[kChTile + c] = n < ep.n_out && ep.bias ? ep.bias[n] : 0.0f;
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+            }
+            const float sx = ep.sx && t < ep.n_tokens ? ep.sx[t] : 1.0f;
+            if (!mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort)) break;
+            tc_fence_after();
+            constexpr int COLS = 128 / sizeof(O);       // channels of a staging row
+#pragma unroll 1
+            for (int c = 0; c < width; c += 32) {
+                const int n = n0 + c;
+                uint32_t rv[32];
+                if (res) {
+                    if (rows == kRowsPlain) {           // lane: a channel
+                        const O *p = res + min(n + lane, ep.n_out - 1);
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) rv[r] = load_bits(p + min(t0 + r, ep.n_tokens - 1) * ep.rs);
+                    } else if (t < ep.n_tokens) {       // lane: a token row
+                        const O *p = res + t * ep.rs + n;
+                        if (n + 32 <= ep.n_out) {
+#pragma unroll
+                            for (int i = 0; i < 8 * (int)sizeof(O); i += 8)
+                                load32(rv + i, p + i * 4 / (int)sizeof(O), rows);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8 * (int)sizeof(O); ++i) {
+                                constexpr int E = 4 / sizeof(O);
+                                rv[i] = n + i * E < ep.n_out ? load_bits(p + i * E) : 0u;
+                                if (E == 2 && n + i * E + 1 < ep.n_out) rv[i] |= load_bits(p + i * E + 1) << 16;
+                            }
+                        }
+                    }
+                }
+                uint32_t r[32];
+                tmem_ld32(tmem_addr(tmem_base, q * 32, b * kChTile + c), r);
+                const float *cs = cols[b] + c;
+                if (ep.act == GDN_ACT_SILU) wide_values<GDN_ACT_SILU, true>(r, cs, sx);
+                else if (ep.act == GDN_ACT_GELU) wide_values<GDN_ACT_GELU, true>(r, cs, sx);
+                else if (has_cols) wide_values<GDN_ACT_NONE, true>(r, cs, sx);
+                else wide_values<GDN_ACT_NONE, false>(r, cs, sx);
+                if (rows != kRowsPlain) {
+                    if constexpr (sizeof(O) == 2) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float lo = __uint_as_float(r[2 * i]), hi = __uint_as_float(r[2 * i + 1]);
+                            if (res) {
+                                const float2 f = unpack_bf16(rv[i]);
+                                lo += f.x;
+                                hi += f.y;
+                            }
+                            r[i] = pack_bf16(lo, hi);
+                        }
+                    } else if (res) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(rv[i]));
+                    }
+                    const int part = c % COLS;          // the first or second half of a bf16 staging row
+                    if (part == 0) {                    // the last store has read the staging rows
+                        if (lane == 0) bulk_wait_read_all();
                         __syncwarp();
                     }
-                }
-                const uint32_t ta = tmem_addr(tmem_base, q * 32, b * BN + s * COLS);
-                const float *cs = cb + s * COLS;
-                if (ep.act == GDN_ACT_SILU)
-                    wide_slice<GDN_ACT_SILU, O, BN>(ta, cs, sx, has_res, my_row, lane & 7);
-                else if (ep.act == GDN_ACT_GELU)
-                    wide_slice<GDN_ACT_GELU, O, BN>(ta, cs, sx, has_res, my_row, lane & 7);
-                else
-                    wide_slice<GDN_ACT_NONE, O, BN>(ta, cs, sx, has_res, my_row, lane & 7);
-                if (s == SLICES - 1) {   // the accumulator is read out
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[b]), 0));
-                }
-                if (flags.y_tma) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (nc < ep.n_out && t0 < ep.n_tokens) tma_store_2d(&my, buf, nc, t0);
-                        bulk_commit();
+#pragma unroll
+                    for (int i = 0; i < 2 * (int)sizeof(O); ++i) {
+                        const int chunk = part * (int)sizeof(O) / 16 + i;
+                        *reinterpret_cast<uint4 *>(staging + lane * 128 + ((chunk ^ (lane & 7)) << 4)) =
+                            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    }
+                    if (part + 32 == COLS || c + 32 >= width) {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (t0 < ep.n_tokens) tma_store_2d(&my, staging, n - part, t0);
+                            bulk_commit();
+                        }
                     }
                 } else {
+                    float *turn = reinterpret_cast<float *>(staging);
+                    __syncwarp();                       // the buffer's last values are read
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) turn[lane * kTurnPitch + j] = __uint_as_float(r[j]);
                     __syncwarp();
-                    plain_rows<O, false>(buf, reinterpret_cast<O *>(ep.y), ep.ys, t0, nc, ep.n_tokens,
-                                         ep.n_out, lane);
-                    // the next user of the buffer may be a copy of the async proxy
-                    fence_async_smem();
-                    __syncwarp();
+                    const bool on = n + lane < ep.n_out;
+                    O *p = reinterpret_cast<O *>(ep.y) + n + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float v = turn[i * kTurnPitch + lane];
+                        if (res) v += bits_value<O>(rv[i]);
+                        if (on && t0 + i < ep.n_tokens) Io<O>::store(p + (t0 + i) * ep.ys, v);
+                    }
                 }
             }
+            tc_fence_before();                          // this warp has read its part of the accumulator
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[b]), 0));
         }
-        tc_fence_before();
-        if (lane == 0) {
-            // given up: residual copies in flight land before the CTA ends
-            for (int j = seen; j < asked; ++j) mbar_drain(&rbar[j % kStagingBufs], (j / kStagingBufs) & 1);
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
+        tc_fence_before();
     }
     __syncwarp();
     cluster_sync_all();        // neither CTA ends while the other may reach its memory
     tc_fence_after();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                     "r"(C::kCols)
+                     "r"(2 * kChTile)
                      : "memory");
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
-template <typename O> constexpr CUtensorMapDataType tmap_type() {
-    return sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+// The plan with the shortest estimate.  A tile of w channels reads 4 KB of
+// tokens and 16 KB w / 256 of weights from shared memory per 32 bytes of k,
+// the measure of its time; the last `rows` token tiles are cut into channel
+// tiles of w so that the last wave of pairs is full (81 x 32 tiles on 76 pairs
+// are 34.1 waves: 35 with one width).
+WidePlan plan_wide(int n_tokens, int n_out, int pairs) {
+    WidePlan best = {};
+    const int nt = (n_tokens + kTokTile - 1) / kTokTile, nn = (n_out + kChTile - 1) / kChTile;
+    auto waves = [&](int64_t tiles) { return (tiles + pairs - 1) / pairs; };
+    int64_t cost = INT64_MAX;
+    for (int rows = 0; rows <= std::min(nt, 16); ++rows)
+        for (int w = 64; w <= (rows ? kChTile - 64 : 64); w += 64) {   // whole staging rows
+            const int64_t full = (int64_t)(nt - rows) * nn, tail = (int64_t)rows * ((n_out + w - 1) / w);
+            const int64_t c = waves(full) * 20 + waves(tail) * (4 + w / 16);
+            if (c < cost) {
+                cost = c;
+                best = {nt - rows, nt, nn, (int)full, w, (int)(full + tail)};
+            }
+        }
+    return best;
 }
 
-// Whether TMA can address these rows: 16-byte aligned, the stride too.
-bool tma_rows(const void *p, int64_t stride, size_t elem) {
-    return (uintptr_t)p % 16 == 0 && (stride * (int64_t)elem) % 16 == 0 && stride < (1ll << 36);
-}
-
-template <int BN, bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
-    using C = WideCfg<BN>;
+template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
     const LinearEpi &e = c.e;
-    CUtensorMap mx, mw, my = {}, mres = {};
-    WideFlags f = {tma_rows(e.y, e.ys, sizeof(O)), e.res && tma_rows(e.res, e.rs, sizeof(O))};
+    const int sms = sm_count() / 2 * 2;
+    GDN_REQUIRE(sms >= 2, GDN_ERR_UNSUPPORTED);
+    GDN_REQUIRE((int64_t)((e.n_tokens + 255) / 256) * ((e.n_out + 31) / 32) < (1 << 30), GDN_ERR_UNSUPPORTED);
+    const WidePlan plan = plan_wide(e.n_tokens, e.n_out, sms / 2);
+    CUtensorMap mx, mw, mt, my = {};
     if (!encode_tmap_operand(&mx, c.x, c.n_in, e.n_tokens, c.xs, kTokHalf, kE4m3) ||
-        !encode_tmap_operand(&mw, c.w, c.n_in, e.n_out, c.ws, BN / 2, kE4m3))
+        !encode_tmap_operand(&mw, c.w, c.n_in, e.n_out, c.ws, kChTile / 2, kE4m3) ||
+        !encode_tmap_operand(&mt, c.w, c.n_in, e.n_out, c.ws, plan.tail_w / 2, kE4m3))
         return GDN_ERR_CUDA;
-    constexpr uint32_t box = 128 / sizeof(O);
-    if (f.y_tma && !encode_tmap_2d(&my, tmap_type<O>(), e.y, e.n_out, e.n_tokens, e.ys * sizeof(O), box, 32, true))
+    auto at = [&](int64_t bytes) {
+        return (uintptr_t)e.y % bytes == 0 && e.ys * (int64_t)sizeof(O) % bytes == 0 &&
+               (!e.res || ((uintptr_t)e.res % bytes == 0 && e.rs * (int64_t)sizeof(O) % bytes == 0));
+    };
+    const int rows = at(32) ? kRows32 : at(16) ? kRows16 : kRowsPlain;
+    if (rows != kRowsPlain &&
+        !encode_tmap_2d(&my, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.y,
+                        e.n_out, e.n_tokens, e.ys * sizeof(O), 128 / sizeof(O), 32, true))
         return GDN_ERR_CUDA;
-    if (f.res_tma &&
-        !encode_tmap_2d(&mres, tmap_type<O>(), e.res, e.n_out, e.n_tokens, e.rs * sizeof(O), box, 32, true))
-        return GDN_ERR_CUDA;
-    auto kernel = linear_wide_kernel<BN, kE4m3, O>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    const WideTiles tiles = {(e.n_tokens + kTokTile - 1) / kTokTile, (e.n_out + BN - 1) / BN};
-    const int64_t n = (int64_t)tiles.nt * tiles.nn;
-    const int pairs = (int)std::min<int64_t>(n, std::max(1, sm_count() / 2));
+    auto kernel = linear_wide_kernel<kE4m3, O>;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
     if (err == cudaSuccess)
-        err = launch_after(kernel, dim3(2 * pairs), dim3(256), C::kSmem, c.stream, mx, mw, my, mres, e,
-                           c.n_in, tiles, f);
+        err = launch_after(kernel, dim3(std::min(2 * plan.n_tiles, sms)), dim3(kWideThreads), kWideSmem,
+                           c.stream, mx, mw, mt, my, e, c.n_in, plan, rows);
     if (err != cudaSuccess) {
         set_last_cuda_error(err);
         return GDN_ERR_LAUNCH;
@@ -425,8 +452,8 @@ template <int BN, bool kE4m3, typename O> gdn_status launch_wide(const LinearCal
 }  // namespace
 
 gdn_status launch_linear_wide(const LinearCall &c, bool e4m3) {
-    if (e4m3) return c.e.out_f32 ? launch_wide<256, true, float>(c) : launch_wide<256, true, __nv_bfloat16>(c);
-    return c.e.out_f32 ? launch_wide<256, false, float>(c) : launch_wide<256, false, __nv_bfloat16>(c);
+    if (e4m3) return c.e.out_f32 ? launch_wide<true, float>(c) : launch_wide<true, __nv_bfloat16>(c);
+    return c.e.out_f32 ? launch_wide<false, float>(c) : launch_wide<false, __nv_bfloat16>(c);
 }
 
 }  // namespace gdn
