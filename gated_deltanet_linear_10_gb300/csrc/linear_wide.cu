@@ -24,14 +24,12 @@ GDN_STATUS_READER(read_status_linear_wide, g_status_linear_wide)
 
 namespace {
 
-constexpr int kTokTile = 256, kTokHalf = 128, kChTile = 256, kStagesWide = 6, kEpiWarps = 4;
+constexpr int kTokTile = 256, kTokHalf = 128, kChTile = 256, kStagesWide = 6, kEpiWarps = 8;
 constexpr int kWideThreads = 128 + 32 * kEpiWarps;
 constexpr int kRaster = 8;     // token tiles of one raster group (below)
-constexpr int kTurnPitch = 33; // floats per row of a warp's 32 x 32 turning buffer
-constexpr uint32_t kStaging = 5 * 1024;   // per warp: 32 rows of 128 bytes, or the turning buffer
+constexpr uint32_t kStaging = 4096;   // per warp: 32 rows of 128 bytes, or 32 x 32 floats to turn
 constexpr uint32_t kStageA = kTokHalf * 128, kStageBytes = kStageA + kChTile / 2 * 128;
-static_assert(32 * kTurnPitch * 4 <= kStaging, "the turning buffer fits");
-constexpr uint32_t kWideSmem = kStagesWide * kStageBytes + kEpiWarps * kStaging + 1024;
+constexpr uint32_t kWideSmem = kStagesWide * kStageBytes + kEpiWarps * kStaging;
 
 // Tiled load into this CTA's shared memory, its bytes counted on a barrier of
 // either CTA of the pair.
@@ -121,6 +119,50 @@ template <typename O> __device__ __forceinline__ float bits_value(uint32_t b) {
     return __uint_as_float(sizeof(O) == 4 ? b : b << 16);
 }
 
+// 32 channels n .. of a row: whole vectors, or element by element behind which
+// the row ends.
+template <typename O>
+__device__ __forceinline__ void load_row(uint32_t *r, const O *p, int n, int n_out, int rows) {
+    constexpr int E = 4 / sizeof(O);                 // elements of a word
+    if (n + 32 <= n_out) {
+#pragma unroll
+        for (int i = 0; i < 32 / E; i += 8) load32(r + i, p + i * E, rows);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32 / E; ++i) {
+            r[i] = n + i * E < n_out ? load_bits(p + i * E) : 0u;
+            if (E == 2 && n + i * E + 1 < n_out) r[i] |= load_bits(p + i * E + 1) << 16;
+        }
+    }
+}
+
+// A warp's 32 token rows x 32 channels of values (r: one token row a lane) to
+// rows that start anywhere: turned through a 32 x 32 buffer (columns permuted
+// by the row, so that both ways touch every bank once), then a lane is a channel.
+template <typename O>
+__device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], float *turn, const LinearEpi &ep, int t0,
+                                           int n, int lane) {
+    __syncwarp();                                    // the buffer's last values are read
+#pragma unroll
+    for (int j = 0; j < 32; ++j) turn[lane * 32 + (j ^ lane)] = __uint_as_float(r[j]);
+    __syncwarp();
+    const bool on = n + lane < ep.n_out;
+    const int last = ep.n_tokens - 1;
+    const O *res = reinterpret_cast<const O *>(ep.res) + min(n + lane, ep.n_out - 1);
+    O *y = reinterpret_cast<O *>(ep.y) + n + lane;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32 && t0 + i0 <= last; i0 += 16) {   // 16 rows in flight
+        uint32_t rv[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rv[i] = ep.res ? load_bits(res + min(t0 + i0 + i, last) * ep.rs) : 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = turn[(i0 + i) * 32 + (lane ^ (i0 + i))] + bits_value<O>(rv[i]);
+            if (on && t0 + i0 + i <= last) Io<O>::store(y + (t0 + i0 + i) * ep.ys, v);
+        }
+    }
+}
+
 // 32 accumulators of one token row -> act(sx sw acc + bias), in place.  cols:
 // the columns' scales in shared memory, their biases kChTile floats on.
 template <int kAct, bool kCols>
@@ -145,14 +187,13 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                    const __grid_constant__ CUtensorMap mw_tail, const __grid_constant__ CUtensorMap my,
                    const __grid_constant__ LinearEpi ep, int n_in, WidePlan plan, int rows) {
     constexpr int S = kStagesWide;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
-    __shared__ __align__(16) float cols[2][2 * kChTile];
+    __shared__ __align__(16) float cols[2 * kChTile];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     constexpr int kElems = kE4m3 ? 128 : 64;                 // k per block of 128 bytes
     const int nk = (n_in + kElems - 1) / kElems;
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
@@ -169,7 +210,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&drained, 1);
-        abort_flag = 0;
+        abort_flag = (smem_u32(smem) & 1023u) != 0;   // the swizzle needs the alignment asked for above
         fence_mbar_init();
     }
     if (warp == 2) {
@@ -186,9 +227,12 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     griddep_wait();            // launched behind the kernel that writes x: nothing is read before it
     volatile int *abort = &abort_flag;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // Loads: this CTA's half of both operands, counted on the leader's barrier.
-        int i = 0;
+        const bool one = elect_lane();
+        const uint32_t lead = peer_smem(smem_u32(full), 0);
+        int s = 0, i = 0;
+        uint32_t phase = 1;              // of the stage's last release; the first S have none
         bool ok = true;
         for (int tile = pair; tile < plan.n_tiles && ok; tile += pairs) {
             int t0, n0, box, width;
@@ -196,20 +240,28 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             const CUtensorMap *map = box == kChTile ? &mw : &mw_tail;
             const uint32_t bytes = 2 * (kStageA + box / 2 * 128);
             const int tr = t0 + (int)rank * kTokHalf, nr = n0 + (int)rank * (width / 2);
-            for (int k = 0; k < nk; ++k, ++i) {
-                const int s = i % S;
-                if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1, abort)) {
+            int kc = 0;
+#pragma unroll 1
+            for (int k = 0; k < nk; ++k, ++i, kc += kElems) {
+                if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
                     ok = false;
                     break;
                 }
-                uint8_t *st = smem + s * kStageBytes;
-                const uint32_t bar = peer_smem(smem_u32(&full[s]), 0);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                tma_load_2d_pair(st, &mx, bar, k * kElems, tr);
-                tma_load_2d_pair(st + kStageA, map, bar, k * kElems, nr);
+                if (one) {
+                    uint8_t *st = smem + s * kStageBytes;
+                    const uint32_t bar = lead + s * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                    tma_load_2d_pair(st, &mx, bar, kc, tr);
+                    tma_load_2d_pair(st + kStageA, map, bar, kc, nr);
+                }
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
         }
-        if (!ok || *abort) {
+        if (one && (!ok || *abort)) {
             // Given up: the copies in flight land before the CTA ends.  The leader
             // waits on the barriers that count them; the peer, which has none of
             // its own, waits far longer (10 ms) than a copy takes.
@@ -268,11 +320,16 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             mbar_drain(&drained, 0);
         }
     } else if (warp >= 4) {
-        // Accumulator lane 32 q + l is token row 32 q + l of this CTA's half.
-        const int q = warp & 3, etid = tid - 128;
-        uint8_t *staging = smem + S * kStageBytes + q * kStaging;
+        // Accumulator lane 32 q + l is token row 32 q + l of this CTA's half; the
+        // two warps of a quadrant take alternate slices of 128 bytes of y.
+        constexpr int COLS = 128 / sizeof(O), PARTS = COLS / 32, WORDS = 8 * sizeof(O);
+        constexpr int STEP = kEpiWarps / 4 * COLS;
+        const int q = warp & 3, half = (warp - 4) >> 2, etid = tid - 128;
+        uint8_t *staging = smem + S * kStageBytes + (warp - 4) * kStaging;
         const bool has_cols = ep.sw || ep.bias || ep.act != GDN_ACT_NONE;
+        const bool ahead = ep.res && rows != kRowsPlain;
         const O *res = reinterpret_cast<const O *>(ep.res);
+        const int start = half * COLS;
         int u = 0;
         for (int tile = pair; tile < plan.n_tiles; tile += pairs, ++u) {
             const int b = u & 1;
@@ -280,102 +337,74 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             plan.at(tile, ep.n_out, t0, n0, box, width);
             t0 += (int)rank * kTokHalf + q * 32;
             const int t = t0 + lane;
+            const bool on_t = t < ep.n_tokens;
             if (has_cols) {
-                float *cb = cols[b];
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");   // the last tile's are read
                 for (int c = etid; c < kChTile; c += 32 * kEpiWarps) {
                     const int n = n0 + c;
-                    cb[c] = n < ep.n_out && ep.sw ? ep.sw[n] : 1.0f;
-                    cb[kChTile + c] = n < ep.n_out && ep.bias ? ep.bias[n] : 0.0f;
+                    cols[c] = n < ep.n_out && ep.sw ? ep.sw[n] : 1.0f;
+                    cols[kChTile + c] = n < ep.n_out && ep.bias ? ep.bias[n] : 0.0f;
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
             }
-            const float sx = ep.sx && t < ep.n_tokens ? ep.sx[t] : 1.0f;
+            const float sx = ep.sx && on_t ? ep.sx[t] : 1.0f;
+            // the residual of a chunk of 32 channels is asked for one chunk ahead
+            const O *res_row = res + (on_t ? t * ep.rs : 0) + n0;
+            uint32_t rv[32];
+            if (ahead && on_t && start < width) load_row<O>(rv, res_row + start, n0 + start, ep.n_out, rows);
             if (!mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort)) break;
             tc_fence_after();
-            constexpr int COLS = 128 / sizeof(O);       // channels of a staging row
 #pragma unroll 1
-            for (int c = 0; c < width; c += 32) {
+            for (int c = start, part = 0; c < width;) {
                 const int n = n0 + c;
-                uint32_t rv[32];
-                if (res) {
-                    if (rows == kRowsPlain) {           // lane: a channel
-                        const O *p = res + min(n + lane, ep.n_out - 1);
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) rv[r] = load_bits(p + min(t0 + r, ep.n_tokens - 1) * ep.rs);
-                    } else if (t < ep.n_tokens) {       // lane: a token row
-                        const O *p = res + t * ep.rs + n;
-                        if (n + 32 <= ep.n_out) {
-#pragma unroll
-                            for (int i = 0; i < 8 * (int)sizeof(O); i += 8)
-                                load32(rv + i, p + i * 4 / (int)sizeof(O), rows);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8 * (int)sizeof(O); ++i) {
-                                constexpr int E = 4 / sizeof(O);
-                                rv[i] = n + i * E < ep.n_out ? load_bits(p + i * E) : 0u;
-                                if (E == 2 && n + i * E + 1 < ep.n_out) rv[i] |= load_bits(p + i * E + 1) << 16;
-                            }
-                        }
-                    }
-                }
+                const int next_c = part + 1 < PARTS && c + 32 < width ? c + 32 : c - part * 32 + STEP;
                 uint32_t r[32];
                 tmem_ld32(tmem_addr(tmem_base, q * 32, b * kChTile + c), r);
-                const float *cs = cols[b] + c;
-                if (ep.act == GDN_ACT_SILU) wide_values<GDN_ACT_SILU, true>(r, cs, sx);
-                else if (ep.act == GDN_ACT_GELU) wide_values<GDN_ACT_GELU, true>(r, cs, sx);
-                else if (has_cols) wide_values<GDN_ACT_NONE, true>(r, cs, sx);
-                else wide_values<GDN_ACT_NONE, false>(r, cs, sx);
+                if (ep.act == GDN_ACT_SILU) wide_values<GDN_ACT_SILU, true>(r, cols + c, sx);
+                else if (ep.act == GDN_ACT_GELU) wide_values<GDN_ACT_GELU, true>(r, cols + c, sx);
+                else if (has_cols) wide_values<GDN_ACT_NONE, true>(r, cols + c, sx);
+                else wide_values<GDN_ACT_NONE, false>(r, cols + c, sx);
                 if (rows != kRowsPlain) {
+                    if (ahead) {
+#pragma unroll
+                        for (int i = 0; i < WORDS; ++i) {
+                            if constexpr (sizeof(O) == 2) {
+                                const float2 f = unpack_bf16(rv[i]);
+                                r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) + f.x);
+                                r[2 * i + 1] = __float_as_uint(__uint_as_float(r[2 * i + 1]) + f.y);
+                            } else {
+                                r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(rv[i]));
+                            }
+                        }
+                        if (on_t && next_c < width) load_row<O>(rv, res_row + next_c, n0 + next_c, ep.n_out, rows);
+                    }
                     if constexpr (sizeof(O) == 2) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float lo = __uint_as_float(r[2 * i]), hi = __uint_as_float(r[2 * i + 1]);
-                            if (res) {
-                                const float2 f = unpack_bf16(rv[i]);
-                                lo += f.x;
-                                hi += f.y;
-                            }
-                            r[i] = pack_bf16(lo, hi);
-                        }
-                    } else if (res) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(rv[i]));
+                        for (int i = 0; i < 16; ++i)
+                            r[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
                     }
-                    const int part = c % COLS;          // the first or second half of a bf16 staging row
                     if (part == 0) {                    // the last store has read the staging rows
                         if (lane == 0) bulk_wait_read_all();
                         __syncwarp();
                     }
 #pragma unroll
-                    for (int i = 0; i < 2 * (int)sizeof(O); ++i) {
-                        const int chunk = part * (int)sizeof(O) / 16 + i;
-                        *reinterpret_cast<uint4 *>(staging + lane * 128 + ((chunk ^ (lane & 7)) << 4)) =
+                    for (int i = 0; i < WORDS / 4; ++i)
+                        *reinterpret_cast<uint4 *>(staging + lane * 128 +
+                                                   (((part * WORDS / 4 + i) ^ (lane & 7)) << 4)) =
                             make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-                    }
-                    if (part + 32 == COLS || c + 32 >= width) {
+                    if (part + 1 == PARTS || c + 32 >= width) {
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            if (t0 < ep.n_tokens) tma_store_2d(&my, staging, n - part, t0);
+                            if (t0 < ep.n_tokens) tma_store_2d(&my, staging, n - part * 32, t0);
                             bulk_commit();
                         }
                     }
                 } else {
-                    float *turn = reinterpret_cast<float *>(staging);
-                    __syncwarp();                       // the buffer's last values are read
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) turn[lane * kTurnPitch + j] = __uint_as_float(r[j]);
-                    __syncwarp();
-                    const bool on = n + lane < ep.n_out;
-                    O *p = reinterpret_cast<O *>(ep.y) + n + lane;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float v = turn[i * kTurnPitch + lane];
-                        if (res) v += bits_value<O>(rv[i]);
-                        if (on && t0 + i < ep.n_tokens) Io<O>::store(p + (t0 + i) * ep.ys, v);
-                    }
+                    wide_plain<O>(r, reinterpret_cast<float *>(staging), ep, t0, n, lane);
                 }
+                part = next_c == c + 32 && PARTS > 1 ? 1 : 0;
+                c = next_c;
             }
             tc_fence_before();                          // this warp has read its part of the accumulator
             __syncwarp();
