@@ -691,6 +691,13 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-6, y=None):
     return y
 
 
+# The bindings below are on a decode step's critical path (a few microseconds a
+# call), so their checks are written out and messages formed only on failure.
+_F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_CODES = {_F32: GDN_F32, _BF16: GDN_BF16, _E4M3: GDN_E4M3}
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _one_device(first, *ts):
     """Every tensor on the CUDA device of the first one; returns its index."""
     dev = first.get_device()
@@ -704,31 +711,31 @@ def _one_device(first, *ts):
 
 def _call(fn, name, dev, *args):
     """fn on the current stream of device `dev`, which is made the current device for the call."""
-    if dev == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            status = fn(*args, _raw_stream(dev))
     if status:
         _check(status, name)
 
 
-def _rows(t, T, n, name):
-    """t is [T, n] with unit column stride; returns its row stride (at least n where T is 1)."""
-    if t.shape != (T, n):
-        raise GdnError(f"{name}: shape {tuple(t.shape)}, not [{T}, {n}]")
+def _rows(t, shape, name):
+    """t has the 2-D shape and unit column stride; returns its row stride (at least a row where there is one)."""
+    if t.shape != shape:
+        raise GdnError(f"{name}: shape {tuple(t.shape)}, not {list(shape)}")
     st, one = t.stride()
-    if one != 1 and n != 1:
+    if one != 1 and shape[1] != 1:
         raise GdnError(f"{name}: unit column stride")
-    if st < n:
-        if T > 1:
+    if st < shape[1]:
+        if shape[0] > 1:
             raise GdnError(f"{name}: rows must not overlap")
-        return n
+        return shape[1]
     return st
 
 
 def _f32_vec(t, n, name):
-    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype != _F32 or t.shape != (n,) or not t.is_contiguous():
         raise GdnError(f"{name}: [{n}] fp32, contiguous")
     return t.data_ptr()
 
@@ -743,35 +750,40 @@ def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, y_dty
     residual_out [T, H] is s in x's dtype, made when a residual is given (pass
     residual_out=residual to update the stream in place)."""
     dev = _one_device(x, weight, residual, residual_out, y, y_scale)
-    _need(x.dim() == 2, "x: [T, H]")
-    T, H = x.shape
-    xs, dt = _rows(x, T, H, "x"), _dtype_code(x)
-    wp = _f32_vec(weight, H, "weight")
-    rs = ros = 0
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2:
+        raise GdnError("x: [T, H]")
+    if dtype != _BF16 and dtype != _F32:
+        raise GdnError(f"unsupported activation dtype {dtype} (fp32 or bf16)")
+    T, H = shape
+    xs, dt = _rows(x, shape, "x"), _CODES[dtype]
+    rs, rp, ros, rop, sp = 0, None, 0, None, None
     if residual is not None:
-        _need(residual.dtype == x.dtype, "residual: x's dtype")
-        rs = _rows(residual, T, H, "residual")
+        if residual.dtype != dtype:
+            raise GdnError("residual: x's dtype")
+        rs, rp = _rows(residual, shape, "residual"), residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+            residual_out = torch.empty((T, H), dtype=dtype, device=x.device)
     if residual_out is not None:
-        _need(residual_out.dtype == x.dtype, "residual_out: x's dtype")
-        ros = _rows(residual_out, T, H, "residual_out")
+        if residual_out.dtype != dtype:
+            raise GdnError("residual_out: x's dtype")
+        ros, rop = _rows(residual_out, shape, "residual_out"), residual_out.data_ptr()
     if y is None:
-        y = torch.empty((T, H), dtype=x.dtype if y_dtype is None else y_dtype, device=x.device)
-    _need(y_dtype is None or y.dtype == y_dtype, "y: y_dtype")
-    quant = y.dtype == torch.float8_e4m3fn
-    _need(quant or y.dtype == x.dtype, "y: x's dtype or float8_e4m3fn")
-    ys = _rows(y, T, H, "y")
+        y = torch.empty((T, H), dtype=dtype if y_dtype is None else y_dtype, device=x.device)
+    elif y_dtype is not None and y.dtype != y_dtype:
+        raise GdnError("y: y_dtype")
+    quant = y.dtype == _E4M3
     if quant:
-        y_scale = torch.empty(T, dtype=torch.float32, device=x.device) if y_scale is None else y_scale
+        if y_scale is None:
+            y_scale = torch.empty(T, dtype=_F32, device=x.device)
         sp = _f32_vec(y_scale, T, "y_scale")
-    else:
-        _need(y_scale is None, "y_scale: only with an 8-bit y")
-        sp = None
-    _call(_lib.gdn_add_rmsnorm, "gdn_add_rmsnorm", dev, x.data_ptr(), xs,
-          None if residual is None else residual.data_ptr(), rs, wp, weight_offset, T, H, eps,
-          None if residual_out is None else residual_out.data_ptr(), ros, y.data_ptr(), ys, sp, dt,
-          GDN_E4M3 if quant else dt)
+    elif y.dtype != dtype:
+        raise GdnError("y: x's dtype or float8_e4m3fn")
+    elif y_scale is not None:
+        raise GdnError("y_scale: only with an 8-bit y")
+    _call(_lib.gdn_add_rmsnorm, "gdn_add_rmsnorm", dev, x.data_ptr(), xs, rp, rs,
+          _f32_vec(weight, H, "weight"), weight_offset, T, H, eps, rop, ros, y.data_ptr(),
+          _rows(y, shape, "y"), sp, dt, GDN_E4M3 if quant else dt)
     return y, y_scale, residual_out
 
 
@@ -782,18 +794,33 @@ def gdn_gated_rmsnorm_quant(o, z, weight, eps=1e-6, y=None, y_scale=None):
     view with a free row stride); weight [dv] fp32.  y viewed as [T, hv*dv] is
     gdn_linear's 8-bit x."""
     dev = _one_device(o, z, weight, y, y_scale)
-    _need(o.dim() == 3 and o.is_contiguous(), "o: [T, hv, dv] contiguous")
-    T, hv, dv = o.shape
-    zs = _heads_view(z, hv, dv, "z")
-    zs = max(zs, hv * dv) if T <= 1 else zs
-    _need(z.shape[0] == T and z.dtype == o.dtype, "z: rows and dtype of o")
-    wp = _f32_vec(weight, dv, "weight")
-    y = torch.empty((T, hv, dv), dtype=torch.float8_e4m3fn, device=o.device) if y is None else y
-    _need(y.dtype == torch.float8_e4m3fn and y.shape == o.shape and y.is_contiguous(),
-          "y: [T, hv, dv] float8_e4m3fn, contiguous")
-    y_scale = torch.empty(T, dtype=torch.float32, device=o.device) if y_scale is None else y_scale
+    shape, dtype = o.shape, o.dtype
+    if len(shape) != 3 or not o.is_contiguous():
+        raise GdnError("o: [T, hv, dv] contiguous")
+    if dtype != _BF16 and dtype != _F32:
+        raise GdnError(f"unsupported activation dtype {dtype} (fp32 or bf16)")
+    T, hv, dv = shape
+    if z.dtype != dtype:
+        raise GdnError("z: o's dtype")
+    if z.shape == shape:
+        zs, head, one = z.stride()
+        if one != 1 or head != dv:
+            raise GdnError("z: heads must be packed")
+        if zs < hv * dv:
+            if T > 1:
+                raise GdnError("z: rows must not overlap")
+            zs = hv * dv
+    else:
+        zs = _rows(z, (T, hv * dv), "z")
+    if y is None:
+        y = torch.empty((T, hv, dv), dtype=_E4M3, device=o.device)
+    elif y.dtype != _E4M3 or y.shape != shape or not y.is_contiguous():
+        raise GdnError("y: [T, hv, dv] float8_e4m3fn, contiguous")
+    if y_scale is None:
+        y_scale = torch.empty(T, dtype=_F32, device=o.device)
     _call(_lib.gdn_gated_rmsnorm_quant, "gdn_gated_rmsnorm_quant", dev, o.data_ptr(), z.data_ptr(),
-          zs, wp, T, hv, dv, eps, y.data_ptr(), _f32_vec(y_scale, T, "y_scale"), _dtype_code(o))
+          zs, _f32_vec(weight, dv, "weight"), T, hv, dv, eps, y.data_ptr(),
+          _f32_vec(y_scale, T, "y_scale"), _CODES[dtype])
     return y, y_scale
 
 
@@ -806,29 +833,43 @@ def gdn_linear(x, weight, x_scale=None, weight_scale=None, bias=None, act="none"
     "gelu"; residual [T, N] in y's dtype.  y [T, N] bf16 (default) or fp32,
     columns of a wider buffer if wanted; y may be residual.  Returns y."""
     dev = _one_device(x, weight, x_scale, weight_scale, bias, residual, y)
-    _need(x.dim() == 2 and weight.dim() == 2, "x: [T, K], weight: [N, K]")
-    T, K = x.shape
-    N = weight.shape[0]
-    _need(x.dtype == weight.dtype, "x, weight: one dtype")
-    if x.dtype == torch.float8_e4m3fn:
-        dt = GDN_E4M3
-    else:
-        dt = _dtype_code(x)
-        _need(x_scale is None and weight_scale is None, "scales: only with 8-bit x and weight")
-    xs, ws = _rows(x, T, K, "x"), _rows(weight, N, K, "weight")
-    sxp = None if x_scale is None else _f32_vec(x_scale, T, "x_scale")
-    swp = None if weight_scale is None else _f32_vec(weight_scale, N, "weight_scale")
-    bp = None if bias is None else _f32_vec(bias, N, "bias")
-    _need(act in ACTIVATIONS, "act: none, silu or gelu")
+    shape, wshape, dtype = x.shape, weight.shape, x.dtype
+    if len(shape) != 2 or len(wshape) != 2:
+        raise GdnError("x: [T, K], weight: [N, K]")
+    T, K = shape
+    N = wshape[0]
+    if dtype != weight.dtype or (dtype != _BF16 and dtype != _E4M3):
+        raise GdnError("x, weight: both bf16 or both float8_e4m3fn")
+    if wshape[1] != K:
+        raise GdnError(f"x {tuple(shape)} and weight {tuple(wshape)} differ in K")
+    swp = sxp = bp = rp = None
+    rs = 0
+    if x_scale is not None or weight_scale is not None:
+        if dtype != _E4M3:
+            raise GdnError("scales: only with 8-bit x and weight")
+        if x_scale is not None:
+            sxp = _f32_vec(x_scale, T, "x_scale")
+        if weight_scale is not None:
+            swp = _f32_vec(weight_scale, N, "weight_scale")
+    if bias is not None:
+        bp = _f32_vec(bias, N, "bias")
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise GdnError(f"act: one of {tuple(ACTIVATIONS)}")
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16 if y_dtype is None else y_dtype, device=x.device)
-    _need(y_dtype is None or y.dtype == y_dtype, "y: y_dtype")
-    ys, rs, rp = _rows(y, T, N, "y"), 0, None
+        y = torch.empty((T, N), dtype=_BF16 if y_dtype is None else y_dtype, device=x.device)
+    elif y_dtype is not None and y.dtype != y_dtype:
+        raise GdnError("y: y_dtype")
+    ydt = y.dtype
+    if ydt != _BF16 and ydt != _F32:
+        raise GdnError("y: bf16 or fp32")
     if residual is not None:
-        _need(residual.dtype == y.dtype, "residual: y's dtype")
-        rs, rp = _rows(residual, T, N, "residual"), residual.data_ptr()
-    _call(_lib.gdn_linear, "gdn_linear", dev, x.data_ptr(), xs, sxp, weight.data_ptr(), ws, swp, bp,
-          rp, rs, T, K, N, ACTIVATIONS[act], y.data_ptr(), ys, dt, _dtype_code(y))
+        if residual.dtype != ydt:
+            raise GdnError("residual: y's dtype")
+        rs, rp = _rows(residual, (T, N), "residual"), residual.data_ptr()
+    _call(_lib.gdn_linear, "gdn_linear", dev, x.data_ptr(), _rows(x, shape, "x"), sxp,
+          weight.data_ptr(), _rows(weight, wshape, "weight"), swp, bp, rp, rs, T, K, N, code,
+          y.data_ptr(), _rows(y, (T, N), "y"), _CODES[dtype], _CODES[ydt])
     return y
 
 

@@ -12,7 +12,11 @@
 // same pass as the sum of squares, since 1 / rms is one factor of the row.
 //
 // One CTA works on a row at a time, kVecs vectors of 16 bytes per thread; the
-// weights stay in registers over the rows of a CTA.
+// weights stay in registers over the rows of a CTA, and a row's loads are
+// issued before the row in front of it is reduced, so that a CTA always has a
+// row in flight.
+//
+// What bounds it: HBM for many rows (measured figures: TODO), the launch for few.
 #include <algorithm>
 
 #include "quant.cuh"
@@ -26,71 +30,101 @@ constexpr int kRmsMaxHidden = 16384;
 constexpr int rms_threads(int n, int vecs, size_t elem) {   // the most a launch below takes
     return n == 1 || (vecs == 4 && elem == 4) ? 1024 : 512;
 }
+constexpr int kRmsSmThreads = 1536;   // resident threads of an SM: 42 registers each
 
 template <typename T, typename O, int N, int kVecs>
-__global__ void __launch_bounds__(rms_threads(N, kVecs, sizeof(T)))
-add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs,
-                                   const float *__restrict__ w, float offset, int n_rows,
-                                   int hidden, float eps, T *res_out, int64_t ros, O *y,
-                                   int64_t ys, float *__restrict__ y_scale) {
+__global__ void __launch_bounds__(rms_threads(N, kVecs, sizeof(T)),
+                                  kRmsSmThreads / rms_threads(N, kVecs, sizeof(T)) * (N * kVecs <= 8 ? 1 : 0) +
+                                      (N * kVecs <= 8 ? 0 : 1))
+add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float *__restrict__ w,
+                   float offset, int n_rows, int hidden, float eps, T *res_out, int64_t ros, O *y,
+                   int64_t ys, float *__restrict__ y_scale) {
     __shared__ float2 part[2][32];
     constexpr bool kQuant = sizeof(O) == 1;
-    griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
+    constexpr int P = (N + 1) / 2;
+    griddep_wait();    // launched behind the kernel that writes x: nothing is read before it
+    griddep_launch();  // what is launched behind this kernel may set itself up
     const int tid = threadIdx.x;
-    float wv[kVecs][N];
+    F2 wv[kVecs][P];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
         const int e = (tid + k * blockDim.x) * N;
+        float f[2 * P] = {};
 #pragma unroll
-        for (int c = 0; c < N; ++c) wv[k][c] = e < hidden ? offset + w[e + c] : 0.f;
+        for (int c = 0; c < N; ++c)
+            if (e < hidden) f[c] = offset + w[e + c];
+#pragma unroll
+        for (int i = 0; i < P; ++i) wv[k][i] = f2(f[2 * i], f[2 * i + 1]);
     }
-    int flip = 0;
-    for (int row = blockIdx.x; row < n_rows; row += gridDim.x, flip ^= 1) {
-        RawVec<T, N> a[kVecs], b[kVecs];
+    RawVec<T, N> a[kVecs], b[kVecs];
+    auto load = [&](int row) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int e = (tid + k * blockDim.x) * N;
-            a[k].zero();
-            b[k].zero();
             if (e < hidden) {
                 a[k].load(x + row * xs + e);
                 if (res) b[k].load(res + row * rs + e);
             }
         }
-        float s[kVecs][N], ss = 0.f, mx = 0.f;
+    };
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        a[k].zero();
+        b[k].zero();
+    }
+    int row = blockIdx.x, flip = 0;
+    if (row < n_rows) load(row);
+    for (; row < n_rows; row += gridDim.x, flip ^= 1) {
+        F2 s[kVecs][P], ss = f2(0.f, 0.f);
+        float mx = 0.f;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            float r[N];
-            a[k].get(s[k]);
-            b[k].get(r);
+            F2 r[P];
+            a[k].pairs(s[k]);
+            b[k].pairs(r);
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-                s[k][c] += r[c];
-                ss = fmaf(s[k][c], s[k][c], ss);
-                if constexpr (kQuant) mx = max_nan(mx, fabsf(s[k][c] * wv[k][c]));
-            }
-            const int e = (tid + k * blockDim.x) * N;
-            if (res_out && e < hidden) store_row<N>(res_out + row * ros + e, s[k]);
+            for (int i = 0; i < P; ++i) s[k][i] = f2_add(s[k][i], r[i]);
         }
-        const float2 red = block_sum_max(ss, mx, part[flip]);
+        if (row + (int)gridDim.x < n_rows) load(row + gridDim.x);
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int e = (tid + k * blockDim.x) * N;
+            if (res_out && e < hidden) {
+                float f[2 * P];
+                unpair<2 * P>(s[k], f);
+                store_row<N>(res_out + row * ros + e, f);
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                ss = f2_fma(s[k][i], s[k][i], ss);
+                s[k][i] = f2_mul(s[k][i], wv[k][i]);
+                if constexpr (kQuant) {
+                    const float2 v = f2_get(s[k][i]);
+                    mx = max_abs_nan(mx, v.x, v.y);
+                }
+            }
+        }
+        const float2 sum = f2_get(ss), red = block_sum_max(sum.x + sum.y, mx, part[flip]);
         const float inv = rsqrtf(red.x / (float)hidden + eps);
-        float q = 1.0f;
+        const F2 inv2 = f2(inv, inv);
+        F2 q2 = inv2;
         if constexpr (kQuant) {
-            const float scale = e4m3_scale(red.y * inv);
-            q = 1.0f / scale;
+            const float scale = e4m3_scale(red.y * inv), q = 1.0f / scale;
+            q2 = f2(q, q);
             if (tid == 0) y_scale[row] = scale;
         }
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int e = (tid + k * blockDim.x) * N;
             if (e >= hidden) continue;
-            float v[N];
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-                v[c] = s[k][c] * wv[k][c] * inv;
-                if constexpr (kQuant) v[c] *= q;
+            for (int i = 0; i < P; ++i) {
+                s[k][i] = f2_mul(s[k][i], inv2);
+                if constexpr (kQuant) s[k][i] = f2_mul(s[k][i], q2);
             }
-            store_row<N>(y + row * ys + e, v);
+            float f[2 * P];
+            unpair<2 * P>(s[k], f);
+            store_row<N>(y + row * ys + e, f);
         }
     }
 }
@@ -102,8 +136,8 @@ static cudaError_t launch_rms_n(const void *x, int64_t xs, const void *res, int6
                                 cudaStream_t s) {
     const int per = N * kVecs;
     const int threads = (((hidden + per - 1) / per) + 31) / 32 * 32;
-    const int per_sm = std::max(1, 2048 / threads);
-    const int grid = std::min(n_rows, sm_count() * per_sm);
+    const int resident = N * kVecs <= 8 ? kRmsSmThreads : rms_threads(N, kVecs, sizeof(T));
+    const int grid = std::min(n_rows, sm_count() * std::min(16, std::max(1, resident / threads)));
     return launch_after(add_rmsnorm_kernel<T, O, N, kVecs>, dim3(grid), dim3(threads), 0, s,
                         (const T *)x, xs, (const T *)res, rs, w, offset, n_rows, hidden, eps,
                         (T *)res_out, ros, (O *)y, ys, y_scale);

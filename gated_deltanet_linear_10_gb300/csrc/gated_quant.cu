@@ -5,8 +5,12 @@
 //
 // One CTA per token at a time; a thread holds kVecs vectors of 8 elements, and
 // the dv / 8 lanes of a head lie within one warp, so the head's mean square is
-// a warp shuffle and only the token's maximum crosses warps.  SiLU takes the
-// fast exponential and division (a few fp32 ulp, far below half an e4m3 step).
+// a warp shuffle and only the token's maximum crosses warps.  A token's loads
+// are issued before the one in front of it is worked on.  SiLU takes the fast
+// power of two and reciprocal (a few fp32 ulp, far below half an e4m3 step, and
+// within what a scale in fp32 has to keep).
+//
+// What bounds it: TODO
 #include <algorithm>
 
 #include "quant.cuh"
@@ -15,26 +19,27 @@ namespace gdn {
 
 constexpr int kGatedMaxRow = 16384;   // hv * dv
 
+constexpr int gated_threads(int vecs) { return vecs == 1 ? 256 : 1024; }   // the most a launch below takes
+constexpr int kGatedSmThreads = 1536;   // resident threads of an SM with one vector each: 42 registers
+
 template <typename T, int DV, int kVecs>
-__global__ void __launch_bounds__(kVecs == 1 ? 512 : 1024)
+__global__ void __launch_bounds__(gated_threads(kVecs), kVecs == 1 ? kGatedSmThreads / 256 : 1)
 gated_quant_kernel(const T *__restrict__ o, const T *__restrict__ z, int64_t zs,
-                                   const float *__restrict__ w, int n_tokens, int row, float eps,
-                                   bool z16, uint8_t *__restrict__ y, float *__restrict__ y_scale) {
-    constexpr int N = 8, LANES = DV / N;
+                   const float *__restrict__ w, int n_tokens, int row, float eps,
+                   bool z16, uint8_t *__restrict__ y, float *__restrict__ y_scale) {
+    constexpr int N = 8, P = N / 2, LANES = DV / N;
     __shared__ float2 part[2][32];
-    griddep_wait();   // launched behind the kernel that writes o: nothing is read before it
+    griddep_wait();    // launched behind the kernel that writes o: nothing is read before it
+    griddep_launch();  // what is launched behind this kernel may set itself up
     const int tid = threadIdx.x;
-    float wv[N];                                  // the lane's place in a head is the same for every vector
+    F2 wv[P];                                     // the lane's place in a head is the same for every vector
 #pragma unroll
-    for (int c = 0; c < N; ++c) wv[c] = w[(tid % LANES) * N + c];
-    int flip = 0;
-    for (int t = blockIdx.x; t < n_tokens; t += gridDim.x, flip ^= 1) {
-        RawVec<T, N> a[kVecs], b[kVecs];
+    for (int i = 0; i < P; ++i) wv[i] = f2(w[(tid % LANES) * N + 2 * i], w[(tid % LANES) * N + 2 * i + 1]);
+    RawVec<T, N> a[kVecs], b[kVecs];
+    auto load = [&](int t) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int e = (tid + k * blockDim.x) * N;
-            a[k].zero();
-            b[k].zero();
             if (e < row) {
                 const T *op = o + (int64_t)t * row + e, *zp = z + (int64_t)t * zs + e;
                 if (z16) {
@@ -46,34 +51,62 @@ gated_quant_kernel(const T *__restrict__ o, const T *__restrict__ z, int64_t zs,
                 }
             }
         }
-        float v[kVecs][N], mx = 0.f;
+    };
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        a[k].zero();
+        b[k].zero();
+    }
+    int t = blockIdx.x, flip = 0;
+    if (t < n_tokens) load(t);
+    for (; t < n_tokens; t += gridDim.x, flip ^= 1) {
+        F2 v[kVecs][P], g[kVecs][P];
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            float g[N], ss = 0.f;
-            a[k].get(v[k]);
-            b[k].get(g);
+            a[k].pairs(v[k]);
+            b[k].pairs(g[k]);
+        }
+        if (t + (int)gridDim.x < n_tokens) load(t + gridDim.x);
+        float mx = 0.f;
 #pragma unroll
-            for (int c = 0; c < N; ++c) ss = fmaf(v[k][c], v[k][c], ss);
+        for (int k = 0; k < kVecs; ++k) {
+            F2 ss2 = f2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                ss2 = f2_fma(v[k][i], v[k][i], ss2);
+                // SiLU(z) = z / (1 + 2^(-z log2 e)); 1 / infinity = 0 for z << 0
+                const float2 e = f2_get(f2_mul(g[k][i], f2(-kLog2e, -kLog2e)));
+                const float2 d = f2_get(f2_add(f2(ex2_approx(e.x), ex2_approx(e.y)), f2(1.0f, 1.0f)));
+                const F2 gate = f2_mul(g[k][i], f2(rcp_approx(d.x), rcp_approx(d.y)));
+                v[k][i] = f2_mul(f2_mul(v[k][i], wv[i]), gate);
+            }
+            const float2 sum = f2_get(ss2);
+            float ss = sum.x + sum.y;
 #pragma unroll
             for (int off = LANES / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
             const float inv = rsqrtf(ss * (1.0f / DV) + eps);
+            const F2 inv2 = f2(inv, inv);
             const bool on = (tid + k * blockDim.x) * N < row;
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-                v[k][c] = v[k][c] * inv * wv[c] * silu_f(g[c]);
-                if (on) mx = max_nan(mx, fabsf(v[k][c]));
+            for (int i = 0; i < P; ++i) {
+                v[k][i] = f2_mul(v[k][i], inv2);
+                const float2 f = f2_get(v[k][i]);
+                if (on) mx = max_abs_nan(mx, f.x, f.y);
             }
         }
-        const float scale = e4m3_scale(block_sum_max(0.f, mx, part[flip]).y);
+        const float scale = e4m3_scale(block_max(mx, part[flip]));
         const float q = 1.0f / scale;
+        const F2 q2 = f2(q, q);
         if (tid == 0) y_scale[t] = scale;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int e = (tid + k * blockDim.x) * N;
             if (e >= row) continue;
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[k][c] *= q;
-            store_row<N>(reinterpret_cast<E4m3 *>(y) + (int64_t)t * row + e, v[k]);
+            for (int i = 0; i < P; ++i) v[k][i] = f2_mul(v[k][i], q2);
+            float f[N];
+            unpair<N>(v[k], f);
+            store_row<N>(reinterpret_cast<E4m3 *>(y) + (int64_t)t * row + e, f);
         }
     }
 }
@@ -85,11 +118,11 @@ static cudaError_t launch_gated_quant(const void *o, const void *z, int64_t zs, 
     const int row = hv * DV, vecs = row / 8;
     auto go = [&](auto kernel, int per) {
         const int threads = ((vecs + per - 1) / per + 31) / 32 * 32;
-        const int grid = std::min(n_tokens, sm_count() * std::max(1, 2048 / threads));
+        const int grid = std::min(n_tokens, sm_count() * std::min(16, std::max(1, (per == 1 ? kGatedSmThreads : 1024) / threads)));
         return launch_after(kernel, dim3(grid), dim3(threads), 0, s, (const T *)o, (const T *)z, zs,
                             w, n_tokens, row, eps, z16, (uint8_t *)y, y_scale);
     };
-    return vecs <= 512 ? go(gated_quant_kernel<T, DV, 1>, 1) : go(gated_quant_kernel<T, DV, 2>, 2);
+    return vecs <= 256 ? go(gated_quant_kernel<T, DV, 1>, 1) : go(gated_quant_kernel<T, DV, 2>, 2);
 }
 
 }  // namespace gdn

@@ -30,9 +30,9 @@ bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64
 // 128 x BT tile, each on its part of k.
 template <int BT> struct NarrowCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = BT >= 128 ? 5 : BT >= 64 ? 3 : 4;
     static constexpr uint32_t kSums = BT * 512;          // BT tokens x 128 channels, fp32
-    static constexpr uint32_t kSmem = kStages * kStage + kSums + 1024;
+    static constexpr uint32_t kSmem = kStages * kStage + kSums;
     static_assert(kStages * kStage >= kSums, "a CTA's own sums fit its stages");
 };
 constexpr int kNarrowThreads = 192;
@@ -46,12 +46,26 @@ __device__ __forceinline__ void bulk_send(uint32_t dst, uint32_t src, uint32_t b
         : "memory");
 }
 
+// The residual of 8 channels, as loaded (bf16: the first 16 bytes).
+struct Res8 {
+    uint4 q[2];
+    __device__ __forceinline__ void load(const LinearEpi &ep, int t, int n) {
+        if (ep.out_f32) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(ep.res) + t * ep.rs + n);
+            q[0] = p[0];
+            q[1] = p[1];
+        } else {
+            q[0] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(ep.res) + t * ep.rs + n);
+        }
+    }
+};
+
 // 8 channels n .. n + 7 of token t: scale, bias, activation, residual, one
-// rounding.  y may be residual: the 8 are read before they are written.
+// rounding.  y may be residual: the 8 are read before they are written.  vec:
+// the 8 exist and are whole vectors, their residual in `r`.
 template <typename O>
-__device__ __forceinline__ void narrow_out8(float (&v)[8], const LinearEpi &ep, int t, int n, const float *sw,
-                                            const float *bias) {
-    const float sx = ep.sx ? ep.sx[t] : 1.0f;
+__device__ __forceinline__ void narrow_out8(float (&v)[8], const LinearEpi &ep, int t, int n, float sx,
+                                            const float *sw, const float *bias, bool vec, const Res8 &r) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sx * sw[i], bias[i]);
     if (ep.act == GDN_ACT_SILU) {
@@ -62,18 +76,17 @@ __device__ __forceinline__ void narrow_out8(float (&v)[8], const LinearEpi &ep, 
         for (int i = 0; i < 8; ++i) v[i] = linear_act<GDN_ACT_GELU>(v[i]);
     }
     O *y = reinterpret_cast<O *>(ep.y) + t * ep.ys + n;
-    const O *res = reinterpret_cast<const O *>(ep.res) + t * ep.rs + n;
-    if (ep.vec8 && n + 8 <= ep.n_out) {
+    if (vec) {
         if (ep.res) {
-            RawVec<O, 8> q;
-            float r[8];
-            q.load(res);
-            q.get(r);
+            float f[8];
+            Vec16<O>::unpack(r.q[0], f);
+            if constexpr (sizeof(O) == 4) Vec16<O>::unpack(r.q[1], f + 4);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
+            for (int i = 0; i < 8; ++i) v[i] += f[i];
         }
         store_row<8>(y, v);
     } else {
+        const O *res = reinterpret_cast<const O *>(ep.res) + t * ep.rs + n;
         const int cnt = min(8, ep.n_out - n);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -101,12 +114,12 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
                      const __grid_constant__ LinearEpi ep, int n_in, int splits) {
     using C = NarrowCfg<BT>;
     constexpr int S = C::kStages;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[S], empty[S], done, arrived;
+    __shared__ float sxs[BT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int rank = splits > 1 ? (int)cta_rank() : 0;
     const int n0 = blockIdx.x / splits * 128, t0 = blockIdx.y * BT;
     constexpr int kElems = kE4m3 ? 128 : 64;                 // k per block of 128 bytes
@@ -114,30 +127,32 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     const int k0 = (int)((int64_t)blocks * rank / splits);
     const int nk = (int)((int64_t)blocks * (rank + 1) / splits) - k0;
     volatile int *abort = &abort_flag;
-    auto load = [&](int i) {
-        const int s = i % S;
+    const bool one = warp < 2 && elect_lane();
+    auto load = [&](int i, int s) {
         uint8_t *st = smem + s * C::kStage;
         mbar_arrive_expect_tx(&full[s], C::kStage);
         tma_load_2d(st, &mw, &full[s], (k0 + i) * kElems, n0);
         tma_load_2d(st + C::kW, &mx, &full[s], (k0 + i) * kElems, t0);
     };
 
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&mx);
-        prefetch_tensormap(&mw);
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+    if (warp == 0) {
+        if (one) {
+            prefetch_tensormap(&mx);
+            prefetch_tensormap(&mw);
+            for (int s = 0; s < S; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            mbar_init(&done, 1);
+            mbar_init(&arrived, 1);
+            abort_flag = (smem_u32(smem) & 1023u) != 0;   // the swizzle needs the alignment asked for above
+            fence_mbar_init();
+            fence_async_smem();
+            griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
+            for (int i = 0; i < min(S, nk); ++i) load(i, i);
         }
-        mbar_init(&done, 1);
-        mbar_init(&arrived, 1);
-        abort_flag = 0;
-        fence_mbar_init();
-        fence_async_smem();
-        griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
-        for (int i = 0; i < min(S, nk); ++i) load(i);
+        __syncwarp();
     }
-    __syncwarp();
     if (warp == 1) {
         tmem_alloc(&tmem_base, BT);
         tmem_relinquish();
@@ -148,24 +163,34 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (splits > 1) cluster_arrive();      // waited for before the first copy to another CTA
     griddep_wait();
 
-    if (warp == 0 && lane == 0) {
-        int i = S;
+    if (warp == 0) {
+        int i = S, s = 0;
+        uint32_t phase = 0;
+#pragma unroll 1
         for (; i < nk; ++i) {
-            if (!mbar_wait(&empty[i % S], ((i / S) - 1) & 1, abort)) break;
-            load(i);
+            if (!mbar_wait_all(&empty[s], phase, abort)) break;
+            if (one) load(i, s);
+            __syncwarp();
+            if (++s == S) {
+                s = 0;
+                phase ^= 1;
+            }
         }
-        if (*abort)
+        griddep_launch();   // what is launched behind this kernel may set itself up
+        if (one && *abort)
             for (int j = i - S; j < min(i, nk); ++j) mbar_drain(&full[j % S], (j / S) & 1);
     } else if (warp == 1) {
         constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
-        const bool one = elect_lane();
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
+        const uint32_t base = smem_u32(smem) >> 4;
+        uint32_t phase = 0;
+        int s = 0;
+#pragma unroll 1
         for (int i = 0; i < nk; ++i) {
-            const int s = i % S;
-            if (!mbar_wait_all(&full[s], (i / S) & 1, abort)) break;
+            if (!mbar_wait_all(&full[s], phase, abort)) break;
             tc_fence_after();
             if (one) {
-                const uint32_t st = smem_u32(smem + s * C::kStage) >> 4;
+                const uint32_t st = base + s * (C::kStage >> 4);
                 const uint64_t da = desc | st, db = desc | (st + (C::kW >> 4));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -173,11 +198,18 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
                 mma_commit(&empty[s]);
             }
             __syncwarp();
+            if (++s == S) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         if (one) {
             mma_commit(&done);
             mbar_drain(&done, 0);
         }
+    } else {
+        for (int t = tid - 64; t < BT; t += kNarrowThreads - 64)
+            sxs[t] = ep.sx && t0 + t < ep.n_tokens ? ep.sx[t0 + t] : 1.0f;
     }
     __syncwarp();
 
@@ -193,6 +225,17 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         sw[i] = on && ep.sw ? ep.sw[n + i] : 1.0f;
         bias[i] = on && ep.bias ? ep.bias[n + i] : 0.0f;
     }
+    // the residual of two of its items ahead: the first two before the sums are there
+    const bool vec = ep.vec8 && n + 8 <= ep.n_out;
+    Res8 res[2];
+    auto ask = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int tok = (i + u * kNarrowThreads) >> 4;
+            if (ep.res && vec && tok < cnt) res[u].load(ep, first + tok, n);
+        }
+    };
+    ask(tid);
     if (warp >= 2 && mbar_wait_all(&done, 0, abort)) {
         // accumulator lane 32 q + l is channel n0 + 32 q + l, its columns the tokens
         tc_fence_after();
@@ -230,20 +273,35 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     }
     if (!*abort) {
 #pragma unroll 1
-        for (int i = tid; i < cnt * 16; i += kNarrowThreads) {
-            const int tok = i >> 4;
-            float v[8] = {};
+        for (int i = tid; i < cnt * 16; i += 2 * kNarrowThreads) {
+            float v[2][8] = {};
 #pragma unroll 1
             for (int r = 0; r < splits; ++r) {
-                const float *p = (r == rank ? own : got) + (r * per + tok) * 128 + g * 8;
-                const float4 a = *reinterpret_cast<const float4 *>(p);
-                const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+                const float *p = (r == rank ? own : got) + r * per * 128 + g * 8;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int tok = min((i + u * kNarrowThreads) >> 4, cnt - 1);
+                    const float4 a = *reinterpret_cast<const float4 *>(p + tok * 128);
+                    const float4 b = *reinterpret_cast<const float4 *>(p + tok * 128 + 4);
+                    v[u][0] += a.x; v[u][1] += a.y; v[u][2] += a.z; v[u][3] += a.w;
+                    v[u][4] += b.x; v[u][5] += b.y; v[u][6] += b.z; v[u][7] += b.w;
+                }
             }
-            if (n < ep.n_out) {
-                if (ep.out_f32) narrow_out8<float>(v, ep, first + tok, n, sw, bias);
-                else narrow_out8<__nv_bfloat16>(v, ep, first + tok, n, sw, bias);
+            const Res8 cur[2] = {res[0], res[1]};
+            ask(i + 2 * kNarrowThreads);
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const int tok = (i + u * kNarrowThreads) >> 4;
+                if (n >= ep.n_out || tok >= cnt) break;
+                const float sx = sxs[rank * per + tok];
+                float(&w)[8] = v[0];
+                if (u) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = v[1][j];
+                }
+                const Res8 c = u ? cur[1] : cur[0];
+                if (ep.out_f32) narrow_out8<float>(w, ep, first + tok, n, sx, sw, bias, vec, c);
+                else narrow_out8<__nv_bfloat16>(w, ep, first + tok, n, sx, sw, bias, vec, c);
             }
         }
     }
@@ -269,7 +327,8 @@ static gdn_status launch_narrow(const LinearCall &c) {
     int splits = 1;
     while (splits < 8 && (int64_t)nn * nt * splits * 2 <= sms && blocks >= splits * 4) splits *= 2;
     auto kernel = linear_narrow_kernel<BT, kE4m3>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static SmemAllowed allowed;
+    cudaError_t e = allowed.ask(kernel, C::kSmem);
     if (e == cudaSuccess)
         e = launch_after_cluster(kernel, splits, dim3(nn * splits, nt), dim3(kNarrowThreads), C::kSmem, c.stream, mx, mw,
                                  c.e, c.n_in, splits);

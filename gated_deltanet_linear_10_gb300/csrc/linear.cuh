@@ -2,6 +2,8 @@
 //   y[t][n] = act(sx[t] sw[n] sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n]
 #pragma once
 
+#include <atomic>
+
 #include "quant.cuh"
 #include "tc.cuh"
 
@@ -20,19 +22,7 @@ struct LinearEpi {
 };
 
 // The activations run beside the products and take issue slots from the warps
-// that feed them, so they are kept short: the approximate reciprocal and power
-// of two of the hardware (a few ulp; results below 2^-126 flushed to 0).
-__device__ __forceinline__ float rcp_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float ex2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-constexpr float kLog2e = 1.44269504089f;
+// that feed them, so they are kept short.
 
 // v / (1 + e^-v); for v << 0 the exponential is infinite and its reciprocal 0.
 __device__ __forceinline__ float silu_short(float v) {
@@ -149,6 +139,22 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, v
 // (e4m3), loaded as boxes of 128 bytes x box_rows in the 128-byte swizzle.
 bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64_t rows,
                          int64_t row_stride_elems, uint32_t box_rows, bool e4m3);
+
+// cudaFuncSetAttribute for a kernel's dynamic shared memory, asked for once per
+// device (a call of its own takes as long as the argument checks).
+struct SmemAllowed {
+    std::atomic<uint64_t> devices{0};
+    template <typename K> cudaError_t ask(K kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // launch_after with clusters of `cluster` CTAs along x.
 template <typename... KArgs, typename... Args>

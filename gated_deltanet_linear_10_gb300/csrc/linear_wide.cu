@@ -261,6 +261,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 }
             }
         }
+        griddep_launch();      // what is launched behind this kernel may set itself up
         if (one && (!ok || *abort)) {
             // Given up: the copies in flight land before the CTA ends.  The leader
             // waits on the barriers that count them; the peer, which has none of
@@ -467,7 +468,8 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
                         e.n_out, e.n_tokens, e.ys * sizeof(O), 128 / sizeof(O), 32, true))
         return GDN_ERR_CUDA;
     auto kernel = linear_wide_kernel<kE4m3, O>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+    static SmemAllowed allowed;
+    cudaError_t err = allowed.ask(kernel, kWideSmem);
     if (err == cudaSuccess)
         err = launch_after(kernel, dim3(std::min(2 * plan.n_tiles, sms)), dim3(kWideThreads), kWideSmem,
                            c.stream, mx, mw, mt, my, e, c.n_in, plan, rows);

@@ -17,12 +17,60 @@ namespace gdn {
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126
 
-// max(a, b), NaN when either is (fmaxf would drop it).
+// max(a, b), NaN when either is (fmaxf would drop it); of |a|, |b|, |c|.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Pairs of fp32 values, two to an instruction.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __uint_as_float(hi)); }
+__device__ __forceinline__ float2 f2_get(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The hardware's reciprocal and power of two (a few ulp; results below 2^-126
+// flushed to 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.44269504089f;
 
 __device__ __forceinline__ float e4m3_scale(float amax) {
     return max_nan(amax * (1.0f / kE4m3Max), kMinScale);
@@ -58,18 +106,34 @@ template <typename T, int N> struct RawVec {
 #pragma unroll
         for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void get(float *out) const {
+    // as N / 2 pairs
+    __device__ __forceinline__ void pairs(F2 *out) const {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(r);
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i)
-            Vec16<T>::unpack(r[i], out + i * Vec16<T>::N);
+            for (int i = 0; i < N / 2; ++i) out[i] = f2_bits(w[2 * i], w[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) out[i] = f2_bits(w[i] << 16, w[i] & 0xffff0000u);
+        }
     }
 };
 template <typename T> struct RawVec<T, 1> {
     T r;
     __device__ __forceinline__ void load(const T *p) { r = *p; }
     __device__ __forceinline__ void zero() { Io<T>::store(&r, 0.f); }
-    __device__ __forceinline__ void get(float *out) const { out[0] = Io<T>::load(&r); }
+    __device__ __forceinline__ void pairs(F2 *out) const { out[0] = f2(Io<T>::load(&r), 0.f); }
 };
+
+// N values out of (N + 1) / 2 pairs.
+template <int N> __device__ __forceinline__ void unpair(const F2 *in, float *out) {
+#pragma unroll
+    for (int i = 0; i < (N + 1) / 2; ++i) {
+        const float2 v = f2_get(in[i]);
+        out[2 * i] = v.x;
+        if (2 * i + 1 < N) out[2 * i + 1] = v.y;
+    }
+}
 
 // Stores N fp32 values as O (N = 1, 4 or 8; vectors aligned to their size).
 template <int N> __device__ __forceinline__ void store_row(float *p, const float *v) {
@@ -122,6 +186,20 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx, float2 *par
         mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     }
     return make_float2(sum, mx);
+}
+
+// The NaN-keeping max alone, in the same way.
+__device__ __forceinline__ float block_max(float mx, float2 *part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (warps == 1) return mx;
+    if (lane == 0) part[warp].x = mx;
+    __syncthreads();
+    mx = lane < warps ? part[lane].x : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    return mx;
 }
 
 }  // namespace gdn
