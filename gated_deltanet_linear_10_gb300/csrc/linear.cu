@@ -35,7 +35,7 @@ template <int BT> struct NarrowCfg {
     static constexpr uint32_t kSmem = kStages * kStage + kSums;
     static_assert(kStages * kStage >= kSums, "a CTA's own sums fit its stages");
 };
-constexpr int kNarrowThreads = 192;
+constexpr int kNarrowThreads = 256;
 
 // Copy of this CTA's shared memory into another CTA's of the cluster, its bytes
 // counted on a barrier of that CTA (16-byte aligned, a multiple of 16 bytes).
@@ -60,40 +60,59 @@ struct Res8 {
     }
 };
 
-// 8 channels n .. n + 7 of token t: scale, bias, activation, residual, one
-// rounding.  y may be residual: the 8 are read before they are written.  vec:
-// the 8 exist and are whole vectors, their residual in `r`.
+// Channels n .. n + 7 of tokens t[0], t[1] (t[u] < 0: none) out: residual, one
+// rounding, store.  y may be residual: it is read before it is written.  vec:
+// the 8 exist and are whole vectors, their residuals in `r`.
 template <typename O>
-__device__ __forceinline__ void narrow_out8(float (&v)[8], const LinearEpi &ep, int t, int n, float sx,
-                                            const float *sw, const float *bias, bool vec, const Res8 &r) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sx * sw[i], bias[i]);
-    if (ep.act == GDN_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = linear_act<GDN_ACT_SILU>(v[i]);
-    } else if (ep.act == GDN_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = linear_act<GDN_ACT_GELU>(v[i]);
-    }
-    O *y = reinterpret_cast<O *>(ep.y) + t * ep.ys + n;
+__device__ __forceinline__ void narrow_out(F2 (&v)[2][4], const LinearEpi &ep, const int (&t)[2], int n, bool vec,
+                                           const Res8 (&r)[2]) {
+    O *y = reinterpret_cast<O *>(ep.y) + n;
     if (vec) {
-        if (ep.res) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (t[u] < 0) continue;
+            if (ep.res) {
+                RawVec<O, 8> raw;
+                F2 q[4];
+                raw.r[0] = r[u].q[0];
+                if constexpr (sizeof(O) == 4) raw.r[1] = r[u].q[1];
+                raw.pairs(q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[u][i] = f2_add(v[u][i], q[i]);
+            }
             float f[8];
-            Vec16<O>::unpack(r.q[0], f);
-            if constexpr (sizeof(O) == 4) Vec16<O>::unpack(r.q[1], f + 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += f[i];
+            unpair<8>(v[u], f);
+            store_row<8>(y + t[u] * ep.ys, f);
         }
-        store_row<8>(y, v);
     } else {
-        const O *res = reinterpret_cast<const O *>(ep.res) + t * ep.rs + n;
+        const O *res = reinterpret_cast<const O *>(ep.res) + n;
         const int cnt = min(8, ep.n_out - n);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+            const int tu = u ? t[1] : t[0];
+            if (tu < 0) continue;
+            float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (ep.res && i < cnt) v[i] += Io<O>::load(res + i);
+            for (int i = 0; i < 4; ++i) {
+                const float2 p = f2_get(u ? v[1][i] : v[0][i]);
+                f[2 * i] = p.x;
+                f[2 * i + 1] = p.y;
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < cnt) Io<O>::store(y + i, v[i]);
+            for (int i = 0; i < 8; ++i)
+                if (ep.res && i < cnt) f[i] += Io<O>::load(res + tu * ep.rs + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < cnt) Io<O>::store(y + tu * ep.ys + i, f[i]);
+        }
+    }
+}
+
+template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = f2_get(v[i / 4][i % 4]);
+        v[i / 4][i % 4] = f2(linear_act<kAct>(f.x), linear_act<kAct>(f.y));
     }
 }
 
@@ -218,12 +237,12 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     float *own = reinterpret_cast<float *>(smem);        // where the operands were
     float *got = reinterpret_cast<float *>(smem + S * C::kStage);
     const int g = tid & 15, n = n0 + g * 8;              // this thread's channels below
-    float sw[8], bias[8];
+    F2 sw[4], bias[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool on = n + i < ep.n_out;
-        sw[i] = on && ep.sw ? ep.sw[n + i] : 1.0f;
-        bias[i] = on && ep.bias ? ep.bias[n + i] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        const bool on = n + 2 * i < ep.n_out, on1 = n + 2 * i + 1 < ep.n_out;
+        sw[i] = f2(on && ep.sw ? ep.sw[n + 2 * i] : 1.0f, on1 && ep.sw ? ep.sw[n + 2 * i + 1] : 1.0f);
+        bias[i] = f2(on && ep.bias ? ep.bias[n + 2 * i] : 0.0f, on1 && ep.bias ? ep.bias[n + 2 * i + 1] : 0.0f);
     }
     // the residual of two of its items ahead: the first two before the sums are there
     const bool vec = ep.vec8 && n + 8 <= ep.n_out;
@@ -236,7 +255,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         }
     };
     ask(tid);
-    if (warp >= 2 && mbar_wait_all(&done, 0, abort)) {
+    if (warp >= 2 && warp < 6 && mbar_wait_all(&done, 0, abort)) {
         // accumulator lane 32 q + l is channel n0 + 32 q + l, its columns the tokens
         tc_fence_after();
         const int quad = warp & 3;
@@ -274,34 +293,36 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (!*abort) {
 #pragma unroll 1
         for (int i = tid; i < cnt * 16; i += 2 * kNarrowThreads) {
-            float v[2][8] = {};
+            const int tok[2] = {i >> 4, (i + kNarrowThreads) >> 4};
+            const int tok1 = min(tok[1], cnt - 1);
+            F2 v[2][4] = {};
 #pragma unroll 1
             for (int r = 0; r < splits; ++r) {
                 const float *p = (r == rank ? own : got) + r * per * 128 + g * 8;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int tok = min((i + u * kNarrowThreads) >> 4, cnt - 1);
-                    const float4 a = *reinterpret_cast<const float4 *>(p + tok * 128);
-                    const float4 b = *reinterpret_cast<const float4 *>(p + tok * 128 + 4);
-                    v[u][0] += a.x; v[u][1] += a.y; v[u][2] += a.z; v[u][3] += a.w;
-                    v[u][4] += b.x; v[u][5] += b.y; v[u][6] += b.z; v[u][7] += b.w;
+                    const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(p + (u ? tok1 : tok[0]) * 128);
+                    const ulonglong2 a = q[0], b = q[1];
+                    v[u][0] = f2_add(v[u][0], a.x);
+                    v[u][1] = f2_add(v[u][1], a.y);
+                    v[u][2] = f2_add(v[u][2], b.x);
+                    v[u][3] = f2_add(v[u][3], b.y);
                 }
             }
             const Res8 cur[2] = {res[0], res[1]};
             ask(i + 2 * kNarrowThreads);
-#pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                const int tok = (i + u * kNarrowThreads) >> 4;
-                if (n >= ep.n_out || tok >= cnt) break;
-                const float sx = sxs[rank * per + tok];
-                float(&w)[8] = v[0];
-                if (u) {
+            const float sx0 = sxs[rank * per + tok[0]], sx1 = sxs[rank * per + tok1];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = v[1][j];
-                }
-                const Res8 c = u ? cur[1] : cur[0];
-                if (ep.out_f32) narrow_out8<float>(w, ep, first + tok, n, sx, sw, bias, vec, c);
-                else narrow_out8<__nv_bfloat16>(w, ep, first + tok, n, sx, sw, bias, vec, c);
+            for (int j = 0; j < 4; ++j) {
+                v[0][j] = f2_fma(v[0][j], f2_mul(f2(sx0, sx0), sw[j]), bias[j]);
+                v[1][j] = f2_fma(v[1][j], f2_mul(f2(sx1, sx1), sw[j]), bias[j]);
+            }
+            if (ep.act == GDN_ACT_SILU) narrow_act<GDN_ACT_SILU>(v);
+            else if (ep.act == GDN_ACT_GELU) narrow_act<GDN_ACT_GELU>(v);
+            if (n < ep.n_out) {
+                const int t[2] = {first + tok[0], tok[1] < cnt ? first + tok[1] : -1};
+                if (ep.out_f32) narrow_out<float>(v, ep, t, n, vec, cur);
+                else narrow_out<__nv_bfloat16>(v, ep, t, n, vec, cur);
             }
         }
     }
