@@ -334,25 +334,47 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
+// How a product of these sizes is cut over narrow tiles, and what that takes in
+// SM cycles by the estimate below.
+struct NarrowPlan {
+    int nn, nt, splits;
+    int64_t cycles;
+};
+
+// A k block takes 567 cycles: a CTA's 128-channel product costs 128 cycles for
+// any number of tokens up to 128, the ring the rest.  Behind and in front of the
+// loop 9,000 (256 x 2048 x 8192 e4m3, k whole), and 3,500 more where the sums
+// are exchanged (256 x 4096 x 2048, k in four).  Every cluster that the device
+// cannot hold at once waits for a whole one.
+template <int BT, bool kE4m3> static cudaError_t plan_narrow(const LinearCall &c, NarrowPlan &best) {
+    using C = NarrowCfg<BT>;
+    static ClustersHeld held[4];
+    auto kernel = linear_narrow_kernel<BT, kE4m3>;
+    const int nn = (c.e.n_out + 127) / 128, nt = (c.e.n_tokens + BT - 1) / BT;
+    const int blocks = (c.n_in + (kE4m3 ? 127 : 63)) / (kE4m3 ? 128 : 64);
+    best.cycles = INT64_MAX;
+    for (int i = 0; i < 4 && (i == 0 || blocks >= 2 << i); ++i) {   // at least two blocks for a CTA
+        int fit = 0;
+        const cudaError_t e = held[i].ask(kernel, 1 << i, kNarrowThreads, C::kSmem, fit);
+        if (e != cudaSuccess) return e;
+        if (fit <= 0) continue;
+        const int64_t waves = ((int64_t)nn * nt + fit - 1) / fit;
+        const int64_t cycles = 9000 + (i ? 3500 : 0) + (waves - 1) * 4000 + waves * ((blocks + (1 << i) - 1) >> i) * 567;
+        if (cycles < best.cycles) best = {nn, nt, 1 << i, cycles};
+    }
+    return cudaSuccess;
+}
+
 template <int BT, bool kE4m3>
-static gdn_status launch_narrow(const LinearCall &c) {
+static gdn_status launch_narrow(const LinearCall &c, const NarrowPlan &plan) {
     using C = NarrowCfg<BT>;
     CUtensorMap mx, mw;
     if (!encode_tmap_operand(&mx, c.x, c.n_in, c.e.n_tokens, c.xs, BT, kE4m3) ||
         !encode_tmap_operand(&mw, c.w, c.n_in, c.e.n_out, c.ws, 128, kE4m3))
         return GDN_ERR_CUDA;
-    // as many CTAs as there are SMs, by cutting k: powers of two up to the 8
-    // CTAs of a portable cluster, each with at least two k blocks
-    const int nn = (c.e.n_out + 127) / 128, nt = (c.e.n_tokens + BT - 1) / BT;
-    const int blocks = (c.n_in + (kE4m3 ? 127 : 63)) / (kE4m3 ? 128 : 64), sms = sm_count();
-    int splits = 1;
-    while (splits < 8 && (int64_t)nn * nt * splits * 2 <= sms && blocks >= splits * 4) splits *= 2;
-    auto kernel = linear_narrow_kernel<BT, kE4m3>;
-    static SmemAllowed allowed;
-    cudaError_t e = allowed.ask(kernel, C::kSmem);
-    if (e == cudaSuccess)
-        e = launch_after_cluster(kernel, splits, dim3(nn * splits, nt), dim3(kNarrowThreads), C::kSmem, c.stream, mx, mw,
-                                 c.e, c.n_in, splits);
+    const cudaError_t e = launch_after_cluster(linear_narrow_kernel<BT, kE4m3>, plan.splits,
+                                               dim3(plan.nn * plan.splits, plan.nt), dim3(kNarrowThreads),
+                                               C::kSmem, c.stream, mx, mw, c.e, c.n_in, plan.splits);
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return GDN_ERR_LAUNCH;
@@ -360,12 +382,23 @@ static gdn_status launch_narrow(const LinearCall &c) {
     return GDN_OK;
 }
 
+// The narrow tiles for up to 128 tokens; beyond, whichever estimate is shorter
+// (measured, narrow and wide: 512 x 4096 x 2048 TODO us, 512 x 2048 x 8192 TODO us).
 template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
     const int t = c.e.n_tokens;
-    if (t >= 512) return launch_linear_wide(c, kE4m3);
-    if (t <= 32) return launch_narrow<32, kE4m3>(c);
-    if (t <= 64) return launch_narrow<64, kE4m3>(c);
-    return launch_narrow<128, kE4m3>(c);
+    NarrowPlan plan = {};
+    cudaError_t e = t <= 32   ? plan_narrow<32, kE4m3>(c, plan)
+                    : t <= 64 ? plan_narrow<64, kE4m3>(c, plan)
+                              : plan_narrow<128, kE4m3>(c, plan);
+    if (e != cudaSuccess) {
+        set_last_cuda_error(e);
+        return GDN_ERR_CUDA;
+    }
+    if (t > 128 && (plan.nt > 65535 || wide_cycles(c, kE4m3) < plan.cycles)) return launch_linear_wide(c, kE4m3);
+    if (plan.cycles == INT64_MAX) return GDN_ERR_UNSUPPORTED;
+    if (t <= 32) return launch_narrow<32, kE4m3>(c, plan);
+    if (t <= 64) return launch_narrow<64, kE4m3>(c, plan);
+    return launch_narrow<128, kE4m3>(c, plan);
 }
 
 }  // namespace gdn

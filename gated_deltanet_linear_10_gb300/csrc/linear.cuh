@@ -2,6 +2,7 @@
 //   y[t][n] = act(sx[t] sw[n] sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n]
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 
 #include "quant.cuh"
@@ -156,25 +157,71 @@ struct SmemAllowed {
     }
 };
 
-// launch_after with clusters of `cluster` CTAs along x.
+// A cluster launch's configuration, behind the kernel before it in the stream.
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    ClusterLaunch(int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t s) {
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+// How many clusters of a kernel the device holds at once; the kernel's dynamic
+// shared memory is allowed on the way.  Asked for once per device.
+struct ClustersHeld {
+    static constexpr int kDevices = 16;
+    std::atomic<int> held[kDevices] = {};   // count + 1
+    template <typename K> cudaError_t ask(K kernel, int cluster, int threads, int smem, int &count) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const int known = dev < kDevices ? held[dev].load(std::memory_order_acquire) : 0;
+        if (known) {
+            count = known - 1;
+            return cudaSuccess;
+        }
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // as much shared memory as there is: two CTAs of an SM where they fit
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+        ClusterLaunch l(cluster, dim3(cluster), dim3(threads), smem, nullptr);
+        l.cfg.numAttrs = 1;                 // the cluster's size
+        e = cudaOccupancyMaxActiveClusters(&count, kernel, &l.cfg);
+        // which counts one CTA of an SM.  Two run there where shared memory and
+        // registers allow: 64 x 4096 x 2048 with k cut over 16 clusters of 8 took
+        // 14.8 us with tiles of 128 KB (15 clusters at once) and 8.6 us with 104 KB.
+        int sm_smem = 0, sm_regs = 0;
+        cudaFuncAttributes a;
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sm_regs, cudaDevAttrMaxRegistersPerMultiprocessor, dev);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
+        if (e != cudaSuccess) return e;
+        const int per_sm = std::min(sm_smem / (int)(smem + a.sharedSizeBytes + 1024),
+                                    sm_regs / ((a.numRegs + 7) / 8 * 8 * threads));
+        count *= std::max(1, std::min(2, per_sm));
+        if (e == cudaSuccess && dev < kDevices) held[dev].store(count + 1, std::memory_order_release);
+        return e;
+    }
+};
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_after_cluster(void (*kernel)(KArgs...), int cluster, dim3 grid, dim3 block,
                                         size_t smem, cudaStream_t s, Args &&...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    const ClusterLaunch l(cluster, grid, block, smem, s);
+    return cudaLaunchKernelEx(&l.cfg, kernel, std::forward<Args>(args)...);
 }
 
 struct LinearCall {
@@ -185,6 +232,8 @@ struct LinearCall {
     cudaStream_t stream;
 };
 
-gdn_status launch_linear_wide(const LinearCall &c, bool e4m3);   // linear_wide.cu
+// linear_wide.cu: the product on CTA pairs, and the cycles of an SM it takes by estimate.
+gdn_status launch_linear_wide(const LinearCall &c, bool e4m3);
+int64_t wide_cycles(const LinearCall &c, bool e4m3);
 
 }  // namespace gdn

@@ -425,34 +425,40 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
-// The plan with the shortest estimate.  A tile of w channels reads 4 KB of
-// tokens and 16 KB w / 256 of weights from shared memory per 32 bytes of k,
-// the measure of its time; the last `rows` token tiles are cut into channel
-// tiles of w so that the last wave of pairs is full (81 x 32 tiles on 76 pairs
-// are 34.1 waves: 35 with one width).
-WidePlan plan_wide(int n_tokens, int n_out, int pairs) {
-    WidePlan best = {};
+// The plan with the shortest estimate, and that in cycles of a k block.  A block
+// takes 512 cycles of a pair on 256 channels, the rate of the tensor cores; on
+// fewer it is the operands' copies that hold it (512 x 2048 x 8192 in channel
+// tiles of 192, 128 and 64: 445, 410 and 410).  The last `rows` token tiles are
+// cut into channel tiles of w where that fills the last wave of pairs better.
+int64_t plan_wide(int n_tokens, int n_out, int pairs, WidePlan &best) {
+    constexpr int kBlockCycles[4] = {410, 410, 445, 512};
     const int nt = (n_tokens + kTokTile - 1) / kTokTile, nn = (n_out + kChTile - 1) / kChTile;
     auto waves = [&](int64_t tiles) { return (tiles + pairs - 1) / pairs; };
     int64_t cost = INT64_MAX;
     for (int rows = 0; rows <= std::min(nt, 16); ++rows)
         for (int w = 64; w <= (rows ? kChTile - 64 : 64); w += 64) {   // whole staging rows
             const int64_t full = (int64_t)(nt - rows) * nn, tail = (int64_t)rows * ((n_out + w - 1) / w);
-            const int64_t c = waves(full) * 20 + waves(tail) * (4 + w / 16);
+            const int64_t c = waves(full) * kBlockCycles[3] + waves(tail) * kBlockCycles[w / 64 - 1];
             if (c < cost) {
                 cost = c;
                 best = {nt - rows, nt, nn, (int)full, w, (int)(full + tail)};
             }
         }
-    return best;
+    return cost;
+}
+
+// Whether the tiles can be counted in 32 bits.
+bool wide_fits(const LinearEpi &e) {
+    return ((int64_t)e.n_tokens + 255) / 256 * (((int64_t)e.n_out + 31) / 32) < (1 << 30);
 }
 
 template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
     const LinearEpi &e = c.e;
     const int sms = sm_count() / 2 * 2;
     GDN_REQUIRE(sms >= 2, GDN_ERR_UNSUPPORTED);
-    GDN_REQUIRE((int64_t)((e.n_tokens + 255) / 256) * ((e.n_out + 31) / 32) < (1 << 30), GDN_ERR_UNSUPPORTED);
-    const WidePlan plan = plan_wide(e.n_tokens, e.n_out, sms / 2);
+    GDN_REQUIRE(wide_fits(e), GDN_ERR_UNSUPPORTED);
+    WidePlan plan;
+    plan_wide(e.n_tokens, e.n_out, sms / 2, plan);
     CUtensorMap mx, mw, mt, my = {};
     if (!encode_tmap_operand(&mx, c.x, c.n_in, e.n_tokens, c.xs, kTokHalf, kE4m3) ||
         !encode_tmap_operand(&mw, c.w, c.n_in, e.n_out, c.ws, kChTile / 2, kE4m3) ||
@@ -481,6 +487,15 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
 }
 
 }  // namespace
+
+// 9,700 cycles in front of the first product and behind the last (512 x 2048 x 8192).
+int64_t wide_cycles(const LinearCall &c, bool e4m3) {
+    const int pairs = sm_count() / 2;
+    if (pairs < 1 || !wide_fits(c.e)) return INT64_MAX;
+    WidePlan plan;
+    const int64_t blocks = (c.n_in + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
+    return 9700 + plan_wide(c.e.n_tokens, c.e.n_out, pairs, plan) * blocks;
+}
 
 gdn_status launch_linear_wide(const LinearCall &c, bool e4m3) {
     if (e4m3) return c.e.out_f32 ? launch_wide<true, float>(c) : launch_wide<true, __nv_bfloat16>(c);
