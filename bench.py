@@ -381,6 +381,7 @@ def run_ours(args):
         extras["decode_gated"] = bench_decode_gated(gdn, workloads, dev, flush)
         extras["mixed"] = bench_mixed(gdn, workloads, dev, flush)
         extras["long"] = bench_long(gdn, workloads, dev, flush, peaks)
+        extras["block"] = bench_block(gdn, workloads, dev, flush)
 
     cpu = None
     if rank == 0:
@@ -712,6 +713,100 @@ def bench_decode_gated(gdn, workloads, dev, flush, steps=50):
             "norm_kernel_ms": round(t_norm, 5),
             "norm_kernel_gbs": round(nbytes / (t_norm / 1e3) / 1e9, 1),
             "gated_tokens_per_s": round(256 / (t_gated / 1e3), 1)}
+
+
+def bench_block(gdn, workloads, dev, flush, steps=20, hidden=2048):
+    """The block around the layer, hidden state to hidden state: residual
+    addition + RMSNorm, the projections into q|k|v, z and the gate inputs, the
+    layer, its gated RMSNorm and the output projection onto the residual stream,
+    with bf16 and with 8-bit operands; for a decode step (256 sequences) and the
+    8-sequence prefill.  Also the block without the layer (norms and products)."""
+    from gated_deltanet_linear_10_gb300 import gdn_add_rmsnorm, gdn_gated_rmsnorm, \
+        gdn_gated_rmsnorm_quant, gdn_linear
+    d = workloads.FULL
+    V, C = d.hv * d.dv, d.channels
+    gen = torch.Generator(device=dev).manual_seed(2031)
+    randn = lambda *s: torch.randn(*s, generator=gen, device=dev)  # noqa: E731
+    shapes = {"qkvz": (C + V, hidden), "a": (d.hv, hidden), "b": (d.hv, hidden), "out": (hidden, V)}
+    weights = {}
+    for key, (n, k) in shapes.items():
+        w = randn(n, k) * k ** -0.5
+        scale = w.abs().amax(1) / 448
+        weights[key] = {False: (w.bfloat16(), None), True: ((w / scale[:, None]).to(torch.float8_e4m3fn), scale)}
+    wn, wo = randn(hidden) * 0.1, torch.rand(d.dv, generator=gen, device=dev) + 0.5
+    res = {}
+    for name, w in (("decode", workloads.decode(pool_device=dev)), ("prefill", workloads.prefill())):
+        pool = w.state_pool if name == "decode" else torch.zeros((16, d.hv, 128, 128), device=dev)
+        T = w.x.shape[0]
+        slots = w.slots.to(dev) if name == "decode" else torch.arange(w.n_seqs, dtype=torch.int32, device=dev)
+        cpool = w.conv_pool.to(dev)
+        conv_w, A_log, dt_bias = w.conv_w.to(dev), w.A_log.to(dev), w.dt_bias.to(dev)
+        x, stream = randn(T, hidden).bfloat16(), randn(T, hidden).bfloat16()
+        out = torch.empty_like(stream)
+        ro = torch.empty_like(stream)
+        bufs = {k: torch.empty((T, n), dtype=torch.bfloat16, device=dev) for k, (n, _) in shapes.items()}
+        o = torch.empty((T, d.hv, 128), dtype=torch.bfloat16, device=dev)
+        if name == "decode":
+            ws = torch.empty(gdn.gdn_decode_step_workspace_size(T, d.hqk, d.hv), dtype=torch.uint8, device=dev)
+        else:
+            cu, fresh = w.cu_seqlens.to(dev), torch.zeros(w.n_seqs, dtype=torch.uint8, device=dev)
+            none = torch.full_like(slots, -1)
+            need = gdn.gdn_prefill_layer_workspace_size(w.n_seqs, T, d.hqk, d.hv)
+            ws = torch.empty(need + 1024, dtype=torch.uint8, device=dev)
+            ws = ws[(-ws.data_ptr()) % 1024:][:need]
+
+        def layer():
+            a, b, xs = bufs["a"], bufs["b"], bufs["qkvz"][:, :C]
+            if name == "decode":
+                gdn.gdn_decode_step_fused(xs, conv_w, cpool, a, b, A_log, dt_bias, d.hqk, pool, slots, o=o,
+                                          workspace=ws)
+            else:
+                gdn.gdn_prefill_layer(xs, conv_w, cpool, slots, fresh, a, b, A_log, dt_bias, cu, d.hqk, pool, none,
+                                      slots, o=o, workspace=ws)
+
+        def block(eight, with_layer=True):
+            proj = lambda key, v, s, **kw: gdn_linear(  # noqa: E731
+                v, weights[key][eight][0], x_scale=s, weight_scale=weights[key][eight][1], **kw)
+            n, ns, _ = gdn_add_rmsnorm(x, wn, residual=stream, weight_offset=1.0, residual_out=ro,
+                                       y_dtype=torch.float8_e4m3fn if eight else None)
+            for key in ("qkvz", "a", "b"):
+                proj(key, n, ns, y=bufs[key])
+            if with_layer:
+                layer()
+            z = bufs["qkvz"][:, C:]
+            if eight:
+                y, ys = gdn_gated_rmsnorm_quant(o, z, wo)
+            else:
+                y, ys = gdn_gated_rmsnorm(o, z.unflatten(1, (d.hv, d.dv)), wo), None
+            proj("out", y.view(T, V), ys, residual=ro, y=out)
+
+        row = {"tokens": T}
+        for key, fn in (("bf16_ms", lambda: block(False)), ("e4m3_ms", lambda: block(True)),
+                        ("bf16_without_layer_ms", lambda: block(False, False)),
+                        ("e4m3_without_layer_ms", lambda: block(True, False))):
+            for _ in range(3):
+                fn()
+                flush.zero_()
+            torch.cuda.synchronize(dev)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                fn()
+            ev = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(steps)]
+            graph.replay()
+            for i in range(steps):
+                flush.zero_()
+                ev[i][0].record()
+                graph.replay()
+                ev[i][1].record()
+            torch.cuda.synchronize(dev)
+            row[key] = round(sum(e[0].elapsed_time(e[1]) for e in ev) / steps, 4)
+            del graph
+        res[name] = row
+        del pool, w
+    assert gdn.gdn_get_device_status(clear=True) == 0
+    return {"workload": f"hidden {hidden}: add + RMSNorm, projections to q|k|v|z and the gates, the layer, gated "
+                        "RMSNorm, output projection + residual; one captured graph a step, L2 flushed between steps",
+            **res}
 
 
 def prefill_flops_per_token(hv, dk, dv, chunk, causal=False):

@@ -173,6 +173,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         __syncwarp();
     }
     if (warp == 1) {
+        griddep_wait();       // no tensor memory is held while an earlier kernel may still ask for its own
         tmem_alloc(&tmem_base, BT);
         tmem_relinquish();
     }
@@ -428,7 +429,9 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     GDN_REQUIRE((uintptr_t)x % 16 == 0 && (uintptr_t)w % 16 == 0 &&
                     (n_tokens == 1 || x_row_stride % per == 0) && (n_out == 1 || w_row_stride % per == 0),
                 GDN_ERR_INVALID_ARG);
-    GDN_REQUIRE(x_row_stride < (1ll << 36) && w_row_stride < (1ll << 36), GDN_ERR_UNSUPPORTED);
+    GDN_REQUIRE(x_row_stride < (1ll << 36) && w_row_stride < (1ll << 36) && y_row_stride < (1ll << 36) &&
+                    residual_row_stride < (1ll << 36),
+                GDN_ERR_UNSUPPORTED);
     const uintptr_t ye = y_dtype == GDN_F32 ? 4 : 2;
     GDN_REQUIRE((uintptr_t)y % ye == 0 && (uintptr_t)residual % ye == 0 && (uintptr_t)x_scale % 4 == 0 &&
                     (uintptr_t)w_scale % 4 == 0 && (uintptr_t)bias % 4 == 0,

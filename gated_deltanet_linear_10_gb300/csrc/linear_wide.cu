@@ -214,6 +214,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         fence_mbar_init();
     }
     if (warp == 2) {
+        griddep_wait();        // no tensor memory is held while an earlier kernel may still ask for its own
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_base)),
                      "r"(2 * kChTile)
@@ -351,6 +352,11 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             const float sx = ep.sx && on_t ? ep.sx[t] : 1.0f;
             // the residual of a chunk of 32 channels is asked for one chunk ahead
             const O *res_row = res + (on_t ? t * ep.rs : 0) + n0;
+            if (ep.res && on_t && half == 0) {            // on its way to L2 while the products run
+                const int span = min(width, ep.n_out - n0);
+                for (int i = 0; i < span; i += 128 / (int)sizeof(O))
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(res_row + i));
+            }
             uint32_t rv[32];
             if (ahead && on_t && start < width) load_row<O>(rv, res_row + start, n0 + start, ep.n_out, rows);
             if (!mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort)) break;

@@ -362,6 +362,7 @@ def test_linear_host_checks(lib):
     assert rc(_0=None) == 1 and rc(_3=None) == 1 and rc(_13=None) == 1
     assert rc(_1=63) == 1 and rc(_4=63) == 1 and rc(_14=95) == 1
     assert rc(_7=A, _8=95) == 1                         # residual rows overlap
+    assert rc(_1=1 << 36) == 2 and rc(_4=1 << 36) == 2 and rc(_14=1 << 36) == 2 and rc(_7=A, _8=1 << 36) == 2
     assert rc(_0=A + 8) == 1 and rc(_3=A + 8) == 1      # operands not on 16 bytes
     assert rc(_1=68) == 1 and rc(_4=68) == 1            # ... nor their rows
     assert rc(_15=2, _1=72) == 1                        # 8 bits: multiples of 16

@@ -139,6 +139,21 @@ def test_no_rows():
     assert q.shape == (0, 2, 32) and qs.shape == (0,)
 
 
+@pytest.mark.parametrize("hidden", [128, 77])
+def test_rows_past_32_bit_offsets(hidden):
+    T, step = 3, 2 ** 30 + 64
+    buf = torch.empty(step * (T - 1) + 4096, dtype=BF16, device=DEV)
+    far = lambda off: buf.as_strided((T, hidden), (step, 1), off)  # noqa: E731
+    x, res, w = _rand(1, T, hidden).to(BF16), _rand(2, T, hidden).to(BF16), _rand(3, hidden)
+    xf, rf = far(0), far(256)
+    xf.copy_(x)
+    rf.copy_(res)
+    y, _, ro = gdn().gdn_add_rmsnorm(xf, w, residual=rf, y=far(512), residual_out=rf)
+    p, _, pro = gdn().gdn_add_rmsnorm(x, w, residual=res)
+    torch.cuda.synchronize()
+    assert bits_equal(y.contiguous(), p) and bits_equal(ro.contiguous(), pro)
+
+
 # ------------------------------------------------- the gated norm in 8 bits --
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -170,3 +170,36 @@ def test_other_streams_at_once_and_graph(T):
     b64.check_linear(ya, ref, size, K)
     assert bits_equal(yb, wb)
     status_clean()
+
+
+@pytest.mark.parametrize("T,N", [(2, 96), (2, 90), (130, 96)])
+def test_rows_past_32_bit_offsets(T, N):
+    """Rows of x, y and the residual that lie more than 2^31 elements behind the first."""
+    K = 128
+    x, w, _, _, _, res = _case(T, T, K, N, BF16, False, BF16)
+    step = 2 ** 31 // (T - 1) // 64 * 64 + 64
+    buf = torch.empty(step * (T - 1) + 4096, dtype=BF16, device=DEV)
+    far = lambda off, n: buf.as_strided((T, n), (step, 1), off)  # noqa: E731
+    xf, rf, yf = far(0, K), far(256, N), far(512, N)
+    xf.copy_(x)
+    rf.copy_(res)
+    y = gdn().gdn_linear(xf, w, residual=rf, y=yf)
+    p = gdn().gdn_linear(x, w, residual=res)
+    torch.cuda.synchronize()
+    assert bits_equal(y.contiguous(), p)
+
+
+def test_first_call_of_a_size_inside_a_capture():
+    """What a call asks the device once (shared memory, clusters) may be asked during a capture."""
+    K, N = 640, 896
+    a, b = _case(1, 40, K, N, E4M3), _case(2, 600, K, N, E4M3)
+    ya, yb = (torch.empty(t, N, dtype=F32, device=DEV) for t in (40, 600))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, y in ((a, ya), (b, yb)):
+            gdn().gdn_linear(c[0], c[1], x_scale=c[2], weight_scale=c[3], y=y)
+    graph.replay()
+    torch.cuda.synchronize()
+    for c, y in ((a, ya), (b, yb)):
+        ref, size = b64.linear(c[0], c[1], c[2], c[3], None, "none", None)
+        b64.check_linear(y, ref, size, K, True)
