@@ -94,7 +94,9 @@ struct WidePlan {
     }
 };
 
-enum WideRows { kRows32, kRows16, kRowsPlain };   // alignment of y's and the residual's rows
+// Where the rows of y and the residual start: on 32, 16, 8, 4 bytes, or anywhere;
+// kRowsOdd: on 2 bytes, y's and the residual's rows alike.
+enum WideRows { kRows32, kRows16, kRows8, kRows4, kRowsOdd, kRowsPlain };
 
 // 32 bytes of a row into registers.
 __device__ __forceinline__ void load32(uint32_t *r, const void *p, int rows) {
@@ -136,32 +138,114 @@ __device__ __forceinline__ void load_row(uint32_t *r, const O *p, int n, int n_o
     }
 }
 
+// The residual of a warp's 32 token rows x 32 channels n .., a channel a lane;
+// in bounds for every lane and row.
+template <typename O>
+__device__ __forceinline__ void plain_ask(uint32_t *rv, const LinearEpi &ep, int t0, int n, int lane) {
+    const O *res = reinterpret_cast<const O *>(ep.res) + min(n + lane, ep.n_out - 1);
+    const int last = ep.n_tokens - 1;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) rv[i] = load_bits(res + min(t0 + i, last) * ep.rs);
+}
+
 // A warp's 32 token rows x 32 channels of values (r: one token row a lane) to
 // rows that start anywhere: turned through a 32 x 32 buffer (columns permuted
-// by the row, so that both ways touch every bank once), then a lane is a channel.
+// by the row, so that both ways touch every bank once), then a lane is a
+// channel.  rv: their residual.
 template <typename O>
-__device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], float *turn, const LinearEpi &ep, int t0,
-                                           int n, int lane) {
+__device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], const uint32_t (&rv)[32], float *turn,
+                                           const LinearEpi &ep, int t0, int n, int lane) {
     __syncwarp();                                    // the buffer's last values are read
 #pragma unroll
     for (int j = 0; j < 32; ++j) turn[lane * 32 + (j ^ lane)] = __uint_as_float(r[j]);
     __syncwarp();
-    const bool on = n + lane < ep.n_out;
-    const int last = ep.n_tokens - 1;
-    const O *res = reinterpret_cast<const O *>(ep.res) + min(n + lane, ep.n_out - 1);
-    O *y = reinterpret_cast<O *>(ep.y) + n + lane;
-#pragma unroll 1
-    for (int i0 = 0; i0 < 32 && t0 + i0 <= last; i0 += 16) {   // 16 rows in flight
-        uint32_t rv[16];
+    const int rows = n + lane < ep.n_out ? ep.n_tokens - t0 : 0;
+    O *y = reinterpret_cast<O *>(ep.y) + n + lane + t0 * ep.ys;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) rv[i] = ep.res ? load_bits(res + min(t0 + i0 + i, last) * ep.rs) : 0u;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float v = turn[(i0 + i) * 32 + (lane ^ (i0 + i))] + bits_value<O>(rv[i]);
-            if (on && t0 + i0 + i <= last) Io<O>::store(y + (t0 + i0 + i) * ep.ys, v);
-        }
+    for (int i = 0; i < 32; ++i) {
+        float v = turn[i * 32 + (lane ^ i)];
+        if (ep.res) v += bits_value<O>(rv[i]);
+        if (i < rows) Io<O>::store(y, v);
+        y += ep.ys;
     }
 }
+
+// The same for bf16 rows that start on 2 E bytes, a lane holding E channels of a
+// row at a time and the warp E rows (E = 4, or E = 2 with rows on 4 bytes or,
+// kOdd, some on 2): a fourth or half of wide_plain's accesses to memory, which
+// held the tile (11036 x 84 x 4854 with a residual: TODO us, with wide_plain
+// 138).  Where an odd row starts between two words, its first lane takes the
+// chunk's first and last channel, the others the words between.
+template <int E, bool kOdd> struct WideWords {
+    static constexpr int LANES = 32 / E, PER = E / 2;      // lanes of a row, words of a lane
+    int h, w, first, second;                               // row within the step, place in it, channels
+    bool split;                                            // first and second are not neighbours
+    __device__ __forceinline__ WideWords(const LinearEpi &ep, int t0, int n, int lane) {
+        h = lane / LANES;
+        w = lane % LANES;
+        const bool odd = kOdd && ((((uintptr_t)ep.y >> 1) + (uint64_t)(t0 + h) * ep.ys + n) & 1);
+        split = odd && w == 0;
+        first = split ? 0 : w * E - (odd ? 1 : 0);
+        second = split ? 31 : first + 1;
+    }
+    // rv[step * PER ..]: the residual's words; an odd row's two ends in rv[step] and rv[16 + step]
+    __device__ __forceinline__ void ask(uint32_t *rv, const LinearEpi &ep, int t0, int n) const {
+        const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(ep.res) + (t0 + h) * ep.rs + n + first;
+        const int rows = ep.n_tokens - t0 - h;
+#pragma unroll
+        for (int k = 0; k < 32 / E; ++k) {
+            if (k * E < rows) {
+                if (kOdd && split) {
+                    rv[k] = load_bits(p);
+                    rv[16 + k] = load_bits(p + 31);
+                } else if constexpr (E == 4) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+                    rv[2 * k] = q.x;
+                    rv[2 * k + 1] = q.y;
+                } else {
+                    rv[k] = *reinterpret_cast<const uint32_t *>(p);
+                }
+            }
+            p += E * ep.rs;
+        }
+    }
+    __device__ __forceinline__ void out(const uint32_t (&r)[32], const uint32_t (&rv)[32], float *turn,
+                                        const LinearEpi &ep, int t0, int n, int lane) const {
+        __syncwarp();                                      // the buffer's last values are read
+#pragma unroll
+        for (int j = 0; j < 32; ++j) turn[lane * 32 + (j ^ lane)] = __uint_as_float(r[j]);
+        __syncwarp();
+        const int rows = ep.n_tokens - t0 - h;
+        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(ep.y) + (t0 + h) * ep.ys + n + first;
+#pragma unroll
+        for (int k = 0; k < 32 / E; ++k) {
+            const int i = k * E + h;
+            const float *row = turn + i * 32;
+            uint32_t q[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                float a = row[(first + 2 * j) ^ i], b = row[(E == 2 ? second : first + 2 * j + 1) ^ i];
+                if (ep.res) {
+                    const uint32_t v = rv[k * PER + j];
+                    a += bits_value<__nv_bfloat16>(kOdd ? v & 0xffffu : v);
+                    b += kOdd && split ? bits_value<__nv_bfloat16>(rv[16 + k]) : __uint_as_float(v & 0xffff0000u);
+                }
+                q[j] = pack_bf16(a, b);
+            }
+            if (k * E < rows) {
+                if (kOdd && split) {
+                    *reinterpret_cast<uint16_t *>(y) = (uint16_t)q[0];
+                    *reinterpret_cast<uint16_t *>(y + 31) = (uint16_t)(q[0] >> 16);
+                } else if constexpr (E == 4) {
+                    *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+                } else {
+                    *reinterpret_cast<uint32_t *>(y) = q[0];
+                }
+            }
+            y += E * ep.ys;
+        }
+    }
+};
 
 // 32 accumulators of one token row -> act(sx sw acc + bias), in place.  cols:
 // the columns' scales in shared memory, their biases kChTile floats on.
@@ -329,36 +413,66 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         const int q = warp & 3, half = (warp - 4) >> 2, etid = tid - 128;
         uint8_t *staging = smem + S * kStageBytes + (warp - 4) * kStaging;
         const bool has_cols = ep.sw || ep.bias || ep.act != GDN_ACT_NONE;
-        const bool ahead = ep.res && rows != kRowsPlain;
         const O *res = reinterpret_cast<const O *>(ep.res);
         const int start = half * COLS;
+        // What a tile needs besides its sums is asked for a tile ahead: the columns'
+        // scales and biases and the row's scale into registers, the residual to L2
+        // and, a chunk ahead, into registers.
+        struct Ahead {
+            int t0, n0, width;
+            float sx, sw, bias;
+        } cur, nxt;
+        auto ahead = [&](int tile, Ahead &a) {
+            int box;
+            a.width = 0;
+            if (tile >= plan.n_tiles) return;
+            plan.at(tile, ep.n_out, a.t0, a.n0, box, a.width);
+            a.t0 += (int)rank * kTokHalf + q * 32;
+            const int t = a.t0 + lane, n = a.n0 + etid;
+            a.sx = ep.sx && t < ep.n_tokens ? ep.sx[t] : 1.0f;
+            if (has_cols) {
+                a.sw = n < ep.n_out && ep.sw ? ep.sw[n] : 1.0f;
+                a.bias = n < ep.n_out && ep.bias ? ep.bias[n] : 0.0f;
+            }
+            if (ep.res && t < ep.n_tokens && half == 0) {
+                const O *p = res + t * ep.rs + a.n0;
+                const int span = min(a.width, ep.n_out - a.n0);
+                for (int i = 0; i < span; i += 128 / (int)sizeof(O))
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+            }
+        };
+        uint32_t rv[32];
+        auto ask = [&](int t0, int n) {                 // the residual of a chunk
+            if (n >= ep.n_out) return;
+            if (rows <= kRows16) {
+                const int t = t0 + lane;
+                if (t < ep.n_tokens) load_row<O>(rv, res + t * ep.rs + n, n, ep.n_out, rows);
+                return;
+            }
+            if constexpr (sizeof(O) == 2) {
+                if (n + 32 <= ep.n_out && rows != kRowsPlain) {
+                    if (rows == kRows8) WideWords<4, false>(ep, t0, n, lane).ask(rv, ep, t0, n);
+                    else if (rows == kRows4) WideWords<2, false>(ep, t0, n, lane).ask(rv, ep, t0, n);
+                    else WideWords<2, true>(ep, t0, n, lane).ask(rv, ep, t0, n);
+                    return;
+                }
+            }
+            plain_ask<O>(rv, ep, t0, n, lane);
+        };
+        static_assert(32 * kEpiWarps == kChTile, "a thread holds one column's scale and bias");
+        ahead(pair, cur);
+        if (ep.res && start < cur.width) ask(cur.t0, cur.n0 + start);
         int u = 0;
-        for (int tile = pair; tile < plan.n_tiles; tile += pairs, ++u) {
-            const int b = u & 1;
-            int t0, n0, box, width;
-            plan.at(tile, ep.n_out, t0, n0, box, width);
-            t0 += (int)rank * kTokHalf + q * 32;
-            const int t = t0 + lane;
-            const bool on_t = t < ep.n_tokens;
+        for (int tile = pair; tile < plan.n_tiles; tile += pairs, ++u, cur = nxt) {
+            const int b = u & 1, t0 = cur.t0, n0 = cur.n0, width = cur.width;
+            const float sx = cur.sx;
             if (has_cols) {
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");   // the last tile's are read
-                for (int c = etid; c < kChTile; c += 32 * kEpiWarps) {
-                    const int n = n0 + c;
-                    cols[c] = n < ep.n_out && ep.sw ? ep.sw[n] : 1.0f;
-                    cols[kChTile + c] = n < ep.n_out && ep.bias ? ep.bias[n] : 0.0f;
-                }
+                cols[etid] = cur.sw;
+                cols[kChTile + etid] = cur.bias;
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
             }
-            const float sx = ep.sx && on_t ? ep.sx[t] : 1.0f;
-            // the residual of a chunk of 32 channels is asked for one chunk ahead
-            const O *res_row = res + (on_t ? t * ep.rs : 0) + n0;
-            if (ep.res && on_t && half == 0) {            // on its way to L2 while the products run
-                const int span = min(width, ep.n_out - n0);
-                for (int i = 0; i < span; i += 128 / (int)sizeof(O))
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(res_row + i));
-            }
-            uint32_t rv[32];
-            if (ahead && on_t && start < width) load_row<O>(rv, res_row + start, n0 + start, ep.n_out, rows);
+            ahead(tile + pairs, nxt);
             if (!mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort)) break;
             tc_fence_after();
 #pragma unroll 1
@@ -371,8 +485,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 else if (ep.act == GDN_ACT_GELU) wide_values<GDN_ACT_GELU, true>(r, cols + c, sx);
                 else if (has_cols) wide_values<GDN_ACT_NONE, true>(r, cols + c, sx);
                 else wide_values<GDN_ACT_NONE, false>(r, cols + c, sx);
-                if (rows != kRowsPlain) {
-                    if (ahead) {
+                if (rows <= kRows16) {
+                    if (res) {
 #pragma unroll
                         for (int i = 0; i < WORDS; ++i) {
                             if constexpr (sizeof(O) == 2) {
@@ -383,8 +497,22 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                                 r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(rv[i]));
                             }
                         }
-                        if (on_t && next_c < width) load_row<O>(rv, res_row + next_c, n0 + next_c, ep.n_out, rows);
                     }
+                } else if (n < ep.n_out) {
+                    float *turn = reinterpret_cast<float *>(staging);
+                    if (sizeof(O) == 4 || rows == kRowsPlain || n + 32 > ep.n_out) {
+                        wide_plain<O>(r, rv, turn, ep, t0, n, lane);
+                    } else if constexpr (sizeof(O) == 2) {
+                        if (rows == kRows8) WideWords<4, false>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
+                        else if (rows == kRows4) WideWords<2, false>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
+                        else WideWords<2, true>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
+                    }
+                }
+                if (res) {
+                    if (next_c < width) ask(t0, n0 + next_c);
+                    else if (start < nxt.width) ask(nxt.t0, nxt.n0 + start);
+                }
+                if (rows <= kRows16) {
                     if constexpr (sizeof(O) == 2) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -407,12 +535,11 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                             bulk_commit();
                         }
                     }
-                } else {
-                    wide_plain<O>(r, reinterpret_cast<float *>(staging), ep, t0, n, lane);
                 }
                 part = next_c == c + 32 && PARTS > 1 ? 1 : 0;
                 c = next_c;
             }
+            if (ep.res && start >= width && start < nxt.width) ask(nxt.t0, nxt.n0 + start);   // no chunk here
             tc_fence_before();                          // this warp has read its part of the accumulator
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[b]), 0));
@@ -474,8 +601,17 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
         return (uintptr_t)e.y % bytes == 0 && e.ys * (int64_t)sizeof(O) % bytes == 0 &&
                (!e.res || ((uintptr_t)e.res % bytes == 0 && e.rs * (int64_t)sizeof(O) % bytes == 0));
     };
-    const int rows = at(32) ? kRows32 : at(16) ? kRows16 : kRowsPlain;
-    if (rows != kRowsPlain &&
+    const bool alike = !e.res || ((((uintptr_t)e.y ^ (uintptr_t)e.res) & 3) == 0 && ((e.ys ^ e.rs) & 1) == 0);
+    // a TMA store writes whole 16 bytes: it would reach behind rows that end within some
+    const bool whole = (int64_t)e.n_out * sizeof(O) % 16 == 0;
+    const int rows = whole && at(32)       ? kRows32
+                     : whole && at(16)     ? kRows16
+                     : sizeof(O) == 4      ? kRowsPlain
+                     : at(8)               ? kRows8
+                     : at(4)               ? kRows4
+                     : alike               ? kRowsOdd
+                                           : kRowsPlain;
+    if (rows <= kRows16 &&
         !encode_tmap_2d(&my, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.y,
                         e.n_out, e.n_tokens, e.ys * sizeof(O), 128 / sizeof(O), 32, true))
         return GDN_ERR_CUDA;

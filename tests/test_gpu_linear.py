@@ -203,3 +203,51 @@ def test_first_call_of_a_size_inside_a_capture():
     for c, y in ((a, ya), (b, yb)):
         ref, size = b64.linear(c[0], c[1], c[2], c[3], None, "none", None)
         b64.check_linear(y, ref, size, K, True)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("N", [1331, 1330, 1332, 1336, 1344])
+@pytest.mark.parametrize("yoff,roff", [(0, 0), (1, 1), (1, 0), (2, 6), (4, 4), (8, 8)])
+def test_many_tokens_rows_that_start_anywhere(N, yoff, roff, out):
+    """y and the residual as columns of wider buffers, at every alignment of the
+    rows (alike or not), odd and even strides: 64 bits, and nothing else written."""
+    T, K = 2030, 72
+    x, w, _, _, b, res = _case(N, T, K, N, BF16, True, out)
+    for pad in (0, 1, 2, 8):
+        if yoff == 0 and pad == 0:
+            continue                                   # packed rows are test_sizes'
+        wide = torch.full((T, N + yoff + pad), 3.0, dtype=out, device=DEV)
+        rwide = torch.full((T, N + roff + pad), float("nan"), dtype=out, device=DEV)
+        y, r = wide[:, yoff:yoff + N], rwide[:, roff:roff + N]
+        r.copy_(res)
+        gdn().gdn_linear(x, w, bias=b, act="silu", residual=r, y=y)
+        torch.cuda.synchronize()
+        ref, size = b64.linear(x, w, None, None, b, "silu", res)
+        b64.check_linear(y, ref, size, K, what=f"pad {pad}")
+        assert torch.all(wide[:, :yoff] == 3.0) and torch.all(wide[:, yoff + N:] == 3.0)
+    plain = gdn().gdn_linear(x, w, bias=b, act="silu", y_dtype=out)
+    again = torch.full((T, N + yoff + 1), 3.0, dtype=out, device=DEV)
+    gdn().gdn_linear(x, w, bias=b, act="silu", y=again[:, yoff:yoff + N])
+    torch.cuda.synchronize()
+    assert bits_equal(again[:, yoff:yoff + N].contiguous(), plain)
+    status_clean()
+
+
+@pytest.mark.parametrize("N", [1331, 1330, 1332, 1344])
+def test_many_tokens_residual_in_place(N):
+    T, K = 5000, 40
+    x, w, _, _, _, res = _case(N, T, K, N, BF16, False, BF16)
+    want = gdn().gdn_linear(x, w, residual=res)
+    y = res.clone()
+    gdn().gdn_linear(x, w, residual=y, y=y)
+    torch.cuda.synchronize()
+    assert bits_equal(y, want)
+    ref, size = b64.linear(x, w, None, None, None, "none", res)
+    b64.check_linear(want, ref, size, K)
+
+
+@pytest.mark.parametrize("T,K,N,dtype", [(20000, 64, 512, BF16), (9000, 300, 2050, E4M3), (1300, 136, 8193, BF16)])
+def test_many_tiles(T, K, N, dtype):
+    """Several tiles for every pair, the last ones narrower, with every part of the epilogue."""
+    for act, residual in (("none", True), ("gelu", False)):
+        _run(T, T, K, N, dtype, BF16, True, act, residual)
