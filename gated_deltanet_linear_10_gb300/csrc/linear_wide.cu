@@ -94,9 +94,9 @@ struct WidePlan {
     }
 };
 
-// Where the rows of y and the residual start: on 32, 16, 8, 4 bytes, or anywhere;
+// Where the rows of y and the residual start: on 32, 16 or 4 bytes, or anywhere;
 // kRowsOdd: on 2 bytes, y's and the residual's rows alike.
-enum WideRows { kRows32, kRows16, kRows8, kRows4, kRowsOdd, kRowsPlain };
+enum WideRows { kRows32, kRows16, kRows4, kRowsOdd, kRowsPlain };
 
 // 32 bytes of a row into registers.
 __device__ __forceinline__ void load32(uint32_t *r, const void *p, int rows) {
@@ -170,43 +170,38 @@ __device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], const uint32
     }
 }
 
-// The same for bf16 rows that start on 2 E bytes, a lane holding E channels of a
-// row at a time and the warp E rows (E = 4, or E = 2 with rows on 4 bytes or,
-// kOdd, some on 2): a fourth or half of wide_plain's accesses to memory, which
-// held the tile (11036 x 84 x 4854 with a residual: TODO us, with wide_plain
-// 138).  Where an odd row starts between two words, its first lane takes the
-// chunk's first and last channel, the others the words between.
-template <int E, bool kOdd> struct WideWords {
-    static constexpr int LANES = 32 / E, PER = E / 2;      // lanes of a row, words of a lane
-    int h, w, first, second;                               // row within the step, place in it, channels
+// The same for bf16 rows that start on 4 bytes or, kOdd, some on 2: a lane holds
+// two channels of a row and the warp two rows at a time, half of wide_plain's
+// accesses to memory (11036 x 84 x 4854 with a residual: 105 us, with wide_plain
+// 138; words of 8 bytes gain nothing more).  Where an odd row starts between two
+// words, its first lane takes the chunk's first and last channel, the others the
+// words between (12183 x 538 x 5715 with a residual: 190 us, with wide_plain 214).
+template <bool kOdd> struct WideWords {
+    int h, first, second;                                  // row of the pair, channels
     bool split;                                            // first and second are not neighbours
     __device__ __forceinline__ WideWords(const LinearEpi &ep, int t0, int n, int lane) {
-        h = lane / LANES;
-        w = lane % LANES;
+        h = lane >> 4;
+        const int w = lane & 15;
         const bool odd = kOdd && ((((uintptr_t)ep.y >> 1) + (uint64_t)(t0 + h) * ep.ys + n) & 1);
         split = odd && w == 0;
-        first = split ? 0 : w * E - (odd ? 1 : 0);
+        first = split ? 0 : w * 2 - (odd ? 1 : 0);
         second = split ? 31 : first + 1;
     }
-    // rv[step * PER ..]: the residual's words; an odd row's two ends in rv[step] and rv[16 + step]
+    // rv[k]: the residual's word of row 2 k + h; an odd row's two ends in rv[k] and rv[16 + k]
     __device__ __forceinline__ void ask(uint32_t *rv, const LinearEpi &ep, int t0, int n) const {
         const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(ep.res) + (t0 + h) * ep.rs + n + first;
         const int rows = ep.n_tokens - t0 - h;
 #pragma unroll
-        for (int k = 0; k < 32 / E; ++k) {
-            if (k * E < rows) {
+        for (int k = 0; k < 16; ++k) {
+            if (2 * k < rows) {
                 if (kOdd && split) {
                     rv[k] = load_bits(p);
                     rv[16 + k] = load_bits(p + 31);
-                } else if constexpr (E == 4) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(p);
-                    rv[2 * k] = q.x;
-                    rv[2 * k + 1] = q.y;
                 } else {
                     rv[k] = *reinterpret_cast<const uint32_t *>(p);
                 }
             }
-            p += E * ep.rs;
+            p += 2 * ep.rs;
         }
     }
     __device__ __forceinline__ void out(const uint32_t (&r)[32], const uint32_t (&rv)[32], float *turn,
@@ -218,31 +213,23 @@ template <int E, bool kOdd> struct WideWords {
         const int rows = ep.n_tokens - t0 - h;
         __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(ep.y) + (t0 + h) * ep.ys + n + first;
 #pragma unroll
-        for (int k = 0; k < 32 / E; ++k) {
-            const int i = k * E + h;
-            const float *row = turn + i * 32;
-            uint32_t q[PER];
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                float a = row[(first + 2 * j) ^ i], b = row[(E == 2 ? second : first + 2 * j + 1) ^ i];
-                if (ep.res) {
-                    const uint32_t v = rv[k * PER + j];
-                    a += bits_value<__nv_bfloat16>(kOdd ? v & 0xffffu : v);
-                    b += kOdd && split ? bits_value<__nv_bfloat16>(rv[16 + k]) : __uint_as_float(v & 0xffff0000u);
-                }
-                q[j] = pack_bf16(a, b);
+        for (int k = 0; k < 16; ++k) {
+            const int i = 2 * k + h;
+            float a = turn[i * 32 + (first ^ i)], b = turn[i * 32 + (second ^ i)];
+            if (ep.res) {
+                a += bits_value<__nv_bfloat16>(rv[k]);
+                b += kOdd && split ? bits_value<__nv_bfloat16>(rv[16 + k]) : __uint_as_float(rv[k] & 0xffff0000u);
             }
-            if (k * E < rows) {
+            const uint32_t q = pack_bf16(a, b);
+            if (2 * k < rows) {
                 if (kOdd && split) {
-                    *reinterpret_cast<uint16_t *>(y) = (uint16_t)q[0];
-                    *reinterpret_cast<uint16_t *>(y + 31) = (uint16_t)(q[0] >> 16);
-                } else if constexpr (E == 4) {
-                    *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+                    *reinterpret_cast<uint16_t *>(y) = (uint16_t)q;
+                    *reinterpret_cast<uint16_t *>(y + 31) = (uint16_t)(q >> 16);
                 } else {
-                    *reinterpret_cast<uint32_t *>(y) = q[0];
+                    *reinterpret_cast<uint32_t *>(y) = q;
                 }
             }
-            y += E * ep.ys;
+            y += 2 * ep.ys;
         }
     }
 };
@@ -451,9 +438,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
             if constexpr (sizeof(O) == 2) {
                 if (n + 32 <= ep.n_out && rows != kRowsPlain) {
-                    if (rows == kRows8) WideWords<4, false>(ep, t0, n, lane).ask(rv, ep, t0, n);
-                    else if (rows == kRows4) WideWords<2, false>(ep, t0, n, lane).ask(rv, ep, t0, n);
-                    else WideWords<2, true>(ep, t0, n, lane).ask(rv, ep, t0, n);
+                    if (rows == kRows4) WideWords<false>(ep, t0, n, lane).ask(rv, ep, t0, n);
+                    else WideWords<true>(ep, t0, n, lane).ask(rv, ep, t0, n);
                     return;
                 }
             }
@@ -503,9 +489,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     if (sizeof(O) == 4 || rows == kRowsPlain || n + 32 > ep.n_out) {
                         wide_plain<O>(r, rv, turn, ep, t0, n, lane);
                     } else if constexpr (sizeof(O) == 2) {
-                        if (rows == kRows8) WideWords<4, false>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
-                        else if (rows == kRows4) WideWords<2, false>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
-                        else WideWords<2, true>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
+                        if (rows == kRows4) WideWords<false>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
+                        else WideWords<true>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
                     }
                 }
                 if (res) {
@@ -607,7 +592,6 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
     const int rows = whole && at(32)       ? kRows32
                      : whole && at(16)     ? kRows16
                      : sizeof(O) == 4      ? kRowsPlain
-                     : at(8)               ? kRows8
                      : at(4)               ? kRows4
                      : alike               ? kRowsOdd
                                            : kRowsPlain;
