@@ -74,21 +74,37 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
 // (all token tiles in one group: 9 % slower at 20668 x 2048 x 8192).
 struct WidePlan {
     int nt_full, nt, nn, n_full, tail_w, n_tiles;
-    __device__ __forceinline__ void at(int tile, int n_out, int &t0, int &n0, int &box, int &width) const {
-        int t, n;
-        if (tile < n_full) {
-            const int per = kRaster * nn, g = tile / per, r = tile - g * per;
-            const int rows = min(kRaster, nt_full - g * kRaster);
-            n = r / rows;
-            t = g * kRaster + (r - n * rows);
-            box = kChTile;
-        } else {
-            const int r = tile - n_full, rows = nt - nt_full;
-            n = r / rows;
-            t = nt_full + (r - n * rows);
-            box = tail_w;
+};
+
+// A pair's walk over the tiles: every `pairs`-th one.  Steps instead of
+// divisions: two of them in every warp cost some 500 cycles a tile.
+struct WideWalk {
+    int tile, base, r;       // base: first token tile of the group, r: tile within the group (tail: within it)
+    __device__ __forceinline__ void start(const WidePlan &p, int first) {
+        tile = r = first;
+        base = 0;
+        settle(p);
+    }
+    __device__ __forceinline__ void next(const WidePlan &p, int pairs) {
+        tile += pairs;
+        r += pairs;
+        settle(p);
+    }
+    __device__ __forceinline__ void settle(const WidePlan &p) {
+        while (base < p.nt_full) {
+            const int size = min(kRaster, p.nt_full - base) * p.nn;
+            if (r < size) break;
+            r -= size;
+            base += min(kRaster, p.nt_full - base);
         }
-        t0 = t * kTokTile;
+    }
+    __device__ __forceinline__ bool more(const WidePlan &p) const { return tile < p.n_tiles; }
+    __device__ __forceinline__ void at(const WidePlan &p, int n_out, int &t0, int &n0, int &box, int &width) const {
+        const bool full = base < p.nt_full;
+        const int rows = full ? min(kRaster, p.nt_full - base) : p.nt - p.nt_full;
+        const int n = rows == kRaster ? r / kRaster : r / rows;
+        box = full ? kChTile : p.tail_w;
+        t0 = (base + r - n * rows) * kTokTile;
         n0 = n * box;
         width = min(box, (n_out - n0 + 31) / 32 * 32);   // the product's N: no wider than the channels left
     }
@@ -306,9 +322,10 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         int s = 0, i = 0;
         uint32_t phase = 1;              // of the stage's last release; the first S have none
         bool ok = true;
-        for (int tile = pair; tile < plan.n_tiles && ok; tile += pairs) {
+        WideWalk walk;
+        for (walk.start(plan, pair); walk.more(plan) && ok; walk.next(plan, pairs)) {
             int t0, n0, box, width;
-            plan.at(tile, ep.n_out, t0, n0, box, width);
+            walk.at(plan, ep.n_out, t0, n0, box, width);
             const CUtensorMap *map = box == kChTile ? &mw : &mw_tail;
             const uint32_t bytes = 2 * (kStageA + box / 2 * 128);
             const int tr = t0 + (int)rank * kTokHalf, nr = n0 + (int)rank * (width / 2);
@@ -351,11 +368,13 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         const uint32_t first = smem_u32(smem) >> 4;       // descriptors count in 16 bytes
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
         const uint32_t idesc0 = kE4m3 ? idesc_e4m3(256, 0) : idesc_bf16(256, 0);
-        int tile = pair, t0, n0, box, width, s = 0;
+        int t0, n0, box, width, s = 0;
         uint32_t phase = 0, st = first;
         bool ok = true;
-        plan.at(tile, ep.n_out, t0, n0, box, width);
-        for (int u = 0; tile < plan.n_tiles && ok; ++u) {
+        WideWalk walk;
+        walk.start(plan, pair);
+        walk.at(plan, ep.n_out, t0, n0, box, width);
+        for (int u = 0; walk.more(plan) && ok; ++u) {
             const int b = u & 1;
             if (u >= 2 && !mbar_wait_all(&acc_empty[b], ((u >> 1) - 1) & 1, abort)) break;
             tc_fence_after();
@@ -381,8 +400,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     phase ^= 1;
                 }
                 if (k == 0) {                             // the next tile, behind this one's products
-                    tile += pairs;
-                    if (tile < plan.n_tiles) plan.at(tile, ep.n_out, t0, n0, box, width);
+                    walk.next(plan, pairs);
+                    if (walk.more(plan)) walk.at(plan, ep.n_out, t0, n0, box, width);
                 }
             }
             if (ok && one) mma_commit_pair(&acc_full[b]);
@@ -409,11 +428,12 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             int t0, n0, width;
             float sx, sw, bias;
         } cur, nxt;
-        auto ahead = [&](int tile, Ahead &a) {
+        WideWalk walk;
+        auto ahead = [&](Ahead &a) {                    // for the tile that the walk has reached
             int box;
             a.width = 0;
-            if (tile >= plan.n_tiles) return;
-            plan.at(tile, ep.n_out, a.t0, a.n0, box, a.width);
+            if (!walk.more(plan)) return;
+            walk.at(plan, ep.n_out, a.t0, a.n0, box, a.width);
             a.t0 += (int)rank * kTokHalf + q * 32;
             const int t = a.t0 + lane, n = a.n0 + etid;
             a.sx = ep.sx && t < ep.n_tokens ? ep.sx[t] : 1.0f;
@@ -446,10 +466,10 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             plain_ask<O>(rv, ep, t0, n, lane);
         };
         static_assert(32 * kEpiWarps == kChTile, "a thread holds one column's scale and bias");
-        ahead(pair, cur);
+        walk.start(plan, pair);
+        ahead(cur);
         if (ep.res && start < cur.width) ask(cur.t0, cur.n0 + start);
-        int u = 0;
-        for (int tile = pair; tile < plan.n_tiles; tile += pairs, ++u, cur = nxt) {
+        for (int u = 0; cur.width > 0; ++u, cur = nxt) {
             const int b = u & 1, t0 = cur.t0, n0 = cur.n0, width = cur.width;
             const float sx = cur.sx;
             if (has_cols) {
@@ -458,7 +478,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 cols[kChTile + etid] = cur.bias;
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
             }
-            ahead(tile + pairs, nxt);
+            walk.next(plan, pairs);
+            ahead(nxt);
             if (!mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort)) break;
             tc_fence_after();
 #pragma unroll 1
