@@ -180,7 +180,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (splits > 1) cluster_arrive();      // waited for before the first copy to another CTA
+    if (splits > 1) cluster_arrive_relaxed();      // waited for before the first copy to another CTA
     griddep_wait();
 
     if (warp == 0) {
@@ -289,7 +289,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         }
         if (cnt > 0 && !mbar_wait(&arrived, 0, abort)) mbar_drain(&arrived, 0);
         __syncwarp();
-        cluster_arrive();                                // this CTA has what was sent to it
+        cluster_arrive_relaxed();                                // this CTA has what was sent to it
     }
     if (!*abort) {
 #pragma unroll 1

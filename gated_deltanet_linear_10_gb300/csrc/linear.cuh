@@ -78,6 +78,12 @@ __device__ __forceinline__ uint32_t cta_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// Relaxed, where there is nothing to pass on but that the arrival happened (or
+// barriers' initialisation, which fence_mbar_init has released): with release
+// every warp first waited for its stores and loads to be done.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }

@@ -310,7 +310,9 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync_all();        // both CTAs' barriers and tensor memory are ready
+    __syncthreads();
+    cluster_arrive_relaxed();  // both CTAs' barriers and tensor memory are ready
+    cluster_wait();
     tc_fence_after();
     griddep_wait();            // launched behind the kernel that writes x: nothing is read before it
     volatile int *abort = &abort_flag;
