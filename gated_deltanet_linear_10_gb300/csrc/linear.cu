@@ -124,6 +124,10 @@ template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
 // result has one order of sums; with one, it has them all.  Then 16 threads
 // write a token's 128 channels.
 //
+// What bounds it at 256 x 4096 x 2048 (10.6 us; floor 3.1): 2,000 cycles to the
+// first products, 9,000 of products (16 blocks at the 567 cycles below), 3,200 of
+// exchange (48 KB a CTA, 1,500 of it latency), 3,500 to write the sums and the
+// output.  One token (1 x 2048 x 8192, 7.8 us; floor 4.9) waits for the weights.
 // The code behind the products runs once per CTA, so it is kept short and
 // rolled: unrolled over 32 tokens with its variants it took 3 to 20 us of
 // instruction fetches and dependent loads at 256 tokens.
@@ -384,7 +388,9 @@ static gdn_status launch_narrow(const LinearCall &c, const NarrowPlan &plan) {
 }
 
 // The narrow tiles for up to 128 tokens; beyond, whichever estimate is shorter
-// (measured, narrow and wide: 512 x 4096 x 2048 TODO us, 512 x 2048 x 8192 TODO us).
+// (narrow and wide measured: 512 x 4096 x 2048 bf16 17.2 and 18.8 us, 512 x 2048 x
+// 8192 29.6 and 16.2, 256 x 2048 x 8192 e4m3 9.8 and 8.6, 256 x 4096 x 2048 bf16
+// 11.7 and 18.2, 777 x 1003 x 1331 16.9 and 13.2).
 template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
     const int t = c.e.n_tokens;
     NarrowPlan plan = {};

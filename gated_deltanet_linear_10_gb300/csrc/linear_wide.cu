@@ -7,10 +7,21 @@
 // in tensor memory: the epilogue warps turn one tile into y while the next
 // one's products run.
 //
-// What bounds it: TODO
+// What bounds it from n_in = 1024 on is the tensor cores' rate and then the
+// power: 256 x 256 x 16 take a pair 128 cycles.  20668 x 2048 x 8192 bf16 is
+// 574,000 cycles of them and takes 595,000, at 1.5 GHz (1.9 without the load):
+// 357 to 362 us, 1,930 TFLOP/s; over seconds some 425 us.  20668 x 4096 x 2048 e4m3
+// with a residual: 104 us, 3,340 TFLOP/s, one of its nine waves half full.
+// What it took, in cycles of a tile (n_in 2048; 16,400 of products): issuing from
+// a converged warp 2,900, six stages instead of five 900 (the ring's latency: with
+// four, 3,300), a converged producer warp 700.  At n_in = 256 a tile is its
+// epilogue: four chunks of 1,000 cycles for a warp (8000 x 256 x 4096: 24 us, 72 MB).
 //
-// Only rows off 16-byte boundaries go through shared memory, turned there so
-// that a warp's lanes access consecutive elements.
+// Epilogue: a thread holds a token row and takes 32 channels at a time to a
+// swizzled staging row of 128 bytes, from which one TMA store writes 32 rows; the
+// residual comes straight from memory, whole sectors of 32 bytes.  Stores from
+// registers instead of staging rows were 4 % slower.  Rows off 16-byte boundaries
+// are turned in shared memory, so that a warp's lanes access neighbours.
 #include <algorithm>
 
 #include "linear.cuh"
