@@ -16,6 +16,12 @@
 // issued before the row in front of it is reduced, so that a CTA always has a
 // row in flight.
 //
+// Rows that start within 16 bytes, all of a token's alike (packed rows of an odd
+// width are), are cut at their memory's 16-byte boundaries all the same (kShift):
+// vector v of a row holds elements v N - p .. v N - p + N - 1, with p where the row
+// starts, and the two ends go element by element.  The grid is a multiple of N
+// rows, so that p and with it the weights are the same for all rows of a CTA.
+//
 // What bounds it: HBM for many rows.  20668 x 2048 bf16 to e4m3 with the
 // residual takes 46.1 us, 6.43 TB/s of its 296 MB (0.95 of the copy rate); 61.9
 // us before the loads went ahead.  With 1024 or 2048 resident threads an SM
@@ -36,27 +42,32 @@ constexpr int rms_threads(int n, int vecs, size_t elem) {   // the most a launch
 }
 constexpr int kRmsSmThreads = 1536;   // resident threads of an SM: 42 registers each
 
-template <typename T, typename O, int N, int kVecs>
+template <typename T, typename O, int N, int kVecs, bool kShift>
 __global__ void __launch_bounds__(rms_threads(N, kVecs, sizeof(T)),
                                   kRmsSmThreads / rms_threads(N, kVecs, sizeof(T)) * (N * kVecs <= 8 ? 1 : 0) +
                                       (N * kVecs <= 8 ? 0 : 1))
 add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float *__restrict__ w,
                    float offset, int n_rows, int hidden, float eps, T *res_out, int64_t ros, O *y,
-                   int64_t ys, float *__restrict__ y_scale) {
+                   int64_t ys, float *__restrict__ y_scale, int first, int step) {
     __shared__ float2 part[2][32];
     constexpr bool kQuant = sizeof(O) == 1;
     constexpr int P = (N + 1) / 2;
     griddep_wait();    // launched behind the kernel that writes x: nothing is read before it
     griddep_launch();  // what is launched behind this kernel may set itself up
     const int tid = threadIdx.x;
+    const int p = kShift ? (int)((first + (uint64_t)blockIdx.x * step) % N) : 0;
+    auto at = [&](int k) { return (int)(tid + k * blockDim.x) * N - p; };
+    // a whole vector, or (kShift) one of the two ends of a row
+    auto whole = [&](int e) { return e < hidden && (!kShift || (e >= 0 && e + N <= hidden)); };
+    auto part_of = [&](int e) { return kShift && e < hidden && !(e >= 0 && e + N <= hidden); };
     F2 wv[kVecs][P];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-        const int e = (tid + k * blockDim.x) * N;
+        const int e = at(k);
         float f[2 * P] = {};
 #pragma unroll
         for (int c = 0; c < N; ++c)
-            if (e < hidden) f[c] = offset + w[e + c];
+            if (kShift ? e + c >= 0 && e + c < hidden : e < hidden) f[c] = offset + w[e + c];
 #pragma unroll
         for (int i = 0; i < P; ++i) wv[k][i] = f2(f[2 * i], f[2 * i + 1]);
     }
@@ -64,10 +75,13 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
     auto load = [&](int row) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int e = (tid + k * blockDim.x) * N;
-            if (e < hidden) {
+            const int e = at(k);
+            if (whole(e)) {
                 a[k].load(x + row * xs + e);
                 if (res) b[k].load(res + row * rs + e);
+            } else if (part_of(e)) {
+                a[k].load_part(x + row * xs + e, -e, hidden - e);
+                if (res) b[k].load_part(res + row * rs + e, -e, hidden - e);
             }
         }
     };
@@ -92,11 +106,12 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
         if (row + (int)gridDim.x < n_rows) load(row + gridDim.x);
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int e = (tid + k * blockDim.x) * N;
+            const int e = at(k);
             if (res_out && e < hidden) {
                 float f[2 * P];
                 unpair<2 * P>(s[k], f);
-                store_row<N>(res_out + row * ros + e, f);
+                if (whole(e)) store_row<N>(res_out + row * ros + e, f);
+                else store_part<N>(res_out + row * ros + e, f, -e, hidden - e);
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -119,7 +134,7 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
         }
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int e = (tid + k * blockDim.x) * N;
+            const int e = at(k);
             if (e >= hidden) continue;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -128,42 +143,57 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
             }
             float f[2 * P];
             unpair<2 * P>(s[k], f);
-            store_row<N>(y + row * ys + e, f);
+            if (whole(e)) store_row<N>(y + row * ys + e, f);
+            else store_part<N>(y + row * ys + e, f, -e, hidden - e);
         }
     }
 }
 
-template <typename T, typename O, int N, int kVecs>
-static cudaError_t launch_rms_n(const void *x, int64_t xs, const void *res, int64_t rs,
+// Where rows start: on vectors; first + row * step elements behind one, all
+// alike; or anywhere.
+struct RmsRows {
+    enum { kVector, kShifted, kAny } kind;
+    int first, step;
+};
+
+template <typename T, typename O, int N, int kVecs, bool kShift>
+static cudaError_t launch_rms_n(RmsRows at, const void *x, int64_t xs, const void *res, int64_t rs,
                                 const float *w, float offset, int n_rows, int hidden, float eps,
                                 void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
                                 cudaStream_t s) {
     const int per = N * kVecs;
-    const int threads = (((hidden + per - 1) / per) + 31) / 32 * 32;
+    const int threads = (((hidden + (kShift ? N - 1 : 0) + per - 1) / per) + 31) / 32 * 32;
     const int resident = N * kVecs <= 8 ? kRmsSmThreads : rms_threads(N, kVecs, sizeof(T));
-    const int grid = std::min(n_rows, sm_count() * std::min(16, std::max(1, resident / threads)));
-    return launch_after(add_rmsnorm_kernel<T, O, N, kVecs>, dim3(grid), dim3(threads), 0, s,
+    int grid = std::min(n_rows, sm_count() * std::min(16, std::max(1, resident / threads)));
+    if (kShift && grid < n_rows) grid = std::max(N, grid / N * N);
+    return launch_after(add_rmsnorm_kernel<T, O, N, kVecs, kShift>, dim3(grid), dim3(threads), 0, s,
                         (const T *)x, xs, (const T *)res, rs, w, offset, n_rows, hidden, eps,
-                        (T *)res_out, ros, (O *)y, ys, y_scale);
+                        (T *)res_out, ros, (O *)y, ys, y_scale, at.first, at.step);
 }
 
 // One vector per thread while that fits a CTA of 512 threads (rows of at most
 // 512 vectors), more beyond.
 template <typename T, typename O>
-static cudaError_t launch_rms(bool vec, const void *x, int64_t xs, const void *res, int64_t rs,
+static cudaError_t launch_rms(RmsRows at, const void *x, int64_t xs, const void *res, int64_t rs,
                               const float *w, float offset, int n_rows, int hidden, float eps,
                               void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
                               cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-#define GDN_RMS(n, v) \
-    launch_rms_n<T, O, n, v>(x, xs, res, rs, w, offset, n_rows, hidden, eps, res_out, ros, y, ys, y_scale, s)
-    if (vec) {
-        if (hidden <= 512 * N) return GDN_RMS(N, 1);
-        if (hidden <= 1024 * N) return GDN_RMS(N, 2);
-        return GDN_RMS(N, 4);
+#define GDN_RMS(n, v, shift)                                                                            \
+    launch_rms_n<T, O, n, v, shift>(at, x, xs, res, rs, w, offset, n_rows, hidden, eps, res_out, ros, y, ys, \
+                                    y_scale, s)
+    if (at.kind == RmsRows::kVector) {
+        if (hidden <= 512 * N) return GDN_RMS(N, 1, false);
+        if (hidden <= 1024 * N) return GDN_RMS(N, 2, false);
+        return GDN_RMS(N, 4, false);
     }
-    if (hidden <= 4096) return GDN_RMS(1, 4);
-    return GDN_RMS(1, 16);
+    if (at.kind == RmsRows::kShifted) {
+        if (hidden + N - 1 <= 512 * N) return GDN_RMS(N, 1, true);
+        if (hidden + N - 1 <= 1024 * N) return GDN_RMS(N, 2, true);
+        if (hidden + N - 1 <= (sizeof(T) == 4 ? 1024 : 512) * N * 4) return GDN_RMS(N, 4, true);
+    }
+    if (hidden <= 4096) return GDN_RMS(1, 4, false);
+    return GDN_RMS(1, 16, false);
 #undef GDN_RMS
 }
 
@@ -194,16 +224,19 @@ extern "C" gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const
                     (uintptr_t)weight % 4 == 0 && (uintptr_t)y_scale % 4 == 0,
                 GDN_ERR_INVALID_ARG);
     // 16-byte vectors of the stream (and the y elements that belong to one)
-    const int64_t n = 16 / (int64_t)elem;
-    const bool vec = hidden % n == 0 && (uintptr_t)x % 16 == 0 && x_row_stride % n == 0 &&
-                     (!residual || ((uintptr_t)residual % 16 == 0 && residual_row_stride % n == 0)) &&
-                     (!residual_out ||
-                      ((uintptr_t)residual_out % 16 == 0 && residual_out_row_stride % n == 0)) &&
-                     (uintptr_t)y % (n * yelem) == 0 && y_row_stride % n == 0;
+    const uint64_t n = 16 / elem;
+    const uint64_t first = (uintptr_t)x / elem % n, step = (uint64_t)x_row_stride % n;
+    auto alike = [&](const void *p, uintptr_t size, int64_t stride) {
+        return !p || ((uintptr_t)p / size % n == first && (n_tokens == 1 || (uint64_t)stride % n == step));
+    };
+    RmsRows at = {RmsRows::kAny, (int)first, (int)step};
+    if (alike(residual, elem, residual_row_stride) && alike(residual_out, elem, residual_out_row_stride) &&
+        alike(y, yelem, y_row_stride))
+        at.kind = first == 0 && hidden % n == 0 && (step == 0 || n_tokens == 1) ? RmsRows::kVector : RmsRows::kShifted;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
 #define GDN_RMS(T, O)                                                                           \
-    launch_rms<T, O>(vec, x, x_row_stride, residual, residual_row_stride, weight, weight_offset, \
+    launch_rms<T, O>(at, x, x_row_stride, residual, residual_row_stride, weight, weight_offset, \
                      (int)n_tokens, hidden, eps, residual_out, residual_out_row_stride, y,        \
                      y_row_stride, y_scale, s)
     if (dtype == GDN_BF16)

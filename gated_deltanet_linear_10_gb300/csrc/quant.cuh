@@ -106,6 +106,12 @@ template <typename T, int N> struct RawVec {
 #pragma unroll
         for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
     }
+    // elements lo .. hi - 1 of the vector at p, the others left as they are
+    __device__ __forceinline__ void load_part(const T *p, int lo, int hi) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i >= lo && i < hi) reinterpret_cast<T *>(r)[i] = p[i];
+    }
     // as N / 2 pairs
     __device__ __forceinline__ void pairs(F2 *out) const {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(r);
@@ -121,6 +127,7 @@ template <typename T, int N> struct RawVec {
 template <typename T> struct RawVec<T, 1> {
     T r;
     __device__ __forceinline__ void load(const T *p) { r = *p; }
+    __device__ __forceinline__ void load_part(const T *, int, int) {}
     __device__ __forceinline__ void zero() { Io<T>::store(&r, 0.f); }
     __device__ __forceinline__ void pairs(F2 *out) const { out[0] = f2(Io<T>::load(&r), 0.f); }
 };
@@ -162,6 +169,13 @@ template <int N> __device__ __forceinline__ void store_row(E4m3 *p, const float 
         *reinterpret_cast<uint2 *>(p) = make_uint2(pack_e4m3x4(v[0], v[1], v[2], v[3]),
                                                    pack_e4m3x4(v[4], v[5], v[6], v[7]));
     }
+}
+
+// Values lo .. hi - 1 of such a vector.
+template <int N, typename O> __device__ __forceinline__ void store_part(O *p, const float *v, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i >= lo && i < hi) store_row<1>(p + i, v + i);
 }
 
 // (sum, NaN-keeping max) over the block; every thread gets both.  `part` is

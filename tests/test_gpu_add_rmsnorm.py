@@ -92,6 +92,45 @@ def test_strided_rows_and_what_lies_between(dtype, out, off, pad):
         assert torch.equal(now[:, off + H:], before[:, off + H:])
 
 
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, E4M3), (F32, E4M3), (F32, F32)])
+@pytest.mark.parametrize("H", [1, 5, 9, 77, 2047, 2050, 2052])
+def test_many_rows_of_odd_widths(H, dtype, out):
+    """More rows than CTAs, packed rows that start anywhere within 16 bytes."""
+    T = 3001
+    x, res, w = _rand(H, T, H).to(dtype), _rand(H + 1, T, H).to(dtype), _rand(2, H)
+    y, scale, ro = _check(x, res, w, 1.0, out)
+    s, ref = b64.add_rmsnorm(x, res, w, 1e-6, 1.0)
+    b64.check_near(ro, s, 2.0 ** -24, b64.HALF[dtype], "residual_out")
+    if out == E4M3:
+        b64.check_quant(y.float(), scale, ref, b64.NORM, "y")
+    else:
+        b64.check_near(y, ref, b64.NORM, b64.HALF[out], "y")
+
+
+@pytest.mark.parametrize("offs", [(0, 1, 0, 0), (1, 1, 1, 2), (3, 3, 3, 3), (2, 2, 5, 2), (0, 0, 0, 4)])
+@pytest.mark.parametrize("out", [BF16, E4M3])
+def test_rows_that_start_unlike_each_other(offs, out):
+    """x, the residual, residual_out and y at columns of their own of wider buffers,
+    alike or not: the bits of packed copies, nothing else written."""
+    T, H = 600, 203
+    wide = [_rand(i, T, H + 8).to(BF16) for i in range(3)]
+    x, res, row = (b[:, o:o + H] for b, o in zip(wide, offs))
+    yw = torch.zeros(T, H + 8, dtype=BF16, device=DEV).to(out)
+    y, w = yw[:, offs[3]:offs[3] + H], _rand(9, H)
+    row0 = wide[2].clone()
+    sc = torch.empty(T, device=DEV) if out == E4M3 else None
+    _check(x, res, w, 0.0, out, y=y, residual_out=row, y_scale=sc)
+    s, ref = b64.add_rmsnorm(x, res, w, 1e-6, 0.0)
+    b64.check_near(row, s, 2.0 ** -24, b64.HALF[BF16], "residual_out")
+    if out == E4M3:
+        b64.check_quant(y.float(), sc, ref, b64.NORM, "y")
+    else:
+        b64.check_near(y, ref, b64.NORM, b64.HALF[BF16], "y")
+    raw = yw.view(torch.uint8) if out == E4M3 else yw
+    for buf, before, o in ((wide[2], row0, offs[2]), (raw, torch.zeros_like(raw), offs[3])):
+        assert torch.equal(buf[:, :o], before[:, :o]) and torch.equal(buf[:, o + H:], before[:, o + H:])
+
+
 @pytest.mark.parametrize("hidden", [2048, 1111])
 def test_in_place(hidden):
     """residual_out over residual and y over x: the bits of separate buffers."""
