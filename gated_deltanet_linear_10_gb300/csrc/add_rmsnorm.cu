@@ -11,16 +11,16 @@
 // The maximum that the 8-bit scale needs is taken over |s (offset + w)| in the
 // same pass as the sum of squares, since 1 / rms is one factor of the row.
 //
-// One CTA works on a row at a time, kVecs vectors of 16 bytes per thread; the
-// weights stay in registers over the rows of a CTA, and a row's loads are
-// issued before the row in front of it is reduced, so that a CTA always has a
-// row in flight.
+// One CTA works on a row at a time, or, up to 32 vectors of 16 bytes wide, each
+// of its 8 warps; kVecs vectors per thread.  The weights stay in registers over
+// the rows of a thread, and a row's loads are issued before the row in front of
+// it is reduced, so that there is always a row in flight.
 //
 // Rows that start within 16 bytes, all of a token's alike (packed rows of an odd
 // width are), are cut at their memory's 16-byte boundaries all the same (kShift):
 // vector v of a row holds elements v N - p .. v N - p + N - 1, with p where the row
 // starts, and the two ends go element by element.  The grid is a multiple of N
-// rows, so that p and with it the weights are the same for all rows of a CTA.
+// rows, so that p and with it the weights are the same for all rows of a thread.
 //
 // What bounds it: HBM for many rows.  20668 x 2048 bf16 to e4m3 with the
 // residual takes 46.1 us, 6.43 TB/s of its 296 MB (0.95 of the copy rate); 61.9
@@ -42,7 +42,7 @@ constexpr int rms_threads(int n, int vecs, size_t elem) {   // the most a launch
 }
 constexpr int kRmsSmThreads = 1536;   // resident threads of an SM: 42 registers each
 
-template <typename T, typename O, int N, int kVecs, bool kShift>
+template <typename T, typename O, int N, int kVecs, bool kShift, int kRows>
 __global__ void __launch_bounds__(rms_threads(N, kVecs, sizeof(T)),
                                   kRmsSmThreads / rms_threads(N, kVecs, sizeof(T)) * (N * kVecs <= 8 ? 1 : 0) +
                                       (N * kVecs <= 8 ? 0 : 1))
@@ -55,7 +55,9 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
     griddep_wait();    // launched behind the kernel that writes x: nothing is read before it
     griddep_launch();  // what is launched behind this kernel may set itself up
     const int tid = threadIdx.x;
-    const int p = kShift ? (int)((first + (uint64_t)blockIdx.x * step) % N) : 0;
+    // kRows rows at a time: one, or each a warp's
+    int row = kRows == 1 ? blockIdx.x : blockIdx.x * kRows + threadIdx.y, flip = 0;
+    const int p = kShift ? (int)((first + (uint64_t)row * step) % N) : 0;
     auto at = [&](int k) { return (int)(tid + k * blockDim.x) * N - p; };
     // a whole vector, or (kShift) one of the two ends of a row
     auto whole = [&](int e) { return e < hidden && (!kShift || (e >= 0 && e + N <= hidden)); };
@@ -90,9 +92,8 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
         a[k].zero();
         b[k].zero();
     }
-    int row = blockIdx.x, flip = 0;
     if (row < n_rows) load(row);
-    for (; row < n_rows; row += gridDim.x, flip ^= 1) {
+    for (; row < n_rows; row += gridDim.x * kRows, flip ^= 1) {
         F2 s[kVecs][P], ss = f2(0.f, 0.f);
         float mx = 0.f;
 #pragma unroll
@@ -103,7 +104,7 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
 #pragma unroll
             for (int i = 0; i < P; ++i) s[k][i] = f2_add(s[k][i], r[i]);
         }
-        if (row + (int)gridDim.x < n_rows) load(row + gridDim.x);
+        if (row + (int)gridDim.x * kRows < n_rows) load(row + gridDim.x * kRows);
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             const int e = at(k);
@@ -156,7 +157,7 @@ struct RmsRows {
     int first, step;
 };
 
-template <typename T, typename O, int N, int kVecs, bool kShift>
+template <typename T, typename O, int N, int kVecs, bool kShift, int kRows>
 static cudaError_t launch_rms_n(RmsRows at, const void *x, int64_t xs, const void *res, int64_t rs,
                                 const float *w, float offset, int n_rows, int hidden, float eps,
                                 void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
@@ -164,36 +165,44 @@ static cudaError_t launch_rms_n(RmsRows at, const void *x, int64_t xs, const voi
     const int per = N * kVecs;
     const int threads = (((hidden + (kShift ? N - 1 : 0) + per - 1) / per) + 31) / 32 * 32;
     const int resident = N * kVecs <= 8 ? kRmsSmThreads : rms_threads(N, kVecs, sizeof(T));
-    int grid = std::min(n_rows, sm_count() * std::min(16, std::max(1, resident / threads)));
+    int grid = std::min((n_rows + kRows - 1) / kRows, sm_count() * std::max(1, resident / (threads * kRows)));
     if (kShift && grid < n_rows) grid = std::max(N, grid / N * N);
-    return launch_after(add_rmsnorm_kernel<T, O, N, kVecs, kShift>, dim3(grid), dim3(threads), 0, s,
+    return launch_after(add_rmsnorm_kernel<T, O, N, kVecs, kShift, kRows>, dim3(grid), dim3(threads, kRows), 0, s,
                         (const T *)x, xs, (const T *)res, rs, w, offset, n_rows, hidden, eps,
                         (T *)res_out, ros, (O *)y, ys, y_scale, at.first, at.step);
 }
 
-// One vector per thread while that fits a CTA of 512 threads (rows of at most
-// 512 vectors), more beyond.
+// One vector per thread while that fits a CTA of 512 threads, more beyond.  A
+// warp per row up to 32 vectors (20000 rows of 203 bf16 to e4m3: 12.3 us, by CTAs
+// of a warp 16.7; with two and four vectors a lane it loses: 301 fp32 43 us, by
+// CTAs of 96 threads 18).  Shifted bf16 rows of less than 128 elements go element
+// by element, their ends being most of them (101: 9.0 us, on vectors 11.3).
 template <typename T, typename O>
 static cudaError_t launch_rms(RmsRows at, const void *x, int64_t xs, const void *res, int64_t rs,
                               const float *w, float offset, int n_rows, int hidden, float eps,
                               void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
                               cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-#define GDN_RMS(n, v, shift)                                                                            \
-    launch_rms_n<T, O, n, v, shift>(at, x, xs, res, rs, w, offset, n_rows, hidden, eps, res_out, ros, y, ys, \
+#define GDN_RMS(n, v, shift) GDN_RMS_ROWS(n, v, shift, 1)
+#define GDN_RMS_ROWS(n, v, shift, rows)                                                                     \
+    launch_rms_n<T, O, n, v, shift, rows>(at, x, xs, res, rs, w, offset, n_rows, hidden, eps, res_out, ros, y, ys, \
                                     y_scale, s)
     if (at.kind == RmsRows::kVector) {
+        if (hidden <= 32 * N) return GDN_RMS_ROWS(N, 1, false, 8);
         if (hidden <= 512 * N) return GDN_RMS(N, 1, false);
         if (hidden <= 1024 * N) return GDN_RMS(N, 2, false);
         return GDN_RMS(N, 4, false);
     }
-    if (at.kind == RmsRows::kShifted) {
+    if (at.kind == RmsRows::kShifted && (sizeof(T) == 4 || hidden >= 128)) {
+        if (hidden + N - 1 <= 32 * N) return GDN_RMS_ROWS(N, 1, true, 8);
         if (hidden + N - 1 <= 512 * N) return GDN_RMS(N, 1, true);
         if (hidden + N - 1 <= 1024 * N) return GDN_RMS(N, 2, true);
         if (hidden + N - 1 <= (sizeof(T) == 4 ? 1024 : 512) * N * 4) return GDN_RMS(N, 4, true);
     }
+    if (hidden <= 128) return GDN_RMS_ROWS(1, 4, false, 8);
     if (hidden <= 4096) return GDN_RMS(1, 4, false);
     return GDN_RMS(1, 16, false);
+#undef GDN_RMS_ROWS
 #undef GDN_RMS
 }
 
@@ -211,7 +220,8 @@ extern "C" gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const
     GDN_REQUIRE(dtype == GDN_F32 || dtype == GDN_BF16, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(y_dtype == dtype || y_dtype == GDN_E4M3, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(n_tokens >= 0 && hidden > 0 && eps >= 0.f, GDN_ERR_INVALID_ARG);
-    GDN_REQUIRE(hidden <= kRmsMaxHidden && n_tokens < (1ll << 31), GDN_ERR_UNSUPPORTED);
+    // a row plus the grid stays within 32 bits
+    GDN_REQUIRE(hidden <= kRmsMaxHidden && n_tokens < (1ll << 31) - (1 << 20), GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
     GDN_REQUIRE(x && weight && y, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE((y_scale != nullptr) == (y_dtype == GDN_E4M3), GDN_ERR_INVALID_ARG);

@@ -139,7 +139,8 @@ extern "C" gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int6
     GDN_REQUIRE(dtype == GDN_F32 || dtype == GDN_BF16, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(n_tokens >= 0 && hv > 0 && eps >= 0.f, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(dv == 16 || dv == 32 || dv == 64 || dv == 128 || dv == 256, GDN_ERR_UNSUPPORTED);
-    GDN_REQUIRE((int64_t)hv * dv <= kGatedMaxRow && n_tokens < (1ll << 31), GDN_ERR_UNSUPPORTED);
+    // a token plus the grid stays within 32 bits
+    GDN_REQUIRE((int64_t)hv * dv <= kGatedMaxRow && n_tokens < (1ll << 31) - (1 << 20), GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
     GDN_REQUIRE(o && z && weight && y && y_scale, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(z_row_stride >= (int64_t)hv * dv, GDN_ERR_INVALID_ARG);

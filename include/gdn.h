@@ -424,7 +424,7 @@ gdn_status gdn_gated_rmsnorm(const void *o, const void *z, int64_t z_row_stride,
  *      z_row_stride a multiple of 4), in `dtype`.
  *   y: [n_tokens][hv][dv] e4m3, contiguous, 8-byte aligned; y_scale:
  *      [n_tokens] fp32.
- * Built: dv in {16, 32, 64, 128, 256}, hv * dv <= 16384.
+ * Built: dv in {16, 32, 64, 128, 256}, hv * dv <= 16384; n_tokens < 2^31 - 2^20.
  */
 gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_stride,
                                    const float *weight, int64_t n_tokens, int32_t hv,
@@ -452,7 +452,7 @@ gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_s
  * y and residual_out must not overlap each other.  Any alignment of whole
  * elements is taken; rows on 16-byte boundaries (and hidden a multiple of 16
  * bytes) run on vector accesses.
- * Built: hidden <= 16384.
+ * Built: hidden <= 16384; n_tokens < 2^31 - 2^20.
  */
 gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *residual,
                            int64_t residual_row_stride, const float *weight,
