@@ -38,7 +38,9 @@ constexpr int kRmsMaxHidden = 16384;
 // T: x, residual and residual_out.  O: y (T or E4m3).  N: elements per vector
 // (16 bytes of T, or 1 where a row is not on 16-byte boundaries).
 constexpr int rms_threads(int n, int vecs, size_t elem) {   // the most a launch below takes
-    return n == 1 || (vecs == 4 && elem == 4) ? 1024 : 512;
+    if (n == 1 || (vecs == 4 && elem == 4)) return 1024;
+    if (vecs == 4) return 512;
+    return n * vecs <= 8 ? 768 : 704;
 }
 constexpr int kRmsSmThreads = 1536;   // resident threads of an SM: 42 registers each
 
@@ -172,7 +174,11 @@ static cudaError_t launch_rms_n(RmsRows at, const void *x, int64_t xs, const voi
                         (T *)res_out, ros, (O *)y, ys, y_scale, at.first, at.step);
 }
 
-// One vector per thread while that fits a CTA of 512 threads, more beyond.  A
+// One vector per thread while that fits a CTA of 768 threads, two of which an SM
+// holds at 42 registers; two per thread up to 704 (bf16, 88 registers) or 768
+// threads, four beyond.  A CTA of 544 threads beats one of 288 with twice the
+// vectors and registers: 10000 x 4095 bf16 to e4m3 takes 77 us, with two 121;
+// 5000 x 8191 at two vectors 73 us, at four 95.  A
 // warp per row up to 32 vectors (20000 rows of 203 bf16 to e4m3: 12.3 us, by CTAs
 // of a warp 16.7; with two and four vectors a lane it loses: 301 fp32 43 us, by
 // CTAs of 96 threads 18).  Shifted bf16 rows of less than 128 elements go element
@@ -183,20 +189,21 @@ static cudaError_t launch_rms(RmsRows at, const void *x, int64_t xs, const void 
                               void *res_out, int64_t ros, void *y, int64_t ys, float *y_scale,
                               cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
+    constexpr int kOne = rms_threads(N, 1, sizeof(T)) * N, kTwo = rms_threads(N, 2, sizeof(T)) * 2 * N;
 #define GDN_RMS(n, v, shift) GDN_RMS_ROWS(n, v, shift, 1)
 #define GDN_RMS_ROWS(n, v, shift, rows)                                                                     \
     launch_rms_n<T, O, n, v, shift, rows>(at, x, xs, res, rs, w, offset, n_rows, hidden, eps, res_out, ros, y, ys, \
                                     y_scale, s)
     if (at.kind == RmsRows::kVector) {
         if (hidden <= 32 * N) return GDN_RMS_ROWS(N, 1, false, 8);
-        if (hidden <= 512 * N) return GDN_RMS(N, 1, false);
-        if (hidden <= 1024 * N) return GDN_RMS(N, 2, false);
+        if (hidden <= kOne) return GDN_RMS(N, 1, false);
+        if (hidden <= kTwo) return GDN_RMS(N, 2, false);
         return GDN_RMS(N, 4, false);
     }
     if (at.kind == RmsRows::kShifted && (sizeof(T) == 4 || hidden >= 128)) {
         if (hidden + N - 1 <= 32 * N) return GDN_RMS_ROWS(N, 1, true, 8);
-        if (hidden + N - 1 <= 512 * N) return GDN_RMS(N, 1, true);
-        if (hidden + N - 1 <= 1024 * N) return GDN_RMS(N, 2, true);
+        if (hidden + N - 1 <= kOne) return GDN_RMS(N, 1, true);
+        if (hidden + N - 1 <= kTwo) return GDN_RMS(N, 2, true);
         if (hidden + N - 1 <= (sizeof(T) == 4 ? 1024 : 512) * N * 4) return GDN_RMS(N, 4, true);
     }
     if (hidden <= 128) return GDN_RMS_ROWS(1, 4, false, 8);
