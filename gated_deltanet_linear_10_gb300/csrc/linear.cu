@@ -142,7 +142,8 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     __shared__ float sxs[BT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's number by a shuffle, so that it is known to be one for the warp
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = splits > 1 ? (int)cta_rank() : 0;
     const int n0 = blockIdx.x / splits * 128, t0 = blockIdx.y * BT;
     constexpr int kElems = kE4m3 ? 128 : 64;                 // k per block of 128 bytes
@@ -206,19 +207,19 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     } else if (warp == 1) {
         constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
-        const uint32_t base = smem_u32(smem) >> 4;
+        const uint32_t base = smem_u32(smem) >> 4, sums = tmem_base;
         uint32_t phase = 0;
         int s = 0;
 #pragma unroll 1
         for (int i = 0; i < nk; ++i) {
             if (!mbar_wait_all(&full[s], phase, abort)) break;
             tc_fence_after();
-            if (one) {
+            if (elect_lane()) {
                 const uint32_t st = base + s * (C::kStage >> 4);
                 const uint64_t da = desc | st, db = desc | (st + (C::kW >> 4));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    linear_mma<kE4m3>(tmem_base, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
+                    linear_mma<kE4m3>(sums, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
                 mma_commit(&empty[s]);
             }
             __syncwarp();
