@@ -290,7 +290,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     __shared__ __align__(16) float cols[2 * kChTile];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = cta_rank();
     constexpr int kElems = kE4m3 ? 128 : 64;                 // k per block of 128 bytes
     const int nk = (n_in + kElems - 1) / kElems;
@@ -399,7 +399,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     break;
                 }
                 tc_fence_after();
-                if (one) {
+                if (elect_lane()) {
                     const uint64_t da = desc | st, db = desc | (st + (kStageA >> 4));
 #pragma unroll
                     for (int q = 0; q < 4; ++q) mma_pair<kE4m3>(d, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
