@@ -124,10 +124,12 @@ template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
 // result has one order of sums; with one, it has them all.  Then 16 threads
 // write a token's 128 channels.
 //
-// What bounds it at 256 x 4096 x 2048 (10.6 us; floor 3.1): 2,000 cycles to the
-// first products, 9,000 of products (16 blocks at the 567 cycles below), 3,200 of
-// exchange (48 KB a CTA, 1,500 of it latency), 3,500 to write the sums and the
-// output.  One token (1 x 2048 x 8192, 7.8 us; floor 4.9) waits for the weights.
+// What bounds it at 256 x 4096 x 2048 (8.8 us; floor 3.1): 2,000 cycles to the
+// first products, 5,500 to 6,500 of products (16 blocks, held by their copies: 256
+// lines of 128 bytes at some 1.6 cycles each; the products alone would take 256
+// cycles a block), 3,200 of exchange (48 KB a CTA, 1,500 of it latency), 3,500 to
+// write the sums and the output.  One token (1 x 2048 x 8192, 6.9 us; floor 4.9)
+// waits for the weights.
 // The code behind the products runs once per CTA, so it is kept short and
 // rolled: unrolled over 32 tokens with its variants it took 3 to 20 us of
 // instruction fetches and dependent loads at 256 tokens.
@@ -207,6 +209,9 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     } else if (warp == 1) {
         constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
+        // What a product is issued with is read from memory once and known to be one for
+        // the warp, and the lane is elected on the spot: 64 cycles for 128 x 128 x 16, where
+        // rereading the base and testing a kept flag took 140.
         const uint32_t base = smem_u32(smem) >> 4, sums = tmem_base;
         uint32_t phase = 0;
         int s = 0;
@@ -347,11 +352,14 @@ struct NarrowPlan {
     int64_t cycles;
 };
 
-// A k block takes 567 cycles: a CTA's 128-channel product costs 128 cycles for
-// any number of tokens up to 128, the ring the rest.  Behind and in front of the
-// loop 9,000 (256 x 2048 x 8192 e4m3, k whole), and 3,500 more where the sums
-// are exchanged (256 x 4096 x 2048, k in four).  Every cluster that the device
-// cannot hold at once waits for a whole one.
+// Fitted to 1 to 2000 tokens on products of 256 x 2048 to 8192 x 1024, with k in one,
+// two, four and eight, bf16 and e4m3: what this estimate picks takes 0.5 % longer
+// than the best of them in the mean, and 7 % at the worst (on sizes it was not fitted
+// to, 17 % in one of 264).  A k block of 128 tokens takes 425 cycles, its copies from
+// L2, and 800 where rows are off the memory's lines (128 x 2056 x 8192, k whole: 16.2
+// us, on lines 12.9); what goes before and after the loop grows with the tokens, and
+// with the CTAs that start at once.  Every cluster that the device cannot hold at once
+// waits for a whole one.
 template <int BT, bool kE4m3> static cudaError_t plan_narrow(const LinearCall &c, NarrowPlan &best) {
     using C = NarrowCfg<BT>;
     static ClustersHeld held[4];
@@ -364,8 +372,12 @@ template <int BT, bool kE4m3> static cudaError_t plan_narrow(const LinearCall &c
         const cudaError_t e = held[i].ask(kernel, 1 << i, kNarrowThreads, C::kSmem, fit);
         if (e != cudaSuccess) return e;
         if (fit <= 0) continue;
-        const int64_t waves = ((int64_t)nn * nt + fit - 1) / fit;
-        const int64_t cycles = 9000 + (i ? 3500 : 0) + (waves - 1) * 4000 + waves * ((blocks + (1 << i) - 1) >> i) * 567;
+        const int block = c.lines() ? (BT == 128 ? 425 : 300) : BT == 128 ? 800 : BT == 64 ? 530 : 360;
+        constexpr int kEnds = BT == 128 ? 8700 : 5000;
+        constexpr int kExchange[4] = {0, 300, 300, 900}, kCtaCycles = 17;
+        const int64_t tiles = (int64_t)nn * nt, waves = (tiles + fit - 1) / fit;
+        const int64_t cycles = waves * (kEnds + kExchange[i] + kCtaCycles * (std::min<int64_t>(tiles, fit) << i) +
+                                        ((blocks + (1 << i) - 1) >> i) * block);
         if (cycles < best.cycles) best = {nn, nt, 1 << i, cycles};
     }
     return cudaSuccess;
@@ -389,9 +401,9 @@ static gdn_status launch_narrow(const LinearCall &c, const NarrowPlan &plan) {
 }
 
 // The narrow tiles for up to 128 tokens; beyond, whichever estimate is shorter
-// (narrow and wide measured: 512 x 4096 x 2048 bf16 17.2 and 18.8 us, 512 x 2048 x
-// 8192 29.6 and 16.2, 256 x 2048 x 8192 e4m3 9.8 and 8.6, 256 x 4096 x 2048 bf16
-// 11.7 and 18.2, 777 x 1003 x 1331 16.9 and 13.2).
+// (narrow and wide measured, bf16: 256 x 4096 x 2048 9.0 and 14.7 us, 512 x 4096 x
+// 2048 12.5 and 16.0, 512 x 2048 x 8192 24.4 and 16.7, 640 x 2048 x 2048 10.5 and
+// 10.4, 256 x 8192 x 1024 11.7 and 25.6; e4m3: 256 x 2048 x 8192 8.6 and 8.1).
 template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
     const int t = c.e.n_tokens;
     NarrowPlan plan = {};
@@ -402,7 +414,7 @@ template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
         set_last_cuda_error(e);
         return GDN_ERR_CUDA;
     }
-    if (t > 128 && (plan.nt > 65535 || wide_cycles(c, kE4m3) < plan.cycles)) return launch_linear_wide(c, kE4m3);
+    if (t > 128 && (plan.nt > 65535 || wide_cycles(c) < plan.cycles)) return launch_linear_wide(c);
     if (plan.cycles == INT64_MAX) return GDN_ERR_UNSUPPORTED;
     if (t <= 32) return launch_narrow<32, kE4m3>(c, plan);
     if (t <= 64) return launch_narrow<64, kE4m3>(c, plan);
@@ -449,6 +461,7 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     c.xs = x_row_stride;
     c.ws = w_row_stride;
     c.n_in = n_in;
+    c.e4m3 = dtype == GDN_E4M3;
     c.stream = (cudaStream_t)stream;
     c.e = {x_scale, w_scale, bias, residual, residual_row_stride, y, y_row_stride,
            (int)n_tokens, n_out, act, y_dtype == GDN_F32, false};

@@ -236,12 +236,18 @@ struct LinearCall {
     const void *x, *w;
     int64_t xs, ws;
     int n_in;
+    bool e4m3;
     LinearEpi e;
     cudaStream_t stream;
+    // whether 128 bytes of a row of x and w are one line of memory, and not parts of two
+    bool lines() const {
+        const int64_t elem = e4m3 ? 1 : 2;
+        return (((uintptr_t)x | (uintptr_t)w | (uint64_t)(xs * elem) | (uint64_t)(ws * elem)) & 127) == 0;
+    }
 };
 
 // linear_wide.cu: the product on CTA pairs, and the cycles of an SM it takes by estimate.
-gdn_status launch_linear_wide(const LinearCall &c, bool e4m3);
-int64_t wide_cycles(const LinearCall &c, bool e4m3);
+gdn_status launch_linear_wide(const LinearCall &c);
+int64_t wide_cycles(const LinearCall &c);
 
 }  // namespace gdn

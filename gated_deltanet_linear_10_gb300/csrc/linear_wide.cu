@@ -580,17 +580,20 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
 // The plan with the shortest estimate, and that in cycles of a k block.  A block
 // takes 512 cycles of a pair on 256 channels, the rate of the tensor cores; on
 // fewer it is the operands' copies that hold it (512 x 2048 x 8192 in channel
-// tiles of 192, 128 and 64: 445, 410 and 410).  The last `rows` token tiles are
-// cut into channel tiles of w where that fills the last wave of pairs better.
-int64_t plan_wide(int n_tokens, int n_out, int pairs, WidePlan &best) {
-    constexpr int kBlockCycles[4] = {410, 410, 445, 512};
+// tiles of 192, 128 and 64: 445, 410 and 410), and where rows are off the memory's
+// lines, on 256 too (512 x 2056 x 8192: 18.4 us, on lines 16.5).  The last `rows`
+// token tiles are cut into channel tiles of w where that fills the last wave of
+// pairs better (8000 x 2048 x 2048: 40.4 us, in tiles of 256 alone 42.9, of 192 44.1).
+int64_t plan_wide(const LinearCall &call, int pairs, WidePlan &best) {
+    constexpr int kBlockCycles[2][4] = {{424, 540, 640, 750}, {410, 410, 445, 512}};
+    const int n_tokens = call.e.n_tokens, n_out = call.e.n_out, *cycles = kBlockCycles[call.lines()];
     const int nt = (n_tokens + kTokTile - 1) / kTokTile, nn = (n_out + kChTile - 1) / kChTile;
     auto waves = [&](int64_t tiles) { return (tiles + pairs - 1) / pairs; };
     int64_t cost = INT64_MAX;
     for (int rows = 0; rows <= std::min(nt, 16); ++rows)
         for (int w = 64; w <= (rows ? kChTile - 64 : 64); w += 64) {   // whole staging rows
             const int64_t full = (int64_t)(nt - rows) * nn, tail = (int64_t)rows * ((n_out + w - 1) / w);
-            const int64_t c = waves(full) * kBlockCycles[3] + waves(tail) * kBlockCycles[w / 64 - 1];
+            const int64_t c = waves(full) * cycles[3] + waves(tail) * cycles[w / 64 - 1];
             if (c < cost) {
                 cost = c;
                 best = {nt - rows, nt, nn, (int)full, w, (int)(full + tail)};
@@ -610,7 +613,7 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
     GDN_REQUIRE(sms >= 2, GDN_ERR_UNSUPPORTED);
     GDN_REQUIRE(wide_fits(e), GDN_ERR_UNSUPPORTED);
     WidePlan plan;
-    plan_wide(e.n_tokens, e.n_out, sms / 2, plan);
+    plan_wide(c, sms / 2, plan);
     CUtensorMap mx, mw, mt, my = {};
     if (!encode_tmap_operand(&mx, c.x, c.n_in, e.n_tokens, c.xs, kTokHalf, kE4m3) ||
         !encode_tmap_operand(&mw, c.w, c.n_in, e.n_out, c.ws, kChTile / 2, kE4m3) ||
@@ -648,17 +651,17 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
 
 }  // namespace
 
-// 9,700 cycles in front of the first product and behind the last (512 x 2048 x 8192).
-int64_t wide_cycles(const LinearCall &c, bool e4m3) {
+// 8,700 cycles in front of the first product and behind the last.
+int64_t wide_cycles(const LinearCall &c) {
     const int pairs = sm_count() / 2;
     if (pairs < 1 || !wide_fits(c.e)) return INT64_MAX;
     WidePlan plan;
-    const int64_t blocks = (c.n_in + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
-    return 9700 + plan_wide(c.e.n_tokens, c.e.n_out, pairs, plan) * blocks;
+    const int64_t blocks = (c.n_in + (c.e4m3 ? 127 : 63)) / (c.e4m3 ? 128 : 64);
+    return 8700 + plan_wide(c, pairs, plan) * blocks;
 }
 
-gdn_status launch_linear_wide(const LinearCall &c, bool e4m3) {
-    if (e4m3) return c.e.out_f32 ? launch_wide<true, float>(c) : launch_wide<true, __nv_bfloat16>(c);
+gdn_status launch_linear_wide(const LinearCall &c) {
+    if (c.e4m3) return c.e.out_f32 ? launch_wide<true, float>(c) : launch_wide<true, __nv_bfloat16>(c);
     return c.e.out_f32 ? launch_wide<false, float>(c) : launch_wide<false, __nv_bfloat16>(c);
 }
 
