@@ -110,10 +110,7 @@ __device__ __forceinline__ void narrow_out(F2 (&v)[2][4], const LinearEpi &ep, c
 
 template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 f = f2_get(v[i / 4][i % 4]);
-        v[i / 4][i % 4] = f2(linear_act<kAct>(f.x), linear_act<kAct>(f.y));
-    }
+    for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = linear_act<kAct>(v[i / 4][i % 4]);
 }
 
 // grid (channel tiles * splits, token tiles); the `splits` CTAs of a tile are a

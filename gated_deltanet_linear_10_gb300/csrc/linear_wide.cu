@@ -200,61 +200,70 @@ __device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], const uint32
 // The same for bf16 rows that start on 4 bytes or, kOdd, some on 2: a lane holds
 // two channels of a row and the warp two rows at a time, half of wide_plain's
 // accesses to memory (11036 x 84 x 4854 with a residual: 105 us, with wide_plain
-// 138; words of 8 bytes gain nothing more).  Where an odd row starts between two
-// words, its first lane takes the chunk's first and last channel, the others the
-// words between (12183 x 538 x 5715 with a residual: 190 us, with wide_plain 214).
+// 138; words of 8 bytes gain nothing more).  An odd row, which starts between two
+// words, gives channels n - 1 .. n + 30 instead, so that these are words too; the
+// last chunk of a run adds the one that is left, and of the tile's first word only
+// the upper half is its own (12183 x 538 x 5715 with a residual: 154 us; with both
+// ends of every chunk apart 179, with wide_plain 203).
 template <bool kOdd> struct WideWords {
-    int h, first, second;                                  // row of the pair, channels
-    bool split;                                            // first and second are not neighbours
-    __device__ __forceinline__ WideWords(const LinearEpi &ep, int t0, int n, int lane) {
+    int h, w;                                              // row of the pair, word of the row
+    bool odd, mine, edge, last;                            // rows of h odd; row t0 + lane odd; half a word; end of a run
+    __device__ __forceinline__ WideWords(const LinearEpi &ep, int t0, int n, int c, int width, int lane) {
         h = lane >> 4;
-        const int w = lane & 15;
-        const bool odd = kOdd && ((((uintptr_t)ep.y >> 1) + (uint64_t)(t0 + h) * ep.ys + n) & 1);
-        split = odd && w == 0;
-        first = split ? 0 : w * 2 - (odd ? 1 : 0);
-        second = split ? 31 : first + 1;
+        w = lane & 15;
+        odd = mine = edge = last = false;
+        if constexpr (kOdd) {
+            const uint64_t at = ((uintptr_t)ep.y >> 1) + (uint64_t)t0 * ep.ys + n;
+            odd = (at + h * ep.ys) & 1;
+            mine = (at + lane * ep.ys) & 1;
+            edge = odd && w == 0 && c == 0;
+            last = c + 32 >= width || n + 64 > ep.n_out;
+        }
     }
-    // rv[k]: the residual's word of row 2 k + h; an odd row's two ends in rv[k] and rv[16 + k]
-    __device__ __forceinline__ void ask(uint32_t *rv, const LinearEpi &ep, int t0, int n) const {
-        const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(ep.res) + (t0 + h) * ep.rs + n + first;
+    // rv[k]: the residual's word of row 2 k + h; rv[16]: that of the channel left over in row t0 + lane
+    __device__ __forceinline__ void ask(uint32_t *rv, const LinearEpi &ep, int t0, int n, int lane) const {
+        const __nv_bfloat16 *res = reinterpret_cast<const __nv_bfloat16 *>(ep.res);
+        const __nv_bfloat16 *p = res + (t0 + h) * ep.rs + n + 2 * w - odd;
         const int rows = ep.n_tokens - t0 - h;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             if (2 * k < rows) {
-                if (kOdd && split) {
-                    rv[k] = load_bits(p);
-                    rv[16 + k] = load_bits(p + 31);
-                } else {
-                    rv[k] = *reinterpret_cast<const uint32_t *>(p);
-                }
+                if (kOdd && edge) rv[k] = load_bits(p + 1);      // shifted when it is used, not before it is here
+                else rv[k] = *reinterpret_cast<const uint32_t *>(p);
             }
             p += 2 * ep.rs;
         }
+        if (kOdd && last && mine && t0 + lane < ep.n_tokens) rv[16] = load_bits(res + (t0 + lane) * ep.rs + n + 31);
     }
-    __device__ __forceinline__ void out(const uint32_t (&r)[32], const uint32_t (&rv)[32], float *turn,
+    // before: the value of channel n - 1
+    __device__ __forceinline__ void out(const uint32_t (&r)[32], uint32_t before, const uint32_t (&rv)[32], float *turn,
                                         const LinearEpi &ep, int t0, int n, int lane) const {
         __syncwarp();                                      // the buffer's last values are read
 #pragma unroll
-        for (int j = 0; j < 32; ++j) turn[lane * 32 + (j ^ lane)] = __uint_as_float(r[j]);
+        for (int j = 0; j < 32; ++j)
+            turn[lane * 32 + (j ^ lane)] = __uint_as_float(kOdd && mine ? (j ? r[j - 1] : before) : r[j]);
         __syncwarp();
         const int rows = ep.n_tokens - t0 - h;
-        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(ep.y) + (t0 + h) * ep.ys + n + first;
+        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(ep.y);
+        if (kOdd && last && mine && t0 + lane < ep.n_tokens) {
+            float v = __uint_as_float(r[31]);
+            if (ep.res) v += bits_value<__nv_bfloat16>(rv[16]);
+            Io<__nv_bfloat16>::store(y + (t0 + lane) * ep.ys + n + 31, v);
+        }
+        y += (t0 + h) * ep.ys + n + 2 * w - odd;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const int i = 2 * k + h;
-            float a = turn[i * 32 + (first ^ i)], b = turn[i * 32 + (second ^ i)];
+            // channels j, j + 1 of row i are at j ^ i and that ^ 1
+            const float2 f = *reinterpret_cast<const float2 *>(turn + (2 * k + h) * 32 + ((2 * w) ^ (2 * k)));
+            float a = h ? f.y : f.x, b = h ? f.x : f.y;
             if (ep.res) {
                 a += bits_value<__nv_bfloat16>(rv[k]);
-                b += kOdd && split ? bits_value<__nv_bfloat16>(rv[16 + k]) : __uint_as_float(rv[k] & 0xffff0000u);
+                b += __uint_as_float(kOdd && edge ? rv[k] << 16 : rv[k] & 0xffff0000u);
             }
             const uint32_t q = pack_bf16(a, b);
             if (2 * k < rows) {
-                if (kOdd && split) {
-                    *reinterpret_cast<uint16_t *>(y) = (uint16_t)q;
-                    *reinterpret_cast<uint16_t *>(y + 31) = (uint16_t)(q >> 16);
-                } else {
-                    *reinterpret_cast<uint32_t *>(y) = q;
-                }
+                if (kOdd && edge) *reinterpret_cast<uint16_t *>(y + 1) = (uint16_t)(q >> 16);
+                else *reinterpret_cast<uint32_t *>(y) = q;
             }
             y += 2 * ep.ys;
         }
@@ -265,18 +274,48 @@ template <bool kOdd> struct WideWords {
 // the columns' scales in shared memory, their biases kChTile floats on.
 template <int kAct, bool kCols>
 __device__ __forceinline__ void wide_values(uint32_t (&r)[32], const float *cols, float sx) {
+    const F2 sx2 = f2(sx, sx);
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-        float4 s = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
+        F2 v[2] = {f2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                   f2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]))};
         if constexpr (kCols) {
-            s = *reinterpret_cast<const float4 *>(cols + j);
-            b = *reinterpret_cast<const float4 *>(cols + kChTile + j);
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(cols + j);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(cols + kChTile + j);
+            v[0] = f2_fma(v[0], f2_mul(sx2, s.x), b.x);
+            v[1] = f2_fma(v[1], f2_mul(sx2, s.y), b.y);
+        } else {
+            v[0] = f2_mul(v[0], sx2);
+            v[1] = f2_mul(v[1], sx2);
         }
-        r[j] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j]), sx * s.x, b.x)));
-        r[j + 1] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j + 1]), sx * s.y, b.y)));
-        r[j + 2] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j + 2]), sx * s.z, b.z)));
-        r[j + 3] = __float_as_uint(linear_act<kAct>(fmaf(__uint_as_float(r[j + 3]), sx * s.w, b.w)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 f = f2_get(linear_act<kAct>(v[i]));
+            r[j + 2 * i] = __float_as_uint(f.x);
+            r[j + 2 * i + 1] = __float_as_uint(f.y);
+        }
     }
+}
+
+// One of them: act(v scale + bias).
+__device__ __forceinline__ uint32_t wide_value(uint32_t v, int act, float scale, float bias) {
+    const float f = fmaf(__uint_as_float(v), scale, bias);
+    F2 p = f2(f, f);
+    if (act == GDN_ACT_SILU) p = linear_act<GDN_ACT_SILU>(p);
+    else if (act == GDN_ACT_GELU) p = linear_act<GDN_ACT_GELU>(p);
+    return __float_as_uint(f2_get(p).x);
+}
+
+// One column of 32 lanes of tensor memory.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r)
+        : "r"(taddr)
+        : "memory");
+    return r;
 }
 
 template <bool kE4m3, typename O>
@@ -462,7 +501,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
         };
         uint32_t rv[32];
-        auto ask = [&](int t0, int n) {                 // the residual of a chunk
+        auto ask = [&](const Ahead &a, int c) {         // the residual of a chunk
+            const int t0 = a.t0, n = a.n0 + c;
             if (n >= ep.n_out) return;
             if (rows <= kRows16) {
                 const int t = t0 + lane;
@@ -471,8 +511,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
             if constexpr (sizeof(O) == 2) {
                 if (n + 32 <= ep.n_out && rows != kRowsPlain) {
-                    if (rows == kRows4) WideWords<false>(ep, t0, n, lane).ask(rv, ep, t0, n);
-                    else WideWords<true>(ep, t0, n, lane).ask(rv, ep, t0, n);
+                    if (rows == kRows4) WideWords<false>(ep, t0, n, c, a.width, lane).ask(rv, ep, t0, n, lane);
+                    else WideWords<true>(ep, t0, n, c, a.width, lane).ask(rv, ep, t0, n, lane);
                     return;
                 }
             }
@@ -481,7 +521,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         static_assert(32 * kEpiWarps == kChTile, "a thread holds one column's scale and bias");
         walk.start(plan, pair);
         ahead(cur);
-        if (ep.res && start < cur.width) ask(cur.t0, cur.n0 + start);
+        if (ep.res && start < cur.width) ask(cur, start);
         for (int u = 0; cur.width > 0; ++u, cur = nxt) {
             const int b = u & 1, t0 = cur.t0, n0 = cur.n0, width = cur.width;
             const float sx = cur.sx;
@@ -499,8 +539,12 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             for (int c = start, part = 0; c < width;) {
                 const int n = n0 + c;
                 const int next_c = part + 1 < PARTS && c + 32 < width ? c + 32 : c - part * 32 + STEP;
-                uint32_t r[32];
+                uint32_t r[32], before = 0;
                 tmem_ld32(tmem_addr(tmem_base, q * 32, b * kChTile + c), r);
+                if (rows == kRowsOdd && c > 0) {
+                    before = tmem_ld1(tmem_addr(tmem_base, q * 32, b * kChTile + c - 1));
+                    before = wide_value(before, ep.act, has_cols ? cols[c - 1] * sx : sx, has_cols ? cols[kChTile + c - 1] : 0.0f);
+                }
                 if (ep.act == GDN_ACT_SILU) wide_values<GDN_ACT_SILU, true>(r, cols + c, sx);
                 else if (ep.act == GDN_ACT_GELU) wide_values<GDN_ACT_GELU, true>(r, cols + c, sx);
                 else if (has_cols) wide_values<GDN_ACT_NONE, true>(r, cols + c, sx);
@@ -523,13 +567,15 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     if (sizeof(O) == 4 || rows == kRowsPlain || n + 32 > ep.n_out) {
                         wide_plain<O>(r, rv, turn, ep, t0, n, lane);
                     } else if constexpr (sizeof(O) == 2) {
-                        if (rows == kRows4) WideWords<false>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
-                        else WideWords<true>(ep, t0, n, lane).out(r, rv, turn, ep, t0, n, lane);
+                        if (rows == kRows4)
+                            WideWords<false>(ep, t0, n, c, width, lane).out(r, 0, rv, turn, ep, t0, n, lane);
+                        else
+                            WideWords<true>(ep, t0, n, c, width, lane).out(r, before, rv, turn, ep, t0, n, lane);
                     }
                 }
                 if (res) {
-                    if (next_c < width) ask(t0, n0 + next_c);
-                    else if (start < nxt.width) ask(nxt.t0, nxt.n0 + start);
+                    if (next_c < width) ask(cur, next_c);
+                    else if (start < nxt.width) ask(nxt, start);
                 }
                 if (rows <= kRows16) {
                     if constexpr (sizeof(O) == 2) {
@@ -558,7 +604,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 part = next_c == c + 32 && PARTS > 1 ? 1 : 0;
                 c = next_c;
             }
-            if (ep.res && start >= width && start < nxt.width) ask(nxt.t0, nxt.n0 + start);   // no chunk here
+            if (ep.res && start >= width && start < nxt.width) ask(nxt, start);   // no chunk here
             tc_fence_before();                          // this warp has read its part of the accumulator
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[b]), 0));
