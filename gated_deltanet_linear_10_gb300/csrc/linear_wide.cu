@@ -188,11 +188,13 @@ __device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], const uint32
     __syncwarp();
     const int rows = n + lane < ep.n_out ? ep.n_tokens - t0 : 0;
     O *y = reinterpret_cast<O *>(ep.y) + n + lane + t0 * ep.ys;
+    float v[32];                                     // all read in front of the first store
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = turn[i * 32 + (lane ^ i)];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        float v = turn[i * 32 + (lane ^ i)];
-        if (ep.res) v += bits_value<O>(rv[i]);
-        if (i < rows) Io<O>::store(y, v);
+        if (ep.res) v[i] += bits_value<O>(rv[i]);
+        if (i < rows) Io<O>::store(y, v[i]);
         y += ep.ys;
     }
 }
@@ -203,7 +205,7 @@ __device__ __forceinline__ void wide_plain(const uint32_t (&r)[32], const uint32
 // 138; words of 8 bytes gain nothing more).  An odd row, which starts between two
 // words, gives channels n - 1 .. n + 30 instead, so that these are words too; the
 // last chunk of a run adds the one that is left, and of the tile's first word only
-// the upper half is its own (12183 x 538 x 5715 with a residual: 154 us; with both
+// the upper half is its own (12183 x 538 x 5715 with a residual: 146 us; with both
 // ends of every chunk apart 179, with wide_plain 203).
 template <bool kOdd> struct WideWords {
     int h, w;                                              // row of the pair, word of the row
@@ -236,12 +238,14 @@ template <bool kOdd> struct WideWords {
         if (kOdd && last && mine && t0 + lane < ep.n_tokens) rv[16] = load_bits(res + (t0 + lane) * ep.rs + n + 31);
     }
     // before: the value of channel n - 1
-    __device__ __forceinline__ void out(const uint32_t (&r)[32], uint32_t before, const uint32_t (&rv)[32], float *turn,
+    __device__ __forceinline__ void out(const uint32_t (&r)[32], uint32_t before, const uint32_t (&rv)[32], uint8_t *turn,
                                         const LinearEpi &ep, int t0, int n, int lane) const {
         __syncwarp();                                      // the buffer's last values are read
+        auto v = [&](int j) { return kOdd && mine ? (j ? r[j - 1] : before) : r[j]; };
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            turn[lane * 32 + (j ^ lane)] = __uint_as_float(kOdd && mine ? (j ? r[j - 1] : before) : r[j]);
+        for (int q = 0; q < 8; ++q)                        // 16 bytes at a time, permuted by the row
+            *reinterpret_cast<uint4 *>(turn + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(v(4 * q), v(4 * q + 1), v(4 * q + 2), v(4 * q + 3));
         __syncwarp();
         const int rows = ep.n_tokens - t0 - h;
         __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(ep.y);
@@ -251,11 +255,16 @@ template <bool kOdd> struct WideWords {
             Io<__nv_bfloat16>::store(y + (t0 + lane) * ep.ys + n + 31, v);
         }
         y += (t0 + h) * ep.ys + n + 2 * w - odd;
+        // All of them are read in front of the first store, which the compiler will not
+        // read behind.
+        float2 f[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)                       // row 2 k + h, its word w
+            f[k] = *reinterpret_cast<const float2 *>(turn + k * 256 + h * 128 + (w & 1) * 8 +
+                                                     (((w >> 1) ^ h ^ (2 * k & 7)) << 4));
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            // channels j, j + 1 of row i are at j ^ i and that ^ 1
-            const float2 f = *reinterpret_cast<const float2 *>(turn + (2 * k + h) * 32 + ((2 * w) ^ (2 * k)));
-            float a = h ? f.y : f.x, b = h ? f.x : f.y;
+            float a = f[k].x, b = f[k].y;
             if (ep.res) {
                 a += bits_value<__nv_bfloat16>(rv[k]);
                 b += __uint_as_float(kOdd && edge ? rv[k] << 16 : rv[k] & 0xffff0000u);
@@ -563,14 +572,13 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                         }
                     }
                 } else if (n < ep.n_out) {
-                    float *turn = reinterpret_cast<float *>(staging);
                     if (sizeof(O) == 4 || rows == kRowsPlain || n + 32 > ep.n_out) {
-                        wide_plain<O>(r, rv, turn, ep, t0, n, lane);
+                        wide_plain<O>(r, rv, reinterpret_cast<float *>(staging), ep, t0, n, lane);
                     } else if constexpr (sizeof(O) == 2) {
                         if (rows == kRows4)
-                            WideWords<false>(ep, t0, n, c, width, lane).out(r, 0, rv, turn, ep, t0, n, lane);
+                            WideWords<false>(ep, t0, n, c, width, lane).out(r, 0, rv, staging, ep, t0, n, lane);
                         else
-                            WideWords<true>(ep, t0, n, c, width, lane).out(r, before, rv, turn, ep, t0, n, lane);
+                            WideWords<true>(ep, t0, n, c, width, lane).out(r, before, rv, staging, ep, t0, n, lane);
                     }
                 }
                 if (res) {
