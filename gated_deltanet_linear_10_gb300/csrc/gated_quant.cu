@@ -22,11 +22,12 @@ namespace gdn {
 
 constexpr int kGatedMaxRow = 16384;   // hv * dv
 
-constexpr int gated_threads(int vecs) { return vecs == 1 ? 256 : 1024; }   // the most a launch below takes
-constexpr int kGatedSmThreads = 1536;   // resident threads of an SM with one vector each: 42 registers
+// Resident threads of an SM with one vector each: 42 registers, fp32 64.
+constexpr int gated_sm_threads(size_t elem) { return elem == 4 ? 1024 : 1536; }
 
-template <typename T, int DV, int kVecs>
-__global__ void __launch_bounds__(gated_threads(kVecs), kVecs == 1 ? kGatedSmThreads / 256 : 1)
+// kThreads: the most of a launch; with two vectors each 64 registers for 1024, 128 for 512.
+template <typename T, int DV, int kVecs, int kThreads>
+__global__ void __launch_bounds__(kThreads, kVecs == 1 ? gated_sm_threads(sizeof(T)) / 256 : 1)
 gated_quant_kernel(const T *__restrict__ o, const T *__restrict__ z, int64_t zs,
                    const float *__restrict__ w, int n_tokens, int row, float eps,
                    bool z16, uint8_t *__restrict__ y, float *__restrict__ y_scale) {
@@ -114,18 +115,23 @@ gated_quant_kernel(const T *__restrict__ o, const T *__restrict__ z, int64_t zs,
     }
 }
 
+// fp32 takes twice the registers a vector: at 42 and 64 of them it spilled (20668 x
+// 3 x 256: 26.8 us, at 64 22.9; 5000 x 32 x 256: 79.8 us, at 128 55.5).  Beyond 1024
+// vectors there is only the 64 (5000 x 64 x 256: 165 us, 4.5 TB/s).
 template <typename T, int DV>
 static cudaError_t launch_gated_quant(const void *o, const void *z, int64_t zs, const float *w,
                                       int n_tokens, int hv, float eps, bool z16, void *y,
                                       float *y_scale, cudaStream_t s) {
     const int row = hv * DV, vecs = row / 8;
-    auto go = [&](auto kernel, int per) {
+    auto go = [&](auto kernel, int per, int resident) {
         const int threads = ((vecs + per - 1) / per + 31) / 32 * 32;
-        const int grid = std::min(n_tokens, sm_count() * std::min(16, std::max(1, (per == 1 ? kGatedSmThreads : 1024) / threads)));
+        const int grid = std::min(n_tokens, sm_count() * std::min(32, std::max(1, resident / threads)));
         return launch_after(kernel, dim3(grid), dim3(threads), 0, s, (const T *)o, (const T *)z, zs,
                             w, n_tokens, row, eps, z16, (uint8_t *)y, y_scale);
     };
-    return vecs <= 256 ? go(gated_quant_kernel<T, DV, 1>, 1) : go(gated_quant_kernel<T, DV, 2>, 2);
+    if (vecs <= 256) return go(gated_quant_kernel<T, DV, 1, 256>, 1, gated_sm_threads(sizeof(T)));
+    if (sizeof(T) == 4 && vecs <= 1024) return go(gated_quant_kernel<T, DV, 2, 512>, 2, 512);
+    return go(gated_quant_kernel<T, DV, 2, 1024>, 2, 1024);
 }
 
 }  // namespace gdn
