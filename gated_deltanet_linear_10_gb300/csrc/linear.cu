@@ -411,7 +411,11 @@ template <bool kE4m3> static gdn_status launch_linear(const LinearCall &c) {
         set_last_cuda_error(e);
         return GDN_ERR_CUDA;
     }
-    if (t > 128 && (plan.nt > 65535 || wide_cycles(c) < plan.cycles)) return launch_linear_wide(c);
+    if (plan.nt > 65535) plan.cycles = INT64_MAX;      // token tiles are a grid dimension
+    if (t > 128) {
+        WidePlan wide;
+        if (plan_linear_wide(c, wide) < plan.cycles) return launch_linear_wide(c, wide);
+    }
     if (plan.cycles == INT64_MAX) return GDN_ERR_UNSUPPORTED;
     if (t <= 32) return launch_narrow<32, kE4m3>(c, plan);
     if (t <= 64) return launch_narrow<64, kE4m3>(c, plan);
@@ -433,7 +437,7 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     GDN_REQUIRE(dtype != GDN_F32, GDN_ERR_UNSUPPORTED);
     GDN_REQUIRE(act >= GDN_ACT_NONE && act <= GDN_ACT_GELU, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(n_tokens >= 0 && n_in > 0 && n_out > 0, GDN_ERR_INVALID_ARG);
-    // token tiles are a grid dimension of at most 65,535
+    // token tiles of the wide kernel
     GDN_REQUIRE(n_tokens <= 65535 * 256 && n_out <= (1 << 30) && n_in <= (1 << 30), GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
     GDN_REQUIRE(x && w && y, GDN_ERR_INVALID_ARG);

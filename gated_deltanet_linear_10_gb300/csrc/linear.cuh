@@ -33,10 +33,11 @@ __device__ __forceinline__ F2 rcp_pair(float a, float b) {
 }
 
 // v / (1 + e^-v).  Below -43.6 (e^-v = 2^63) it stays at the value there, -5e-18.
+// A NaN stays out of the factors, which the other value shares.
 __device__ __forceinline__ F2 silu_short(float a, float b) {
-    a = max_nan(a, -43.6f);
-    b = max_nan(b, -43.6f);
-    return f2_mul(f2(a, b), rcp_pair(1.0f + ex2_approx(-kLog2e * a), 1.0f + ex2_approx(-kLog2e * b)));
+    constexpr float kLeast = -43.6f;
+    return f2_mul(f2(max_nan(a, kLeast), max_nan(b, kLeast)),
+                  rcp_pair(1.0f + ex2_approx(-kLog2e * fmaxf(a, kLeast)), 1.0f + ex2_approx(-kLog2e * fmaxf(b, kLeast))));
 }
 
 // GELU by the rational approximation of erfc of Abramowitz and Stegun, Handbook
@@ -259,8 +260,18 @@ struct LinearCall {
     }
 };
 
-// linear_wide.cu: the product on CTA pairs, and the cycles of an SM it takes by estimate.
-gdn_status launch_linear_wide(const LinearCall &c);
-int64_t wide_cycles(const LinearCall &c);
+// The tiles: token rows [0, nt_full) in channel tiles of 256, the token
+// rows behind them in channel tiles of tail_w.  Order: groups of eight token
+// tiles; within a group the token tile runs fastest, then the channel tile, so
+// the tiles in flight at one time share about as many token rows as weight rows
+// (all token tiles in one group: 9 % slower at 20668 x 2048 x 8192).
+struct WidePlan {
+    int nt_full, nt, nn, n_full, tail_w, n_tiles;
+};
+
+// linear_wide.cu: the product on CTA pairs; its plan, with the cycles of an SM that
+// it takes by estimate (INT64_MAX: not built), and its launch.
+int64_t plan_linear_wide(const LinearCall &c, WidePlan &plan);
+gdn_status launch_linear_wide(const LinearCall &c, const WidePlan &plan);
 
 }  // namespace gdn

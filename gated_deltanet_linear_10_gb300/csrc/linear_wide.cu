@@ -78,15 +78,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
             : "memory");
 }
 
-// The tiles: token rows [0, nt_full) in channel tiles of kChTile, the token
-// rows behind them in channel tiles of tail_w.  Order: groups of kRaster token
-// tiles; within a group the token tile runs fastest, then the channel tile, so
-// the tiles in flight at one time share about as many token rows as weight rows
-// (all token tiles in one group: 9 % slower at 20668 x 2048 x 8192).
-struct WidePlan {
-    int nt_full, nt, nn, n_full, tail_w, n_tiles;
-};
-
 // A pair's walk over the tiles: every `pairs`-th one.  Steps instead of
 // divisions: two of them in every warp cost some 500 cycles a tile.
 struct WideWalk {
@@ -661,13 +652,9 @@ bool wide_fits(const LinearEpi &e) {
     return ((int64_t)e.n_tokens + 255) / 256 * (((int64_t)e.n_out + 31) / 32) < (1 << 30);
 }
 
-template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
+template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c, const WidePlan &plan) {
     const LinearEpi &e = c.e;
     const int sms = sm_count() / 2 * 2;
-    GDN_REQUIRE(sms >= 2, GDN_ERR_UNSUPPORTED);
-    GDN_REQUIRE(wide_fits(e), GDN_ERR_UNSUPPORTED);
-    WidePlan plan;
-    plan_wide(c, sms / 2, plan);
     CUtensorMap mx, mw, mt, my = {};
     if (!encode_tmap_operand(&mx, c.x, c.n_in, e.n_tokens, c.xs, kTokHalf, kE4m3) ||
         !encode_tmap_operand(&mw, c.w, c.n_in, e.n_out, c.ws, kChTile / 2, kE4m3) ||
@@ -706,17 +693,16 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c) {
 }  // namespace
 
 // 8,700 cycles in front of the first product and behind the last.
-int64_t wide_cycles(const LinearCall &c) {
+int64_t plan_linear_wide(const LinearCall &c, WidePlan &plan) {
     const int pairs = sm_count() / 2;
     if (pairs < 1 || !wide_fits(c.e)) return INT64_MAX;
-    WidePlan plan;
     const int64_t blocks = (c.n_in + (c.e4m3 ? 127 : 63)) / (c.e4m3 ? 128 : 64);
     return 8700 + plan_wide(c, pairs, plan) * blocks;
 }
 
-gdn_status launch_linear_wide(const LinearCall &c) {
-    if (c.e4m3) return c.e.out_f32 ? launch_wide<true, float>(c) : launch_wide<true, __nv_bfloat16>(c);
-    return c.e.out_f32 ? launch_wide<false, float>(c) : launch_wide<false, __nv_bfloat16>(c);
+gdn_status launch_linear_wide(const LinearCall &c, const WidePlan &plan) {
+    if (c.e4m3) return c.e.out_f32 ? launch_wide<true, float>(c, plan) : launch_wide<true, __nv_bfloat16>(c, plan);
+    return c.e.out_f32 ? launch_wide<false, float>(c, plan) : launch_wide<false, __nv_bfloat16>(c, plan);
 }
 
 }  // namespace gdn

@@ -251,3 +251,41 @@ def test_many_tiles(T, K, N, dtype):
     """Several tiles for every pair, the last ones narrower, with every part of the epilogue."""
     for act, residual in (("none", True), ("gelu", False)):
         _run(T, T, K, N, dtype, BF16, True, act, residual)
+
+
+@pytest.mark.parametrize("N", [33, 35, 63, 65, 95, 97, 127, 129, 191, 223, 255, 257, 287, 321, 1025, 1055, 1057, 1087])
+def test_many_tokens_odd_widths(N):
+    """Packed rows of an odd width start on 2 and on 4 bytes in turn; their ends fall
+    anywhere in the pieces that a warp writes."""
+    for act, residual in (("none", False), ("silu", True)):
+        y = _run(N, 2100, 40, N, BF16, BF16, True, act, residual)
+    x, w, _, _, b, res = _case(N, 2100, 40, N, BF16, True, BF16)
+    buf = res.clone()
+    gdn().gdn_linear(x, w, bias=b, act="silu", residual=buf, y=buf)
+    torch.cuda.synchronize()
+    assert bits_equal(buf, y)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [5, 100, 2100])
+def test_activations_far_out(T, act, out):
+    """Values of any size in any channel leave the channels beside them alone."""
+    K, far = 64, [1e30, -1e30, 3e38, -3e38, 1e4, -1e4, 200.0, -200.0, 90.0, -90.0, 45.0, -45.0, 20.0, -20.0,
+                  float("inf"), float("-inf"), float("nan")]
+    x, w, _, _, b, _ = _case(T, T, K, 4 * len(far), BF16, True)
+    for i, v in enumerate(far):                          # far, near, near, far
+        b[4 * i] = b[4 * i + 3] = v
+    y = gdn().gdn_linear(x, w, bias=b, act=act, y_dtype=out)
+    torch.cuda.synchronize()
+    status_clean()
+    finite = torch.isfinite(b)
+    ref, size = b64.linear(x, w[finite], None, None, b[finite], act, None)
+    b64.check_linear(y[:, finite], ref, size, K)
+    near = b.abs() < 10
+    ref, size = b64.linear(x, w[near], None, None, b[near], act, None)
+    b64.check_linear(y[:, near], ref, size, K)
+    assert torch.all(y[:, b == float("inf")] == float("inf"))
+    assert torch.all(torch.isnan(y[:, torch.isnan(b)]))
+    if act == "silu":                                    # its limit
+        assert torch.all(y[:, b == float("-inf")].abs() <= 1e-17)
