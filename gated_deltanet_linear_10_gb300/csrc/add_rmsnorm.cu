@@ -230,7 +230,7 @@ extern "C" gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const
     // a row plus the grid stays within 32 bits
     GDN_REQUIRE(hidden <= kRmsMaxHidden && n_tokens < (1ll << 31) - (1 << 20), GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
-    GDN_REQUIRE(x && weight && y, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(x && weight && y && y != residual_out, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE((y_scale != nullptr) == (y_dtype == GDN_E4M3), GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(x_row_stride >= hidden && y_row_stride >= hidden, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(!residual || residual_row_stride >= hidden, GDN_ERR_INVALID_ARG);

@@ -440,7 +440,7 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     // token tiles of the wide kernel
     GDN_REQUIRE(n_tokens <= 65535 * 256 && n_out <= (1 << 30) && n_in <= (1 << 30), GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
-    GDN_REQUIRE(x && w && y, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(x && w && y && y != x && y != w, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(x_row_stride >= n_in && w_row_stride >= n_in && y_row_stride >= n_out &&
                     (!residual || residual_row_stride >= n_out),
                 GDN_ERR_INVALID_ARG);

@@ -450,8 +450,9 @@ gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_s
  *      y_row_stride; y may be x or residual (same pointer and stride) when
  *      y_dtype == dtype.  y_scale: [n_tokens] fp32 with GDN_E4M3, else NULL.
  * y and residual_out must not overlap each other.  Any alignment of whole
- * elements is taken; rows on 16-byte boundaries (and hidden a multiple of 16
- * bytes) run on vector accesses.
+ * elements is taken; where the rows of x, residual, residual_out and y start
+ * alike within 16 bytes (of x's elements), packed ones of an odd width too,
+ * they run on vector accesses.
  * Built: hidden <= 16384; n_tokens < 2^31 - 2^20.
  */
 gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *residual,

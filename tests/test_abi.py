@@ -303,7 +303,7 @@ def test_add_rmsnorm_host_checks(lib):
     f = lib.gdn_add_rmsnorm
     f.argtypes = [V, I64, V, I64, V, F32, I64, I32, F32, V, I64, V, I64, V, I32, I32, V]
     A = 1 << 20
-    base = [A, 64, A, 64, A, 0.0, 4, 64, 1e-6, A, 64, A, 64, None, 1, 1, None]
+    base = [A, 64, A, 64, A, 0.0, 4, 64, 1e-6, A, 64, 2 * A, 64, None, 1, 1, None]
 
     def rc(**at):
         a = list(base)
@@ -320,6 +320,7 @@ def test_add_rmsnorm_host_checks(lib):
     assert rc(_0=None) == 1 and rc(_4=None) == 1 and rc(_11=None) == 1
     assert rc(_1=63) == 1 and rc(_3=63) == 1 and rc(_10=63) == 1 and rc(_12=63) == 1
     assert rc(_15=2) == 1 and rc(_13=A) == 1            # e4m3 without scales, scales without e4m3
+    assert rc(_11=A) == 1                               # y on residual_out
     assert rc(_0=A + 1) == 1 and rc(_2=A + 1) == 1 and rc(_9=A + 1) == 1 and rc(_4=A + 2) == 1
     assert rc(_0=None, _6=0) == 0                       # no rows: no launch
 
@@ -346,7 +347,7 @@ def test_linear_host_checks(lib):
     f = lib.gdn_linear
     f.argtypes = [V, I64, V, V, I64, V, V, V, I64, I64, I32, I32, I32, V, I64, I32, I32, V]
     A = 1 << 20
-    base = [A, 64, None, A, 64, None, None, None, 0, 4, 64, 96, 0, A, 96, 1, 1, None]
+    base = [A, 64, None, 2 * A, 64, None, None, None, 0, 4, 64, 96, 0, 3 * A, 96, 1, 1, None]
 
     def rc(**at):
         a = list(base)
@@ -360,6 +361,7 @@ def test_linear_host_checks(lib):
     assert rc(_9=-1) == 1 and rc(_10=0) == 1 and rc(_11=0) == 1
     assert rc(_9=65535 * 256 + 1) == 2
     assert rc(_0=None) == 1 and rc(_3=None) == 1 and rc(_13=None) == 1
+    assert rc(_13=A) == 1 and rc(_13=2 * A) == 1        # y on an operand
     assert rc(_1=63) == 1 and rc(_4=63) == 1 and rc(_14=95) == 1
     assert rc(_7=A, _8=95) == 1                         # residual rows overlap
     assert rc(_1=1 << 36) == 2 and rc(_4=1 << 36) == 2 and rc(_14=1 << 36) == 2 and rc(_7=A, _8=1 << 36) == 2
