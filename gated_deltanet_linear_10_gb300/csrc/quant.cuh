@@ -112,6 +112,12 @@ template <typename T, int N> struct RawVec {
         for (int i = 0; i < N; ++i)
             if (i >= lo && i < hi) reinterpret_cast<T *>(r)[i] = p[i];
     }
+    // zero but for the elements lo .. hi - 1
+    __device__ __forceinline__ void keep(int lo, int hi) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < lo || i >= hi) reinterpret_cast<T *>(r)[i] = T(0.0f);
+    }
     // as N / 2 pairs
     __device__ __forceinline__ void pairs(F2 *out) const {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(r);
@@ -128,6 +134,7 @@ template <typename T> struct RawVec<T, 1> {
     T r;
     __device__ __forceinline__ void load(const T *p) { r = *p; }
     __device__ __forceinline__ void load_part(const T *, int, int) {}
+    __device__ __forceinline__ void keep(int, int) {}
     __device__ __forceinline__ void zero() { Io<T>::store(&r, 0.f); }
     __device__ __forceinline__ void pairs(F2 *out) const { out[0] = f2(Io<T>::load(&r), 0.f); }
 };
