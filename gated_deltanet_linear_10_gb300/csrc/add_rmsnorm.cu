@@ -78,7 +78,8 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
     RawVec<T, N> a[kVecs], b[kVecs];
     // An end of a row.  bf16: the whole vector, with what lies beside the row, unless
     // that is beside all rows; elements, two to a register, would be waited for here
-    // (20668 x 2047 to bf16: 67.9 us, with the vector 57.7).
+    // (20668 x 2047 to bf16: 67.9 us, with the vector 57.7; 54.7 with few stores of
+    // the ends, 55.3 at 2048).
     constexpr bool kBeside = kShift && sizeof(T) == 2;
     auto load_end = [&](RawVec<T, N> &v, const T *p, int row, int e) {
         if (kBeside && (e >= 0 || row > 0) && (e + N <= hidden || row + 1 < n_rows)) v.load(p);
@@ -109,14 +110,18 @@ add_rmsnorm_kernel(const T *x, int64_t xs, const T *res, int64_t rs, const float
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             F2 r[P];
-            if (kBeside && part_of(at(k))) {
-                a[k].keep(-at(k), hidden - at(k));
-                b[k].keep(-at(k), hidden - at(k));
-            }
             a[k].pairs(s[k]);
             b[k].pairs(r);
 #pragma unroll
             for (int i = 0; i < P; ++i) s[k][i] = f2_add(s[k][i], r[i]);
+            if (kBeside && part_of(at(k))) {         // what lies beside the row is not its own
+                const int lo = -at(k), hi = hidden + lo;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float2 v = f2_get(s[k][i]);
+                    s[k][i] = f2(2 * i < lo || 2 * i >= hi ? 0.f : v.x, 2 * i + 1 < lo || 2 * i + 1 >= hi ? 0.f : v.y);
+                }
+            }
         }
         if (row + (int)gridDim.x * kRows < n_rows) load(row + gridDim.x * kRows);
 #pragma unroll
@@ -189,9 +194,9 @@ static cudaError_t launch_rms_n(RmsRows at, const void *x, int64_t xs, const voi
 // One vector per thread while that fits a CTA of 768 threads, two of which an SM
 // holds at 42 registers; two per thread up to 704 (bf16, 88 registers) or 768
 // threads, four beyond.  A CTA of 544 threads beats one of 288 with twice the
-// vectors and registers: 10000 x 4095 bf16 to e4m3 takes 77 us, with two 121;
-// 5000 x 8191 at two vectors 73 us, at four 95.  A
-// warp per row up to 32 vectors (20000 rows of 203 bf16 to e4m3: 12.3 us, by CTAs
+// vectors and registers: 10000 x 4095 bf16 to e4m3 took 77 us, with two 121 (60
+// since the rows' ends are cheaper); 5000 x 8191 at two vectors 73 us, at four 95 (56
+// since).  A warp per row up to 32 vectors (20000 rows of 203 bf16 to e4m3: 12.3 us, by CTAs
 // of a warp 16.7; with two and four vectors a lane it loses: 301 fp32 43 us, by
 // CTAs of 96 threads 18).  Shifted bf16 rows of less than 128 elements go element
 // by element, their ends being most of them (101: 9.0 us, on vectors 11.3).
@@ -212,7 +217,7 @@ static cudaError_t launch_rms(RmsRows at, const void *x, int64_t xs, const void 
         if (hidden <= kTwo) return GDN_RMS(N, 2, false);
         return GDN_RMS(N, 4, false);
     }
-    if (at.kind == RmsRows::kShifted && (sizeof(T) == 4 || hidden >= 128)) {   // bf16: more than a vector
+    if (at.kind == RmsRows::kShifted && hidden >= (sizeof(T) == 4 ? N : 128)) {   // no vector with both ends
         if (hidden + N - 1 <= 32 * N) return GDN_RMS_ROWS(N, 1, true, 8);
         if (hidden + N - 1 <= kOne) return GDN_RMS(N, 1, true);
         if (hidden + N - 1 <= kTwo) return GDN_RMS(N, 2, true);

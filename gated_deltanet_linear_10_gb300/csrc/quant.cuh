@@ -112,12 +112,6 @@ template <typename T, int N> struct RawVec {
         for (int i = 0; i < N; ++i)
             if (i >= lo && i < hi) reinterpret_cast<T *>(r)[i] = p[i];
     }
-    // zero but for the elements lo .. hi - 1
-    __device__ __forceinline__ void keep(int lo, int hi) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < lo || i >= hi) reinterpret_cast<T *>(r)[i] = T(0.0f);
-    }
     // as N / 2 pairs
     __device__ __forceinline__ void pairs(F2 *out) const {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(r);
@@ -134,7 +128,6 @@ template <typename T> struct RawVec<T, 1> {
     T r;
     __device__ __forceinline__ void load(const T *p) { r = *p; }
     __device__ __forceinline__ void load_part(const T *, int, int) {}
-    __device__ __forceinline__ void keep(int, int) {}
     __device__ __forceinline__ void zero() { Io<T>::store(&r, 0.f); }
     __device__ __forceinline__ void pairs(F2 *out) const { out[0] = f2(Io<T>::load(&r), 0.f); }
 };
@@ -178,11 +171,71 @@ template <int N> __device__ __forceinline__ void store_row(E4m3 *p, const float 
     }
 }
 
-// Values lo .. hi - 1 of such a vector.
-template <int N, typename O> __device__ __forceinline__ void store_part(O *p, const float *v, int lo, int hi) {
+// Bytes lo .. of a vector of W words (lo > 0), or its bytes .. hi - 1 (lo <= 0), at
+// most four stores; p on the vector's size.
+template <int W> __device__ __forceinline__ void store_bytes(uint8_t *p, const uint32_t (&w)[W], int lo, int hi) {
+    auto word = [&](int b) {
+        uint32_t v = w[0];
+#pragma unroll
+        for (int i = 1; i < W; ++i) v = b >= 4 * i ? w[i] : v;
+        return v;
+    };
+    int b = lo > 0 ? lo : 0;
+    if (lo > 0) {
+        if (b & 1) {
+            p[b] = (uint8_t)(word(b) >> (b & 2 ? 24 : 8));
+            b += 1;
+        }
+        if (b & 2) {
+            *reinterpret_cast<uint16_t *>(p + b) = (uint16_t)(word(b) >> 16);
+            b += 2;
+        }
+        if (W > 1 && (b & 4)) {
+            *reinterpret_cast<uint32_t *>(p + b) = word(b);
+            b += 4;
+        }
+        if (W > 2 && (b & 8)) *reinterpret_cast<uint2 *>(p + 8) = make_uint2(w[W - 2], w[W - 1]);
+    } else {
+        if (W > 2 && (hi & 8)) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[W > 1 ? 1 : 0]);
+            b = 8;
+        }
+        if (W > 1 && (hi & 4)) {
+            *reinterpret_cast<uint32_t *>(p + b) = word(b);
+            b += 4;
+        }
+        if (hi & 2) {
+            *reinterpret_cast<uint16_t *>(p + b) = (uint16_t)word(b);
+            b += 2;
+        }
+        if (hi & 1) p[b] = (uint8_t)(word(b) >> (hi & 2 ? 16 : 0));
+    }
+}
+
+// An end of a row: values lo .. of such a vector (lo > 0), or its values .. hi - 1.
+template <int N> __device__ __forceinline__ void store_part(float *p, const float *v, int lo, int hi) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (i >= lo && i < hi) store_row<1>(p + i, v + i);
+}
+template <int N> __device__ __forceinline__ void store_part(__nv_bfloat16 *p, const float *v, int lo, int hi) {
+    if constexpr (N > 1) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        store_bytes(reinterpret_cast<uint8_t *>(p), w, 2 * lo, 2 * hi);
+    }
+}
+template <int N> __device__ __forceinline__ void store_part(E4m3 *p, const float *v, int lo, int hi) {
+    if constexpr (N > 1) {
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) w[i] = pack_e4m3x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        store_bytes(reinterpret_cast<uint8_t *>(p), w, lo, hi);
+    }
 }
 
 // (sum, NaN-keeping max) over the block; every thread gets both.  `part` is
