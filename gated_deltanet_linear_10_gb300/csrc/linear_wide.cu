@@ -403,6 +403,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
         }
         griddep_launch();      // what is launched behind this kernel may set itself up
+        // the last stages' releases have come
+        for (int j = i > S ? i - S : 0; ok && j < i; ++j) ok = mbar_wait_all(&empty[j % S], (j / S) & 1, abort);
         if (one && (!ok || *abort)) {
             // Given up: the copies in flight land before the CTA ends.  The leader
             // waits on the barriers that count them; the peer, which has none of
@@ -463,6 +465,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             mma_commit_pair(&drained);    // every product issued is done before the pair ends
             mbar_drain(&drained, 0);
         }
+    } else if (warp == 1) {
+        if (elect_lane()) mbar_drain(&drained, 0);
     } else if (warp >= 4) {
         // Accumulator lane 32 q + l is token row 32 q + l of this CTA's half; the
         // two warps of a quadrant take alternate slices of 128 bytes of y.
@@ -606,14 +610,21 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             if (ep.res && start >= width && start < nxt.width) ask(nxt, start);   // no chunk here
             tc_fence_before();                          // this warp has read its part of the accumulator
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[b]), 0));
+            // the tile after next waits for it (an arrival that nobody waits for could come too late)
+            if (lane == 0 && walk.tile + pairs < plan.n_tiles) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[b]), 0));
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) bulk_wait_read_all();    // the staging rows stay until they are read
         __syncwarp();
         tc_fence_before();
     }
-    __syncwarp();
-    cluster_sync_all();        // neither CTA ends while the other may reach its memory
+    __syncthreads();
+    // Neither CTA ends while the other may reach its memory: every arrival from the
+    // other one has been waited for above, so nothing is handed over here, unless the
+    // pair has given up.  (With release a CTA waited for its stores to y first, some
+    // 1,200 cycles.)
+    if (*abort) cluster_arrive();
+    else cluster_arrive_relaxed();
+    cluster_wait();
     tc_fence_after();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
