@@ -701,11 +701,11 @@ _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurre
 def _one_device(first, *ts):
     """Every tensor on the CUDA device of the first one; returns its index."""
     dev = first.get_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            dev = -1
     if dev < 0:
         raise GdnError("all tensors must be on one CUDA device")
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise GdnError("all tensors must be on one CUDA device")
     return dev
 
 
@@ -724,6 +724,8 @@ def _rows(t, shape, name):
     """t has the 2-D shape and unit column stride; returns its row stride (at least a row where there is one)."""
     if t.shape != shape:
         raise GdnError(f"{name}: shape {tuple(t.shape)}, not {list(shape)}")
+    if t.is_contiguous():
+        return shape[1]
     st, one = t.stride()
     if one != 1 and shape[1] != 1:
         raise GdnError(f"{name}: unit column stride")
@@ -735,7 +737,7 @@ def _rows(t, shape, name):
 
 
 def _f32_vec(t, n, name):
-    if t.dtype != _F32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not _F32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise GdnError(f"{name}: [{n}] fp32, contiguous")
     return t.data_ptr()
 
