@@ -46,26 +46,42 @@ __device__ __forceinline__ void bulk_send(uint32_t dst, uint32_t src, uint32_t b
         : "memory");
 }
 
-// The residual of 8 channels, as loaded (bf16: the first 16 bytes).
+// Channels of a thread, in pairs i = 0 .. 3: 8 in a row where rows are vectors of
+// 8, else one pair of every 32, so that a token's 16 threads access neighbours.
+__device__ __forceinline__ int narrow_channel(bool vec, int g, int i) { return vec ? g * 8 + 2 * i : g * 2 + 32 * i; }
+
+// The residual of a thread's channels n + narrow_channel of token t, as loaded: a
+// vector (bf16: the first 16 bytes), or a channel a word.
 struct Res8 {
     uint4 q[2];
-    __device__ __forceinline__ void load(const LinearEpi &ep, int t, int n) {
-        if (ep.out_f32) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(ep.res) + t * ep.rs + n);
-            q[0] = p[0];
-            q[1] = p[1];
+    template <typename O> __device__ __forceinline__ void load_as(const LinearEpi &ep, bool vec, int t, int n, int g) {
+        const O *p = reinterpret_cast<const O *>(ep.res) + t * ep.rs + n;
+        if (vec) {
+            const uint4 *v = reinterpret_cast<const uint4 *>(p + g * 8);
+            q[0] = v[0];
+            if (sizeof(O) == 4) q[1] = v[1];
         } else {
-            q[0] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(ep.res) + t * ep.rs + n);
+            uint32_t *w = reinterpret_cast<uint32_t *>(q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = narrow_channel(false, g, i / 2) + i % 2;
+                if (n + c >= ep.n_out) continue;
+                if constexpr (sizeof(O) == 4) w[i] = reinterpret_cast<const uint32_t *>(p)[c];
+                else w[i] = reinterpret_cast<const uint16_t *>(p)[c];
+            }
         }
+    }
+    __device__ __forceinline__ void load(const LinearEpi &ep, bool vec, int t, int n, int g) {
+        if (ep.out_f32) load_as<float>(ep, vec, t, n, g);
+        else load_as<__nv_bfloat16>(ep, vec, t, n, g);
     }
 };
 
-// Channels n .. n + 7 of tokens t[0], t[1] (t[u] < 0: none) out: residual, one
-// rounding, store.  y may be residual: it is read before it is written.  vec:
-// the 8 exist and are whole vectors, their residuals in `r`.
+// A thread's channels of tokens t[0], t[1] (t[u] < 0: none) out: residual, one
+// rounding, store.  y may be residual: it is read before it is written.
 template <typename O>
-__device__ __forceinline__ void narrow_out(F2 (&v)[2][4], const LinearEpi &ep, const int (&t)[2], int n, bool vec,
-                                           const Res8 (&r)[2]) {
+__device__ __forceinline__ void narrow_out(F2 (&v)[2][4], const LinearEpi &ep, const int (&t)[2], int n, int g,
+                                           bool vec, const Res8 (&r)[2]) {
     O *y = reinterpret_cast<O *>(ep.y) + n;
     if (vec) {
 #pragma unroll
@@ -82,28 +98,22 @@ __device__ __forceinline__ void narrow_out(F2 (&v)[2][4], const LinearEpi &ep, c
             }
             float f[8];
             unpair<8>(v[u], f);
-            store_row<8>(y + t[u] * ep.ys, f);
+            store_row<8>(y + g * 8 + t[u] * ep.ys, f);
         }
     } else {
-        const O *res = reinterpret_cast<const O *>(ep.res) + n;
-        const int cnt = min(8, ep.n_out - n);
-#pragma unroll 1
+#pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int tu = u ? t[1] : t[0];
-            if (tu < 0) continue;
+            if (t[u] < 0) continue;
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(r[u].q);
             float f[8];
+            unpair<8>(v[u], f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 p = f2_get(u ? v[1][i] : v[0][i]);
-                f[2 * i] = p.x;
-                f[2 * i + 1] = p.y;
+            for (int i = 0; i < 8; ++i) {
+                const int c = narrow_channel(false, g, i / 2) + i % 2;
+                if (n + c >= ep.n_out) continue;
+                if (ep.res) f[i] += __uint_as_float(sizeof(O) == 4 ? w[i] : w[i] << 16);
+                Io<O>::store(y + t[u] * ep.ys + c, f[i]);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (ep.res && i < cnt) f[i] += Io<O>::load(res + tu * ep.rs + i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < cnt) Io<O>::store(y + tu * ep.ys + i, f[i]);
         }
     }
 }
@@ -244,22 +254,24 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     const int first = t0 + rank * per, cnt = min(per, ep.n_tokens - first);   // those it writes (cnt <= 0: none)
     float *own = reinterpret_cast<float *>(smem);        // where the operands were
     float *got = reinterpret_cast<float *>(smem + S * C::kStage);
-    const int g = tid & 15, n = n0 + g * 8;              // this thread's channels below
+    const int g = tid & 15;                              // this thread's channels below
+    const bool vec = ep.vec8;
     F2 sw[4], bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool on = n + 2 * i < ep.n_out, on1 = n + 2 * i + 1 < ep.n_out;
-        sw[i] = f2(on && ep.sw ? ep.sw[n + 2 * i] : 1.0f, on1 && ep.sw ? ep.sw[n + 2 * i + 1] : 1.0f);
-        bias[i] = f2(on && ep.bias ? ep.bias[n + 2 * i] : 0.0f, on1 && ep.bias ? ep.bias[n + 2 * i + 1] : 0.0f);
+        const int n = n0 + narrow_channel(vec, g, i);
+        const bool on = n < ep.n_out, on1 = n + 1 < ep.n_out;
+        sw[i] = f2(on && ep.sw ? ep.sw[n] : 1.0f, on1 && ep.sw ? ep.sw[n + 1] : 1.0f);
+        bias[i] = f2(on && ep.bias ? ep.bias[n] : 0.0f, on1 && ep.bias ? ep.bias[n + 1] : 0.0f);
     }
     // the residual of two of its items ahead: the first two before the sums are there
-    const bool vec = ep.vec8 && n + 8 <= ep.n_out;
+    const bool any = !vec || n0 + g * 8 < ep.n_out;
     Res8 res[2];
     auto ask = [&](int i) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int tok = (i + u * kNarrowThreads) >> 4;
-            if (ep.res && vec && tok < cnt) res[u].load(ep, first + tok, n);
+            if (ep.res && any && tok < cnt) res[u].load(ep, vec, first + tok, n0, g);
         }
     };
     ask(tid);
@@ -306,15 +318,22 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
             F2 v[2][4] = {};
 #pragma unroll 1
             for (int r = 0; r < splits; ++r) {
-                const float *p = (r == rank ? own : got) + r * per * 128 + g * 8;
+                const float *p = (r == rank ? own : got) + r * per * 128;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(p + (u ? tok1 : tok[0]) * 128);
-                    const ulonglong2 a = q[0], b = q[1];
-                    v[u][0] = f2_add(v[u][0], a.x);
-                    v[u][1] = f2_add(v[u][1], a.y);
-                    v[u][2] = f2_add(v[u][2], b.x);
-                    v[u][3] = f2_add(v[u][3], b.y);
+                    const float *q = p + (u ? tok1 : tok[0]) * 128;
+                    if (vec) {
+                        const ulonglong2 *q4 = reinterpret_cast<const ulonglong2 *>(q + g * 8);
+                        const ulonglong2 a = q4[0], b = q4[1];
+                        v[u][0] = f2_add(v[u][0], a.x);
+                        v[u][1] = f2_add(v[u][1], a.y);
+                        v[u][2] = f2_add(v[u][2], b.x);
+                        v[u][3] = f2_add(v[u][3], b.y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[u][i] = f2_add(v[u][i], *reinterpret_cast<const F2 *>(q + narrow_channel(false, g, i)));
+                    }
                 }
             }
             const Res8 cur[2] = {res[0], res[1]};
@@ -327,10 +346,10 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
             }
             if (ep.act == GDN_ACT_SILU) narrow_act<GDN_ACT_SILU>(v);
             else if (ep.act == GDN_ACT_GELU) narrow_act<GDN_ACT_GELU>(v);
-            if (n < ep.n_out) {
+            if (any) {
                 const int t[2] = {first + tok[0], tok[1] < cnt ? first + tok[1] : -1};
-                if (ep.out_f32) narrow_out<float>(v, ep, t, n, vec, cur);
-                else narrow_out<__nv_bfloat16>(v, ep, t, n, vec, cur);
+                if (ep.out_f32) narrow_out<float>(v, ep, t, n0, g, vec, cur);
+                else narrow_out<__nv_bfloat16>(v, ep, t, n0, g, vec, cur);
             }
         }
     }
@@ -467,7 +486,7 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     c.e = {x_scale, w_scale, bias, residual, residual_row_stride, y, y_row_stride,
            (int)n_tokens, n_out, act, y_dtype == GDN_F32, false};
     // 8 channels at a time: 16 bytes of bf16, 32 of fp32
-    c.e.vec8 = (uintptr_t)y % 16 == 0 && y_row_stride * (int64_t)ye % 16 == 0 &&
+    c.e.vec8 = n_out % 8 == 0 && (uintptr_t)y % 16 == 0 && y_row_stride * (int64_t)ye % 16 == 0 &&
                (!residual || ((uintptr_t)residual % 16 == 0 && residual_row_stride * (int64_t)ye % 16 == 0));
     return dtype == GDN_E4M3 ? launch_linear<true>(c) : launch_linear<false>(c);
 }
