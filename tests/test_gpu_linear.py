@@ -289,3 +289,22 @@ def test_activations_far_out(T, act, out):
     assert torch.all(torch.isnan(y[:, torch.isnan(b)]))
     if act == "silu":                                    # its limit
         assert torch.all(y[:, b == float("-inf")].abs() <= 1e-17)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("N", [1, 2, 33, 131, 333, 1004])
+@pytest.mark.parametrize("T", [1, 33, 100, 128])
+def test_few_tokens_odd_widths(T, N, out):
+    """Rows that are no vectors of 8 channels, with every part of the epilogue, k cut
+    over a cluster or not, and the residual in place."""
+    for K in (40, 1500):
+        y = _run(T + N, T, K, N, BF16, out, True, "gelu", True)
+        x, w, _, _, b, res = _case(T + N, T, K, N, BF16, True, out)
+        for off in (0, 1, 2):                              # columns of a wider buffer
+            wide = torch.full((T, N + off + 5), 3.0, dtype=out, device=DEV)
+            wide[:, off:off + N] = res
+            cut = wide[:, off:off + N]
+            gdn().gdn_linear(x, w, bias=b, act="gelu", residual=cut, y=cut)
+            torch.cuda.synchronize()
+            assert bits_equal(cut.contiguous(), y)
+            assert torch.all(wide[:, :off] == 3.0) and torch.all(wide[:, off + N:] == 3.0)
