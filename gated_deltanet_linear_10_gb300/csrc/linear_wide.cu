@@ -9,8 +9,8 @@
 //
 // What bounds it from n_in = 1024 on is the tensor cores' rate and then the
 // power: 256 x 256 x 16 take a pair 128 cycles.  20668 x 2048 x 8192 bf16 is
-// 574,000 cycles of them and takes 595,000, at 1.5 GHz (1.9 without the load):
-// 357 to 362 us, 1,930 TFLOP/s; over seconds some 425 us.  20668 x 4096 x 2048 e4m3
+// 574,000 cycles of them and takes some 590,000, at 1.5 GHz (1.9 without the load):
+// 353 to 363 us, 1,950 TFLOP/s; over seconds some 425 us.  20668 x 4096 x 2048 e4m3
 // with a residual: 104 us, 3,340 TFLOP/s, one of its nine waves half full.
 // What it took, in cycles of a tile (n_in 2048; 16,400 of products): issuing from
 // a converged warp 2,900, six stages instead of five 900 (the ring's latency: with

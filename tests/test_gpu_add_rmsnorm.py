@@ -277,3 +277,31 @@ def test_other_stream_and_graph():
     for a, b in zip(want, (y.view(torch.uint8), ys, ro, q.view(torch.uint8), qs)):
         assert torch.equal(a, b)
     status_clean()
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, E4M3), (F32, E4M3), (F32, F32)])
+@pytest.mark.parametrize("H", [131, 203, 1111, 4095, 8191])
+@pytest.mark.parametrize("pad", [0, 6])
+def test_what_lies_beside_a_row_stays_out(H, dtype, out, pad):
+    """NaNs in other rows and between the rows, which share 16 bytes with a row's ends."""
+    T, off = 400, 3 if pad else 0
+    xw, rw = (torch.full((T, H + pad), float("nan"), dtype=dtype, device=DEV) for _ in range(2))
+    x, res, w = xw[:, off:off + H], rw[:, off:off + H], _rand(1, H)
+    x.copy_(_rand(2, T, H))
+    res.copy_(_rand(3, T, H))
+    x[1::3] = float("nan")
+    res[0] = float("inf")
+    row = torch.full((T, H + pad), float("nan"), dtype=dtype, device=DEV)[:, off:off + H]
+    yw = torch.zeros(T, H + pad, device=DEV).to(out)
+    y, scale, ro = gdn().gdn_add_rmsnorm(x, w, residual=res, y=yw[:, off:off + H], residual_out=row)
+    torch.cuda.synchronize()
+    good = torch.ones(T, dtype=torch.bool, device=DEV)
+    good[1::3] = False
+    good[0] = False
+    s, ref = b64.add_rmsnorm(x[good], res[good], w, 1e-6, 0.0)
+    b64.check_near(ro[good], s, 2.0 ** -24, b64.HALF[dtype], "residual_out")
+    if out == E4M3:
+        b64.check_quant(y.float()[good], scale[good], ref, b64.NORM, "y")
+    else:
+        b64.check_near(y[good], ref, b64.NORM, b64.HALF[out], "y")
+    assert torch.all(torch.isnan(y.float()[1::3]))
