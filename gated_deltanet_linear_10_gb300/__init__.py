@@ -895,10 +895,13 @@ def gdn_get_device_status(clear=True, device=None) -> int:
     return int(out.value)
 
 
-def gdn_debug_set_wait_limit(limit_ns=0, drop_prep_loads=False, device=None):
-    """Test control of the two-kernel prefill's failure path: the limit of its
-    bounded waits (0 = the default, one second) and whether the prep kernel
-    skips its K|Q loads (its waits then run out and the call sets
-    DEVSTAT_TIMEOUT; its results are undefined).  Synchronises the stream."""
-    _check(_lib.gdn_debug_set_wait_limit(int(limit_ns), int(bool(drop_prep_loads)),
+def gdn_debug_set_wait_limit(limit_ns=0, drop_prep_loads=False, device=None, drop_linear_loads=0):
+    """Test control of the failure path of the two-kernel prefill and of
+    gdn_linear: the limit of their bounded waits (0 = the default, one second),
+    whether the prep kernel skips its K|Q loads, and which loads gdn_linear
+    skips (0 none, 1 all, 2 those behind a CTA's first block or tile).  Its waits
+    then run out and the call sets DEVSTAT_TIMEOUT; its results are undefined.
+    Synchronises the stream."""
+    _need(drop_linear_loads in (0, 1, 2), "drop_linear_loads: 0, 1 or 2")
+    _check(_lib.gdn_debug_set_wait_limit(int(limit_ns), int(bool(drop_prep_loads)) + 2 * drop_linear_loads,
                                          _stream(device)), "gdn_debug_set_wait_limit")

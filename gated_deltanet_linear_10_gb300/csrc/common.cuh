@@ -41,6 +41,9 @@ cudaError_t launch_decode_stream_beside(const __nv_bfloat16 *q, int64_t qs,
                                         const int32_t *idx, __nv_bfloat16 *o, int *ctr,
                                         cudaStream_t s);
 int sm_count();              // multiprocessors of the current device
+// linear.cu: the linear product's wait limit on the current device, and the loads
+// its calls leave out (0 none, 1 all, 2 those behind a CTA's first)
+cudaError_t set_linear_failure(uint64_t limit_ns, int drop, cudaStream_t s);
 
 // Per-TU readers of the status word (defined next to each word).
 gdn_status read_status_gating(uint32_t *out, int clear, cudaStream_t s);

@@ -7,6 +7,8 @@
 // The weights' rows are the 128 lanes of the accumulator and the tokens its
 // columns, so that a single token costs one narrow product per weight tile and
 // the tile follows the number of tokens.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "linear.cuh"
@@ -17,6 +19,15 @@ using namespace tc;
 
 GDN_DECLARE_STATUS_WORD(g_status_linear)
 GDN_STATUS_READER(read_status_linear, g_status_linear)
+
+// Test control of the failure path (gdn_debug_set_wait_limit).
+static std::atomic<int> g_linear_drop{kDropNone};
+cudaError_t set_linear_failure(uint64_t limit_ns, int drop, cudaStream_t s) {
+    g_linear_drop.store(drop, std::memory_order_relaxed);
+    const cudaError_t e = cudaMemcpyToSymbolAsync(tc::g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0,
+                                                  cudaMemcpyHostToDevice, s);
+    return e != cudaSuccess ? e : set_linear_wide_limit(limit_ns, s);
+}
 
 bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64_t rows,
                          int64_t row_stride_elems, uint32_t box_rows, bool e4m3) {
@@ -131,6 +142,10 @@ template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
 // result has one order of sums; with one, it has them all.  Then 16 threads
 // write a token's 128 channels.
 //
+// Where a wait has run out, the exchange takes place all the same, with whatever
+// there is, so that every copy has a CTA that counts it; nothing is written to y.
+// keep: k blocks of a CTA that are loaded, all of them but for tests of that path.
+//
 // What bounds it at 256 x 4096 x 2048 (8.8 us; floor 3.1): 2,000 cycles to the
 // first products, 5,500 to 6,500 of products (16 blocks, held by their copies: 256
 // lines of 128 bytes at some 1.6 cycles each; the products alone would take 256
@@ -143,7 +158,7 @@ template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
 template <int BT, bool kE4m3>
 __global__ void __launch_bounds__(kNarrowThreads)
 linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                     const __grid_constant__ LinearEpi ep, int n_in, int splits) {
+                     const __grid_constant__ LinearEpi ep, int n_in, int splits, int keep) {
     using C = NarrowCfg<BT>;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -162,6 +177,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     volatile int *abort = &abort_flag;
     const bool one = warp < 2 && elect_lane();
     auto load = [&](int i, int s) {
+        if (i >= keep) return;
         uint8_t *st = smem + s * C::kStage;
         mbar_arrive_expect_tx(&full[s], C::kStage);
         tma_load_2d(st, &mw, &full[s], (k0 + i) * kElems, n0);
@@ -197,13 +213,14 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (splits > 1) cluster_arrive_relaxed();      // waited for before the first copy to another CTA
     griddep_wait();
 
+    int issued = min(S, nk);                                 // of warp 0
     if (warp == 0) {
-        int i = S, s = 0;
+        int s = 0;
         uint32_t phase = 0;
 #pragma unroll 1
-        for (; i < nk; ++i) {
+        for (; issued < nk; ++issued) {
             if (!mbar_wait_all(&empty[s], phase, abort)) break;
-            if (one) load(i, s);
+            if (one) load(issued, s);
             __syncwarp();
             if (++s == S) {
                 s = 0;
@@ -211,8 +228,6 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
             }
         }
         griddep_launch();   // what is launched behind this kernel may set itself up
-        if (one && *abort)
-            for (int j = i - S; j < min(i, nk); ++j) mbar_drain(&full[j % S], (j / S) & 1);
     } else if (warp == 1) {
         constexpr uint32_t idesc = kE4m3 ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
@@ -296,7 +311,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     }
     __syncthreads();
     if (splits > 1) {
-        if (tid == 0 && !*abort) {
+        if (tid == 0) {
             if (cnt > 0) mbar_arrive_expect_tx(&arrived, (splits - 1) * cnt * 512);
             for (int o = 1; o < splits; ++o) {           // each starts with another one
                 const int to = (rank + o) & (splits - 1);
@@ -308,7 +323,15 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
         }
         if (cnt > 0 && !mbar_wait(&arrived, 0, abort)) mbar_drain(&arrived, 0);
         __syncwarp();
-        cluster_arrive_relaxed();                                // this CTA has what was sent to it
+        // This CTA has what was sent to it, or tells the others that it has given up: then
+        // none ends before all copies have had their time.
+        if (__any_sync(0xffffffffu, *abort)) {
+            if (warp == 0 && lane < splits) set_peer_flag(&abort_flag, lane);
+            __syncwarp();
+            cluster_arrive();
+        } else {
+            cluster_arrive_relaxed();
+        }
     }
     if (!*abort) {
 #pragma unroll 1
@@ -357,6 +380,10 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (splits > 1) cluster_wait();                      // and the others what it sent
     __syncthreads();
     tc_fence_after();
+    if (one && warp == 0 && *abort) {                    // the copies in flight land before the CTA ends
+        for (int j = max(0, issued - S); j < issued; ++j) mbar_drain(&full[j % S], (j / S) & 1);
+        if (splits > 1) let_copies_land();
+    }
     if (warp == 1) tmem_dealloc(tmem_base, BT);
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
@@ -408,7 +435,8 @@ static gdn_status launch_narrow(const LinearCall &c, const NarrowPlan &plan) {
         return GDN_ERR_CUDA;
     const cudaError_t e = launch_after_cluster(linear_narrow_kernel<BT, kE4m3>, plan.splits,
                                                dim3(plan.nn * plan.splits, plan.nt), dim3(kNarrowThreads),
-                                               C::kSmem, c.stream, mx, mw, c.e, c.n_in, plan.splits);
+                                               C::kSmem, c.stream, mx, mw, c.e, c.n_in, plan.splits,
+                                               c.drop == kDropNone ? INT_MAX : c.drop & kDropAll ? 0 : 1);
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return GDN_ERR_LAUNCH;
@@ -483,6 +511,7 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     c.n_in = n_in;
     c.e4m3 = dtype == GDN_E4M3;
     c.stream = (cudaStream_t)stream;
+    c.drop = g_linear_drop.load(std::memory_order_relaxed);
     c.e = {x_scale, w_scale, bias, residual, residual_row_stride, y, y_row_stride,
            (int)n_tokens, n_out, act, y_dtype == GDN_F32, false};
     // 8 channels at a time: 16 bytes of bf16, 32 of fp32

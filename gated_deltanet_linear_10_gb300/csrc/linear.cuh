@@ -115,6 +115,10 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// Sets an int of this name in CTA `rank`'s shared memory.
+__device__ __forceinline__ void set_peer_flag(int *flag, uint32_t rank) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_smem(tc::smem_u32(flag), rank)), "r"(1) : "memory");
+}
 // True in one lane of the (whole, converged) warp.  The warp that issues the
 // products stays converged and issues them under this predicate: from a branch
 // that one lane took alone (lane == 0) the same loop issued 155 cycles a
@@ -135,6 +139,14 @@ __device__ __forceinline__ bool mbar_wait_all(uint64_t *bar, uint32_t parity, vo
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
     volatile int give_up = 0;
     tc::mbar_wait(bar, parity, &give_up);
+}
+
+// A cluster that has given up, once all of its CTAs have sent what they send: far
+// longer than a copy takes.
+__device__ __forceinline__ void let_copies_land() {
+    const uint64_t t = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t < 10000000ull) {
+    }
 }
 
 // mbar_wait for a whole warp that has time: one lane looks, and sleeps between looks.
@@ -242,6 +254,11 @@ inline cudaError_t launch_after_cluster(void (*kernel)(KArgs...), int cluster, d
     return cudaLaunchKernelEx(&l.cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Test control of the failure path: loads that a call does not issue, so that its
+// waits for them run out.  Behind the first: all but a pair's first tile, or a narrow
+// CTA's first block.
+enum LinearDrop { kDropNone = 0, kDropAll = 1, kDropBehindFirst = 2 };   // 3: as all
+
 struct LinearCall {
     const void *x, *w;
     int64_t xs, ws;
@@ -249,6 +266,7 @@ struct LinearCall {
     bool e4m3;
     LinearEpi e;
     cudaStream_t stream;
+    int drop;       // the failure path's test control (LinearDrop), 0 otherwise
     // whether 128 bytes of a row of x and w are one line of memory, and not parts of two
     bool lines() const {
         const int64_t elem = e4m3 ? 1 : 2;
@@ -268,6 +286,7 @@ struct WidePlan {
 // linear_wide.cu: the product on CTA pairs; its plan, with the cycles of an SM that
 // it takes by estimate (INT64_MAX: not built), and its launch.
 int64_t plan_linear_wide(const LinearCall &c, WidePlan &plan);
+cudaError_t set_linear_wide_limit(uint64_t limit_ns, cudaStream_t s);
 gdn_status launch_linear_wide(const LinearCall &c, const WidePlan &plan);
 
 }  // namespace gdn

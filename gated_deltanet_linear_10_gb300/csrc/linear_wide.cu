@@ -22,6 +22,8 @@
 // residual comes straight from memory, whole sectors of 32 bytes.  Stores from
 // registers instead of staging rows were 4 % slower.  Rows off 16-byte boundaries
 // are turned in shared memory, so that a warp's lanes access neighbours.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "linear.cuh"
@@ -32,6 +34,10 @@ using namespace tc;
 
 GDN_DECLARE_STATUS_WORD(g_status_linear_wide)
 GDN_STATUS_READER(read_status_linear_wide, g_status_linear_wide)
+
+cudaError_t set_linear_wide_limit(uint64_t limit_ns, cudaStream_t s) {
+    return cudaMemcpyToSymbolAsync(tc::g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0, cudaMemcpyHostToDevice, s);
+}
 
 namespace {
 
@@ -322,7 +328,7 @@ template <bool kE4m3, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                    const __grid_constant__ CUtensorMap mw_tail, const __grid_constant__ CUtensorMap my,
-                   const __grid_constant__ LinearEpi ep, int n_in, WidePlan plan, int rows) {
+                   const __grid_constant__ LinearEpi ep, int n_in, WidePlan plan, int rows, int keep) {
     constexpr int S = kStagesWide;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
@@ -388,7 +394,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     ok = false;
                     break;
                 }
-                if (one) {
+                if (one && i < keep) {
                     uint8_t *st = smem + s * kStageBytes;
                     const uint32_t bar = lead + s * 8;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
@@ -412,9 +418,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             if (rank == 0) {
                 for (int j = i > S ? i - S : 0; j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1);
             } else {
-                const uint64_t t = globaltimer_ns();
-                while (globaltimer_ns() - t < 10000000ull) {
-                }
+                let_copies_land();
             }
         }
     } else if (warp == 1 && rank == 0) {
@@ -526,6 +530,9 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         walk.start(plan, pair);
         ahead(cur);
         if (ep.res && start < cur.width) ask(cur, start);
+        // A warp that has given up walks the tiles that are left without work: the others
+        // may have seen this tile's sums and wait for it at the barriers of the next.
+        bool gone = false;
         for (int u = 0; cur.width > 0; ++u, cur = nxt) {
             const int b = u & 1, t0 = cur.t0, n0 = cur.n0, width = cur.width;
             const float sx = cur.sx;
@@ -537,7 +544,8 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
             walk.next(plan, pairs);
             ahead(nxt);
-            if (!mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort)) break;
+            gone = gone || !mbar_wait_warp(&acc_full[b], (u >> 1) & 1, abort);
+            if (gone) continue;
             tc_fence_after();
 #pragma unroll 1
             for (int c = start, part = 0; c < width;) {
@@ -688,12 +696,13 @@ template <bool kE4m3, typename O> gdn_status launch_wide(const LinearCall &c, co
         !encode_tmap_2d(&my, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.y,
                         e.n_out, e.n_tokens, e.ys * sizeof(O), 128 / sizeof(O), 32, true))
         return GDN_ERR_CUDA;
+    const int keep = c.drop == kDropNone ? INT_MAX : c.drop & kDropAll ? 0 : (c.n_in + (kE4m3 ? 127 : 63)) / (kE4m3 ? 128 : 64);
     auto kernel = linear_wide_kernel<kE4m3, O>;
     static SmemAllowed allowed;
     cudaError_t err = allowed.ask(kernel, kWideSmem);
     if (err == cudaSuccess)
         err = launch_after(kernel, dim3(std::min(2 * plan.n_tiles, sms)), dim3(kWideThreads), kWideSmem,
-                           c.stream, mx, mw, mt, my, e, c.n_in, plan, rows);
+                           c.stream, mx, mw, mt, my, e, c.n_in, plan, rows, keep);
     if (err != cudaSuccess) {
         set_last_cuda_error(err);
         return GDN_ERR_LAUNCH;

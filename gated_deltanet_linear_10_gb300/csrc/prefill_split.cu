@@ -1094,18 +1094,20 @@ gdn_status prefill_scan(const void *q, int64_t qs, const void *k, int64_t ks, co
 
 using namespace gdn;
 
-// Test control of the failure path of the two-kernel prefill: the wait limit
-// of its kernels and the prep kernel's K|Q loads (see gdn.h).
-extern "C" gdn_status gdn_debug_set_wait_limit(uint64_t limit_ns, int32_t drop_prep_loads,
+// Test control of the failure path of the two-kernel prefill and the linear
+// product: the wait limit of their kernels and the loads they leave out (see gdn.h).
+extern "C" gdn_status gdn_debug_set_wait_limit(uint64_t limit_ns, int32_t drop_loads,
                                                void *stream) {
+    GDN_REQUIRE((drop_loads & ~7) == 0, GDN_ERR_INVALID_ARG);
     const uint64_t lim = limit_ns ? limit_ns : tc::kWaitLimitNs;
-    const int drop = drop_prep_loads != 0;
+    const int drop = drop_loads & 1;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = cudaMemcpyToSymbolAsync(tc::g_wait_limit_ns, &lim, sizeof(lim), 0,
                                             cudaMemcpyHostToDevice, s);
     if (e == cudaSuccess)
         e = cudaMemcpyToSymbolAsync(g_prep_drop_loads, &drop, sizeof(drop), 0,
                                     cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = set_linear_failure(lim, drop_loads >> 1, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);   // the sources live on this stack
     if (e != cudaSuccess) {
         set_last_cuda_error(e);

@@ -20,8 +20,9 @@ namespace tc {
 
 // A bounded wait gives up after this long and reports a timeout.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;   // 1 s
-// The limit in force: one copy per translation unit (a debug entry point
-// may shorten it for the two-kernel prefill; kWaitLimitNs otherwise).
+// The limit in force: one copy per translation unit (a debug entry point may
+// shorten it for the two-kernel prefill and the linear product; kWaitLimitNs
+// otherwise).
 static __device__ uint64_t g_wait_limit_ns = kWaitLimitNs;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

@@ -657,16 +657,20 @@ gdn_status gdn_state_snapshot(void *pool, int64_t n_slots, int64_t slot_bytes,
 /*
  * Test control of the failure path (not for production use).  Sets the limit
  * of every bounded wait inside the two-kernel tensor-core prefill (the prep
- * and chain kernels of gdn_prefill_chunked with a workspace) to limit_ns
- * nanoseconds on the current device; 0 restores the default of one second.
- * With drop_prep_loads != 0 the prep kernel issues none of its K|Q tile
- * loads, so the waits for them run out after the limit: the kernel then
- * skips its stores, drains, frees its tensor memory, returns and sets
- * GDN_DEVSTAT_TIMEOUT, and the results of that call are undefined (every
- * index stays in bounds; the context stays usable).  Synchronises `stream`.
- * Restore both (0, 0) before production calls.
+ * and chain kernels of gdn_prefill_chunked with a workspace) and inside
+ * gdn_linear's kernels to limit_ns nanoseconds on the current device; 0
+ * restores the default of one second.  drop_loads: a sum of
+ *   1  the prep kernel issues none of its K|Q tile loads,
+ *   2  gdn_linear's calls (of the process) issue no loads of x and w,
+ *   4  ... none behind the first k block (few tokens) or the first tile of a
+ *      pair of CTAs (many tokens),
+ * so that the waits for them run out after the limit: the kernel then skips
+ * its stores (of what did not come), drains, frees its tensor memory, returns
+ * and sets GDN_DEVSTAT_TIMEOUT, and the results of that call are undefined
+ * (every index stays in bounds; the context stays usable).  Synchronises
+ * `stream`.  Restore both (0, 0) before production calls.
  */
-gdn_status gdn_debug_set_wait_limit(uint64_t limit_ns, int32_t drop_prep_loads,
+gdn_status gdn_debug_set_wait_limit(uint64_t limit_ns, int32_t drop_loads,
                                     void *stream);
 
 /*
