@@ -469,8 +469,6 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             mma_commit_pair(&drained);    // every product issued is done before the pair ends
             mbar_drain(&drained, 0);
         }
-    } else if (warp == 1) {
-        if (elect_lane()) mbar_drain(&drained, 0);
     } else if (warp >= 4) {
         // Accumulator lane 32 q + l is token row 32 q + l of this CTA's half; the
         // two warps of a quadrant take alternate slices of 128 bytes of y.
@@ -626,6 +624,12 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         tc_fence_before();
     }
     __syncthreads();
+    // The leader's products are done, as this CTA has been told: looked at only now,
+    // since the limit of a wait runs from where it begins and a call may take longer.
+    if (warp == 1 && rank == 1) {
+        if (elect_lane()) mbar_drain(&drained, 0);
+        __syncwarp();
+    }
     // Neither CTA ends while the other may reach its memory: every arrival from the
     // other one has been waited for above, so nothing is handed over here, unless the
     // pair has given up.  (With release a CTA waited for its stores to y first, some
@@ -634,6 +638,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     else cluster_arrive_relaxed();
     cluster_wait();
     tc_fence_after();
+    if (tid == 0 && *abort) let_copies_land();   // arrivals that were not waited for
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(2 * kChTile)

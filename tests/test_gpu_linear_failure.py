@@ -64,3 +64,19 @@ def test_two_kernel_limit_leaves_the_product_alone():
         gdn().gdn_debug_set_wait_limit(0)
     assert torch.all(y == 64)
     status_clean()
+
+
+def test_a_call_may_take_longer_than_the_limit():
+    """The limit is one of each wait: a call of some 400 us at 100 us ends as usual."""
+    T, K, N = 20000, 2048, 8192
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, w = (torch.randn(n, K, generator=g, device=DEV).to(BF16) for n in (T, N))
+    want = gdn().gdn_linear(x, w)
+    gdn().gdn_debug_set_wait_limit(100_000)
+    try:
+        y = gdn().gdn_linear(x, w)
+        torch.cuda.synchronize()
+        status_clean()
+    finally:
+        gdn().gdn_debug_set_wait_limit(0)
+    assert torch.equal(y.view(torch.int16), want.view(torch.int16))
