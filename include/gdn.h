@@ -484,7 +484,8 @@ gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *resi
  * The result of a row does not depend on the other rows or on the call's
  * timing; it may differ in the last fp32 bits between numbers of tokens (the
  * order of the sum over k follows the tile that the sizes choose).
- * Built: GDN_BF16 and GDN_E4M3 operands; n_tokens <= 16,776,960.
+ * Built: GDN_BF16 and GDN_E4M3 operands; n_tokens <= 16,776,960, n_in <= 2^24,
+ * n_out <= 2^30, row strides < 2^36.
  */
 gdn_status gdn_linear(const void *x, int64_t x_row_stride, const float *x_scale,
                       const void *w, int64_t w_row_stride, const float *w_scale,

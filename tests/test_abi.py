@@ -384,3 +384,12 @@ def test_block_binding_refuses_before_the_library():
         gdn.gdn_linear(x, x)
     with pytest.raises(gdn.GdnError, match="CUDA"):
         gdn.gdn_gated_rmsnorm_quant(x.view(2, 2, 32), x.view(2, 2, 32), torch.ones(32))
+
+
+def test_linear_sizes_past_what_is_built(lib):
+    """n_in past 2^24: a tile's sum could take longer than the waits for it allow."""
+    f = lib.gdn_linear
+    f.argtypes = [V, I64, V, V, I64, V, V, V, I64, I64, I32, I32, I32, V, I64, I32, I32, V]
+    A, K = 1 << 20, (1 << 24) + 8
+    assert f(A, K, None, 2 * A, K, None, None, None, 0, 4, K, 96, 0, 3 * A, 96, 1, 1, None) == 2
+    assert f(A, 1 << 30, None, 2 * A, 1 << 30, None, None, None, 0, 300, 1 << 30, 96, 0, 3 * A, 96, 1, 1, None) == 2
