@@ -303,25 +303,28 @@ __device__ __forceinline__ void wide_values(uint32_t (&r)[32], const float *cols
     }
 }
 
-// One of them: act(v scale + bias).
-__device__ __forceinline__ uint32_t wide_value(uint32_t v, int act, float scale, float bias) {
-    const float f = fmaf(__uint_as_float(v), scale, bias);
-    F2 p = f2(f, f);
-    if (act == GDN_ACT_SILU) p = linear_act<GDN_ACT_SILU>(p);
-    else if (act == GDN_ACT_GELU) p = linear_act<GDN_ACT_GELU>(p);
-    return __float_as_uint(f2_get(p).x);
+// The second of a pair of them, from both: the activations share a reciprocal, so a
+// channel's last bits depend on the one that it is paired with.
+__device__ __forceinline__ uint32_t wide_second(F2 v, int act, const float *cols, bool has_cols, float sx) {
+    const F2 sx2 = f2(sx, sx);
+    if (has_cols)
+        v = f2_fma(v, f2_mul(sx2, *reinterpret_cast<const F2 *>(cols)), *reinterpret_cast<const F2 *>(cols + kChTile));
+    else v = f2_mul(v, sx2);
+    if (act == GDN_ACT_SILU) v = linear_act<GDN_ACT_SILU>(v);
+    else if (act == GDN_ACT_GELU) v = linear_act<GDN_ACT_GELU>(v);
+    return __float_as_uint(f2_get(v).y);
 }
 
-// One column of 32 lanes of tensor memory.
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
-    uint32_t r;
+// Two columns of 32 lanes of tensor memory.
+__device__ __forceinline__ F2 tmem_ld2(uint32_t taddr) {
+    uint32_t a, b;
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r)
+        : "=r"(a), "=r"(b)
         : "r"(taddr)
         : "memory");
-    return r;
+    return f2_bits(a, b);
 }
 
 template <bool kE4m3, typename O>
@@ -551,10 +554,9 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 const int next_c = part + 1 < PARTS && c + 32 < width ? c + 32 : c - part * 32 + STEP;
                 uint32_t r[32], before = 0;
                 tmem_ld32(tmem_addr(tmem_base, q * 32, b * kChTile + c), r);
-                if (rows == kRowsOdd && c > 0) {
-                    before = tmem_ld1(tmem_addr(tmem_base, q * 32, b * kChTile + c - 1));
-                    before = wide_value(before, ep.act, has_cols ? cols[c - 1] * sx : sx, has_cols ? cols[kChTile + c - 1] : 0.0f);
-                }
+                if (rows == kRowsOdd && c > 0)
+                    before = wide_second(tmem_ld2(tmem_addr(tmem_base, q * 32, b * kChTile + c - 2)), ep.act,
+                                         cols + c - 2, has_cols, sx);
                 if (ep.act == GDN_ACT_SILU) wide_values<GDN_ACT_SILU, true>(r, cols + c, sx);
                 else if (ep.act == GDN_ACT_GELU) wide_values<GDN_ACT_GELU, true>(r, cols + c, sx);
                 else if (has_cols) wide_values<GDN_ACT_NONE, true>(r, cols + c, sx);
