@@ -476,7 +476,9 @@ gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *resi
  *      elements and multiples of 16 bytes (of any size >= n_in: n_in itself
  *      may be odd).  What lies between n_in and the stride is not read.
  *   x_scale [n_tokens], w_scale [n_out]: fp32, NULL = 1.
- *   bias: [n_out] fp32 or NULL.  act: gdn_act.
+ *   bias: [n_out] fp32 or NULL.  act: gdn_act, to a relative error of
+ *      2^-19 (1 + v^2 / 16) of act(v), v the fp32 sum; SiLU stays at its value at
+ *      -43.6 (-5e-18) below that, GELU is 0 below -13.1.
  *   residual: rows of n_out elements in y_dtype, or NULL.
  *   y: rows of n_out elements, GDN_BF16 or GDN_F32, row stride y_row_stride
  *      (>= n_out: y may be columns of a wider buffer).  y may be residual

@@ -1,6 +1,6 @@
 """The activations of gdn_linear alone, on products of zero, so that act(bias) is
-what is rounded: the same bits for a token in any row, whichever channels share a
-word with it."""
+what is rounded: their error over the whole range against 64 bits, and the same
+bits for a token in any row, whichever channels share a word with it."""
 import pytest
 import torch
 
@@ -22,6 +22,24 @@ def _of_bias(T, b, act, out):
     torch.cuda.synchronize()
     status_clean()
     return y
+
+
+# |act(v)| is kept to 2^-19 (1 + v^2 / 16) of itself.  The power of two takes an
+# argument of |v| log2(e) (SiLU) or v^2 log2(e) / 2 (GELU), rounded twice: 2^-23 of
+# it times ln 2, 6e-8 v^2 for GELU; the instruction's own 2^-22 of the result.  The
+# shared reciprocal: 5 half steps (2^-24), doubled by GELU's polynomial in it (slope
+# at most 1.95); its fit 2.7e-7, 8 steps of Horner's rule 2e-7, 3 more products.
+# 1.5e-6 + 6e-8 v^2 in all.
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [3, 100, 2100])
+def test_error_over_the_range(T, act, out):
+    b = torch.cat([torch.linspace(-12.5, 12.5, 6001), torch.linspace(-1, 1, 2003), torch.tensor([1e-30, -1e-30, 0.0])]).to(DEV)
+    y = _of_bias(T, b, act, out).double()
+    ref = _act(b.double(), act)
+    tol = ref.abs() * (2.0 ** -19 * (1 + b.double() ** 2 / 16) + (2.0 ** -8 if out == BF16 else 0.0)) + 1e-37
+    bad = ~((y - ref).abs() <= tol)
+    assert not bad.any(), f"{int(bad.sum())} off, first at bias {float(b[bad.nonzero()[0][1]])}"
 
 
 def _before(act, mid):
