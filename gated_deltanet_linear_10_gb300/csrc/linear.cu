@@ -174,10 +174,10 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     const int blocks = (n_in + kElems - 1) / kElems;
     const int k0 = (int)((int64_t)blocks * rank / splits);
     const int nk = (int)((int64_t)blocks * (rank + 1) / splits) - k0;
+    const int nload = min(nk, keep);
     volatile int *abort = &abort_flag;
     const bool one = warp < 2 && elect_lane();
     auto load = [&](int i, int s) {
-        if (i >= keep) return;
         uint8_t *st = smem + s * C::kStage;
         mbar_arrive_expect_tx(&full[s], C::kStage);
         tma_load_2d(st, &mw, &full[s], (k0 + i) * kElems, n0);
@@ -198,7 +198,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
             fence_mbar_init();
             fence_async_smem();
             griddep_wait();   // launched behind the kernel that writes x: nothing is read before it
-            for (int i = 0; i < min(S, nk); ++i) load(i, i);
+            for (int i = 0; i < min(S, nload); ++i) load(i, i);
         }
         __syncwarp();
     }
@@ -213,12 +213,12 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (splits > 1) cluster_arrive_relaxed();      // waited for before the first copy to another CTA
     griddep_wait();
 
-    int issued = min(S, nk);                                 // of warp 0
+    int issued = min(S, nload);                              // of warp 0
     if (warp == 0) {
         int s = 0;
         uint32_t phase = 0;
 #pragma unroll 1
-        for (; issued < nk; ++issued) {
+        for (; issued < nload; ++issued) {
             if (!mbar_wait_all(&empty[s], phase, abort)) break;
             if (one) load(issued, s);
             __syncwarp();
@@ -322,16 +322,14 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
             }
         }
         if (cnt > 0 && !mbar_wait(&arrived, 0, abort)) mbar_drain(&arrived, 0);
-        __syncwarp();
         // This CTA has what was sent to it, or tells the others that it has given up: then
         // none ends before all copies have had their time.
-        if (__any_sync(0xffffffffu, *abort)) {
-            if (warp == 0 && lane < splits) set_peer_flag(&abort_flag, lane);
-            __syncwarp();
-            cluster_arrive();
-        } else {
-            cluster_arrive_relaxed();
+        if (tid == 0 && *abort) {
+            for (int o = 0; o < splits; ++o) set_peer_flag(&abort_flag, o);
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
+        __syncwarp();
+        cluster_arrive_relaxed();
     }
     if (!*abort) {
 #pragma unroll 1
@@ -380,12 +378,13 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_consta
     if (splits > 1) cluster_wait();                      // and the others what it sent
     __syncthreads();
     tc_fence_after();
-    if (one && warp == 0 && *abort) {                    // the copies in flight land before the CTA ends
+    if (warp == 1) tmem_dealloc(tmem_base, BT);
+    if (tid == 0 && abort_flag) {
+        flag_status(GDN_DEVSTAT_TIMEOUT);
+        // the copies in flight land before the CTA ends
         for (int j = max(0, issued - S); j < issued; ++j) mbar_drain(&full[j % S], (j / S) & 1);
         if (splits > 1) let_copies_land();
     }
-    if (warp == 1) tmem_dealloc(tmem_base, BT);
-    if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
 // How a product of these sizes is cut over narrow tiles, and what that takes in

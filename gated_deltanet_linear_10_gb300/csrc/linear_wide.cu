@@ -385,6 +385,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         bool ok = true;
         WideWalk walk;
         for (walk.start(plan, pair); walk.more(plan) && ok; walk.next(plan, pairs)) {
+            const bool go = one && i < keep;   // all tiles' loads, but for tests of the failure path
             int t0, n0, box, width;
             walk.at(plan, ep.n_out, t0, n0, box, width);
             const CUtensorMap *map = box == kChTile ? &mw : &mw_tail;
@@ -397,7 +398,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     ok = false;
                     break;
                 }
-                if (one && i < keep) {
+                if (go) {
                     uint8_t *st = smem + s * kStageBytes;
                     const uint32_t bar = lead + s * 8;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
@@ -640,12 +641,14 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     else cluster_arrive_relaxed();
     cluster_wait();
     tc_fence_after();
-    if (tid == 0 && *abort) let_copies_land();   // arrivals that were not waited for
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(2 * kChTile)
                      : "memory");
-    if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
+    if (tid == 0 && abort_flag) {
+        flag_status(GDN_DEVSTAT_TIMEOUT);
+        let_copies_land();     // arrivals that were not waited for
+    }
 }
 
 // The plan with the shortest estimate, and that in cycles of a k block.  A block
