@@ -58,13 +58,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs once the products issued
-// so far by this thread are done.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+// Arrives on the barrier at this offset in the CTAs of the mask (1: the leader, 3: both)
+// once the products issued so far by this thread are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint16_t mask = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
 }
 template <bool kE4m3>
@@ -470,7 +470,7 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             __syncwarp();
         }
         if (one) {
-            mma_commit_pair(&drained);    // every product issued is done before the pair ends
+            mma_commit_pair(&drained, 1);     // every product issued is done before the leader lets the pair end
             mbar_drain(&drained, 0);
         }
     } else if (warp >= 4) {
@@ -627,12 +627,6 @@ linear_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         tc_fence_before();
     }
     __syncthreads();
-    // The leader's products are done, as this CTA has been told: looked at only now,
-    // since the limit of a wait runs from where it begins and a call may take longer.
-    if (warp == 1 && rank == 1) {
-        if (elect_lane()) mbar_drain(&drained, 0);
-        __syncwarp();
-    }
     // Neither CTA ends while the other may reach its memory: every arrival from the
     // other one has been waited for above, so nothing is handed over here, unless the
     // pair has given up.  (With release a CTA waited for its stores to y first, some
