@@ -257,6 +257,15 @@ extern "C" gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const
                     (uintptr_t)residual_out % elem == 0 && (uintptr_t)y % yelem == 0 &&
                     (uintptr_t)weight % 4 == 0 && (uintptr_t)y_scale % 4 == 0,
                 GDN_ERR_INVALID_ARG);
+    // in place a row lies on the one it is made from: another row's CTA would overwrite it
+    auto own_row = [&](const void *out, int64_t out_bytes, const void *in, int64_t in_bytes) {
+        return out != in || !in || n_tokens == 1 || out_bytes == in_bytes;
+    };
+    const int64_t yb = y_row_stride * (int64_t)yelem, rob = residual_out_row_stride * (int64_t)elem;
+    const int64_t xb = x_row_stride * (int64_t)elem, rb = residual_row_stride * (int64_t)elem;
+    GDN_REQUIRE(own_row(y, yb, x, xb) && own_row(y, yb, residual, rb) && own_row(residual_out, rob, x, xb) &&
+                    own_row(residual_out, rob, residual, rb),
+                GDN_ERR_INVALID_ARG);
     // 16-byte vectors of the stream (and the y elements that belong to one)
     const uint64_t n = 16 / elem;
     const uint64_t first = (uintptr_t)x / elem % n, step = (uint64_t)x_row_stride % n;

@@ -148,7 +148,7 @@ extern "C" gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int6
     // a token plus the grid stays within 32 bits
     GDN_REQUIRE((int64_t)hv * dv <= kGatedMaxRow && n_tokens < (1ll << 31) - (1 << 20), GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
-    GDN_REQUIRE(o && z && weight && y && y_scale, GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(o && z && weight && y && y_scale && y != o && y != z, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(z_row_stride >= (int64_t)hv * dv, GDN_ERR_INVALID_ARG);
     const uintptr_t elem = dtype == GDN_F32 ? 4 : 2;
     GDN_REQUIRE((uintptr_t)o % (4 * elem) == 0 && (uintptr_t)z % (4 * elem) == 0 &&

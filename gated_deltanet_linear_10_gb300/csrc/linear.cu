@@ -491,6 +491,7 @@ extern "C" gdn_status gdn_linear(const void *x, int64_t x_row_stride, const floa
     GDN_REQUIRE(x_row_stride >= n_in && w_row_stride >= n_in && y_row_stride >= n_out &&
                     (!residual || residual_row_stride >= n_out),
                 GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(y != residual || n_tokens == 1 || y_row_stride == residual_row_stride, GDN_ERR_INVALID_ARG);
     // the operands' rows start on 16-byte boundaries (TMA); a single row has no stride
     const int64_t per = dtype == GDN_E4M3 ? 16 : 8;
     GDN_REQUIRE((uintptr_t)x % 16 == 0 && (uintptr_t)w % 16 == 0 &&

@@ -422,8 +422,8 @@ gdn_status gdn_gated_rmsnorm(const void *o, const void *z, int64_t z_row_stride,
  * A token with a NaN gets a NaN scale and NaN values; one of zeros gets zeros.
  *   o, z, weight, eps: as gdn_gated_rmsnorm (o and z aligned to 4 elements,
  *      z_row_stride a multiple of 4), in `dtype`.
- *   y: [n_tokens][hv][dv] e4m3, contiguous, 8-byte aligned; y_scale:
- *      [n_tokens] fp32.
+ *   y: [n_tokens][hv][dv] e4m3, contiguous, 8-byte aligned, not over o or z;
+ *      y_scale: [n_tokens] fp32.
  * Built: dv in {16, 32, 64, 128, 256}, hv * dv <= 16384; n_tokens < 2^31 - 2^20.
  */
 gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_stride,
@@ -448,7 +448,8 @@ gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_s
  *   weight: [hidden] fp32; weight_offset: 0, or 1 for the (1 + w) form.
  *   y: rows of `hidden` elements in y_dtype (`dtype` or GDN_E4M3), row stride
  *      y_row_stride; y may be x or residual (same pointer and stride) when
- *      y_dtype == dtype.  y_scale: [n_tokens] fp32 with GDN_E4M3, else NULL.
+ *      y_dtype == dtype.  The same pointer with another stride (in bytes) is
+ *      refused.  y_scale: [n_tokens] fp32 with GDN_E4M3, else NULL.
  * y and residual_out must not overlap each other.  Any alignment of whole
  * elements is taken; where the rows of x, residual, residual_out and y start
  * alike within 16 bytes (of x's elements), packed ones of an odd width too,

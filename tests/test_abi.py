@@ -393,3 +393,23 @@ def test_linear_sizes_past_what_is_built(lib):
     A, K = 1 << 20, (1 << 24) + 8
     assert f(A, K, None, 2 * A, K, None, None, None, 0, 4, K, 96, 0, 3 * A, 96, 1, 1, None) == 2
     assert f(A, 1 << 30, None, 2 * A, 1 << 30, None, None, None, 0, 300, 1 << 30, 96, 0, 3 * A, 96, 1, 1, None) == 2
+
+
+def test_block_operators_refuse_rows_laid_over_others(lib):
+    """In place a row lies on the one it is made from.  The same buffer with another row
+    stride, or with rows of other bytes, would be overwritten before it is read."""
+    A = 1 << 20
+    f = lib.gdn_add_rmsnorm
+    f.argtypes = [V, I64, V, I64, V, F32, I64, I32, F32, V, I64, V, I64, V, I32, I32, V]
+    norm = lambda y, ys, sc, ydt, x=A, xs=64, r=2 * A, rs=64, ro=3 * A, ros=64: f(  # noqa: E731
+        x, xs, r, rs, A // 2, 0.0, 4, 64, 1e-6, ro, ros, y, ys, sc, 1, ydt, None)
+    assert norm(A, 64, A // 4, 2) == 1 and norm(2 * A, 64, A // 4, 2) == 1     # e4m3 on x, on the residual
+    assert norm(A, 72, None, 1) == 1 and norm(2 * A, 72, None, 1) == 1         # another stride
+    assert norm(4 * A, 64, None, 1, ro=A, ros=80) == 1 and norm(4 * A, 64, None, 1, ro=2 * A, ros=80) == 1
+    g = lib.gdn_gated_rmsnorm_quant
+    g.argtypes = [V, V, I64, V, I64, I32, I32, F32, V, V, I32, V]
+    assert g(A, 2 * A, 512, A // 2, 4, 4, 128, 1e-6, A, A // 4, 1, None) == 1
+    assert g(A, 2 * A, 512, A // 2, 4, 4, 128, 1e-6, 2 * A, A // 4, 1, None) == 1
+    h = lib.gdn_linear
+    h.argtypes = [V, I64, V, V, I64, V, V, V, I64, I64, I32, I32, I32, V, I64, I32, I32, V]
+    assert h(A, 64, None, 2 * A, 64, None, None, 3 * A, 104, 4, 64, 96, 0, 3 * A, 96, 1, 1, None) == 1
