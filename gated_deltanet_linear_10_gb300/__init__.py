@@ -695,7 +695,11 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-6, y=None):
 # call), so their checks are written out and messages formed only on failure.
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _CODES = {_F32: GDN_F32, _BF16: GDN_BF16, _E4M3: GDN_E4M3}
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# torch's own short forms of its public calls, where it has them (torch.cuda.current_stream
+# makes a stream object, a microsecond a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _one_device(first, *ts):

@@ -413,3 +413,14 @@ def test_block_operators_refuse_rows_laid_over_others(lib):
     h = lib.gdn_linear
     h.argtypes = [V, I64, V, V, I64, V, V, V, I64, I64, I32, I32, I32, V, I64, I32, I32, V]
     assert h(A, 64, None, 2 * A, 64, None, None, 3 * A, 104, 4, 64, 96, 0, 3 * A, 96, 1, 1, None) == 1
+
+
+@pytest.mark.parametrize("missing", ["_cuda_getDevice", "_cuda_getCurrentRawStream"])
+def test_the_package_needs_no_private_call_of_torch(lib, missing):
+    """Builds of torch without a device or of another version may lack them."""
+    import subprocess
+    import sys
+    code = (f"import torch; del torch._C.{missing}; import gated_deltanet_linear_10_gb300 as g; "
+            "assert callable(g._current_device) and callable(g._raw_stream); print(g.version())")
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert res.returncode == 0 and "sm_103a" in res.stdout, res.stderr
