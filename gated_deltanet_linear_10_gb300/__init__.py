@@ -810,7 +810,7 @@ def gdn_gated_rmsnorm_quant(o, z, weight, eps=1e-6, y=None, y_scale=None):
         raise GdnError("z: o's dtype")
     if z.shape == shape:
         zs, head, one = z.stride()
-        if one != 1 or head != dv:
+        if one != 1 or (head != dv and hv != 1):
             raise GdnError("z: heads must be packed")
         if zs < hv * dv:
             if T > 1:
