@@ -146,12 +146,13 @@ template <int kAct> __device__ __forceinline__ void narrow_act(F2 (&v)[2][4]) {
 // there is, so that every copy has a CTA that counts it; nothing is written to y.
 // keep: k blocks of a CTA that are loaded, all of them but for tests of that path.
 //
-// What bounds it at 256 x 4096 x 2048 (8.8 us; floor 3.1): 2,000 cycles to the
+// What bounds it at 256 x 4096 x 2048 (8.8 us with the weights in L2, 10.2 with weights
+// from HBM; at the memory's rate 3.1): 2,000 cycles to the
 // first products, 5,500 to 6,500 of products (16 blocks, held by their copies: 256
 // lines of 128 bytes at some 1.6 cycles each; the products alone would take 256
 // cycles a block), 3,200 of exchange (48 KB a CTA, 1,500 of it latency), 3,500 to
-// write the sums and the output.  One token (1 x 2048 x 8192, 6.9 us; floor 4.9)
-// waits for the weights.
+// write the sums and the output.  One token (1 x 2048 x 8192, 6.9 to 7.2 us, from HBM
+// 8.6; 4.9) waits for the weights.
 // The code behind the products runs once per CTA, so it is kept short and
 // rolled: unrolled over 32 tokens with its variants it took 3 to 20 us of
 // instruction fetches and dependent loads at 256 tokens.
@@ -394,7 +395,7 @@ struct NarrowPlan {
     int64_t cycles;
 };
 
-// Fitted to 1 to 2000 tokens on products of 256 x 2048 to 8192 x 1024, with k in one,
+// Fitted, with the weights in L2, to 1 to 2000 tokens on products of 256 x 2048 to 8192 x 1024, with k in one,
 // two, four and eight, bf16 and e4m3: what this estimate picks takes 0.5 % longer
 // than the best of them in the mean, and 7 % at the worst (on sizes it was not fitted
 // to, 17 % in one of 264).  A k block of 128 tokens takes 425 cycles, its copies from

@@ -47,7 +47,9 @@ __device__ __forceinline__ F2 silu_short(float a, float b) {
 // Chebyshev points; p = 0.58 gives the least, 2.7e-7), so that the small values below
 // zero keep their digits too: with the roundings the result's relative error is at
 // most 2^-19 (1 + v^2 / 16).  The handbook's own five terms hold an absolute 1.5e-7,
-// 4e-3 of GELU(-6).  Values below 2^-126 become 0 (v < -13.1).
+// 4e-3 of GELU(-6), and take 2 to 3 % less time where the epilogue bounds a call (14261 x
+// 692 x 909 e4m3: 35.9 us, with these eight 36.9; 20668 x 2048 x 8192: the same).
+// Values below 2^-126 become 0 (v < -13.1).
 __device__ __forceinline__ F2 gelu_short(float a, float b) {
     constexpr float kP = 0.58f * 0.70710678118f, kMost = 9.2e18f;
     constexpr float kC[8] = {0.163665797f, 0.162445677f, 0.14720637f, 0.0243334345f,

@@ -10,8 +10,9 @@
 // What bounds it from n_in = 1024 on is the tensor cores' rate and then the
 // power: 256 x 256 x 16 take a pair 128 cycles.  20668 x 2048 x 8192 bf16 is
 // 574,000 cycles of them and takes some 590,000, at 1.5 GHz (1.9 without the load):
-// 353 to 363 us, 1,950 TFLOP/s; over seconds some 425 us.  20668 x 4096 x 2048 e4m3
-// with a residual: 104 us, 3,340 TFLOP/s, one of its nine waves half full.
+// 353 to 365 us, 1,950 TFLOP/s; over seconds 411 to 425 us.  20668 x 4096 x 2048 e4m3
+// with a residual: 104 to 114 us, 3,340 TFLOP/s at best, over seconds 120 to 124, one of
+// its nine waves half full.
 // What it took, in cycles of a tile (n_in 2048; 16,400 of products): issuing from
 // a converged warp 2,900, six stages instead of five 900 (the ring's latency: with
 // four, 3,300), a converged producer warp 700.  At n_in = 256 a tile is its

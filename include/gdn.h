@@ -441,7 +441,8 @@ gdn_status gdn_gated_rmsnorm_quant(const void *o, const void *z, int64_t z_row_s
  *   y = v, or with y_dtype == GDN_E4M3
  *   y_scale = max(max |v| / 448, 2^-126) and y = v / y_scale rounded to e4m3.
  * A row with a NaN or an infinity gives NaNs in its y; one of zeros zeros
- * (eps > 0).
+ * (eps > 0).  The squares are summed in fp32: a finite row whose sum of squares
+ * passes 3.4e38 gives zeros too.
  *   x, residual, residual_out: rows of `hidden` elements in `dtype`, each with
  *      its own row stride (>= hidden).  residual, residual_out: NULL leaves
  *      them out.  residual_out may be residual or x (same pointer and stride).
@@ -485,8 +486,9 @@ gdn_status gdn_add_rmsnorm(const void *x, int64_t x_row_stride, const void *resi
  *      (>= n_out: y may be columns of a wider buffer).  y may be residual
  *      (same pointer and stride); it must not overlap x or w.
  * The result of a row does not depend on the other rows or on the call's
- * timing; it may differ in the last fp32 bits between numbers of tokens (the
- * order of the sum over k follows the tile that the sizes choose).
+ * timing.  It may differ in the last fp32 bits between calls whose sizes differ,
+ * or whose x or w start or step otherwise within 128 bytes: the order of the
+ * sum over k follows the kernel and the cut of k that these choose.
  * Built: GDN_BF16 and GDN_E4M3 operands; n_tokens <= 16,776,960, n_in <= 2^24,
  * n_out <= 2^30, row strides < 2^36.
  */
