@@ -34,6 +34,8 @@ EXPORTS = (
     "gdn_debug_set_wait_limit", "gdn_prefill_chunked_gated", "gdn_mtp_step_fused",
     "gdn_decode_step_workspace_size", "gdn_prefill_layer", "gdn_prefill_layer_workspace_size",
     "gdn_prefill_layer_gated", "gdn_add_rmsnorm", "gdn_gated_rmsnorm_quant", "gdn_linear",
+    "gdn_linear_block", "gdn_moe_route", "gdn_moe_route_workspace_size", "gdn_block_quant",
+    "gdn_grouped_linear", "gdn_moe_combine",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -70,6 +72,13 @@ _SIGS = {
     "gdn_gated_rmsnorm_quant": [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _i32, _vp],
     "gdn_linear": [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp,
                    _i64, _i32, _i32, _vp],
+    "gdn_linear_block": [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _i32, _vp],
+    "gdn_moe_route": [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
+                      ctypes.c_size_t, _vp],
+    "gdn_block_quant": [_vp, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _i32, _vp],
+    "gdn_grouped_linear": [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32,
+                           _i32, _vp, _i64, _i32, _i32, _vp],
+    "gdn_moe_combine": [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _i32, _vp],
     "gdn_decode_recurrent_gated": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp, _vp, _vp, _i64,
                                    _vp, _f32, _vp, _i32, _vp],
@@ -101,6 +110,8 @@ _lib.gdn_decode_step_workspace_size.argtypes = [_i32, _i32, _i32]
 _lib.gdn_decode_step_workspace_size.restype = ctypes.c_size_t
 _lib.gdn_prefill_layer_workspace_size.argtypes = [_i32, _i64, _i32, _i32]
 _lib.gdn_prefill_layer_workspace_size.restype = ctypes.c_size_t
+_lib.gdn_moe_route_workspace_size.argtypes = [_i64, _i32]
+_lib.gdn_moe_route_workspace_size.restype = ctypes.c_size_t
 
 
 class GdnError(RuntimeError):
@@ -693,7 +704,7 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-6, y=None):
 
 # The bindings below are on a decode step's critical path (a few microseconds a
 # call), so their checks are written out and messages formed only on failure.
-_F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_F32, _BF16, _E4M3, _I32 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int32
 _CODES = {_F32: GDN_F32, _BF16: GDN_BF16, _E4M3: GDN_E4M3}
 # torch's own short forms of its public calls, where it has them (torch.cuda.current_stream
 # makes a stream object, a microsecond a call).
@@ -876,6 +887,187 @@ def gdn_linear(x, weight, x_scale=None, weight_scale=None, bias=None, act="none"
     _call(_lib.gdn_linear, "gdn_linear", dev, x.data_ptr(), _rows(x, shape, "x"), sxp,
           weight.data_ptr(), _rows(weight, wshape, "weight"), swp, bp, rp, rs, T, K, N, code,
           y.data_ptr(), _rows(y, (T, N), "y"), _CODES[dtype], _CODES[ydt])
+    return y
+
+
+def _vec(t, dtype, shape, name):
+    """t is contiguous with this type and shape; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise GdnError(f"{name}: {list(shape)} {dtype}, contiguous")
+    return t.data_ptr()
+
+
+def _out(y, y_dtype, shape, device):
+    """The products' output: y as given, or a new one; its code and row stride."""
+    if y is None:
+        y = torch.empty(shape, dtype=_BF16 if y_dtype is None else y_dtype, device=device)
+    elif y_dtype is not None and y.dtype != y_dtype:
+        raise GdnError("y: y_dtype")
+    if y.dtype != _BF16 and y.dtype != _F32:
+        raise GdnError("y: bf16 or fp32")
+    return y, _CODES[y.dtype], _rows(y, shape, "y")
+
+
+def gdn_linear_block(x, weight, x_scale, weight_scale, y_dtype=None, y=None):
+    """y = x @ weight.T for float8_e4m3fn x [T, K] and weight [N, K] with one fp32
+    scale for each block of 128 in K: x_scale [T, ceil(K / 128)] (as
+    gdn_block_quant gives), weight_scale [ceil(N / 128), ceil(K / 128)].  Unit
+    column stride, rows on 16-byte boundaries (K itself may be odd).  y [T, N] bf16
+    (default) or fp32, columns of a wider buffer if wanted.  Returns y."""
+    dev = _one_device(x, weight, x_scale, weight_scale, y)
+    shape, wshape = x.shape, weight.shape
+    if len(shape) != 2 or len(wshape) != 2 or wshape[1] != shape[1]:
+        raise GdnError("x: [T, K], weight: [N, K]")
+    if x.dtype != _E4M3 or weight.dtype != _E4M3:
+        raise GdnError("x, weight: float8_e4m3fn")
+    T, K = shape
+    N = wshape[0]
+    kb = (K + 127) // 128
+    y, code, ys = _out(y, y_dtype, (T, N), x.device)
+    _call(_lib.gdn_linear_block, "gdn_linear_block", dev, x.data_ptr(), _rows(x, shape, "x"),
+          _vec(x_scale, _F32, (T, kb), "x_scale"), weight.data_ptr(), _rows(weight, wshape, "weight"),
+          _vec(weight_scale, _F32, ((N + 127) // 128, kb), "weight_scale"), T, K, N, y.data_ptr(), ys, code)
+    return y
+
+
+def gdn_moe_route_workspace_size(n_tokens, n_experts) -> int:
+    return int(_lib.gdn_moe_route_workspace_size(n_tokens, n_experts))
+
+
+def gdn_moe_route(logits, top_k, renormalize=True, ids=None, weights=None, offsets=None, rows=None,
+                  slots=None, workspace=None):
+    """The top_k experts of each token and the pairs (token, choice) sorted by
+    expert.  logits [T, E] fp32 or bf16 (a view with a free row stride).  Returns
+    ids [T, top_k] int32 (largest logit first, ties by the lowest index), weights
+    [T, top_k] fp32 (their softmax, over all experts or, with renormalize, over
+    the chosen), offsets [E + 1], rows [T * top_k] (the token of each sorted row)
+    and slots [T, top_k] (the sorted row of each pair), int32.
+
+    workspace: None allocates what gdn_moe_route_workspace_size asks for; a uint8
+    CUDA tensor is used as given."""
+    dev = _one_device(logits, ids, weights, offsets, rows, slots, workspace)
+    shape, dtype, device = logits.shape, logits.dtype, logits.device
+    if len(shape) != 2:
+        raise GdnError("logits: [T, E]")
+    if dtype != _BF16 and dtype != _F32:
+        raise GdnError(f"unsupported logits dtype {dtype} (fp32 or bf16)")
+    T, E = shape
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=_I32, device=device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=_F32, device=device)
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=_I32, device=device)
+    if rows is None:
+        rows = torch.empty(T * top_k, dtype=_I32, device=device)
+    if slots is None:
+        slots = torch.empty((T, top_k), dtype=_I32, device=device)
+    if workspace is None:
+        need = gdn_moe_route_workspace_size(T, E)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif not workspace.is_contiguous():
+        raise GdnError("workspace: contiguous")
+    wp, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call(_lib.gdn_moe_route, "gdn_moe_route", dev, logits.data_ptr(), _rows(logits, shape, "logits"), T, E,
+          top_k, 1 if renormalize else 0, _vec(ids, _I32, (T, top_k), "ids"),
+          _vec(weights, _F32, (T, top_k), "weights"), _vec(offsets, _I32, (E + 1,), "offsets"),
+          _vec(rows, _I32, (T * top_k,), "rows"), _vec(slots, _I32, (T, top_k), "slots"), _CODES[dtype], wp, wbytes)
+    return ids, weights, offsets, rows, slots
+
+
+def gdn_block_quant(x, glu=False, y=None, y_scale=None):
+    """x, or with glu SiLU(x[:, :n]) * x[:, n:], in 8 bits with one fp32 scale for
+    each block of 128 channels.  x [T, n] (glu: [T, 2 n]) fp32 or bf16 (a view with
+    a free row stride).  Returns y [T, n] float8_e4m3fn, whose rows start on
+    16-byte boundaries (a view of a wider buffer where n is no multiple of 16)
+    unless it is given, and y_scale [T, ceil(n / 128)]: the x and x_scale of
+    gdn_linear_block and gdn_grouped_linear."""
+    dev = _one_device(x, y, y_scale)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or (glu and shape[1] % 2):
+        raise GdnError("x: [T, n], with glu [T, 2 n]")
+    if dtype != _BF16 and dtype != _F32:
+        raise GdnError(f"unsupported activation dtype {dtype} (fp32 or bf16)")
+    T, n = shape[0], shape[1] // 2 if glu else shape[1]
+    if y is None:
+        y = torch.empty((T, (n + 15) // 16 * 16), dtype=_E4M3, device=x.device)
+        if n % 16:
+            y = y[:, :n]
+    elif y.dtype != _E4M3:
+        raise GdnError("y: float8_e4m3fn")
+    if y_scale is None:
+        y_scale = torch.empty((T, (n + 127) // 128), dtype=_F32, device=x.device)
+    _call(_lib.gdn_block_quant, "gdn_block_quant", dev, x.data_ptr(), _rows(x, shape, "x"), T, n, 1 if glu else 0,
+          y.data_ptr(), _rows(y, (T, n), "y"), _vec(y_scale, _F32, (T, (n + 127) // 128), "y_scale"), _CODES[dtype])
+    return y, y_scale
+
+
+def gdn_grouped_linear(x, weight, offsets, rows=None, x_scale=None, weight_scale=None, y_dtype=None, y=None):
+    """y[r] = weight[e] @ x[rows[r]] for offsets[e] <= r < offsets[e + 1] (rows
+    None: x[r]), with offsets [E + 1] and rows [R] int32 as gdn_moe_route gives.
+    x [n_x, K], weight [E, N, K]: both bf16, or both float8_e4m3fn with x_scale
+    [n_x, ceil(K / 128)] and weight_scale [E, ceil(N / 128), ceil(K / 128)] fp32;
+    unit column stride, rows (and experts) on 16-byte boundaries (K itself may be
+    odd).  y [R, N] bf16 (default) or fp32; rows from offsets[E] on are left as
+    they were, so a y that is not given holds anything there.  Returns y."""
+    dev = _one_device(x, weight, offsets, rows, x_scale, weight_scale, y)
+    shape, wshape, dtype = x.shape, weight.shape, x.dtype
+    if len(shape) != 2 or len(wshape) != 3 or wshape[2] != shape[1]:
+        raise GdnError("x: [n_x, K], weight: [E, N, K]")
+    if dtype != weight.dtype or (dtype != _BF16 and dtype != _E4M3):
+        raise GdnError("x, weight: both bf16 or both float8_e4m3fn")
+    n_x, K = shape
+    E, N, _ = wshape
+    R, rp, sxp, swp = n_x, None, None, None
+    if rows is not None:
+        R = rows.numel()
+        rp = _vec(rows, _I32, (R,), "rows")
+    if dtype == _E4M3:
+        if x_scale is None or weight_scale is None:
+            raise GdnError("x_scale, weight_scale: needed with 8-bit x and weight")
+        kb = (K + 127) // 128
+        sxp = _vec(x_scale, _F32, (n_x, kb), "x_scale")
+        swp = _vec(weight_scale, _F32, (E, (N + 127) // 128, kb), "weight_scale")
+    elif x_scale is not None or weight_scale is not None:
+        raise GdnError("scales: only with 8-bit x and weight")
+    we, ws, one = weight.stride()
+    if (one != 1 and K != 1) or (ws < K and N > 1):
+        raise GdnError("weight: unit column stride, rows that do not overlap")
+    ws = max(ws, K) if N > 1 else K
+    if E == 1:
+        we = N * ws
+    y, code, ys = _out(y, y_dtype, (R, N), x.device)
+    _call(_lib.gdn_grouped_linear, "gdn_grouped_linear", dev, x.data_ptr(), _rows(x, shape, "x"), sxp, n_x, rp,
+          weight.data_ptr(), ws, we, swp, _vec(offsets, _I32, (E + 1,), "offsets"), E, R, K, N, y.data_ptr(), ys,
+          _CODES[dtype], code)
+    return y
+
+
+def gdn_moe_combine(x, slots, weights, residual=None, y=None):
+    """y[t] = residual[t] + sum_j weights[t, j] x[slots[t, j]], summed in fp32.
+    x [R, H] fp32 or bf16, slots [T, k] int32 (< 0: left out), weights [T, k]
+    fp32, residual [T, H] in x's dtype; free row strides.  y [T, H] may be
+    residual.  Returns y."""
+    dev = _one_device(x, slots, weights, residual, y)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or slots.dim() != 2:
+        raise GdnError("x: [R, H], slots: [T, k]")
+    if dtype != _BF16 and dtype != _F32:
+        raise GdnError(f"unsupported activation dtype {dtype} (fp32 or bf16)")
+    T, k = slots.shape
+    R, H = shape
+    rs, rp = 0, None
+    if residual is not None:
+        if residual.dtype != dtype:
+            raise GdnError("residual: x's dtype")
+        rs, rp = _rows(residual, (T, H), "residual"), residual.data_ptr()
+    if y is None:
+        y = torch.empty((T, H), dtype=dtype, device=x.device)
+    elif y.dtype != dtype:
+        raise GdnError("y: x's dtype")
+    _call(_lib.gdn_moe_combine, "gdn_moe_combine", dev, x.data_ptr(), _rows(x, shape, "x"), R,
+          _vec(slots, _I32, (T, k), "slots"), _vec(weights, _F32, (T, k), "weights"), rp, rs, T, k, H,
+          y.data_ptr(), _rows(y, (T, H), "y"), _CODES[dtype])
     return y
 
 

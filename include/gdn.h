@@ -500,6 +500,130 @@ gdn_status gdn_linear(const void *x, int64_t x_row_stride, const float *x_scale,
                       int32_t dtype, int32_t y_dtype, void *stream);
 
 /*
+ * The product of a projection in 8 bits with one fp32 scale for each block of
+ * 128 in k, as such weights come (128 x 128 blocks of w, 1 x 128 of x):
+ *   y[t][n] = sum_b x_scale[t][b] w_scale[n / 128][b]
+ *                   sum_{128 b <= k < 128 (b + 1)} x[t][k] w[n][k]
+ * A block's sum is formed by the tensor cores, the sum over the blocks in fp32
+ * registers; rounded once, to y_dtype.
+ *   x: [n_tokens] rows of n_in e4m3, w: [n_out] rows of n_in e4m3, 16-byte
+ *      aligned, row strides multiples of 16 (n_in itself may be odd).  What lies
+ *      between n_in and the stride is not read.
+ *   x_scale: [n_tokens][ceil(n_in / 128)] fp32, w_scale:
+ *      [ceil(n_out / 128)][ceil(n_in / 128)] fp32, both contiguous; gdn_block_quant
+ *      writes such x and x_scale.
+ *   y: rows of n_out elements, GDN_BF16 or GDN_F32, row stride y_row_stride
+ *      (>= n_out: y may be columns of a wider buffer).  It must not overlap an input.
+ * The result of a row does not depend on the other rows or on the call's timing.
+ * Limits: n_tokens <= 16,776,960, n_in and n_out <= 2^20, row strides < 2^36
+ * (beyond: GDN_ERR_UNSUPPORTED).
+ */
+gdn_status gdn_linear_block(const void *x, int64_t x_row_stride, const float *x_scale,
+                            const void *w, int64_t w_row_stride, const float *w_scale,
+                            int64_t n_tokens, int32_t n_in, int32_t n_out, void *y,
+                            int64_t y_row_stride, int32_t y_dtype, void *stream);
+
+/*
+ * Router of the block's mixture of experts (its MLP takes 10 of 512 experts per
+ * token): per token
+ *   p = softmax(logits),  ids = the top_k experts with the largest logits, the
+ *   largest first, ties by the lowest index;  weights = p[ids], or with
+ *   renormalize != 0 p[ids] / sum of p[ids];
+ * and the pairs (token, choice) sorted by expert and within an expert by token,
+ * the order in which gdn_grouped_linear takes them:
+ *   offsets: [n_experts + 1], expert e has the sorted rows offsets[e] ..
+ *      offsets[e + 1] - 1 (offsets[n_experts] = n_tokens * top_k);
+ *   rows: [n_tokens * top_k], the token of each sorted row;
+ *   slots: [n_tokens][top_k], the sorted row of each pair (for gdn_moe_combine).
+ *   logits: rows of n_experts elements, row stride logits_row_stride, GDN_F32 or
+ *      GDN_BF16.  -infinity closes an expert to a token: such experts come last
+ *      (still by index, so that ids are always top_k different experts) and
+ *      have weight 0, all of them in a row of nothing else.  A NaN counts as
+ *      larger than every number; it and +infinity make the row's weights NaN.
+ *   ids: [n_tokens][top_k] int32, weights: [n_tokens][top_k] fp32.
+ *   workspace: at least gdn_moe_route_workspace_size(n_tokens, n_experts) bytes,
+ *      16-byte aligned, owned by the caller and not shared with a call in flight
+ *      on another stream.
+ * n_tokens == 0 writes the offsets (zeros) alone; only they are needed then.
+ * Limits: n_experts <= 1024, top_k <= 32 (and <= n_experts),
+ * n_tokens * top_k < 2^31 - 2^20.
+ */
+size_t gdn_moe_route_workspace_size(int64_t n_tokens, int32_t n_experts);
+gdn_status gdn_moe_route(const void *logits, int64_t logits_row_stride, int64_t n_tokens,
+                         int32_t n_experts, int32_t top_k, int32_t renormalize, int32_t *ids,
+                         float *weights, int32_t *offsets, int32_t *rows, int32_t *slots,
+                         int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Activations to 8 bits with one fp32 scale for each block of 128 channels:
+ *   v[t][j] = x[t][j], or with glu != 0 SiLU(x[t][j]) * x[t][n + j]
+ *   y_scale[t][b] = max(max_{j in block b} |v[t][j]| / 448, 2^-126)
+ *   y[t][j] = v[t][j] / y_scale[t][j / 128] rounded to e4m3
+ * A block with a NaN gets a NaN scale and NaN values; one of zeros gets zeros.
+ *   x: rows of n (glu: 2 n, the gate first) elements in `dtype` (GDN_F32 or
+ *      GDN_BF16), row stride x_row_stride.
+ *   y: rows of n e4m3, row stride y_row_stride (>= n), not over x; with a stride
+ *      that is a multiple of 16 it is the x of gdn_linear_block and
+ *      gdn_grouped_linear.  y_scale: [n_rows][ceil(n / 128)] fp32, contiguous.
+ * Any alignment of whole elements is taken; rows of 16-byte vectors are faster.
+ * Limits: n <= 2^29, n_rows < 2^31.
+ */
+gdn_status gdn_block_quant(const void *x, int64_t x_row_stride, int64_t n_rows, int32_t n,
+                           int32_t glu, void *y, int64_t y_row_stride, float *y_scale,
+                           int32_t dtype, void *stream);
+
+/*
+ * Products of rows with the weights of their expert:
+ *   y[r][n] = sum_k x[i][k] w[e][n][k]   for offsets[e] <= r < offsets[e + 1],
+ *   i = rows[r], or r where rows is NULL;
+ * in bf16, or in e4m3 with the block scales of gdn_linear_block.  Experts of any
+ * number of rows, none included; rows from offsets[n_experts] on (and in front of
+ * offsets[0]) are left as they were.
+ *   x: [n_x] rows of n_in elements, w: [n_experts][n_out] rows of n_in elements,
+ *      both in `dtype` (GDN_BF16 or GDN_E4M3), 16-byte aligned; x_row_stride,
+ *      w_row_stride and w_expert_stride multiples of 16 bytes (n_in may be odd).
+ *   x_scale: [n_x][ceil(n_in / 128)], w_scale: [n_experts][ceil(n_out / 128)]
+ *      [ceil(n_in / 128)] fp32, contiguous, with GDN_E4M3; NULL with GDN_BF16.
+ *   rows: [n_rows] int32 or NULL (then n_x == n_rows).  An index < 0 gives a row
+ *      of zeros; one >= n_x too, and sets GDN_DEVSTAT_BAD_INDEX.
+ *   offsets: [n_experts + 1] int32, non-decreasing, within 0 .. n_rows; else
+ *      nothing is written and GDN_DEVSTAT_BAD_SEQLEN is set.
+ *   y: [n_rows] rows of n_out elements, GDN_BF16 or GDN_F32, row stride
+ *      y_row_stride (>= n_out).  It must not overlap an input.
+ * The result of a row does not depend on the other rows of the call's data or on
+ * its timing.  It may differ in the last fp32 bits between calls whose sizes
+ * differ: these choose the order of the sum over k.
+ * Limits: n_rows and n_x <= 16,776,960, n_in and n_out <= 2^20, n_experts <= 1024,
+ * strides < 2^36.
+ */
+gdn_status gdn_grouped_linear(const void *x, int64_t x_row_stride, const float *x_scale,
+                              int64_t n_x, const int32_t *rows, const void *w,
+                              int64_t w_row_stride, int64_t w_expert_stride,
+                              const float *w_scale, const int32_t *offsets, int32_t n_experts,
+                              int64_t n_rows, int32_t n_in, int32_t n_out, void *y,
+                              int64_t y_row_stride, int32_t dtype, int32_t y_dtype, void *stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   y[t] = residual[t] + sum_j weights[t][j] x[slots[t][j]]
+ * summed in fp32 in the order of j, the residual last, rounded once.
+ *   x: [n_rows] rows of `hidden` elements in `dtype` (GDN_F32 or GDN_BF16).
+ *   slots: [n_tokens][top_k] int32 (an index < 0 is left out of the sum, one >=
+ *      n_rows too, and sets GDN_DEVSTAT_BAD_INDEX), weights: [n_tokens][top_k] fp32.
+ *   residual: rows of `hidden` elements in `dtype`, or NULL.
+ *   y: rows of `hidden` elements in `dtype`; it may be residual (same pointer and
+ *      stride) and must not overlap x.
+ * Each with its row stride (>= hidden); any alignment of whole elements is taken,
+ * rows of 16-byte vectors are faster.
+ * Limits: n_rows < 2^31, n_tokens * top_k < 2^31, top_k <= 1024, n_tokens * hidden < 2^39.
+ */
+gdn_status gdn_moe_combine(const void *x, int64_t x_row_stride, int64_t n_rows,
+                           const int32_t *slots, const float *weights, const void *residual,
+                           int64_t residual_row_stride, int64_t n_tokens, int32_t top_k,
+                           int32_t hidden, void *y, int64_t y_row_stride, int32_t dtype,
+                           void *stream);
+
+/*
  * gdn_decode_recurrent with the gated RMSNorm above fused into its output:
  * writes y = RMSNorm(o) * norm_weight * SiLU(z) instead of o.  Arguments as
  * gdn_decode_recurrent, plus z (rows i * tokens_per_seq + t, stride
