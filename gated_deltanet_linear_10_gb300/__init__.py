@@ -1092,11 +1092,12 @@ def gdn_get_device_status(clear=True, device=None) -> int:
 
 
 def gdn_debug_set_wait_limit(limit_ns=0, drop_prep_loads=False, device=None, drop_linear_loads=0):
-    """Test control of the failure path of the two-kernel prefill and of
-    gdn_linear: the limit of their bounded waits (0 = the default, one second),
-    whether the prep kernel skips its K|Q loads, and which loads gdn_linear
-    skips (0 none, 1 all, 2 those behind a CTA's first block or tile).  Its waits
-    then run out and the call sets DEVSTAT_TIMEOUT; its results are undefined.
+    """Test control of the failure path of the two-kernel prefill and of the
+    products (gdn_linear, gdn_linear_block, gdn_grouped_linear): the limit of their
+    bounded waits (0 = the default, one second), whether the prep kernel skips its
+    K|Q loads, and which loads the products skip (0 none, 1 all, 2 those behind a
+    CTA's first block or tile).  Its waits then run out and the call sets
+    DEVSTAT_TIMEOUT; its results are undefined.
     Synchronises the stream."""
     _need(drop_linear_loads in (0, 1, 2), "drop_linear_loads: 0, 1 or 2")
     _check(_lib.gdn_debug_set_wait_limit(int(limit_ns), int(bool(drop_prep_loads)) + 2 * drop_linear_loads,

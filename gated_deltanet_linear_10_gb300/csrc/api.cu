@@ -11,7 +11,8 @@ GDN_DECLARE_STATUS_WORD(g_status_api)
 gdn_status read_status_norm(uint32_t *out, int clear, cudaStream_t s);   // rmsnorm.cu
 gdn_status read_status_linear(uint32_t *out, int clear, cudaStream_t s);        // linear.cu
 gdn_status read_status_linear_wide(uint32_t *out, int clear, cudaStream_t s);   // linear_wide.cu
-gdn_status read_status_grouped(uint32_t *out, int clear, cudaStream_t s);       // grouped.cu
+gdn_status read_status_grouped_narrow(uint32_t *out, int clear, cudaStream_t s);   // grouped_narrow.cu
+gdn_status read_status_grouped_wide(uint32_t *out, int clear, cudaStream_t s);     // grouped_wide.cu
 gdn_status read_status_moe(uint32_t *out, int clear, cudaStream_t s);           // moe.cu
 GDN_STATUS_READER(read_status_api, g_status_api)
 
@@ -110,7 +111,8 @@ gdn_status gdn_get_device_status(uint32_t *out, int32_t clear, void *stream) {
     if ((st = read_status_mtp_step(out, clear, s)) != GDN_OK) return st;
     if ((st = read_status_linear(out, clear, s)) != GDN_OK) return st;
     if ((st = read_status_linear_wide(out, clear, s)) != GDN_OK) return st;
-    if ((st = read_status_grouped(out, clear, s)) != GDN_OK) return st;
+    if ((st = read_status_grouped_narrow(out, clear, s)) != GDN_OK) return st;
+    if ((st = read_status_grouped_wide(out, clear, s)) != GDN_OK) return st;
     if ((st = read_status_moe(out, clear, s)) != GDN_OK) return st;
     return GDN_OK;
 }

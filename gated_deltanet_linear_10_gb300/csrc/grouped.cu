@@ -1,128 +1,34 @@
 // Products of rows with the weights of their expert, in bf16 or in e4m3 with an
 // fp32 scale for each block of 128 in k, and the product of all rows with one
-// weight in the latter form:
-//   y_r = sum_b sx[x row of r][b] sw[e][n / 128][b] sum_{k in b} x[x row of r][k] w[e][n][k]
-// for offsets[e] <= r < offsets[e + 1].
+// weight in the latter form: argument checks, operand maps and the choice of a kernel.
 #include <algorithm>
 
-#include "linear.cuh"
 #include "grouped.cuh"
 
 namespace gdn {
 
-GDN_DECLARE_STATUS_WORD(g_status_grouped)
-GDN_STATUS_READER(read_status_grouped, g_status_grouped)
-
-template <bool kE4m3> __device__ __forceinline__ float grouped_value(const void *p, int64_t i) {
-    if constexpr (kE4m3) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(reinterpret_cast<const __nv_fp8_storage_t *>(p)[i], __NV_E4M3);
-        return __half2float(*reinterpret_cast<const __half *>(&h));
-    } else {
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
-    }
+// A single row (or expert) has no stride; a map wants one all the same.
+bool encode_tmap_experts(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows) {
+    const int64_t elem = c.e4m3 ? 1 : 2, row = ((int64_t)c.n_in + 15) / 16 * 16;
+    const int64_t ws = c.n_out == 1 ? row : c.ws, we = c.n_experts == 1 ? ws * c.n_out : c.we;
+    return encode_tmap_3d(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.w, c.n_in,
+                          c.n_out, c.n_experts, ws * elem, we * elem, 128 / (uint32_t)elem, box_rows);
+}
+bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows) {
+    return encode_tmap_operand(map, c.x, c.n_in, c.n_x, c.xs, c.rows ? 1 : box_rows, c.e4m3);
 }
 
-// Tiles of 64 rows x 64 channels; 4 x 4 of them a thread.
-template <bool kE4m3, typename O>
-__global__ void __launch_bounds__(256) grouped_simple_kernel(const GroupedCall c) {
-    constexpr int KS = 32;
-    __shared__ float xs[KS][65], ws[KS][65];
-    __shared__ int found[3];
-    griddep_wait();
-    griddep_launch();
-    const int tid = threadIdx.x, n0 = blockIdx.x * 64;
-    if (tid == 0) {
-        int first = 0, end = c.n_rows, e = 0, left = blockIdx.y;
-        bool bad = false;
-        if (c.offsets) {
-            int at = -1, r0 = 0, r1 = 0;
-            for (int i = 0; i < c.n_experts; ++i) {
-                const int a = c.offsets[i], b = c.offsets[i + 1];
-                bad |= a < 0 || b < a || b > c.n_rows;
-                const int tiles = (b - a + 63) / 64;
-                if (at < 0 && left < tiles) {
-                    at = i;
-                    r0 = a;
-                    r1 = b;
-                }
-                if (at < 0) left -= tiles;
-            }
-            e = at;
-            first = r0;
-            end = r1;
-        }
-        if (bad) flag_status(GDN_DEVSTAT_BAD_SEQLEN);
-        found[0] = bad ? -1 : e;
-        found[1] = first + left * 64;
-        found[2] = end;
-    }
-    __syncthreads();
-    const int e = found[0], r0 = found[1], r1 = found[2];
-    if (e < 0) return;
-    const int tx = tid & 15, ty = tid >> 4;
-    float sum[4][4] = {}, part[4][4] = {};
-    int64_t xrow[4];
-    auto x_row = [&](int r) -> int64_t {
-        if (r >= r1) return -1;
-        if (!c.rows) return r;
-        const int64_t v = c.rows[r];
-        if (v >= c.n_x) flag_status(GDN_DEVSTAT_BAD_INDEX);
-        return v >= 0 && v < c.n_x ? v : -1;
-    };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) xrow[i] = x_row(r0 + ty * 4 + i);
-    for (int k0 = 0; k0 < c.n_in; k0 += KS) {
-        for (int i = tid; i < 64 * KS; i += 256) {
-            const int k = i % KS, r = i / KS;
-            const int64_t xr = x_row(r0 + r);
-            xs[k][r] = xr >= 0 && k0 + k < c.n_in ? grouped_value<kE4m3>(c.x, xr * c.xs + k0 + k) : 0.f;
-            ws[k][r] = n0 + r < c.n_out && k0 + k < c.n_in
-                           ? grouped_value<kE4m3>(c.w, e * c.we + (int64_t)(n0 + r) * c.ws + k0 + k) : 0.f;
-        }
-        __syncthreads();
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xs[k][ty * 4 + i], ws[k][tx + 16 * j], part[i][j]);
-        __syncthreads();
-        if (!kE4m3 || k0 % 128 == 96 || k0 + KS >= c.n_in) {
-            const int b = k0 / 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float f = 1.0f;
-                    const int n = n0 + tx + 16 * j;
-                    if (kE4m3 && xrow[i] >= 0 && n < c.n_out)
-                        f = c.sx[xrow[i] * c.kb + b] * c.sw[((int64_t)e * c.nb + n / 128) * c.kb + b];
-                    sum[i][j] = fmaf(part[i][j], f, sum[i][j]);
-                    part[i][j] = 0.f;
-                }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = r0 + ty * 4 + i, n = n0 + tx + 16 * j;
-            if (r < r1 && n < c.n_out)
-                Io<O>::store(reinterpret_cast<O *>(c.y) + r * c.ys + n, xrow[i] < 0 ? 0.f : sum[i][j]);
-        }
-}
-
+// By the rows that an expert has in the mean (the host knows no more): up to 64 go to
+// narrow tiles of twice as many rows, beyond 128 wide tiles pay where there are enough
+// of them for the pairs.
 static gdn_status launch_grouped(const GroupedCall &c, cudaStream_t s) {
-    const int tiles = (int)std::min<int64_t>(65535, ((int64_t)c.n_rows + 63) / 64 + (c.offsets ? c.n_experts : 0));
-    auto go = [&](auto kernel) {
-        return launch_after(kernel, dim3((c.n_out + 63) / 64, tiles), dim3(256), 0, s, c);
-    };
-    const cudaError_t e = c.e4m3 ? (c.out_f32 ? go(grouped_simple_kernel<true, float>) : go(grouped_simple_kernel<true, __nv_bfloat16>))
-                                 : (c.out_f32 ? go(grouped_simple_kernel<false, float>) : go(grouped_simple_kernel<false, __nv_bfloat16>));
-    if (e != cudaSuccess) {
-        set_last_cuda_error(e);
-        return GDN_ERR_LAUNCH;
-    }
-    return GDN_OK;
+    const int drop = linear_drop();
+    const int mean = (c.n_rows + c.n_experts - 1) / c.n_experts;
+    const int64_t wide = ((int64_t)c.n_rows / 256 + (c.offsets ? std::min(c.n_experts, c.n_rows) : 1)) *
+                         ((c.n_out + 255) / 256);
+    if (mean > 128 && wide >= sm_count() / 2) return launch_grouped_wide(c, drop, s);
+    const int rows = c.offsets ? 2 * mean : mean;
+    return launch_grouped_narrow(c, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, drop, s);
 }
 
 }  // namespace gdn

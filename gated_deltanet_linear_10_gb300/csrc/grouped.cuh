@@ -1,7 +1,11 @@
-// The products grouped by expert and with block scales (internal header).
+// The products grouped by expert and with block scales (internal header):
+//   y_r = sum_b sx[i][b] sw[e][n / 128][b] sum_{k in b} x[i][k] w[e][n][k],
+//   i = rows[r], offsets[e] <= r < offsets[e + 1]
+// (bf16: no scales and one block).  The product of all rows with one weight is
+// the case of one expert, without offsets.
 #pragma once
 
-#include "common.cuh"
+#include "linear.cuh"
 
 namespace gdn {
 
@@ -17,6 +21,144 @@ struct GroupedCall {
     int64_t ys;
     int n_rows, n_x, n_experts, n_in, n_out, kb, nb;
     bool e4m3, out_f32;
+    bool vec16;                      // rows of y on 16-byte boundaries, whole 16 bytes of them
 };
+
+// grouped_narrow.cu: a tile's weight rows on the accumulator's lanes, its tokens the
+// columns; grouped_wide.cu: tokens on the lanes, a pair of CTAs a tile.
+gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int drop, cudaStream_t s);
+gdn_status launch_grouped_wide(const GroupedCall &c, int drop, cudaStream_t s);
+cudaError_t set_grouped_narrow_limit(uint64_t limit_ns, cudaStream_t s);
+cudaError_t set_grouped_wide_limit(uint64_t limit_ns, cudaStream_t s);
+int linear_drop();                   // the failure path's test control (LinearDrop)
+
+// The operands' maps: w as [n_experts][n_out][n_in] in boxes of 128 bytes x box_rows,
+// x as rows in boxes of 128 bytes x box_rows or, gathered, of one row.
+bool encode_tmap_experts(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows);
+bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows);
+
+// ------------------------------------------------------------ device side --
+// Which rows an expert has and how many tiles of rows lie in front of it, in shared
+// memory; built by the whole CTA from the offsets.
+struct GroupTable {
+    int first[kGroupedExperts + 1], start[kGroupedExperts + 1];
+    int part[32];
+    int bad;
+};
+
+// All threads; returns the number of row tiles, 0 where the offsets are no offsets
+// (then *bad).  Ends with a barrier.
+__device__ __forceinline__ int build_group_table(GroupTable &g, const GroupedCall &c, int tile_rows, bool *bad) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    *bad = false;
+    if (!c.offsets) {
+        if (tid == 0) {
+            g.first[0] = g.start[0] = 0;
+            g.first[1] = (c.n_rows + tile_rows - 1) / tile_rows;
+            g.start[1] = c.n_rows;
+        }
+        __syncthreads();
+        return g.first[1];
+    }
+    const int per = (c.n_experts + nt - 1) / nt, e0 = tid * per, e1 = min(e0 + per, c.n_experts);
+    int sum = 0, wrong = 0;
+    if (e0 < e1) {
+        int a = c.offsets[e0];
+        wrong |= a < 0;
+        for (int e = e0; e < e1; ++e) {
+            const int b = c.offsets[e + 1];
+            wrong |= b < a || b > c.n_rows;
+            sum += (b - a + tile_rows - 1) / tile_rows;
+            g.start[e] = a;
+            a = b;
+        }
+        if (e1 == c.n_experts) g.start[e1] = a;
+    }
+    wrong = __syncthreads_or(wrong);
+    int scan = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += o;
+    }
+    if (lane == 31) g.part[warp] = scan;
+    __syncthreads();
+    int front = scan - sum;
+    for (int i = 0; i < warp; ++i) front += g.part[i];
+    for (int e = e0; e < e1; ++e) {
+        g.first[e] = front;
+        front += (g.start[e + 1] - g.start[e] + tile_rows - 1) / tile_rows;
+    }
+    if (e0 < e1 && e1 == c.n_experts) g.first[e1] = front;
+    __syncthreads();
+    *bad = wrong != 0;
+    return wrong ? 0 : g.first[c.n_experts];
+}
+
+// A tile: rows r0 .. r1 - 1 (r1: the expert's end, not the tile's), channel tile n.
+struct GroupTile {
+    int e, r0, r1, n;
+};
+
+// By a whole warp.  Within an expert groups of kGroupRaster row tiles take the channel
+// tiles one after the other, row tiles fastest: the tiles in flight share weights and rows.
+constexpr int kGroupRaster = 8;
+__device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, int experts, int tile, int nn, int tile_rows) {
+    const int lane = threadIdx.x & 31, rt = tile / nn;
+    const int hi = __popc(__ballot_sync(0xffffffffu, g.first[min(32 * (lane + 1), experts)] <= rt));
+    const int e = 32 * hi + __popc(__ballot_sync(0xffffffffu, g.first[min(32 * hi + lane + 1, experts)] <= rt));
+    GroupTile t;
+    t.e = e;
+    const int f = g.first[e], tiles = g.first[e + 1] - f, r = tile - f * nn;
+    const int base = r / (kGroupRaster * nn) * kGroupRaster, rr = r - base * nn;
+    const int rows = min(kGroupRaster, tiles - base);
+    t.n = rows == 1 ? rr : rr / rows;
+    t.r0 = g.start[e] + (base + rr - t.n * rows) * tile_rows;
+    t.r1 = g.start[e + 1];
+    return t;
+}
+
+// The row of x that sorted row r takes, n_x (which reads as zeros) where there is none.
+__device__ __forceinline__ int group_x_row(const GroupedCall &c, int r, int r1) {
+    if (r >= r1) return c.n_x;
+    if (!c.rows) return r;
+    const int i = c.rows[r];
+    return i < 0 || i >= c.n_x ? c.n_x : i;
+}
+
+// Four rows of x, 128 bytes of each, into 512 bytes of an operand tile.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, const int4 &r) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// 16 columns of 32 lanes of tensor memory, on their way until tmem_wait16.
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Every load of this thread has come; r is named so that nothing reads it before.
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
 
 }  // namespace gdn

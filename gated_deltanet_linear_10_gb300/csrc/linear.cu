@@ -11,6 +11,7 @@
 
 #include <algorithm>
 
+#include "grouped.cuh"
 #include "linear.cuh"
 
 namespace gdn {
@@ -24,10 +25,13 @@ GDN_STATUS_READER(read_status_linear, g_status_linear)
 static std::atomic<int> g_linear_drop{kDropNone};
 cudaError_t set_linear_failure(uint64_t limit_ns, int drop, cudaStream_t s) {
     g_linear_drop.store(drop, std::memory_order_relaxed);
-    const cudaError_t e = cudaMemcpyToSymbolAsync(tc::g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0,
-                                                  cudaMemcpyHostToDevice, s);
-    return e != cudaSuccess ? e : set_linear_wide_limit(limit_ns, s);
+    cudaError_t e = cudaMemcpyToSymbolAsync(tc::g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0,
+                                            cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = set_linear_wide_limit(limit_ns, s);
+    if (e == cudaSuccess) e = set_grouped_narrow_limit(limit_ns, s);
+    return e != cudaSuccess ? e : set_grouped_wide_limit(limit_ns, s);
 }
+int linear_drop() { return g_linear_drop.load(std::memory_order_relaxed); }
 
 bool encode_tmap_operand(CUtensorMap *map, const void *base, int64_t cols, int64_t rows,
                          int64_t row_stride_elems, uint32_t box_rows, bool e4m3) {

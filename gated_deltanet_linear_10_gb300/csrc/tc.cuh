@@ -309,4 +309,8 @@ bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t cols, uint
 bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
                     uint64_t rows, uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
                     bool swizzle128);
+// Planes of rows, in boxes of one plane and in the 128-byte swizzle.
+bool encode_tmap_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+                    uint64_t rows, uint64_t planes, uint64_t row_stride_bytes,
+                    uint64_t plane_stride_bytes, uint32_t box_cols, uint32_t box_rows);
 }  // namespace gdn

@@ -34,6 +34,21 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+                    uint64_t rows, uint64_t planes, uint64_t row_stride_bytes,
+                    uint64_t plane_stride_bytes, uint32_t box_cols, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn || rows == 0 || cols == 0 || planes == 0) return false;
+    cuuint64_t dims[3] = {cols, rows, planes};
+    cuuint64_t strides[2] = {row_stride_bytes, plane_stride_bytes};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
                          uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows,
                          bool swizzle128) {

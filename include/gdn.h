@@ -787,12 +787,13 @@ gdn_status gdn_state_snapshot(void *pool, int64_t n_slots, int64_t slot_bytes,
 /*
  * Test control of the failure path (not for production use).  Sets the limit
  * of every bounded wait inside the two-kernel tensor-core prefill (the prep
- * and chain kernels of gdn_prefill_chunked with a workspace) and inside
- * gdn_linear's kernels to limit_ns nanoseconds on the current device; 0
+ * and chain kernels of gdn_prefill_chunked with a workspace) and inside the
+ * kernels of gdn_linear, gdn_linear_block and gdn_grouped_linear to limit_ns nanoseconds on the current device; 0
  * restores the default of one second.  drop_loads: a sum of
  *   1  the prep kernel issues none of its K|Q tile loads,
- *   2  gdn_linear's calls (of the process) issue no loads of x and w,
- *   4  ... none behind the first k block (few tokens) or the first tile of a
+ *   2  calls of gdn_linear, gdn_linear_block and gdn_grouped_linear (of the
+ *      process) issue no loads of x and w,
+ *   4  ... none behind a CTA's first k block (few tokens) or the first tile of a
  *      pair of CTAs (many tokens),
  * so that the waits for them run out after the limit: the kernel then skips
  * its stores (of what did not come), drains, frees its tensor memory, returns
