@@ -21,7 +21,9 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
 // By the rows that an expert has in the mean (the host knows no more): up to 64 go to
 // narrow tiles of twice as many rows, beyond 128 wide tiles pay where there are enough
 // of them for the pairs.
-static gdn_status launch_grouped(const GroupedCall &c, cudaStream_t s) {
+static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
+    const int64_t ye = c.out_f32 ? 4 : 2;
+    c.vec16 = (uintptr_t)c.y % 16 == 0 && c.n_out * ye % 16 == 0 && (c.n_rows == 1 || c.ys * ye % 16 == 0);
     const int drop = linear_drop();
     const int mean = (c.n_rows + c.n_experts - 1) / c.n_experts;
     const int64_t wide = ((int64_t)c.n_rows / 256 + (c.offsets ? std::min(c.n_experts, c.n_rows) : 1)) *

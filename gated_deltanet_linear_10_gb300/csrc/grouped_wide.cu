@@ -27,8 +27,11 @@ cudaError_t set_grouped_wide_limit(uint64_t limit_ns, cudaStream_t s) {
 
 namespace {
 
-constexpr int kGwStages = 6, kGwEpiWarps = 8, kGwThreads = 64 + 32 * kGwEpiWarps;
+constexpr int kGwStages = 6, kGwEpiWarps = 8, kGwThreads = 128 + 32 * kGwEpiWarps;
 constexpr int kGwRows = 256, kGwChannels = 256;
+// Registers of a thread: 168 at launch; the first warpgroup gives up what the summing
+// ones take (72 x 128 + 216 x 256 = 168 x 384).
+constexpr int kGwRegsFew = 72, kGwRegsMany = 216;
 constexpr uint32_t kGwX = 128 * 128, kGwHalf = 64 * 128, kGwStage = kGwX + 2 * kGwHalf;
 constexpr uint32_t kGwRowBytes = 80;     // a staging row: 64 bytes of y, and 16 that keep 8 rows off each other's banks
 constexpr uint32_t kGwStaging = 32 * kGwRowBytes;
@@ -181,6 +184,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     tc_fence_after();
     if (bad && tid == 0 && blockIdx.x == 0) flag_status(GDN_DEVSTAT_BAD_SEQLEN);
 
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGwRegsFew));
     if (warp == 0) {
         // This CTA's 128 rows of x and half of each half's weight rows, counted on the leader's barrier.
         const bool one = elect_lane();
@@ -290,10 +294,11 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
             mbar_drain(&drained, 0);
         }
         __syncwarp();
-    } else if (warp >= 2) {
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGwRegsMany));
         // Accumulator lane 32 q + l is token row 32 q + l of this CTA's 128.
-        const int q = warp & 3, h = (warp - 2) >> 2;
-        uint8_t *staging = smem + S * kGwStage + (warp - 2) * kGwStaging;
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        uint8_t *staging = smem + S * kGwStage + (warp - 4) * kGwStaging;
         int u = 0;
         bool ok = true, wrong = false;
         for (int t = pair; t < tiles && ok; t += pairs) {
@@ -330,21 +335,24 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                 }
                 tc_fence_after();
                 const uint32_t from = tmem_addr(tmem_base, q * 32, (b * 2 + h) * 128);
-                uint32_t r[2][16];
-                tmem_ask16(from, r[0]);
+                uint32_t r[2][32];
+                tmem_ask32(from, r[0]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    tmem_wait16(r[j & 1]);
-                    if (j < 7) tmem_ask16(from + (j + 1) * 16, r[(j + 1) & 1]);
+                for (int j = 0; j < 4; ++j) {
+                    tmem_wait32(r[j & 1]);
+                    if (j < 3) {
+                        tmem_ask32(from + (j + 1) * 32, r[(j + 1) & 1]);
+                    } else {                               // all of it has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[h][b]), 0));
+                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         const F2 v = f2_bits(r[j & 1][2 * i], r[j & 1][2 * i + 1]);
-                        acc[j * 8 + i] = kBlock ? f2_fma(v, f, acc[j * 8 + i]) : v;
+                        acc[j * 16 + i] = kBlock ? f2_fma(v, f, acc[j * 16 + i]) : v;
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[h][b]), 0));
                 f0 = a1 * b1;
                 a1 = a2;
                 b1 = b2;
