@@ -100,6 +100,35 @@ def test_sizes(K, N, dtype):
         _run(K + N, [2, 9, 1, 0, 5], K, N, dtype, F32, gather=gather)
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("N", [1400, 1411, 1664, 1665, 2048, 2178])
+def test_many_rows_an_expert(N, dtype, out):
+    """Tiles on pairs of CTAs: channels that end in either half of a tile, k of one block and of many, ragged rows."""
+    for counts, K in (([300, 0, 513, 700, 129, 1, 128, 255], 200), ([1, 2000, 0, 0, 31], 64), ([900, 900], 1160)):
+        _run(N, counts, K, N, dtype, out)
+        _run(N, counts, K, N, dtype, out, gather=77)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("off,pad", [(0, 8), (8, 0), (1, 3), (2, 2)])
+def test_many_rows_an_expert_strided(off, pad, dtype):
+    counts, K, N = [300, 0, 513, 700, 129, 1, 128, 255], 144, 1672
+    R = sum(counts)
+    x, w, sx, sw = _operands(N, 90, len(counts), K, N, dtype)
+    rows = torch.randint(-1, 90, (R,), device=DEV, dtype=torch.int32)
+    want = gdn().gdn_grouped_linear(x, w, _offsets(counts), rows=rows, x_scale=sx, weight_scale=sw)
+    ref, size = m64.grouped(x, w, _offsets(counts), rows, sx, sw)
+    m64.check_product(want, ref, size, K, dtype == E4M3)
+    assert torch.all(want[rows < 0] == 0)
+    wide = torch.full((R + 1, N + off + pad), 3.0, dtype=BF16, device=DEV)
+    gdn().gdn_grouped_linear(x, w, _offsets(counts), rows=rows, x_scale=sx, weight_scale=sw, y=wide[:R, off:off + N])
+    torch.cuda.synchronize()
+    status_clean()
+    assert bits_equal(wide[:R, off:off + N].contiguous(), want)
+    assert torch.all(wide[R] == 3.0) and torch.all(wide[:, :off] == 3.0) and torch.all(wide[:, off + N:] == 3.0)
+
+
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("counts", [[5, 0, 3], [200, 0, 500]])
 def test_rows_behind_the_last_and_bad_rows(counts, dtype):
