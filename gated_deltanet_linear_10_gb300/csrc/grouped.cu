@@ -24,6 +24,7 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
 static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     const int64_t ye = c.out_f32 ? 4 : 2;
     c.vec16 = (uintptr_t)c.y % 16 == 0 && c.n_out * ye % 16 == 0 && (c.n_rows == 1 || c.ys * ye % 16 == 0);
+    c.sx16 = (uintptr_t)c.sx % 16 == 0 && c.kb % 4 == 0;
     const int drop = linear_drop();
     const int mean = (c.n_rows + c.n_experts - 1) / c.n_experts;
     const int64_t wide = ((int64_t)c.n_rows / 256 + (c.offsets ? std::min(c.n_experts, c.n_rows) : 1)) *

@@ -22,6 +22,7 @@ struct GroupedCall {
     int n_rows, n_x, n_experts, n_in, n_out, kb, nb;
     bool e4m3, out_f32;
     bool vec16;                      // rows of y on 16-byte boundaries, whole 16 bytes of them
+    bool sx16;                       // rows of sx on 16-byte boundaries
 };
 
 // grouped_narrow.cu: a tile's weight rows on the accumulator's lanes, its tokens the
@@ -124,6 +125,23 @@ __device__ __forceinline__ int group_x_row(const GroupedCall &c, int r, int r1) 
     if (!c.rows) return r;
     const int i = c.rows[r];
     return i < 0 || i >= c.n_x ? c.n_x : i;
+}
+
+// How long what is read or written should stay in L2.
+__device__ __forceinline__ uint64_t l2_first() {     // it makes room first
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_last() {      // it stays
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 
 // Four rows of x, 128 bytes of each, into 512 bytes of an operand tile.

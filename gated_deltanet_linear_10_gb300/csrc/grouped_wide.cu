@@ -2,16 +2,22 @@
 // 256 tokens x 256 channels (tcgen05 cta_group::2, M = 256), the tokens on the
 // accumulator's lanes.
 //
-// With block scales every block of 128 in k is a product of its own, which eight
-// warps of either CTA take out of tensor memory and add, times its factor, to sums in
-// registers.  A thread is one token and 128 channels, so the factor sx sw is one
-// number a block and half a tile.  The half tiles of 128 channels have two
-// accumulators each: the way from a product's issue over its sums' reading to the
-// accumulator's release is longer than two products of a whole tile take, but not
-// than four of a half.  In bf16 the accumulators are summed over all of k and
-// alternate between tiles.
+// With block scales every block of 128 in k is a product of its own, which four warps
+// of either CTA take out of tensor memory and add, times its factor, to sums in
+// registers.  A thread is one token and half a tile's channels, so the factor sx sw is
+// one number a block.  The two halves of 128 channels are pipelines of their own: a
+// warp that issues the products, two accumulators, and the warps that sum them.  What
+// bounds a block is the instructions around it, each warp's in turn (a wait that finds
+// its barrier done takes some 165 cycles, four products and their commits 200): one
+// issuing warp for both halves took 1,100 cycles a block, the products 512.  In bf16
+// the accumulators are summed over all of k and alternate between tiles.
 //
-// Where rows are gathered, two warps copy them to shared memory in pieces of 16 bytes:
+// The factors come through shared memory, from a warp that reads them eight blocks at a
+// time: read by the summing warps themselves, a word of 32 rows a block, they took a
+// fifth of the time (gathered rows: 897 us, with one row's factors for all 697).  What
+// can wait polls with one lane and sleeps: more polling warps slow the chain down.
+//
+// Where rows are gathered, three warps copy them to shared memory in pieces of 16 bytes:
 // a TMA gather of four rows took 84 cycles (20668 x 10 rows 2048 x 1024 e4m3: 2780
 // cycles a block of 128, of which 1750 for the rows to come).
 #include <limits.h>
@@ -33,17 +39,33 @@ cudaError_t set_grouped_wide_limit(uint64_t limit_ns, cudaStream_t s) {
 
 namespace {
 
-constexpr int kGwStages = 4, kGwEpiWarps = 8, kGwThreads = 128 + 32 * kGwEpiWarps;
+constexpr int kGwStages = 4, kGwEpiWarps = 8;
+// Warps: 0 loads by TMA, 1 and 2 products, 3 looks up tiles and makes the factors, 4 to 11
+// sums, 12 to 14 gathered rows, 15 hands them over.
+constexpr int kGwThreads = 512, kGwTile = 3, kGwFirstEpi = 4, kGwFirstGather = 12, kGwGather = 3, kGwRelay = 15;
+constexpr int kGwChunk = 8;              // blocks whose factors are handed over at a time
 constexpr int kGwRows = 256, kGwChannels = 256;
-// Registers of a thread: 168 at launch; the first warpgroup gives up what the summing
-// ones take (88 x 128 + 208 x 256 = 168 x 384).
-constexpr int kGwRegsFew = 88, kGwRegsMany = 208;
+// Registers of a thread: 128 at launch; the summing warpgroups take what the others
+// give up (64 x 256 + 192 x 256 = 128 x 512).
+constexpr int kGwRegsFew = 64, kGwRegsMany = 192;
 constexpr uint32_t kGwX = 128 * 128, kGwHalf = 64 * 128, kGwStage = kGwX + 2 * kGwHalf;
 // Staging of a warp: two tiles of 32 rows x 128 bytes in the 128-byte swizzle.
 constexpr uint32_t kGwStaging = 2 * 4096;
-constexpr uint32_t kGwSmem = kGwStages * kGwStage + kGwEpiWarps * kGwStaging;
-constexpr int kGwLag = 2;                // gathered stages in flight behind the one being asked for
+constexpr uint32_t kGwFactors = 2 * kGwChunk * 128 * 4;       // [half][block][row], fp32
+constexpr uint32_t kGwSmem = kGwStages * kGwStage + kGwEpiWarps * kGwStaging + 2 * kGwFactors;
 
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Loads into this CTA's shared memory, their bytes counted on a barrier of either CTA.
 __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y) {
     asm volatile(
@@ -53,16 +75,28 @@ __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, 
         : "memory");
 }
 __device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
-                                             int32_t z) {
+                                             int32_t z, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
         : "memory");
 }
 // 16 bytes of global into shared memory, those from `bytes` on as zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// (the size as a register makes that a slow sequence)
+__device__ __forceinline__ void copy16_if(bool on, uint32_t dst, const void *src) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}\n" ::"r"(dst),
+        "l"(src), "r"((uint32_t)on)
+        : "memory");
+}
+// Arrives on a barrier, whose count has it already, when this thread's copies so far have come.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Arrives on the barrier at this offset in both CTAs (mask 3) or the leader (1) once
 // the products issued so far by this thread are done.
@@ -89,21 +123,21 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
             : "memory");
 }
 
-// A warp's 32 rows x 64 channels of the tile's halves out, through its staging tiles:
+// A warp's 32 rows x 128 channels n0 .. out, through its staging tiles:
 // by a TMA store that goes on behind the call; where the expert ends within the rows,
-// in pieces of 16 bytes, and where rows are no whole pieces, element by element.  n0:
-// the warp's channels of half 0, those of half 1 are 128 on.  (Rows of bulk copies, one
-// a lane, took 5,500 cycles a tile and held up the loads behind them.)
+// in pieces of 16 bytes, and where rows are no whole pieces, element by element.
+// (Rows of bulk copies, one a lane, took 5,500 cycles a tile and held up the loads
+// behind them.)
 template <typename O>
-__device__ __forceinline__ void wide_store(const F2 (&acc)[2][32], uint8_t *staging, const CUtensorMap *my,
+__device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging, const CUtensorMap *my,
                                            const GroupedCall &c, int row0, int r1, int n0, bool there, int lane) {
-    constexpr int COLS = 128 / sizeof(O), TILES = 64 / COLS;          // channels of a tile, tiles of a half
+    constexpr int COLS = 128 / sizeof(O);              // channels of a staging tile
     const int rows = r1 - row0;                        // of the warp's 32, those that there are (or more)
     O *y = reinterpret_cast<O *>(c.y) + (int64_t)row0 * c.ys;
     uint8_t *mine = staging + lane * 128;
 #pragma unroll
-    for (int i = 0; i < 2 * TILES; ++i) {
-        const int h = i / TILES, n = n0 + h * 128 + i % TILES * COLS, left = c.n_out - n;
+    for (int i = 0; i < 128 / COLS; ++i) {
+        const int n = n0 + i * COLS, left = c.n_out - n;
         if (left <= 0 || rows <= 0) break;
         uint8_t *tile = staging + i % 2 * 4096, *row = mine + i % 2 * 4096;
         if (i % 2 == 0) {                              // the last stores have read the tiles
@@ -112,7 +146,7 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[2][32], uint8_t *stag
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const F2 *p = acc[h] + (i % TILES * COLS + j * (16 / (int)sizeof(O))) / 2;
+            const F2 *p = acc + (i * COLS + j * (16 / (int)sizeof(O))) / 2;
             uint4 v;
             if constexpr (sizeof(O) == 2) {
                 const float2 a = f2_get(p[0]), b = f2_get(p[1]), d = f2_get(p[2]), e = f2_get(p[3]);
@@ -155,18 +189,26 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[2][32], uint8_t *stag
     }
 }
 
-// A tile as the loads and the products need it, looked up one tile ahead.
-struct WideTile {
-    int e, r0, r1, n0;
-    bool both;                                         // channels in both halves
+// What the warps of a CTA know of a tile, by way of shared memory: one warp looks the
+// tiles up, a tile ahead (in every warp that took registers which its loop over the
+// blocks then missed, and 500 cycles for two divisions).
+constexpr int kGwTiles = 4;
+struct WideTiles {
+    int4 at[kGwTiles];                  // first row, the expert's end, first channel, expert
+    uint32_t there[kGwTiles][4];        // which of this CTA's 128 rows there are
+    int row[kGwTiles][128];             // and the rows of x that they take
+    uint64_t full[kGwTiles], empty[kGwTiles];
 };
-__device__ __forceinline__ WideTile wide_tile(const GroupTable &g, const GroupedCall &c, int tile, int tiles, int nn) {
-    WideTile w = {};
-    if (tile < tiles) {
-        const GroupTile t = find_group_tile(g, c.n_experts, tile, nn, kGwRows);
-        w = {t.e, t.r0, t.r1, t.n * kGwChannels, t.n * kGwChannels + 128 < c.n_out};
-    }
-    return w;
+// The j-th tile of this CTA, for a whole warp.
+__device__ __forceinline__ bool take_tile(WideTiles &w, int j, int4 &a, volatile int *abort, uint32_t *there = nullptr,
+                                          int quarter = 0) {
+    const int s = j % kGwTiles;
+    if (!mbar_wait_all(&w.full[s], (j / kGwTiles) & 1, abort)) return false;
+    a = w.at[s];
+    if (there) *there = w.there[s][quarter];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&w.empty[s]);
+    return true;
 }
 
 template <bool kBlock, typename O>
@@ -176,7 +218,9 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     constexpr int S = kGwStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GroupTable table;
-    __shared__ uint64_t full[S], empty[S], acc_full[2][2], acc_empty[2][2], drained;   // [half][accumulator]
+    __shared__ uint64_t full[S], empty[S], gathered[S], acc_full[2][2], acc_empty[2][2], drained[2], sc_full[2], sc_empty[2];   // [half][accumulator]
+    constexpr int H = kBlock ? 2 : 1;      // issuing warps; one product makes both halves in bf16
+    __shared__ WideTiles wide;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -184,20 +228,31 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     constexpr int kElems = kBlock ? 128 : 64;
     const int nk = (c.n_in + kElems - 1) / kElems, nn = (c.n_out + kGwChannels - 1) / kGwChannels;
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    float *factors = reinterpret_cast<float *>(smem + S * kGwStage + kGwEpiWarps * kGwStaging);
     volatile int *abort = &abort_flag;
 
     if (tid == 0) {
         prefetch_tensormap(&mx);
         prefetch_tensormap(&mw);
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], c.rows ? 5 : 1);       // the loads by TMA, two gathering warps of either CTA
-            mbar_init(&empty[s], 1);
+            mbar_init(&full[s], c.rows ? 3 : 1);       // the loads by TMA, either CTA's gathered rows
+            mbar_init(&gathered[s], 32 * kGwGather);
+            mbar_init(&empty[s], H);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&acc_full[i >> 1][i & 1], 1);
-            mbar_init(&acc_empty[i >> 1][i & 1], 2 * kGwEpiWarps);
+            mbar_init(&acc_empty[i >> 1][i & 1], 2 * kGwEpiWarps / H);
         }
-        mbar_init(&drained, 1);
+        for (int i = 0; i < kGwTiles; ++i) {
+            mbar_init(&wide.full[i], 1);
+            // the loads, the products, the gathered rows and the sums
+            mbar_init(&wide.empty[i], 1 + (rank == 0 ? H : 0) + (c.rows ? kGwGather : 0) + kGwEpiWarps);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&drained[h], 1);
+            mbar_init(&sc_full[h], 1);
+            mbar_init(&sc_empty[h], kGwEpiWarps);
+        }
         abort_flag = (smem_u32(smem) & 1023u) != 0;
         fence_mbar_init();
     }
@@ -217,20 +272,27 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     tc_fence_after();
     if (bad && tid == 0 && blockIdx.x == 0) flag_status(GDN_DEVSTAT_BAD_SEQLEN);
 
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGwRegsFew));
+    if (warp < kGwFirstEpi || warp >= kGwFirstGather)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGwRegsFew));
     if (warp == 0) {
         // Half of the weight rows and this CTA's 128 rows of x, counted on the leader's barrier.
         const bool one = elect_lane();
         const uint32_t lead = peer_smem(smem_u32(full), 0);
+        const uint64_t policy = c.offsets ? l2_first() : l2_normal();
         int s = 0, i = 0;
         uint32_t phase = 1;
         bool ok = true;
-        WideTile a = wide_tile(table, c, pair, tiles, nn), next = a;
-        for (int t = pair; t < tiles && ok; t += pairs, a = next) {
+        for (int t = pair, j = 0; t < tiles && ok; t += pairs, ++j) {
+            int4 a;
+            if (!take_tile(wide, j, a, abort)) {
+                ok = false;
+                break;
+            }
+            const bool both = a.z + 128 < c.n_out;
             // the product of a whole tile takes channels 0 .. 127 from the leader, that of a half 0 .. 63
-            const bool whole = !kBlock && a.both;
-            const int n0 = a.n0 + rank * (whole ? 128 : 64), n1 = n0 + (whole ? 64 : 128);
-            const uint32_t bytes = 2 * ((c.rows ? 0 : kGwX) + kGwHalf + (a.both ? kGwHalf : 0));
+            const bool whole = !kBlock && both;
+            const int n0 = a.z + rank * (whole ? 128 : 64), n1 = n0 + (whole ? 64 : 128), r0 = a.x + rank * 128;
+            const uint32_t bytes = 2 * ((c.rows ? 0 : kGwX) + kGwHalf + (both ? kGwHalf : 0));
 #pragma unroll 1
             for (int k = 0; k < nk; ++k, ++i) {
                 if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
@@ -241,12 +303,11 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                 const uint32_t bar = lead + s * 8;
                 if (i < keep && one) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                    if (!c.rows) pair_load_2d(st, &mx, bar, k * kElems, a.r0 + rank * 128);
-                    pair_load_3d(st + kGwX, &mw, bar, k * kElems, n0, a.e);
-                    if (a.both) pair_load_3d(st + kGwX + kGwHalf, &mw, bar, k * kElems, n1, a.e);
+                    if (!c.rows) pair_load_2d(st, &mx, bar, k * kElems, r0);
+                    pair_load_3d(st + kGwX, &mw, bar, k * kElems, n0, a.w, policy);
+                    if (both) pair_load_3d(st + kGwX + kGwHalf, &mw, bar, k * kElems, n1, a.w, policy);
                 }
                 __syncwarp();
-                if (k == 0) next = wide_tile(table, c, t + pairs, tiles, nn);
                 if (++s == S) {
                     s = 0;
                     phase ^= 1;
@@ -266,214 +327,292 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                 let_copies_land();
             }
         }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp <= H && rank == 0) {
+        const int h = warp - 1;
         constexpr uint32_t half = kBlock ? idesc_e4m3(256, 128) : idesc_bf16(256, 128);
         constexpr uint32_t full_tile = idesc_bf16(256, 256);
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
-        const uint32_t base = smem_u32(smem) >> 4, sums = tmem_base;
-        int s = 0, u[2] = {0, 0};          // accumulators of a half used so far
+        const uint32_t base = smem_u32(smem) >> 4, sums = tmem_base + h * 128, xh = (kGwX + h * kGwHalf) >> 4;
+        int s = 0, u = 0;                  // u: accumulators used so far
         uint32_t phase = 0, st = base;
-        bool ok = true, both = wide_tile(table, c, pair, tiles, nn).both, next = both;
-        for (int t = pair; t < tiles && ok; t += pairs, both = next) {
+        bool ok = true;
+        for (int t = pair, j = 0; t < tiles && ok; t += pairs, ++j) {
+            int4 a;
+            if (!take_tile(wide, j, a, abort)) {
+                ok = false;
+                break;
+            }
+            const bool both = a.z + 128 < c.n_out;
+            const uint32_t idesc = kBlock || !both ? half : full_tile;
+            const bool mine = h == 0 || both;          // else the stages are handed back as they are
 #pragma unroll 1
             for (int k = 0; k < nk; ++k) {
-                if (!mbar_wait_all(&full[s], phase, abort)) {
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int h = 0; h < (kBlock ? 2 : 1); ++h) {
-                    if (h == 1 && !both) break;
-                    const int b = u[h] & 1;
-                    if (kBlock || k == 0) {
-                        if (u[h] >= 2 && !mbar_wait_all(&acc_empty[h][b], ((u[h] >> 1) - 1) & 1, abort)) ok = false;
-                        if (!ok) break;
-                    }
-                    tc_fence_after();
-                    const bool last = kBlock || k == nk - 1;
-                    if (elect_lane()) {
-                        const uint32_t d = sums + (b * 2 + h) * 128;
-                        const uint64_t da = desc | st, db = desc | (st + ((kGwX + h * kGwHalf) >> 4));
-                        const uint32_t idesc = kBlock || !both ? half : full_tile;
+                // the operands first, which have mostly come: less lies behind the accumulator's release
+                ok = mbar_wait_all(&full[s], phase, abort);
+                if (ok && (kBlock || k == 0) && mine && u >= 2)
+                    ok = mbar_wait_all(&acc_empty[h][u & 1], ((u >> 1) - 1) & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                const bool last = kBlock || k == nk - 1;
+                if (elect_lane()) {
+                    if (mine) {
+                        const uint32_t d = sums + (u & 1) * 256;
+                        const uint64_t da = desc | st, db = desc | (st + xh);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             pair_mma<kBlock>(d, da + 2 * q, db + 2 * q, idesc, q > 0 || (!kBlock && k > 0));
-                        if (last) pair_commit(&acc_full[h][b]);
-                        if (!kBlock || h == 1 || !both) pair_commit(&empty[s]);
+                        if (last) pair_commit(&acc_full[h][u & 1]);
                     }
-                    __syncwarp();
-                    if (last) ++u[h];
+                    pair_commit(&empty[s]);
                 }
-                if (!ok) break;
+                __syncwarp();
+                if (last && mine) ++u;
                 st += kGwStage >> 4;
                 if (++s == S) {
                     s = 0;
                     st = base;
                     phase ^= 1;
                 }
-                if (k == 0) next = wide_tile(table, c, t + pairs, tiles, nn).both;   // behind the products
             }
         }
         // every arrival of the peer's has come, every product is done, before the pair may end
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            for (int j = max(0, u[h] - 2); ok && j < u[h]; ++j) ok = mbar_wait_all(&acc_empty[h][j & 1], (j >> 1) & 1, abort);
+        for (int j = max(0, u - 2); ok && j < u; ++j) ok = mbar_wait_all(&acc_empty[h][j & 1], (j >> 1) & 1, abort);
         if (elect_lane()) {
-            pair_commit(&drained, 1);
-            mbar_drain(&drained, 0);
+            pair_commit(&drained[h], 1);
+            mbar_drain(&drained[h], 0);
         }
         __syncwarp();
-    } else if (warp == 2 || warp == 3) {
-        // Gathered rows: a lane copies 16 bytes of every eighth row, a warp four whole rows
-        // at a time, and hands over a stage when its copies have come.
+    } else if (warp == kGwRelay) {
+        // Gathered rows are in this CTA's shared memory; the fence puts them before the tensor
+        // core's reads there, which the leader's product starts after the arrival: a relaxed one
+        // (with release at the cluster it waited for other copies in flight, 2,000 cycles).
         if (c.rows) {
             const uint32_t lead = peer_smem(smem_u32(full), 0);
-            const int sub = (warp - 2) * 4 + (lane >> 3);                  // of eight rows
-            const uint32_t to = smem_u32(smem) + sub * 128 + (((lane & 7) ^ sub) << 4);
-            const int64_t stride = c.xs * (kBlock ? 1 : 2);
+            int s = 0;
+            uint32_t phase = 0;
+            const int64_t all = tiles > pair ? (int64_t)((tiles - pair + pairs - 1) / pairs) * nk : 0;
+#pragma unroll 1
+            for (int64_t i = 0; i < min(all, (int64_t)keep); ++i) {
+                if (!mbar_wait_all(&gathered[s], phase, abort)) break;
+                fence_async_smem();
+                if (lane == 0) mbar_arrive_cluster(lead + s * 8);
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp >= kGwFirstGather) {
+        // A lane copies 16 bytes of a row, a warp four whole rows at a time and every third four.
+        // Where there is no row the stage keeps what it holds: a row of the product that is not
+        // written, or written as zeros.
+        if (c.rows) {
+            constexpr int N = (32 + kGwGather - 1) / kGwGather;
+            const int first = warp - kGwFirstGather, sub = lane >> 3;       // of 32 fours; row of it
+            const uint32_t to = smem_u32(smem) + sub * 128;
+            // the 16 bytes' place in the swizzled rows of even fours, and of odd ones
+            const uint32_t even = ((lane & 7) ^ sub) << 4, odd = ((lane & 7) ^ (sub + 4)) << 4;
+            const uint32_t stride16 = (uint32_t)(c.xs * (kBlock ? 1 : 2) / 16);   // a row in pieces (below 2^32: strides < 2^36)
             const int bytes = c.n_in * (kBlock ? 1 : 2) - (lane & 7) * 16;  // of the row from this lane's first on
+            const int whole = c.n_in * (kBlock ? 1 : 2) / 128;              // blocks of 128 bytes
             int s = 0, i = 0;
             uint32_t phase = 1;
             bool ok = true;
-            int row[16], next_row[16];
-            auto look = [&](int tile, int (&r)[16]) {
-                const WideTile a = wide_tile(table, c, tile, tiles, nn);
-                const int r0 = a.r0 + rank * 128 + sub;
+            for (int t = pair, tile = 0; t < tiles && ok; t += pairs, ++tile) {
+                const int slot = tile % kGwTiles;
+                if (!mbar_wait_all(&wide.full[slot], (tile / kGwTiles) & 1, abort)) break;
+                int row[N];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) r[j] = tile < tiles ? group_x_row(c, r0 + j * 8, a.r1) : c.n_x;
-            };
-            look(pair, row);
-            auto hand_over = [&](int j) {                                   // stage of block j
-                // The copies lie in this CTA's own shared memory and, by the fence, before the tensor
-                // core's reads there, which the leader's product starts after the arrival: a relaxed
-                // one (with release at the cluster it waited for the copies still in flight, 2,000
-                // cycles a block).
-                fence_async_smem();
+                for (int j = 0; j < N; ++j) {
+                    const int four = first + j * kGwGather;
+                    row[j] = four < 32 ? wide.row[slot][four * 4 + sub] : c.n_x;
+                }
                 __syncwarp();
-                if (lane == 0 && j < keep) mbar_arrive_cluster(lead + j % S * 8);
-            };
-            for (int t = pair; t < tiles && ok; t += pairs) {
+                if (lane == 0) mbar_arrive(&wide.empty[slot]);
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + (lane & 7) * 16;
 #pragma unroll 1
-                for (int k = 0; k < nk; ++k, ++i) {
+                for (int k = 0; k < nk; ++k, ++i, src += 128) {
                     if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
                         ok = false;
                         break;
                     }
-                    const int n = min(16, max(0, bytes - k * 128));
-                    const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + k * 128 + (lane & 7) * 16;
                     if (i < keep) {
+                        const uint32_t st = to + s * kGwStage + first * 512;
+                        if (k < whole) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const bool on = row[j] < c.n_x && n > 0;
-                            copy16(to + s * kGwStage + j * 1024, on ? src + row[j] * stride : c.x, on ? n : 0);
+                            for (int j = 0; j < N; ++j)
+                                copy16_if(row[j] < c.n_x, st + j * kGwGather * 512 + ((first + j * kGwGather) & 1 ? odd : even),
+                                          src + ((uint64_t)row[j] * stride16 << 4));
+                        } else {
+                            const int n = min(16, max(0, bytes - k * 128));
+#pragma unroll 1
+                            for (int j = 0; j < N; ++j) {
+                                int at = row[0];
+#pragma unroll
+                                for (int z = 1; z < N; ++z) at = z == j ? row[z] : at;      // no array in memory
+                                if (at < c.n_x)
+                                    copy16(st + j * kGwGather * 512 + ((first + j * kGwGather) & 1 ? odd : even),
+                                           n > 0 ? src + ((uint64_t)at * stride16 << 4) : c.x, n);
+                            }
                         }
+                        copies_arrive(&gathered[s]);
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (i >= kGwLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kGwLag) : "memory");
-                        hand_over(i - kGwLag);
-                    }
-                    if (k == 0) look(t + pairs, next_row);
                     if (++s == S) {
                         s = 0;
                         phase ^= 1;
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) row[j] = next_row[j];
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            for (int j = max(0, i - kGwLag); ok && j < i; ++j) hand_over(j);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
-    } else if (warp >= 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGwRegsMany));
-        // Accumulator lane 32 q + l is token row 32 q + l of this CTA's 128; the two warps
-        // of a quadrant take 64 channels each of either half.
-        const int q = warp & 3, part = (warp - 4) >> 2;
-        uint8_t *staging = smem + S * kGwStage + (warp - 4) * kGwStaging;
-        int u[2] = {0, 0};
+    } else if (warp == kGwTile) {
+        // Looks up the tiles, and makes the factors sx sw of the CTA's 128 rows, eight blocks at
+        // a time, for either half.
+        int v = 0;
         bool ok = true, wrong = false;
-        WideTile a = wide_tile(table, c, pair, tiles, nn), next = a;
-        auto x_row = [&](const WideTile &w) {
-            const int r = w.r0 + rank * 128 + q * 32 + lane;
-            if (c.rows && r < w.r1) wrong |= c.rows[r] >= c.n_x;
-            return group_x_row(c, r, w.r1);
-        };
-        int xr = x_row(a), next_xr = xr;
-        for (int t = pair; t < tiles && ok; t += pairs, a = next, xr = next_xr) {
-            const bool there = xr < c.n_x;
-            const float *sx = kBlock ? c.sx + (int64_t)(there ? xr : 0) * c.kb : nullptr;
-            const float *sw = kBlock ? c.sw + ((int64_t)a.e * c.nb + a.n0 / 128) * c.kb : nullptr;
-            const int second = a.both ? c.kb : 0;           // the other half's scales
-            F2 acc[2][32];
+        int xr[4], next_xr[4];
+        const float *sw = nullptr, *next_sw = nullptr;
+        auto tell = [&](int t, int j) {
+            if (t >= tiles) return true;
+            const GroupTile g = find_group_tile(table, c.n_experts, t, nn, kGwRows);
+            const int s = j % kGwTiles, n0 = g.n * kGwChannels;
+            uint32_t there[4];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i / 32][i % 32] = f2(0.f, 0.f);
-            // factors two blocks ahead
-            float f0 = 1.f, f1 = 1.f, xa = 0.f, wa = 0.f, wb = 0.f;
-            if (kBlock) {
-                f0 = sx[0] * sw[0];
-                f1 = sx[0] * sw[second];
-                if (nk > 1) {
-                    xa = sx[1];
-                    wa = sw[1];
-                    wb = sw[second + 1];
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int r = g.r0 + rank * 128 + i * 32 + lane;
+                next_xr[i] = group_x_row(c, r, g.r1);
+                if (c.rows && r < g.r1) wrong |= c.rows[r] >= c.n_x;
+                there[i] = __ballot_sync(0xffffffffu, next_xr[i] < c.n_x);
             }
+            if (kBlock) next_sw = c.sw + ((int64_t)g.e * c.nb + n0 / 128) * c.kb + (lane < kGwChunk || n0 + 128 >= c.n_out ? 0 : c.kb);
+            if (j >= kGwTiles && !mbar_wait_warp(&wide.empty[s], (j / kGwTiles - 1) & 1, abort)) return false;
+            if (lane == 0) {
+                wide.at[s] = make_int4(g.r0, g.r1, n0, g.e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) wide.there[s][i] = there[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wide.row[s][i * 32 + lane] = next_xr[i];
+                if (next_xr[i] >= c.n_x) next_xr[i] = 0;   // whose scale is read, and not used
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wide.full[s]);
+            return true;
+        };
+        ok = tell(pair, 0);
+        for (int t = pair, j = 0; t < tiles && ok; t += pairs, ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xr[i] = next_xr[i];
+            sw = next_sw;
+            ok = tell(t + pairs, j + 1);
+            for (int k0 = 0; kBlock && k0 < nk && ok; k0 += kGwChunk, ++v) {
+                // lane i: the weight's scale of block k0 + i % 8 in half i / 8
+                const int kw = k0 + lane % kGwChunk;
+                const float w = lane < 2 * kGwChunk && kw < nk ? sw[kw] : 0.f;
+                if (v >= 2 && !mbar_wait_warp(&sc_empty[v & 1], ((v >> 1) - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                float *to = factors + (v & 1) * (kGwFactors / 4) + lane;
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const float *sx = c.sx + (int64_t)(i < 2 ? i ? xr[1] : xr[0] : i < 3 ? xr[2] : xr[3]) * c.kb + k0;
+                    float x[kGwChunk];
+                    if (k0 + kGwChunk <= nk && c.sx16) {
+                        const float4 p = reinterpret_cast<const float4 *>(sx)[0], q = reinterpret_cast<const float4 *>(sx)[1];
+                        x[0] = p.x; x[1] = p.y; x[2] = p.z; x[3] = p.w;
+                        x[4] = q.x; x[5] = q.y; x[6] = q.z; x[7] = q.w;
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < kGwChunk; ++z) x[z] = k0 + z < nk ? sx[z] : 0.f;
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2 * kGwChunk; ++z)
+                        to[z * 128 + i * 32] = x[z % kGwChunk] * __shfl_sync(0xffffffffu, w, z);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[v & 1]);
+            }
+        }
+        if (wrong) flag_status(GDN_DEVSTAT_BAD_INDEX);
+    } else if (warp >= kGwFirstEpi && warp < kGwFirstGather) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGwRegsMany));
+        // Accumulator lane 32 q + l is token row 32 q + l of this CTA's 128; four warps a half.
+        const int q = warp & 3, h = (warp - kGwFirstEpi) >> 2, p = kBlock ? h : 0;
+        uint8_t *staging = smem + S * kGwStage + (warp - kGwFirstEpi) * kGwStaging;
+        int u = 0, v = 0;                  // accumulators and chunks of factors used so far
+        bool ok = true, ready = false;     // the next accumulator is known to be there
+        for (int t = pair, tile = 0; t < tiles && ok; t += pairs, ++tile) {
+            int4 a;
+            uint32_t there;
+            if (!take_tile(wide, tile, a, abort, &there, q)) break;
+            const bool mine = !kBlock || h == 0 || a.z + 128 < c.n_out;
+            F2 acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = f2(0.f, 0.f);
+            float f0 = 1.f;
+            const float *from_f = factors;
 #pragma unroll 1
             for (int k = 0; k < (kBlock ? nk : 1); ++k) {
-                float xn = 0.f, wn = 0.f, wm = 0.f;
-                if (kBlock && k + 2 < nk) {
-                    xn = sx[k + 2];
-                    wn = sw[k + 2];
-                    wm = sw[second + k + 2];
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && !a.both) break;
-                    constexpr bool kWhole = !kBlock;           // one product for both halves
-                    int &uses = u[kWhole ? 0 : h];
-                    const int b = uses & 1;
-                    if ((!kWhole || h == 0) && !mbar_wait_all(&acc_full[kWhole ? 0 : h][b], (uses >> 1) & 1, abort)) {
+                if (kBlock && k % kGwChunk == 0) {
+                    if (!mbar_wait_all(&sc_full[v & 1], (v >> 1) & 1, abort)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t from = tmem_addr(tmem_base, q * 32, (b * 2 + h) * 128 + part * 64);
-                    const float f = h ? f1 : f0;
-                    uint32_t r[2][32];
-                    tmem_ask32(from, r[0]);
-                    tmem_ask32(from + 32, r[1]);
-                    tmem_wait32(r[0]);
-                    tmem_wait32(r[1]);
-                    tc_fence_before();                         // all of it has been read
+                    from_f = factors + (v & 1) * (kGwFactors / 4) + h * kGwChunk * 128 + q * 32 + lane;
+                    f0 = *from_f;
+                }
+                // a chunk's last factor is read: its block is still to come
+                const bool end = kBlock && (k % kGwChunk == kGwChunk - 1 || k == nk - 1);
+                if (end) {
                     __syncwarp();
-                    if (!kWhole || h == 1 || !a.both) {
-                        if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[kWhole ? 0 : h][b]), 0));
-                        ++uses;
+                    if (lane == 0) mbar_arrive(&sc_empty[v & 1]);
+                    ++v;
+                }
+                if (!mine) continue;                       // no channels: only the factors pass
+                const F2 f = f2(f0, f0);
+                const int b = u & 1;
+                if (!ready && !mbar_wait_all(&acc_full[p][b], (u >> 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t from = tmem_addr(tmem_base, q * 32, (b * 2 + h) * 128);
+                uint32_t r[2][32];
+                tmem_ask32(from, r[0]);
+                ++u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    tmem_wait32(r[j & 1]);
+                    if (j < 3) {
+                        tmem_ask32(from + (j + 1) * 32, r[(j + 1) & 1]);
+                    } else {                               // all of it has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[p][b]), 0));
+                        // the next block's barrier and factor, while this one's last products are added
+                        ready = mbar_test(&acc_full[p][u & 1], (u >> 1) & 1);
+                        if (kBlock && !end) {
+                            from_f += 128;
+                            f0 = *from_f;
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const F2 v = f2_bits(r[i / 16][i % 16 * 2], r[i / 16][i % 16 * 2 + 1]);
-                        acc[h][i] = kBlock ? f2_fma(v, f2(f, f), acc[h][i]) : v;
+                    for (int i = 0; i < 16; ++i) {
+                        const F2 v2 = f2_bits(r[j & 1][2 * i], r[j & 1][2 * i + 1]);
+                        acc[j * 16 + i] = kBlock ? f2_fma(v2, f, acc[j * 16 + i]) : v2;
                     }
                 }
-                if (!ok) break;
-                if (k == 0) {
-                    next = wide_tile(table, c, t + pairs, tiles, nn);
-                    next_xr = x_row(next);
-                }
-                f0 = xa * wa;
-                f1 = xa * wb;
-                xa = xn;
-                wa = wn;
-                wb = wm;
+                ready = __all_sync(0xffffffffu, ready);
             }
             if (!ok) break;
-            wide_store<O>(acc, staging, &my, c, a.r0 + rank * 128 + q * 32, a.r1, a.n0 + part * 64, there, lane);
+            if (mine)
+                wide_store<O>(acc, staging, &my, c, a.x + rank * 128 + q * 32, a.y, a.z + h * 128, there >> lane & 1, lane);
         }
         if (lane == 0) bulk_wait_read_all();       // the staging tiles stay until they are read
         __syncwarp();
-        if (wrong) flag_status(GDN_DEVSTAT_BAD_INDEX);
         tc_fence_before();
     }
     __syncthreads();
