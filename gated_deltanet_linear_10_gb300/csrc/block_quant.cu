@@ -2,7 +2,8 @@
 // row, as the products with block scales read them:
 //   v = x, or SiLU(x[:n]) x[n:]
 //   scale[t][b] = max(max_{j in block b} |v_tj| / 448, 2^-126), q = v / scale
-// 16 lanes hold a block, 8 channels each; the block's maximum is four shuffles.
+// 16 lanes hold a block, 8 channels each; the block's maximum is four shuffles.  A
+// thread asks for the channels of two blocks before it works on the first.
 #include <algorithm>
 
 #include "quant.cuh"
@@ -11,64 +12,93 @@ namespace gdn {
 
 constexpr int kQuantBlock = 128;
 
+// Quotients by a number that the host knows, of dividends below 2^31.
+struct QuickDiv {
+    uint32_t mul, shift;
+    explicit QuickDiv(uint32_t d) {
+        shift = 0;
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((1ull << (32 + shift)) + d - 1) / d - (1ull << 32));     // of 33 bits, the highest left out
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 // kVec: rows and blocks on vectors of 8 channels; else lane l holds channels l + 16 i.
 template <typename T, bool kGlu, bool kVec>
 __global__ void __launch_bounds__(256)
-block_quant_kernel(const T *__restrict__ x, int64_t xs, int64_t items, int n, int blocks, uint8_t *__restrict__ y,
-                   int64_t ys, float *__restrict__ y_scale) {
+block_quant_kernel(const T *__restrict__ x, int64_t xs, int64_t items, int n, int blocks, QuickDiv by_blocks,
+                   uint8_t *__restrict__ y, int64_t ys, float *__restrict__ y_scale) {
+    constexpr int U = 2;
     griddep_wait();
     griddep_launch();
     const int l = threadIdx.x & 15;
     const int64_t step = (int64_t)gridDim.x * 16;
+    const bool small = items < (1ll << 31);
     // whole warps stay in the loop: their shuffles take both halves
-    for (int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); i - ((threadIdx.x >> 4) & 1) < items; i += step) {
-        const bool on = i < items;
-        const int64_t t = on ? i / blocks : 0;
-        const int b = on ? (int)(i - t * blocks) : 0;
-        const int c0 = b * kQuantBlock + (kVec ? l * 8 : l);
-        float v[8] = {};
-        const T *p = x + t * xs + c0;
-        if (kVec) {
-            if (on && c0 < n) {
-                RawVec<T, 8> raw, raw2;
-                raw.load(p);
-                if (kGlu) raw2.load(p + n);
-                F2 a[4], u[4];
-                raw.pairs(a);
-                unpair<8>(a, v);
-                if (kGlu) {
-                    raw2.pairs(u);
-                    float f[8];
-                    unpair<8>(u, f);
+    const int64_t half = (threadIdx.x >> 4) & 1;
+    for (int64_t i0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); i0 - half < items; i0 += U * step) {
+        int64_t t[U];
+        int c0[U];
+        RawVec<T, 8> gate[U], up[U];
+        float v[U][8] = {};
+        bool on[U];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = silu_f(v[j]) * f[j];
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * step;
+            on[u] = i < items;
+            t[u] = !on[u] ? 0 : small ? by_blocks((uint32_t)i) : i / blocks;
+            c0[u] = (on[u] ? (int)(i - t[u] * blocks) : 0) * kQuantBlock + (kVec ? l * 8 : l);
+            const T *p = x + t[u] * xs + c0[u];
+            if (kVec) {
+                if (on[u] && c0[u] < n) {
+                    gate[u].load(p);
+                    if (kGlu) up[u].load(p + n);
+                } else {
+                    gate[u].zero();
+                    up[u].zero();
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (on[u] && c0[u] + 16 * j < n) {
+                        v[u][j] = Io<T>::load(p + 16 * j);
+                        if (kGlu) v[u][j] = silu_f(v[u][j]) * Io<T>::load(p + n + 16 * j);
+                    }
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (on && c0 + 16 * j < n) {
-                    v[j] = Io<T>::load(p + 16 * j);
-                    if (kGlu) v[j] = silu_f(v[j]) * Io<T>::load(p + n + 16 * j);
-                }
         }
-        float mx = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) mx = max_abs_nan(mx, v[j], v[j + 1]);
+        for (int u = 0; u < U; ++u) {
+            if (kVec) {
+                F2 a[4], b[4];
+                gate[u].pairs(a);
+                if (kGlu) {
+                    up[u].pairs(b);
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float scale = e4m3_scale(mx), q = 1.0f / scale;
-        if (!on) continue;
-        if (l == 0) y_scale[i] = scale;
-        uint8_t *o = y + t * ys + c0;
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 g = f2_get(a[j]);
+                        a[j] = f2_mul(f2(silu_f(g.x), silu_f(g.y)), b[j]);
+                    }
+                }
+                unpair<8>(a, v[u]);
+            }
+            float mx = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= q;
-        if (kVec) {
-            if (c0 < n) store_row<8>(reinterpret_cast<E4m3 *>(o), v);
-        } else {
+            for (int j = 0; j < 8; j += 2) mx = max_abs_nan(mx, v[u][j], v[u][j + 1]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + 16 * j < n) store_row<1>(reinterpret_cast<E4m3 *>(o + 16 * j), v + j);
+            for (int off = 8; off > 0; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float scale = e4m3_scale(mx), q = 1.0f / scale;
+            if (!on[u]) continue;
+            if (l == 0) y_scale[i0 + u * step] = scale;
+            uint8_t *o = y + t[u] * ys + c0[u];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[u][j] *= q;
+            if (kVec) {
+                if (c0[u] < n) store_row<8>(reinterpret_cast<E4m3 *>(o), v[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c0[u] + 16 * j < n) store_row<1>(reinterpret_cast<E4m3 *>(o + 16 * j), v[u] + j);
+            }
         }
     }
 }
@@ -96,7 +126,7 @@ extern "C" gdn_status gdn_block_quant(const void *x, int64_t x_row_stride, int64
     auto go = [&](auto kernel, auto one) {
         using T = decltype(one);
         return launch_after(kernel, dim3(grid), dim3(256), 0, (cudaStream_t)stream, (const T *)x, x_row_stride, items, n,
-                            blocks, (uint8_t *)y, y_row_stride, y_scale);
+                            blocks, QuickDiv(blocks), (uint8_t *)y, y_row_stride, y_scale);
     };
     cudaError_t e;
 #define GDN_BQ(T)                                                                       \

@@ -2,14 +2,21 @@
 // and sorts the pairs (token, choice) by expert, and the weighted sum that brings
 // the experts' rows back to the tokens.
 //
-// Router.  One warp a token.  The order of the logits is that of 32-bit keys
-// (key_of), ties by the lowest index; the k largest are taken one after the
-// other.  The sort is a counting sort: a chunk of 64 tokens keeps, per expert, a
-// word of 64 bits with the tokens that ask for it, so that a pair's place within
-// its chunk is a population count of the bits below it.  That order (by expert,
-// then by token) depends on no timing.
+// Router.  One warp a token, the logits as 32-bit keys of the same order (key_of).
+// The top-th largest of the lanes' largest keys is a bound that at least `top`
+// experts reach and few others do; these go to shared memory, and an expert's place
+// among them is the number of larger ones (ties: of lower index).  290 instructions a
+// token of 512 experts instead of 650 for taking the largest ten times.
+//
+// The sort is a counting sort: a chunk of up to 64 tokens keeps, per expert, a word
+// of 64 bits with the tokens that ask for it, so that a pair's place within its chunk
+// is a population count of the bits below it.  That order (by expert, then by token)
+// depends on no timing.  Up to 512 tokens are one launch of one cluster, whose CTAs
+// read each other's words; more are three launches: choices and counts, sums over the
+// chunks, places.
 #include <algorithm>
 
+#include "linear.cuh"
 #include "quant.cuh"
 
 namespace gdn {
@@ -19,88 +26,236 @@ GDN_STATUS_READER(read_status_moe, g_status_moe)
 
 constexpr int kMaxExperts = 1024, kMaxTop = 32;
 constexpr int kChunk = 64;                 // tokens of a chunk
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 256, kTopThreads = 512;
+constexpr int kClusterTokens = 512;        // the most of the single launch: eight chunks
 
-// Larger logits have larger keys; -0 equals 0 and a NaN is above everything.
-// 0 is no logit's key.
+// Larger logits have larger keys; -0 equals 0 (by the addition, which also makes every
+// NaN the same, above everything).  0 is no logit's key.
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t b = __float_as_uint(v + 0.0f);
-    return v != v ? 0xffffffffu : b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u);
+    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k == 0xffffffffu ? 0x7fffffffu : k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu));
+    return __uint_as_float(k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu));
 }
 
-// A warp's token: lane j < top gets the j-th choice.  PER: experts of a lane.
-template <typename T, int PER>
-__device__ __forceinline__ void route_token(const T *row, int experts, int top, bool renorm, int lane, int &id,
-                                            float &weight) {
+// A warp's token: its `top` choices to ids and weights, each(expert, place) for every one
+// of them.  PER: experts of a lane, VEC of them neighbours; cands: kCands words of the
+// warp's own, for the candidates.
+template <typename T, int PER, int VEC, int kCands, typename F>
+__device__ __forceinline__ void route_token(const T *row, int experts, int top, bool renorm, int lane, uint64_t *cands,
+                                            int32_t *ids, float *weights, F each) {
     uint32_t key[PER];
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = e < experts ? key_of(Io<T>::load(row + e)) : 0u;
-    }
-    float all = 0.f;
-    uint32_t mine = 0, first = 0;
-    id = 0;
-    for (int j = 0; j < top; ++j) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-        best = __reduce_max_sync(0xffffffffu, best);
-        int at = kMaxExperts;
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == best) at = i * 32 + lane;
-        at = __reduce_min_sync(0xffffffffu, at);
-        if (j == 0) {
-            first = best;
-            if (!renorm) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (key[i]) all += expf(key_value(key[i]) - key_value(first));
-            }
+    for (int i = 0; i < PER; i += VEC) {
+        const int e = i * 32 + lane * VEC;
+        float v[VEC];
+        if constexpr (VEC == 1) {
+            v[0] = e < experts ? Io<T>::load(row + e) : 0.f;
+        } else if (e < experts) {
+            Vec16<T>::load(row + e, v);
         }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            key[i + j] = e < experts ? key_of(v[j]) : 0u;
+            most = max(most, key[i + j]);
+        }
+    }
+    // the bound
+    uint32_t left = most, bound = 0, first = 0;
+    for (int n = 0; n < top;) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, left);
+        if (n == 0) first = best;
+        bound = best;
+        if (best == 0) break;                  // fewer lanes with an expert than choices: all experts
+        const bool hit = left == best;
+        n += __popc(__ballot_sync(0xffffffffu, hit));
+        if (hit) left = 0;
+    }
+    bound = max(bound, 1u);
+    const float top1 = key_value(first);
+    float all = 0.f;
+    if (!renorm) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (at == i * 32 + lane) key[i] = 0;
-        if (lane == j) {
-            mine = best;
-            id = at;
-        }
-    }
-    const float top1 = key_value(first);
-    const float p = lane < top ? expf(key_value(mine) - top1) : 0.f;
-    if (renorm) all = p;
+            if (key[i]) all += expf(key_value(key[i]) - top1);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-    weight = top1 == -INFINITY ? 0.f : p / all;      // no expert is open to the token
+        for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+    }
+    int cnt = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) cnt += key[i] >= bound;
+    int scan = cnt;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += o;
+    }
+    const int total = __shfl_sync(0xffffffffu, scan, 31);
+    // a candidate: its key, then its index turned round, so that the larger word goes first
+    auto word = [&](int i) { return (uint64_t)key[i] << 32 | (uint32_t)~(i / VEC * VEC * 32 + lane * VEC + i % VEC); };
+    __syncwarp();                              // the last token's are read
+    if (total <= kCands) {
+        int at = scan - cnt;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (key[i] >= bound) cands[at++] = word(i);
+        __syncwarp();
+    } else {                                   // many alike: the largest, one after the other
+        for (int j = 0; j < top; ++j) {
+            uint64_t best = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint64_t w = key[i] ? word(i) : 0;
+                best = w > best ? w : best;
+            }
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+            const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+            const uint64_t is = (uint64_t)hi << 32 | lo;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (word(i) == is) key[i] = 0;
+            if (lane == 0) cands[j] = is;
+        }
+        __syncwarp();
+    }
+    const int n = total <= kCands ? total : top;
+    float p[kCands / 32];
+    int rank[kCands / 32];
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kCands / 32; ++q) {
+        rank[q] = kCands;
+        if (q * 32 >= n) continue;
+        const uint64_t mine = q * 32 + lane < n ? cands[q * 32 + lane] : 0;
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += cands[j] > mine;
+        rank[q] = mine ? r : kCands;
+        p[q] = rank[q] < top ? expf(key_value((uint32_t)(mine >> 32)) - top1) : 0.f;
+        sum += p[q];
+    }
+    if (renorm) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        all = sum;
+    }
+#pragma unroll
+    for (int q = 0; q < kCands / 32; ++q)
+        if (rank[q] < top) {
+            const int id = (int)~(uint32_t)cands[q * 32 + lane];
+            ids[rank[q]] = id;
+            weights[rank[q]] = top1 == -INFINITY ? 0.f : p[q] / all;      // no expert is open to the token
+            each(id, rank[q]);
+        }
 }
 
 // A chunk's tokens: ids and weights out, and per expert how many ask for it.
-template <typename T, int PER>
-__global__ void __launch_bounds__(kRouteThreads)
+template <typename T, int PER, int VEC>
+__global__ void __launch_bounds__(kTopThreads)
 route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int experts, int top, bool renorm,
                  int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ counts) {
     __shared__ int count[kMaxExperts];
+    __shared__ uint64_t cands[kTopThreads / 32][64];
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * kChunk;
-    for (int e = tid; e < experts; e += kRouteThreads) count[e] = 0;
+    for (int e = tid; e < experts; e += kTopThreads) count[e] = 0;
     __syncthreads();
-    for (int t = t0 + (tid >> 5); t < min(t0 + kChunk, n_tokens); t += kRouteThreads / 32) {
-        int id;
-        float w;
-        route_token<T, PER>(logits + t * ls, experts, top, renorm, lane, id, w);
-        if (lane < top) {
-            ids[(int64_t)t * top + lane] = id;
-            weights[(int64_t)t * top + lane] = w;
-            atomicAdd(&count[id], 1);
-        }
-    }
+    for (int t = t0 + (tid >> 5); t < min(t0 + kChunk, n_tokens); t += kTopThreads / 32)
+        route_token<T, PER, VEC, 64>(logits + t * ls, experts, top, renorm, lane, cands[tid >> 5], ids + (int64_t)t * top,
+                                     weights + (int64_t)t * top, [&](int id, int) { atomicAdd(&count[id], 1); });
     __syncthreads();
     griddep_launch();
-    for (int e = tid; e < experts; e += kRouteThreads) counts[(int64_t)blockIdx.x * experts + e] = count[e];
+    for (int e = tid; e < experts; e += kTopThreads) counts[(int64_t)blockIdx.x * experts + e] = count[e];
+}
+
+// Experts' sums in front of each one, by the whole CTA: v[i] of expert tid * Q + i becomes
+// the sum of those before it; returns the sum of all.
+template <int Q> __device__ __forceinline__ int scan_experts(int (&v)[Q], int *warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const int x = v[i];
+        v[i] = sum;
+        sum += x;
+    }
+    int scan = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += o;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int front = scan - sum, all = 0;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
+        if (i < warp) front += warp_sum[i];
+        all += warp_sum[i];
+    }
+#pragma unroll
+    for (int i = 0; i < Q; ++i) v[i] += front;
+    return all;
+}
+
+__device__ __forceinline__ uint64_t load_of_rank(const void *p, uint32_t rank) {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer_smem(tc::smem_u32(p), rank)) : "memory");
+    return v;
+}
+// Up to kClusterTokens tokens in one launch: a cluster of 1, 2, 4 or 8 CTAs, a chunk each.
+constexpr int kClusterThreads = 1024;
+template <typename T, int PER, int VEC>
+__global__ void __launch_bounds__(kClusterThreads)
+route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int experts, int top, bool renorm,
+                     int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ offsets,
+                     int32_t *__restrict__ rows, int32_t *__restrict__ slots) {
+    __shared__ unsigned long long mask[kMaxExperts];
+    __shared__ int base[kMaxExperts], warp_sum[32];
+    __shared__ uint64_t cands[kClusterThreads / 32][64];
+    __shared__ uint16_t pick[kChunk * kMaxTop];
+    static_assert(kClusterThreads >= kMaxExperts, "a thread an expert");
+    const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x;
+    const uint32_t rank = cta_rank();
+    const int per = (n_tokens + ctas - 1) / ctas, t0 = rank * per, n = max(0, min(per, n_tokens - t0));
+    mask[tid] = 0;
+    griddep_wait();
+    griddep_launch();
+    __syncthreads();
+    for (int t = tid >> 5; t < n; t += kClusterThreads / 32) {
+        int32_t *to = ids + (int64_t)(t0 + t) * top;
+        route_token<T, PER, VEC, 64>(logits + (t0 + t) * ls, experts, top, renorm, lane, cands[tid >> 5], to,
+                                 weights + (int64_t)(t0 + t) * top,
+                                 [&](int id, int place) {
+                                     atomicOr(&mask[id], 1ull << t);
+                                     pick[t * top + place] = (uint16_t)id;
+                                 });
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    int v[1] = {0}, before = 0;
+    if (tid < experts)
+        for (int r = 0; r < ctas; ++r) {
+            const int c = __popcll(r == (int)rank ? mask[tid] : load_of_rank(&mask[tid], r));
+            v[0] += c;
+            if (r < (int)rank) before += c;
+        }
+    const int all = scan_experts(v, warp_sum);
+    if (tid < experts) {
+        base[tid] = v[0] + before;
+        if (rank == 0) offsets[tid] = v[0];
+    }
+    if (rank == 0 && tid == 0) offsets[experts] = all;
+    __syncthreads();
+    for (int i = tid; i < n * top; i += kClusterThreads) {
+        const int t = i / top, e = pick[i];
+        const int r = base[e] + __popcll(mask[e] & ((1ull << t) - 1));
+        rows[r] = t0 + t;
+        slots[(int64_t)t0 * top + i] = r;
+    }
+    cluster_arrive_relaxed();
+    cluster_wait();                             // no CTA ends while another one may read its words
 }
 
 // Per expert the sum over the chunks in front of each one, in place, and over all
@@ -137,37 +292,23 @@ route_place_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ 
     __shared__ int base[kMaxExperts], warp_sum[kRouteThreads / 32];
     griddep_wait();
     griddep_launch();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t0 = blockIdx.x * kChunk;
+    const int tid = threadIdx.x, t0 = blockIdx.x * kChunk;
     const int n = min(kChunk, n_tokens - t0) * top;           // pairs (none: only the offsets)
-    // experts in front of each one, four of them a thread
-    constexpr int Q = kMaxExperts / kRouteThreads;
-    int v[Q], sum = 0;
+    constexpr int Q = kMaxExperts / kRouteThreads;          // experts of a thread
+    int v[Q];
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const int e = tid * Q + i;
-        v[i] = sum;
-        sum += e < experts && totals ? totals[e] : 0;
-    }
-    int scan = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, scan, off);
-        if (lane >= off) scan += o;
-    }
-    if (lane == 31) warp_sum[warp] = scan;
+    for (int i = 0; i < Q; ++i) v[i] = tid * Q + i < experts && totals ? totals[tid * Q + i] : 0;
     for (int e = tid; e < experts; e += kRouteThreads) mask[e] = 0;
-    __syncthreads();
-    int front = scan - sum;
-    for (int i = 0; i < warp; ++i) front += warp_sum[i];
+    const int all = scan_experts(v, warp_sum);
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
         const int e = tid * Q + i;
         if (e < experts) {
-            base[e] = front + v[i] + (n > 0 ? counts[(int64_t)blockIdx.x * experts + e] : 0);
-            if (blockIdx.x == 0) offsets[e] = front + v[i];
+            base[e] = v[i] + (n > 0 ? counts[(int64_t)blockIdx.x * experts + e] : 0);
+            if (blockIdx.x == 0) offsets[e] = v[i];
         }
     }
-    if (blockIdx.x == 0 && tid == kRouteThreads - 1) offsets[experts] = front + sum;
+    if (blockIdx.x == 0 && tid == 0) offsets[experts] = all;
     for (int i = tid; i < n; i += kRouteThreads) atomicOr(&mask[ids[(int64_t)t0 * top + i]], 1ull << (i / top));
     __syncthreads();
     for (int i = tid; i < n; i += kRouteThreads) {
@@ -178,60 +319,112 @@ route_place_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ 
     }
 }
 
-template <typename T>
-static cudaError_t launch_top(const void *logits, int64_t ls, int n, int experts, int top, bool renorm, int32_t *ids,
-                              float *weights, int32_t *counts, cudaStream_t s) {
-    auto go = [&](auto kernel) {
-        return launch_after(kernel, dim3((n + kChunk - 1) / kChunk), dim3(kRouteThreads), 0, s, (const T *)logits, ls, n,
-                            experts, top, renorm, ids, weights, counts);
-    };
+// go(kernels of PER experts a lane, VEC of them neighbours): vectors of 16 bytes where the
+// rows allow them, else an expert a lane and step.
+template <typename T, typename F> static cudaError_t for_experts(const void *logits, int64_t ls, int n, int experts, F go) {
+    constexpr int V = Vec16<T>::N;
+    const bool vec = experts % V == 0 && (uintptr_t)logits % 16 == 0 && (n == 1 || ls % V == 0);
     const int per = (experts + 31) / 32;
-    if (per <= 1) return go(route_top_kernel<T, 1>);
-    if (per <= 2) return go(route_top_kernel<T, 2>);
-    if (per <= 4) return go(route_top_kernel<T, 4>);
-    if (per <= 8) return go(route_top_kernel<T, 8>);
-    if (per <= 16) return go(route_top_kernel<T, 16>);
-    return go(route_top_kernel<T, 32>);
+#define GDN_EXPERTS(PER) (PER >= V && vec ? go.template operator()<PER, (PER >= V ? V : 1)>() : go.template operator()<PER, 1>())
+    if (per <= 1) return GDN_EXPERTS(1);
+    if (per <= 2) return GDN_EXPERTS(2);
+    if (per <= 4) return GDN_EXPERTS(4);
+    if (per <= 8) return GDN_EXPERTS(8);
+    if (per <= 16) return GDN_EXPERTS(16);
+    return GDN_EXPERTS(32);
+#undef GDN_EXPERTS
 }
 
-// y = residual + the weighted rows of a token, one thread a vector of N channels.
+struct RouteCall {
+    const void *logits;
+    int64_t ls;
+    int n, experts, top;
+    bool renorm;
+    int32_t *ids;
+    float *weights;
+    int32_t *offsets, *rows, *slots, *counts;
+    cudaStream_t s;
+};
+template <typename T> struct LaunchTop {
+    const RouteCall &c;
+    template <int PER, int VEC> cudaError_t operator()() const {
+        return launch_after(route_top_kernel<T, PER, VEC>, dim3((c.n + kChunk - 1) / kChunk), dim3(kTopThreads), 0, c.s,
+                            (const T *)c.logits, c.ls, c.n, c.experts, c.top, c.renorm, c.ids, c.weights, c.counts);
+    }
+};
+template <typename T> struct LaunchCluster {
+    const RouteCall &c;
+    template <int PER, int VEC> cudaError_t operator()() const {
+        const int ctas = c.n <= 32 ? 1 : c.n <= 64 ? 2 : c.n <= 128 ? 4 : 8;       // a token a warp, or two
+        return launch_after_cluster(route_cluster_kernel<T, PER, VEC>, ctas, dim3(ctas), dim3(kClusterThreads), 0, c.s,
+                                    (const T *)c.logits, c.ls, c.n, c.experts, c.top, c.renorm, c.ids, c.weights, c.offsets,
+                                    c.rows, c.slots);
+    }
+};
+template <typename T> static cudaError_t launch_route(const RouteCall &c, int32_t *totals) {
+    if (c.n <= kClusterTokens) return for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchCluster<T>{c});
+    const int chunks = (c.n + kChunk - 1) / kChunk;
+    cudaError_t e = for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchTop<T>{c});
+    if (e == cudaSuccess)
+        e = launch_after(route_scan_kernel, dim3((c.experts + 31) / 32), dim3(1024), 0, c.s, c.counts, chunks, c.experts, totals);
+    if (e == cudaSuccess)
+        e = launch_after(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, c.s, (const int32_t *)c.ids,
+                         (const int32_t *)c.counts, (const int32_t *)totals, c.n, c.experts, c.top, c.offsets, c.rows, c.slots);
+    return e;
+}
+
+// y = residual + the weighted rows of a token, one thread a vector of N channels, kAhead
+// rows asked for before the first is added.  `split`: CTAs of a token, or 0 where a CTA
+// has `per` whole tokens.
+constexpr int kAhead = 5, kCombineThreads = 256;
 template <typename T, int N>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(const T *__restrict__ x, int64_t xs, int64_t n_rows, const int32_t *__restrict__ slots,
-               const float *__restrict__ weights, const T *res, int64_t rs, int top, int64_t items, int vecs, T *y,
-               int64_t ys) {
+               const float *__restrict__ weights, const T *res, int64_t rs, int n_tokens, int top, uint32_t vecs,
+               uint32_t split, uint32_t per, T *y, int64_t ys) {
     griddep_wait();
     griddep_launch();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= items) return;
-    const int64_t t = i / vecs;
-    const int c = (int)(i - t * vecs) * N;
+    const uint32_t own = split ? 0 : threadIdx.x / vecs;
+    const int64_t t = split ? blockIdx.x / split : (int64_t)blockIdx.x * per + own;
+    const uint32_t v = split ? blockIdx.x % split * kCombineThreads + threadIdx.x : threadIdx.x - own * vecs;
+    if (t >= n_tokens || v >= vecs || own >= (split ? 1 : per)) return;
+    const int64_t c = (int64_t)v * N;
+    const int32_t *s = slots + t * top;
+    const float *w = weights + t * top;
     constexpr int P = (N + 1) / 2;
+    RawVec<T, N> last;
+    if (res) last.load(res + t * rs + c);
     F2 sum[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) sum[p] = f2(0.f, 0.f);
-    for (int j = 0; j < top; ++j) {
-        const int64_t r = slots[t * top + j];
-        if (r < 0) continue;
-        if (r >= n_rows) {
-            flag_status(GDN_DEVSTAT_BAD_INDEX);
-            continue;
-        }
-        const float w = weights[t * top + j];
-        RawVec<T, N> raw;
-        raw.load(x + r * xs + c);
-        F2 v[P];
-        raw.pairs(v);
+    for (int j0 = 0; j0 < top; j0 += kAhead) {
+        RawVec<T, N> raw[kAhead];
+        float f[kAhead];
+        bool on[kAhead];
 #pragma unroll
-        for (int p = 0; p < P; ++p) sum[p] = f2_fma(f2(w, w), v[p], sum[p]);
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t r = j0 + j < top ? s[j0 + j] : -1;
+            on[j] = r >= 0 && r < n_rows;
+            if (r >= n_rows) flag_status(GDN_DEVSTAT_BAD_INDEX);
+            if (on[j]) {
+                f[j] = w[j0 + j];
+                raw[j].load(x + r * xs + c);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (on[j]) {
+                F2 q[P];
+                raw[j].pairs(q);
+#pragma unroll
+                for (int p = 0; p < P; ++p) sum[p] = f2_fma(f2(f[j], f[j]), q[p], sum[p]);
+            }
     }
     if (res) {
-        RawVec<T, N> raw;
-        raw.load(res + t * rs + c);
-        F2 v[P];
-        raw.pairs(v);
+        F2 q[P];
+        last.pairs(q);
 #pragma unroll
-        for (int p = 0; p < P; ++p) sum[p] = f2_add(sum[p], v[p]);
+        for (int p = 0; p < P; ++p) sum[p] = f2_add(sum[p], q[p]);
     }
     float f[N];
     unpair<N>(sum, f);
@@ -243,7 +436,7 @@ combine_kernel(const T *__restrict__ x, int64_t xs, int64_t n_rows, const int32_
 using namespace gdn;
 
 extern "C" size_t gdn_moe_route_workspace_size(int64_t n_tokens, int32_t n_experts) {
-    if (n_tokens <= 0 || n_experts <= 0) return 0;
+    if (n_tokens <= kClusterTokens || n_experts <= 0) return 0;
     return (size_t)((n_tokens + kChunk - 1) / kChunk + 1) * n_experts * sizeof(int32_t);
 }
 
@@ -262,25 +455,19 @@ extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_strid
         e = launch_after(route_place_kernel, dim3(1), dim3(kRouteThreads), 0, s, (const int32_t *)nullptr,
                          (const int32_t *)nullptr, (const int32_t *)nullptr, 0, n_experts, top_k, offsets, rows, slots);
     } else {
-        GDN_REQUIRE(logits && ids && weights && rows && slots && workspace, GDN_ERR_INVALID_ARG);
+        const bool space = n_tokens > kClusterTokens;
+        GDN_REQUIRE(logits && ids && weights && rows && slots && (workspace || !space), GDN_ERR_INVALID_ARG);
         GDN_REQUIRE(n_tokens == 1 || logits_row_stride >= n_experts, GDN_ERR_INVALID_ARG);
         GDN_REQUIRE((uintptr_t)logits % (dtype == GDN_F32 ? 4 : 2) == 0 && (uintptr_t)ids % 4 == 0 &&
-                        (uintptr_t)weights % 4 == 0 && (uintptr_t)rows % 4 == 0 && (uintptr_t)slots % 4 == 0 &&
-                        (uintptr_t)workspace % 16 == 0,
+                        (uintptr_t)weights % 4 == 0 && (uintptr_t)rows % 4 == 0 && (uintptr_t)slots % 4 == 0,
                     GDN_ERR_INVALID_ARG);
-        GDN_REQUIRE(workspace_bytes >= gdn_moe_route_workspace_size(n_tokens, n_experts), GDN_ERR_INVALID_ARG);
-        const int n = (int)n_tokens, chunks = (n + kChunk - 1) / kChunk;
-        int32_t *totals = (int32_t *)workspace, *counts = totals + n_experts;
-        e = dtype == GDN_F32 ? launch_top<float>(logits, logits_row_stride, n, n_experts, top_k, renormalize != 0, ids,
-                                                 weights, counts, s)
-                             : launch_top<__nv_bfloat16>(logits, logits_row_stride, n, n_experts, top_k,
-                                                         renormalize != 0, ids, weights, counts, s);
-        if (e == cudaSuccess)
-            e = launch_after(route_scan_kernel, dim3((n_experts + 31) / 32), dim3(1024), 0, s, counts, chunks, n_experts,
-                             totals);
-        if (e == cudaSuccess)
-            e = launch_after(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, s, (const int32_t *)ids,
-                             (const int32_t *)counts, (const int32_t *)totals, n, n_experts, top_k, offsets, rows, slots);
+        GDN_REQUIRE(!space || ((uintptr_t)workspace % 16 == 0 &&
+                               workspace_bytes >= gdn_moe_route_workspace_size(n_tokens, n_experts)),
+                    GDN_ERR_INVALID_ARG);
+        int32_t *totals = (int32_t *)workspace;
+        const RouteCall c = {logits, logits_row_stride, (int)n_tokens, n_experts, top_k, renormalize != 0, ids, weights,
+                             offsets, rows, slots, space ? totals + n_experts : nullptr, s};
+        e = dtype == GDN_F32 ? launch_route<float>(c, totals) : launch_route<__nv_bfloat16>(c, totals);
     }
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
@@ -310,14 +497,16 @@ extern "C" gdn_status gdn_moe_combine(const void *x, int64_t x_row_stride, int64
     const bool vec = hidden % n == 0 && ((uintptr_t)x | (uintptr_t)y | (uintptr_t)residual) % 16 == 0 &&
                      (n_rows <= 1 || x_row_stride % n == 0) && (n_tokens == 1 || y_row_stride % n == 0) &&
                      (!residual || n_tokens == 1 || residual_row_stride % n == 0);
-    const int vecs = vec ? (int)(hidden / n) : hidden;
-    const int64_t items = n_tokens * vecs, blocks = (items + 255) / 256;
+    const uint32_t vecs = vec ? (uint32_t)(hidden / n) : (uint32_t)hidden;
+    const uint32_t split = vecs >= kCombineThreads ? (vecs + kCombineThreads - 1) / kCombineThreads : 0;
+    const uint32_t per = split ? 1 : kCombineThreads / vecs;
+    const int64_t blocks = split ? n_tokens * split : (n_tokens + per - 1) / per;
     GDN_REQUIRE(blocks < (1ll << 31), GDN_ERR_UNSUPPORTED);
     auto go = [&](auto kernel, auto one) {
         using T = decltype(one);
-        return launch_after(kernel, dim3((unsigned)blocks), dim3(256), 0, (cudaStream_t)stream, (const T *)x, x_row_stride,
-                            n_rows, slots, weights, (const T *)residual, residual_row_stride, top_k, items, vecs, (T *)y,
-                            y_row_stride);
+        return launch_after(kernel, dim3((unsigned)blocks), dim3(kCombineThreads), 0, (cudaStream_t)stream, (const T *)x,
+                            x_row_stride, n_rows, slots, weights, (const T *)residual, residual_row_stride, (int)n_tokens,
+                            top_k, vecs, split, per, (T *)y, y_row_stride);
     };
     cudaError_t e;
     if (dtype == GDN_F32) e = vec ? go(combine_kernel<float, 4>, 0.0f) : go(combine_kernel<float, 1>, 0.0f);

@@ -541,9 +541,9 @@ gdn_status gdn_linear_block(const void *x, int64_t x_row_stride, const float *x_
  *      have weight 0, all of them in a row of nothing else.  A NaN counts as
  *      larger than every number; it and +infinity make the row's weights NaN.
  *   ids: [n_tokens][top_k] int32, weights: [n_tokens][top_k] fp32.
- *   workspace: at least gdn_moe_route_workspace_size(n_tokens, n_experts) bytes,
- *      16-byte aligned, owned by the caller and not shared with a call in flight
- *      on another stream.
+ *   workspace: at least gdn_moe_route_workspace_size(n_tokens, n_experts) bytes
+ *      (none, and NULL, for up to 512 tokens), 16-byte aligned, owned by the caller
+ *      and not shared with a call in flight on another stream.
  * n_tokens == 0 writes the offsets (zeros) alone; only they are needed then.
  * Limits: n_experts <= 1024, top_k <= 32 (and <= n_experts),
  * n_tokens * top_k < 2^31 - 2^20.
