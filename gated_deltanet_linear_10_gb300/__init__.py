@@ -899,9 +899,12 @@ def _vec(t, dtype, shape, name):
 
 def _out(y, y_dtype, shape, device):
     """The products' output: y as given, or a new one; its code and row stride."""
+    if y is None and (y_dtype is None or y_dtype in (_BF16, _F32)):
+        y_dtype = y_dtype or _BF16
+        return torch.empty(shape, dtype=y_dtype, device=device), _CODES[y_dtype], shape[1]
     if y is None:
-        y = torch.empty(shape, dtype=_BF16 if y_dtype is None else y_dtype, device=device)
-    elif y_dtype is not None and y.dtype != y_dtype:
+        raise GdnError("y: bf16 or fp32")
+    if y_dtype is not None and y.dtype != y_dtype:
         raise GdnError("y: y_dtype")
     if y.dtype != _BF16 and y.dtype != _F32:
         raise GdnError("y: bf16 or fp32")
@@ -952,26 +955,39 @@ def gdn_moe_route(logits, top_k, renormalize=True, ids=None, weights=None, offse
     if dtype != _BF16 and dtype != _F32:
         raise GdnError(f"unsupported logits dtype {dtype} (fp32 or bf16)")
     T, E = shape
+    empty, lp, ls = torch.empty, logits.data_ptr(), _rows(logits, shape, "logits")
+    # outputs made here need no check
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=_I32, device=device)
+        ids = empty((T, top_k), dtype=_I32, device=device)
+    else:
+        _vec(ids, _I32, (T, top_k), "ids")
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=_F32, device=device)
+        weights = empty((T, top_k), dtype=_F32, device=device)
+    else:
+        _vec(weights, _F32, (T, top_k), "weights")
     if offsets is None:
-        offsets = torch.empty(E + 1, dtype=_I32, device=device)
+        offsets = empty(E + 1, dtype=_I32, device=device)
+    else:
+        _vec(offsets, _I32, (E + 1,), "offsets")
     if rows is None:
-        rows = torch.empty(T * top_k, dtype=_I32, device=device)
+        rows = empty(T * top_k, dtype=_I32, device=device)
+    else:
+        _vec(rows, _I32, (T * top_k,), "rows")
     if slots is None:
-        slots = torch.empty((T, top_k), dtype=_I32, device=device)
+        slots = empty((T, top_k), dtype=_I32, device=device)
+    else:
+        _vec(slots, _I32, (T, top_k), "slots")
+    wp = wbytes = None
     if workspace is None:
-        need = gdn_moe_route_workspace_size(T, E)
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        need = _lib.gdn_moe_route_workspace_size(T, E)
+        if need:
+            workspace = empty(need, dtype=torch.uint8, device=device)
     elif not workspace.is_contiguous():
         raise GdnError("workspace: contiguous")
-    wp, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call(_lib.gdn_moe_route, "gdn_moe_route", dev, logits.data_ptr(), _rows(logits, shape, "logits"), T, E,
-          top_k, 1 if renormalize else 0, _vec(ids, _I32, (T, top_k), "ids"),
-          _vec(weights, _F32, (T, top_k), "weights"), _vec(offsets, _I32, (E + 1,), "offsets"),
-          _vec(rows, _I32, (T * top_k,), "rows"), _vec(slots, _I32, (T, top_k), "slots"), _CODES[dtype], wp, wbytes)
+    if workspace is not None:
+        wp, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(_lib.gdn_moe_route, "gdn_moe_route", dev, lp, ls, T, E, top_k, 1 if renormalize else 0, ids.data_ptr(),
+          weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _CODES[dtype], wp, wbytes or 0)
     return ids, weights, offsets, rows, slots
 
 
@@ -990,15 +1006,20 @@ def gdn_block_quant(x, glu=False, y=None, y_scale=None):
         raise GdnError(f"unsupported activation dtype {dtype} (fp32 or bf16)")
     T, n = shape[0], shape[1] // 2 if glu else shape[1]
     if y is None:
-        y = torch.empty((T, (n + 15) // 16 * 16), dtype=_E4M3, device=x.device)
+        ys = (n + 15) // 16 * 16
+        y = torch.empty((T, ys), dtype=_E4M3, device=x.device)
         if n % 16:
             y = y[:, :n]
     elif y.dtype != _E4M3:
         raise GdnError("y: float8_e4m3fn")
+    else:
+        ys = _rows(y, (T, n), "y")
     if y_scale is None:
         y_scale = torch.empty((T, (n + 127) // 128), dtype=_F32, device=x.device)
+    else:
+        _vec(y_scale, _F32, (T, (n + 127) // 128), "y_scale")
     _call(_lib.gdn_block_quant, "gdn_block_quant", dev, x.data_ptr(), _rows(x, shape, "x"), T, n, 1 if glu else 0,
-          y.data_ptr(), _rows(y, (T, n), "y"), _vec(y_scale, _F32, (T, (n + 127) // 128), "y_scale"), _CODES[dtype])
+          y.data_ptr(), ys, y_scale.data_ptr(), _CODES[dtype])
     return y, y_scale
 
 
@@ -1062,12 +1083,14 @@ def gdn_moe_combine(x, slots, weights, residual=None, y=None):
             raise GdnError("residual: x's dtype")
         rs, rp = _rows(residual, (T, H), "residual"), residual.data_ptr()
     if y is None:
-        y = torch.empty((T, H), dtype=dtype, device=x.device)
+        y, ys = torch.empty((T, H), dtype=dtype, device=x.device), H
     elif y.dtype != dtype:
         raise GdnError("y: x's dtype")
+    else:
+        ys = _rows(y, (T, H), "y")
     _call(_lib.gdn_moe_combine, "gdn_moe_combine", dev, x.data_ptr(), _rows(x, shape, "x"), R,
           _vec(slots, _I32, (T, k), "slots"), _vec(weights, _F32, (T, k), "weights"), rp, rs, T, k, H,
-          y.data_ptr(), _rows(y, (T, H), "y"), _CODES[dtype])
+          y.data_ptr(), ys, _CODES[dtype])
     return y
 
 

@@ -28,7 +28,7 @@ template <typename T, bool kGlu, bool kVec>
 __global__ void __launch_bounds__(256)
 block_quant_kernel(const T *__restrict__ x, int64_t xs, int64_t items, int n, int blocks, QuickDiv by_blocks,
                    uint8_t *__restrict__ y, int64_t ys, float *__restrict__ y_scale) {
-    constexpr int U = 2;
+    constexpr int U = 1;
     griddep_wait();
     griddep_launch();
     const int l = threadIdx.x & 15;
@@ -122,7 +122,7 @@ extern "C" gdn_status gdn_block_quant(const void *x, int64_t x_row_stride, int64
                      (n_rows == 1 || (x_row_stride * (int64_t)elem % 16 == 0 && y_row_stride % 8 == 0));
     const int blocks = (n + kQuantBlock - 1) / kQuantBlock;
     const int64_t items = n_rows * blocks;
-    const int grid = (int)std::min<int64_t>((items + 15) / 16, (int64_t)sm_count() * 8);
+    const int grid = (int)std::min<int64_t>((items + 15) / 16, (int64_t)sm_count() * 64);
     auto go = [&](auto kernel, auto one) {
         using T = decltype(one);
         return launch_after(kernel, dim3(grid), dim3(256), 0, (cudaStream_t)stream, (const T *)x, x_row_stride, items, n,

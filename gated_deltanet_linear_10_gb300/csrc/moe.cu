@@ -25,8 +25,15 @@ GDN_DECLARE_STATUS_WORD(g_status_moe)
 GDN_STATUS_READER(read_status_moe, g_status_moe)
 
 constexpr int kMaxExperts = 1024, kMaxTop = 32;
-constexpr int kChunk = 64;                 // tokens of a chunk
-constexpr int kRouteThreads = 256, kTopThreads = 512;
+constexpr int kChunk = 64;                 // the most tokens of a chunk
+constexpr int kRouteThreads = 256;
+// Tokens of a chunk: whole rounds of a CTA's eight warps, and as few as leave the chunks
+// one wave of four CTAs an SM (20668 tokens in chunks of 64, two waves: 31 us, of 40 ...).
+constexpr int kWave = 608;
+static int chunk_of(int64_t n) {
+    const int64_t per = (n + kWave - 1) / kWave;
+    return (int)std::min<int64_t>(kChunk, (per + 7) / 8 * 8);
+}
 constexpr int kClusterTokens = 512;        // the most of the single launch: eight chunks
 
 // Larger logits have larger keys; -0 equals 0 (by the addition, which also makes every
@@ -62,18 +69,20 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
             most = max(most, key[i + j]);
         }
     }
-    // the bound
-    uint32_t left = most, bound = 0, first = 0;
-    for (int n = 0; n < top;) {
-        const uint32_t best = __reduce_max_sync(0xffffffffu, left);
-        if (n == 0) first = best;
-        bound = best;
-        if (best == 0) break;                  // fewer lanes with an expert than choices: all experts
-        const bool hit = left == best;
-        n += __popc(__ballot_sync(0xffffffffu, hit));
-        if (hit) left = 0;
+    // the bound: each lane's place among the 32, the smallest of those that come first
+    uint32_t *lanes = reinterpret_cast<uint32_t *>(cands);
+    __syncwarp();                              // the last token's are read
+    lanes[lane] = most;
+    __syncwarp();
+    int place = 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(lanes + j);
+        place += (q.x > most) + (q.y > most) + (q.z > most) + (q.w > most);
     }
-    bound = max(bound, 1u);
+    // (no lane's, where fewer lanes than choices have an expert: all experts)
+    const uint32_t bound = max(__reduce_min_sync(0xffffffffu, place < top ? most : 0xffffffffu), 1u);
+    const uint32_t first = __reduce_max_sync(0xffffffffu, most);
     const float top1 = key_value(first);
     float all = 0.f;
     if (!renorm) {
@@ -95,7 +104,7 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
     const int total = __shfl_sync(0xffffffffu, scan, 31);
     // a candidate: its key, then its index turned round, so that the larger word goes first
     auto word = [&](int i) { return (uint64_t)key[i] << 32 | (uint32_t)~(i / VEC * VEC * 32 + lane * VEC + i % VEC); };
-    __syncwarp();                              // the last token's are read
+    __syncwarp();                              // the lanes' largest are read
     if (total <= kCands) {
         int at = scan - cnt;
 #pragma unroll
@@ -130,6 +139,7 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
         if (q * 32 >= n) continue;
         const uint64_t mine = q * 32 + lane < n ? cands[q * 32 + lane] : 0;
         int r = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) r += cands[j] > mine;
         rank[q] = mine ? r : kCands;
         p[q] = rank[q] < top ? expf(key_value((uint32_t)(mine >> 32)) - top1) : 0.f;
@@ -152,21 +162,21 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
 
 // A chunk's tokens: ids and weights out, and per expert how many ask for it.
 template <typename T, int PER, int VEC>
-__global__ void __launch_bounds__(kTopThreads)
-route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int experts, int top, bool renorm,
+__global__ void __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 2)
+route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int chunk, int experts, int top, bool renorm,
                  int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ counts) {
     __shared__ int count[kMaxExperts];
-    __shared__ uint64_t cands[kTopThreads / 32][64];
+    __shared__ uint64_t cands[kRouteThreads / 32][64];
     griddep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * kChunk;
-    for (int e = tid; e < experts; e += kTopThreads) count[e] = 0;
+    const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * chunk;
+    for (int e = tid; e < experts; e += kRouteThreads) count[e] = 0;
     __syncthreads();
-    for (int t = t0 + (tid >> 5); t < min(t0 + kChunk, n_tokens); t += kTopThreads / 32)
+    for (int t = t0 + (tid >> 5); t < min(t0 + chunk, n_tokens); t += kRouteThreads / 32)
         route_token<T, PER, VEC, 64>(logits + t * ls, experts, top, renorm, lane, cands[tid >> 5], ids + (int64_t)t * top,
                                      weights + (int64_t)t * top, [&](int id, int) { atomicAdd(&count[id], 1); });
     __syncthreads();
     griddep_launch();
-    for (int e = tid; e < experts; e += kTopThreads) counts[(int64_t)blockIdx.x * experts + e] = count[e];
+    for (int e = tid; e < experts; e += kRouteThreads) counts[(int64_t)blockIdx.x * experts + e] = count[e];
 }
 
 // Experts' sums in front of each one, by the whole CTA: v[i] of expert tid * Q + i becomes
@@ -235,12 +245,16 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
     cluster_arrive();
     cluster_wait();
     int v[1] = {0}, before = 0;
-    if (tid < experts)
-        for (int r = 0; r < ctas; ++r) {
-            const int c = __popcll(r == (int)rank ? mask[tid] : load_of_rank(&mask[tid], r));
-            v[0] += c;
-            if (r < (int)rank) before += c;
+    if (tid < experts) {
+        uint64_t word[8];                       // all asked for before the first is counted
+#pragma unroll
+        for (int r = 0; r < 8; ++r) word[r] = r < ctas ? load_of_rank(&mask[tid], r) : 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            v[0] += __popcll(word[r]);
+            if (r < (int)rank) before += __popcll(word[r]);
         }
+    }
     const int all = scan_experts(v, warp_sum);
     if (tid < experts) {
         base[tid] = v[0] + before;
@@ -286,14 +300,14 @@ route_scan_kernel(int32_t *__restrict__ counts, int chunks, int experts, int32_t
 // Each pair to its place.
 __global__ void __launch_bounds__(kRouteThreads)
 route_place_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
-                   const int32_t *__restrict__ totals, int n_tokens, int experts, int top,
+                   const int32_t *__restrict__ totals, int n_tokens, int chunk, int experts, int top,
                    int32_t *__restrict__ offsets, int32_t *__restrict__ rows, int32_t *__restrict__ slots) {
     __shared__ unsigned long long mask[kMaxExperts];
     __shared__ int base[kMaxExperts], warp_sum[kRouteThreads / 32];
     griddep_wait();
     griddep_launch();
-    const int tid = threadIdx.x, t0 = blockIdx.x * kChunk;
-    const int n = min(kChunk, n_tokens - t0) * top;           // pairs (none: only the offsets)
+    const int tid = threadIdx.x, t0 = blockIdx.x * chunk;
+    const int n = min(chunk, n_tokens - t0) * top;           // pairs (none: only the offsets)
     constexpr int Q = kMaxExperts / kRouteThreads;          // experts of a thread
     int v[Q];
 #pragma unroll
@@ -338,7 +352,7 @@ template <typename T, typename F> static cudaError_t for_experts(const void *log
 struct RouteCall {
     const void *logits;
     int64_t ls;
-    int n, experts, top;
+    int n, chunk, experts, top;
     bool renorm;
     int32_t *ids;
     float *weights;
@@ -348,8 +362,8 @@ struct RouteCall {
 template <typename T> struct LaunchTop {
     const RouteCall &c;
     template <int PER, int VEC> cudaError_t operator()() const {
-        return launch_after(route_top_kernel<T, PER, VEC>, dim3((c.n + kChunk - 1) / kChunk), dim3(kTopThreads), 0, c.s,
-                            (const T *)c.logits, c.ls, c.n, c.experts, c.top, c.renorm, c.ids, c.weights, c.counts);
+        return launch_after(route_top_kernel<T, PER, VEC>, dim3((c.n + c.chunk - 1) / c.chunk), dim3(kRouteThreads), 0, c.s,
+                            (const T *)c.logits, c.ls, c.n, c.chunk, c.experts, c.top, c.renorm, c.ids, c.weights, c.counts);
     }
 };
 template <typename T> struct LaunchCluster {
@@ -363,13 +377,13 @@ template <typename T> struct LaunchCluster {
 };
 template <typename T> static cudaError_t launch_route(const RouteCall &c, int32_t *totals) {
     if (c.n <= kClusterTokens) return for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchCluster<T>{c});
-    const int chunks = (c.n + kChunk - 1) / kChunk;
+    const int chunks = (c.n + c.chunk - 1) / c.chunk;
     cudaError_t e = for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchTop<T>{c});
     if (e == cudaSuccess)
         e = launch_after(route_scan_kernel, dim3((c.experts + 31) / 32), dim3(1024), 0, c.s, c.counts, chunks, c.experts, totals);
     if (e == cudaSuccess)
         e = launch_after(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, c.s, (const int32_t *)c.ids,
-                         (const int32_t *)c.counts, (const int32_t *)totals, c.n, c.experts, c.top, c.offsets, c.rows, c.slots);
+                         (const int32_t *)c.counts, (const int32_t *)totals, c.n, c.chunk, c.experts, c.top, c.offsets, c.rows, c.slots);
     return e;
 }
 
@@ -378,7 +392,7 @@ template <typename T> static cudaError_t launch_route(const RouteCall &c, int32_
 // has `per` whole tokens.
 constexpr int kAhead = 5, kCombineThreads = 256;
 template <typename T, int N>
-__global__ void __launch_bounds__(kCombineThreads)
+__global__ void __launch_bounds__(kCombineThreads, 4)
 combine_kernel(const T *__restrict__ x, int64_t xs, int64_t n_rows, const int32_t *__restrict__ slots,
                const float *__restrict__ weights, const T *res, int64_t rs, int n_tokens, int top, uint32_t vecs,
                uint32_t split, uint32_t per, T *y, int64_t ys) {
@@ -437,7 +451,7 @@ using namespace gdn;
 
 extern "C" size_t gdn_moe_route_workspace_size(int64_t n_tokens, int32_t n_experts) {
     if (n_tokens <= kClusterTokens || n_experts <= 0) return 0;
-    return (size_t)((n_tokens + kChunk - 1) / kChunk + 1) * n_experts * sizeof(int32_t);
+    return (size_t)((n_tokens + chunk_of(n_tokens) - 1) / chunk_of(n_tokens) + 1) * n_experts * sizeof(int32_t);
 }
 
 extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_stride, int64_t n_tokens, int32_t n_experts,
@@ -453,7 +467,7 @@ extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_strid
     cudaError_t e;
     if (n_tokens == 0) {
         e = launch_after(route_place_kernel, dim3(1), dim3(kRouteThreads), 0, s, (const int32_t *)nullptr,
-                         (const int32_t *)nullptr, (const int32_t *)nullptr, 0, n_experts, top_k, offsets, rows, slots);
+                         (const int32_t *)nullptr, (const int32_t *)nullptr, 0, kChunk, n_experts, top_k, offsets, rows, slots);
     } else {
         const bool space = n_tokens > kClusterTokens;
         GDN_REQUIRE(logits && ids && weights && rows && slots && (workspace || !space), GDN_ERR_INVALID_ARG);
@@ -465,7 +479,7 @@ extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_strid
                                workspace_bytes >= gdn_moe_route_workspace_size(n_tokens, n_experts)),
                     GDN_ERR_INVALID_ARG);
         int32_t *totals = (int32_t *)workspace;
-        const RouteCall c = {logits, logits_row_stride, (int)n_tokens, n_experts, top_k, renormalize != 0, ids, weights,
+        const RouteCall c = {logits, logits_row_stride, (int)n_tokens, chunk_of(n_tokens), n_experts, top_k, renormalize != 0, ids, weights,
                              offsets, rows, slots, space ? totals + n_experts : nullptr, s};
         e = dtype == GDN_F32 ? launch_route<float>(c, totals) : launch_route<__nv_bfloat16>(c, totals);
     }
