@@ -15,7 +15,7 @@ bool encode_tmap_experts(CUtensorMap *map, const GroupedCall &c, uint32_t box_ro
                           c.n_out, c.n_experts, ws * elem, we * elem, 128 / (uint32_t)elem, box_rows);
 }
 bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows) {
-    return encode_tmap_operand(map, c.x, c.n_in, c.n_x, c.xs, c.rows ? 1 : box_rows, c.e4m3);
+    return encode_tmap_operand(map, c.x, c.n_in, c.n_x, c.xs, box_rows, c.e4m3);
 }
 
 // By the rows that an expert has in the mean (the host knows no more): up to 64 go to

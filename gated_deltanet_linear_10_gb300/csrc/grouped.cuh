@@ -33,8 +33,8 @@ cudaError_t set_grouped_narrow_limit(uint64_t limit_ns, cudaStream_t s);
 cudaError_t set_grouped_wide_limit(uint64_t limit_ns, cudaStream_t s);
 int linear_drop();                   // the failure path's test control (LinearDrop)
 
-// The operands' maps: w as [n_experts][n_out][n_in] in boxes of 128 bytes x box_rows,
-// x as rows in boxes of 128 bytes x box_rows or, gathered, of one row.
+// The operands' maps, in boxes of 128 bytes x box_rows: w as [n_experts][n_out][n_in],
+// x as rows (not used where they are gathered).
 bool encode_tmap_experts(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows);
 bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows);
 
@@ -61,19 +61,22 @@ __device__ __forceinline__ int build_group_table(GroupTable &g, const GroupedCal
         __syncthreads();
         return g.first[1];
     }
+    // as many experts a thread as it takes (at least 256 threads), their offsets asked for together
+    constexpr int Q = 4;
     const int per = (c.n_experts + nt - 1) / nt, e0 = tid * per, e1 = min(e0 + per, c.n_experts);
     int sum = 0, wrong = 0;
     if (e0 < e1) {
-        int a = c.offsets[e0];
-        wrong |= a < 0;
-        for (int e = e0; e < e1; ++e) {
-            const int b = c.offsets[e + 1];
-            wrong |= b < a || b > c.n_rows;
-            sum += (b - a + tile_rows - 1) / tile_rows;
-            g.start[e] = a;
-            a = b;
+        int o[Q + 1];
+#pragma unroll
+        for (int i = 0; i <= Q; ++i) o[i] = c.offsets[min(e0 + i, e1)];
+        wrong |= o[0] < 0;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            wrong |= o[i + 1] < o[i] || o[i + 1] > c.n_rows;
+            sum += (o[i + 1] - o[i] + tile_rows - 1) / tile_rows;
+            if (e0 + i <= e1) g.start[e0 + i] = o[i];
         }
-        if (e1 == c.n_experts) g.start[e1] = a;
+        if (e0 + Q <= e1) g.start[e0 + Q] = o[Q];
     }
     wrong = __syncthreads_or(wrong);
     int scan = sum;
@@ -111,7 +114,7 @@ __device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, int ex
     GroupTile t;
     t.e = e;
     const int f = g.first[e], tiles = g.first[e + 1] - f, r = tile - f * nn;
-    const int base = r / (kGroupRaster * nn) * kGroupRaster, rr = r - base * nn;
+    const int base = r < kGroupRaster * nn ? 0 : r / (kGroupRaster * nn) * kGroupRaster, rr = r - base * nn;
     const int rows = min(kGroupRaster, tiles - base);
     t.n = rows == 1 ? rr : rr / rows;
     t.r0 = g.start[e] + (base + rr - t.n * rows) * tile_rows;
@@ -144,13 +147,33 @@ __device__ __forceinline__ uint64_t l2_normal() {
     return p;
 }
 
-// Four rows of x, 128 bytes of each, into 512 bytes of an operand tile.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, const int4 &r) {
+// 16 bytes of global into shared memory, those from `bytes` on as zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// (the size as a register makes that a slow sequence)
+__device__ __forceinline__ void copy16_if(bool on, uint32_t dst, const void *src) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(tc::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}\n" ::"r"(dst),
+        "l"(src), "r"((uint32_t)on)
         : "memory");
+}
+// Arrives on a barrier, whose count has it already, when this thread's copies so far have come.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
                                             int32_t z) {
@@ -163,31 +186,27 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
 
 // Columns of 32 lanes of tensor memory, on their way until every load of the thread
 // has come (tmem_wait; r is named there so that nothing reads it before).
-__device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ask(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+        : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+                 :);
 }
-__device__ __forceinline__ void tmem_ask32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ask(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
+        : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
+                 :);
 }
 
 }  // namespace gdn

@@ -2,10 +2,14 @@
 // rows are the lanes of the accumulator and up to BT of its tokens the columns, so
 // that a tile of few rows costs little more than reading its weights.
 //
-// Persistent CTAs, a warp for each part: loads (weights as tiles, the tokens' rows
-// gathered), products, scales, and four that sum the blocks.  With block scales
+// Persistent CTAs, a warp for each part: loads (tiles by TMA; gathered rows in pieces
+// of 16 bytes, by a warp: a TMA gather of four rows takes 150 cycles and held one
+// token's block at 620), products, scales, and four or eight that sum the blocks.  With block scales
 // every block of 128 in k is a product of its own into one of four accumulators;
-// the summing warps add it, times sx sw of its column, to registers.
+// the summing warps add it, times sx sw of its column, to registers.  A block takes
+// such a warp some 500 cycles of waits and latencies, so two groups of four share the
+// columns of a tile of 64 or 128 rows (256 x 2048 x 8192: with one group 15.9 us, with
+// two 12.7).
 #include <limits.h>
 
 #include <algorithm>
@@ -26,18 +30,23 @@ cudaError_t set_grouped_narrow_limit(uint64_t limit_ns, cudaStream_t s) {
 namespace {
 
 constexpr int kScaleChunk = 8;         // blocks whose scales are handed over at a time
-constexpr int kGnThreads = 7 * 32;
+// Warps: 0 loads by TMA, 1 products, 2 scales, 3 on sums, the last one gathered rows: 12 at
+// most, which leave a thread 168 registers.
+constexpr int kGnScale = 2, kGnFirstSum = 3, kGnGather = 1;
 
 template <int BT> struct GnCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
     static constexpr int kStages = BT == 16 ? 11 : BT == 32 ? 10 : BT == 64 ? 8 : 6;
     static constexpr int kAccs = 4;
+    static constexpr int kSums = BT >= 64 ? 8 : 4;        // summing warps, groups of four share the columns
+    static constexpr int kWidth = BT * 4 / kSums;         // columns of one
+    static constexpr int kThreads = 32 * (kGnFirstSum + kSums + kGnGather);
     static constexpr uint32_t kScales = 2 * kScaleChunk * BT * 4;
     static constexpr uint32_t kSmem = kStages * kStage + kScales;
 };
 
 template <int BT, bool kBlock>
-__global__ void __launch_bounds__(kGnThreads)
+__global__ void __launch_bounds__(GnCfg<BT>::kThreads)
 grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                       const __grid_constant__ GroupedCall c, int keep) {
     using C = GnCfg<BT>;
@@ -58,16 +67,16 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         prefetch_tensormap(&mx);
         prefetch_tensormap(&mw);
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], c.rows ? 1 + 32 * kGnGather : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < A; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], C::kSums);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], 4);
+            mbar_init(&sc_empty[i], C::kSums);
         }
         mbar_init(&drained, 1);
         abort_flag = (smem_u32(smem) & 1023u) != 0;
@@ -92,12 +101,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
-            int4 rows;
-            if (c.rows) {
-                const int r = a.r0 + lane * 4;
-                rows = make_int4(group_x_row(c, r, a.r1), group_x_row(c, r + 1, a.r1), group_x_row(c, r + 2, a.r1),
-                                 group_x_row(c, r + 3, a.r1));
-            }
+            const uint32_t bytes = c.rows ? C::kW : C::kStage;
 #pragma unroll 1
             for (int k = 0; k < nk; ++k, ++i) {
                 if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
@@ -105,15 +109,10 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     break;
                 }
                 uint8_t *st = smem + s * C::kStage;
-                const uint32_t bar = smem_u32(&full[s]);
-                if (i < keep) {
-                    if (one) {
-                        mbar_arrive_expect_tx(&full[s], C::kStage);
-                        tma_load_3d(st, &mw, bar, k * kElems, a.n * 128, a.e);
-                        if (!c.rows) tma_load_2d(st + C::kW, &mx, &full[s], k * kElems, a.r0);
-                    }
-                    __syncwarp();
-                    if (c.rows && lane < BT / 4) tma_gather4(st + C::kW + lane * 512, &mx, bar, k * kElems, rows);
+                if (i < keep && one) {
+                    mbar_arrive_expect_tx(&full[s], bytes);
+                    tma_load_3d(st, &mw, smem_u32(&full[s]), k * kElems, a.n * 128, a.e);
+                    if (!c.rows) tma_load_2d(st + C::kW, &mx, &full[s], k * kElems, a.r0);
                 }
                 __syncwarp();
                 if (++s == S) {
@@ -124,24 +123,29 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         }
         griddep_launch();
         for (int j = i > S ? i - S : 0; ok && j < i; ++j) ok = mbar_wait_all(&empty[j % S], (j / S) & 1, abort);
-        if (one && (!ok || *abort))        // given up: the copies in flight land before the CTA ends
-            for (int j = i > S ? i - S : 0; j < min(i, keep); ++j) mbar_drain(&full[j % S], (j / S) & 1);
+        if (one && (!ok || *abort)) {      // given up: the copies in flight land before the CTA ends
+            if (c.rows) let_copies_land(); // the barriers count the gathered rows too
+            else
+                for (int j = i > S ? i - S : 0; j < min(i, keep); ++j) mbar_drain(&full[j % S], (j / S) & 1);
+        }
     } else if (warp == 1) {
         constexpr uint32_t idesc = kBlock ? idesc_e4m3(128, BT) : idesc_bf16(128, BT);
         const uint64_t desc = sdesc_sw128(0, 0, 1024);
         const uint32_t base = smem_u32(smem) >> 4, sums = tmem_base;
         int s = 0, u = 0;                  // u: accumulators used so far
         uint32_t phase = 0;
-        bool ok = true;
+        bool ok = true, ready = false;     // operands and accumulator of the next block are known to be there
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
 #pragma unroll 1
             for (int k = 0; k < nk; ++k) {
-                if ((kBlock || k == 0) && u >= A && !mbar_wait_all(&acc_empty[u % A], (u / A - 1) & 1, abort)) ok = false;
-                if (!ok || !mbar_wait_all(&full[s], phase, abort)) {
-                    ok = false;
-                    break;
+                if (!ready) {
+                    ok = mbar_wait_all(&full[s], phase, abort);
+                    if (ok && (kBlock || k == 0) && u >= A) ok = mbar_wait_all(&acc_empty[u % A], (u / A - 1) & 1, abort);
+                    if (!ok) break;
                 }
                 tc_fence_after();
+                if (c.rows) fence_async_smem();           // rows that threads have written, before the product reads them
+                const bool last = kBlock || k == nk - 1;
                 if (elect_lane()) {
                     const uint32_t st = base + s * (C::kStage >> 4), d = sums + u % A * BT;
                     const uint64_t da = desc | st, db = desc | (st + (C::kW >> 4));
@@ -149,14 +153,18 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     for (int q = 0; q < 4; ++q)
                         linear_mma<kBlock>(d, da + 2 * q, db + 2 * q, idesc, q > 0 || (!kBlock && k > 0));
                     mma_commit(&empty[s]);
-                    if (kBlock || k == nk - 1) mma_commit(&acc_full[u % A]);
+                    if (last) mma_commit(&acc_full[u % A]);
                 }
                 __syncwarp();
-                if (kBlock || k == nk - 1) ++u;
+                if (last) ++u;
                 if (++s == S) {
                     s = 0;
                     phase ^= 1;
                 }
+                // (a wait that finds its barrier done takes 150 cycles, two looks ahead of time hardly any)
+                ready = mbar_test(&full[s], phase);
+                if (last && u >= A) ready = mbar_test(&acc_empty[u % A], (u / A - 1) & 1) && ready;
+                ready = __all_sync(0xffffffffu, ready);
             }
         }
         if (elect_lane()) {
@@ -164,7 +172,60 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             mbar_drain(&drained, 0);
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp >= kGnFirstSum + C::kSums) {
+        // A lane copies 16 bytes of a row, the warp four whole rows at a time.  Where there is no row the stage keeps what it holds: a column that is not
+        // written, or written as zeros.
+        if (c.rows) {
+            constexpr int N = BT / 4;
+            const int sub = lane >> 3;                                      // of four rows
+            const uint32_t to = smem_u32(smem) + C::kW + sub * 128;
+            // the 16 bytes' place in the swizzled rows of even fours, and of odd ones
+            const uint32_t even = ((lane & 7) ^ sub) << 4, odd = ((lane & 7) ^ (sub + 4)) << 4;
+            const int64_t stride = c.xs * (kBlock ? 1 : 2);
+            const int bytes = c.n_in * (kBlock ? 1 : 2) - (lane & 7) * 16;  // of the row from this lane's first on
+            const int whole = c.n_in * (kBlock ? 1 : 2) / 128;              // blocks of 128 bytes
+            int s = 0, i = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
+                int row[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) row[j] = group_x_row(c, a.r0 + sub + j * 4, a.r1);
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + (lane & 7) * 16;
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k, ++i, src += 128) {
+                    if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (i < keep) {
+                        const uint32_t st = to + s * C::kStage;
+                        if (k < whole) {
+#pragma unroll
+                            for (int j = 0; j < N; ++j)
+                                copy16_if(row[j] < c.n_x, st + j * 512 + (j & 1 ? odd : even), src + row[j] * stride);
+                        } else {
+                            const int n = min(16, max(0, bytes - k * 128));
+#pragma unroll 1
+                            for (int j = 0; j < N; ++j) {
+                                int at = row[0];
+#pragma unroll
+                                for (int z = 1; z < N; ++z) at = z == j ? row[z] : at;      // no array in memory
+                                if (at < c.n_x) copy16(st + j * 512 + (j & 1 ? odd : even), n > 0 ? src + at * stride : c.x, n);
+                            }
+                        }
+                        copies_arrive(&full[s]);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else if (warp == kGnScale) {
         // Scales of the next blocks, times the weight's, and which rows there are.
         int slot = 0, v = 0;
         bool ok = true, wrong = false;
@@ -212,69 +273,76 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             }
         }
         if (wrong) flag_status(GDN_DEVSTAT_BAD_INDEX);
-    } else {
+    } else if (warp >= kGnFirstSum) {
         // Accumulator lane 32 q + l is channel 32 q + l of the tile.
-        const int q = warp & 3;
-        int u = 0, slot = 0, v = 0;
-        bool ok = true;
+        constexpr int W = C::kWidth, L = W < 32 ? 16 : 32;       // columns, and of a load
+        const int q = warp & 3, c0 = ((warp - kGnFirstSum) >> 2) * W;
+        int u = 0, v = 0;                  // accumulators and chunks used so far
+        bool ok = true, ready = false;     // the next accumulator is known to be there
+        const int blocks = kBlock ? nk : 1;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
-            F2 acc[BT / 2];
+            F2 acc[W / 2];
 #pragma unroll
-            for (int i = 0; i < BT / 2; ++i) acc[i] = f2(0.f, 0.f);
-            uint32_t there[(BT + 31) / 32];
+            for (int i = 0; i < W / 2; ++i) acc[i] = f2(0.f, 0.f);
+            uint32_t there[(W + 31) / 32];
 #pragma unroll 1
-            for (int k = 0; k < (kBlock ? nk : 1); ++k, ++u) {
-                if (k % kScaleChunk == 0 && !mbar_wait_all(&sc_full[slot], (v / 2) & 1, abort)) ok = false;
-                if (!ok || !mbar_wait_all(&acc_full[u % A], (u / A) & 1, abort)) {
+            for (int k0 = 0; k0 < blocks && ok; k0 += kScaleChunk, ++v) {
+                const int slot = v & 1, n = min(blocks - k0, kScaleChunk);
+                if (!mbar_wait_all(&sc_full[slot], (v >> 1) & 1, abort)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t from = tmem_addr(tmem_base, q * 32, u % A * BT);
-                const float *sc = scales + (slot * kScaleChunk + k % kScaleChunk) * BT;
-                uint32_t r[2][16];
-                tmem_ask16(from, r[0]);
 #pragma unroll
-                for (int j = 0; j < BT / 16; ++j) {
-                    tmem_wait16(r[j & 1]);
-                    if (j + 1 < BT / 16) tmem_ask16(from + (j + 1) * 16, r[(j + 1) & 1]);
+                for (int i = 0; i < (W + 31) / 32; ++i) there[i] = valid[slot][c0 / 32 + i];
+                const float *sc = scales + slot * kScaleChunk * BT + c0;
+#pragma unroll 1
+                for (int k = 0; k < n; ++k, sc += BT) {
+                    if (!ready && !mbar_wait_all(&acc_full[u % A], (u / A) & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t from = tmem_addr(tmem_base, q * 32, u % A * BT + c0);
+                    uint32_t r[W / L > 1 ? 2 : 1][L];
+                    tmem_ask(from, r[0]);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const uint32_t *p = r[j & 1] + i;
-                        F2 &lo = acc[j * 8 + i / 2], &hi = acc[j * 8 + i / 2 + 1];
-                        if (kBlock) {
-                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + j * 16 + i);
-                            lo = f2_fma(f2_bits(p[0], p[1]), f.x, lo);
-                            hi = f2_fma(f2_bits(p[2], p[3]), f.y, hi);
+                    for (int j = 0; j < W / L; ++j) {
+                        tmem_wait(r[j & 1]);
+                        if (j + 1 < W / L) {
+                            tmem_ask(from + (j + 1) * L, r[(j + 1) & 1]);
                         } else {
-                            lo = f2_bits(p[0], p[1]);
-                            hi = f2_bits(p[2], p[3]);
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&acc_empty[u % A]);
+                            ++u;
+                            ready = mbar_test(&acc_full[u % A], (u / A) & 1);
+                        }
+#pragma unroll
+                        for (int i = 0; i < L; i += 4) {
+                            const uint32_t *p = r[j & 1] + i;
+                            F2 &lo = acc[(j * L + i) / 2], &hi = acc[(j * L + i) / 2 + 1];
+                            if (kBlock) {
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + j * L + i);
+                                lo = f2_fma(f2_bits(p[0], p[1]), f.x, lo);
+                                hi = f2_fma(f2_bits(p[2], p[3]), f.y, hi);
+                            } else {
+                                lo = f2_bits(p[0], p[1]);
+                                hi = f2_bits(p[2], p[3]);
+                            }
                         }
                     }
+                    ready = __all_sync(0xffffffffu, ready);
                 }
-                tc_fence_before();
-                if (!kBlock || k == nk - 1) {
-#pragma unroll
-                    for (int i = 0; i < (BT + 31) / 32; ++i) there[i] = valid[slot][i];
-                }
-                const bool last = !kBlock || k == nk - 1 || k % kScaleChunk == kScaleChunk - 1;
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&acc_empty[u % A]);
-                    if (last) mbar_arrive(&sc_empty[slot]);
-                }
-                if (last) {
-                    slot ^= 1;
-                    ++v;
-                }
+                if (lane == 0) mbar_arrive(&sc_empty[slot]);
             }
             if (!ok) break;
-            const int n = a.n * 128 + q * 32 + lane, cnt = min(BT, a.r1 - a.r0);
+            const int n = a.n * 128 + q * 32 + lane, cnt = min(W, a.r1 - a.r0 - c0);
             if (n < c.n_out) {
-                const int64_t at = (int64_t)a.r0 * c.ys + n;
+                const int64_t at = (int64_t)(a.r0 + c0) * c.ys + n;
 #pragma unroll
-                for (int i = 0; i < BT; ++i) {
+                for (int i = 0; i < W; ++i) {
                     const float2 f = f2_get(acc[i / 2]);
                     const float val = there[i / 32] >> (i % 32) & 1 ? (i & 1 ? f.y : f.x) : 0.f;
                     if (i < cnt) {
@@ -303,7 +371,7 @@ template <int BT, bool kBlock> gdn_status launch(const GroupedCall &c, int drop,
     const int64_t tiles = (((int64_t)c.n_rows + BT - 1) / BT + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     if (e == cudaSuccess)
-        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(kGnThreads), C::kSmem, s, mx,
+        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(C::kThreads), C::kSmem, s, mx,
                          mw, c, drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : 1);
     if (e != cudaSuccess) {
         set_last_cuda_error(e);

@@ -54,18 +54,6 @@ constexpr uint32_t kGwStaging = 2 * 4096;
 constexpr uint32_t kGwFactors = 2 * kGwChunk * 128 * 4;       // [half][block][row], fp32
 constexpr uint32_t kGwSmem = kGwStages * kGwStage + kGwEpiWarps * kGwStaging + 2 * kGwFactors;
 
-// Whether a phase is over, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // Loads into this CTA's shared memory, their bytes counted on a barrier of either CTA.
 __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y) {
     asm volatile(
@@ -81,22 +69,6 @@ __device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, 
         " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
         : "memory");
-}
-// 16 bytes of global into shared memory, those from `bytes` on as zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// (the size as a register makes that a slow sequence)
-__device__ __forceinline__ void copy16_if(bool on, uint32_t dst, const void *src) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-        "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}\n" ::"r"(dst),
-        "l"(src), "r"((uint32_t)on)
-        : "memory");
-}
-// Arrives on a barrier, whose count has it already, when this thread's copies so far have come.
-__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Arrives on the barrier at this offset in both CTAs (mask 3) or the leader (1) once
 // the products issued so far by this thread are done.
@@ -335,7 +307,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
         const uint32_t base = smem_u32(smem) >> 4, sums = tmem_base + h * 128, xh = (kGwX + h * kGwHalf) >> 4;
         int s = 0, u = 0;                  // u: accumulators used so far
         uint32_t phase = 0, st = base;
-        bool ok = true;
+        bool ok = true, ready = false;     // operands and accumulator of the next block are known to be there
         for (int t = pair, j = 0; t < tiles && ok; t += pairs, ++j) {
             int4 a;
             if (!take_tile(wide, j, a, abort)) {
@@ -347,11 +319,13 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
             const bool mine = h == 0 || both;          // else the stages are handed back as they are
 #pragma unroll 1
             for (int k = 0; k < nk; ++k) {
-                // the operands first, which have mostly come: less lies behind the accumulator's release
-                ok = mbar_wait_all(&full[s], phase, abort);
-                if (ok && (kBlock || k == 0) && mine && u >= 2)
-                    ok = mbar_wait_all(&acc_empty[h][u & 1], ((u >> 1) - 1) & 1, abort);
-                if (!ok) break;
+                if (!ready) {
+                    // the operands first, which have mostly come: less lies behind the accumulator's release
+                    ok = mbar_wait_all(&full[s], phase, abort);
+                    if (ok && (kBlock || k == 0) && mine && u >= 2)
+                        ok = mbar_wait_all(&acc_empty[h][u & 1], ((u >> 1) - 1) & 1, abort);
+                    if (!ok) break;
+                }
                 tc_fence_after();
                 const bool last = kBlock || k == nk - 1;
                 if (elect_lane()) {
@@ -373,6 +347,10 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                     st = base;
                     phase ^= 1;
                 }
+                // (a wait that finds its barrier done takes 150 cycles, two looks ahead of time hardly any)
+                ready = mbar_test(&full[s], phase);
+                if (last && u >= 2) ready = mbar_test(&acc_empty[h][u & 1], ((u >> 1) - 1) & 1) && ready;
+                ready = __all_sync(0xffffffffu, ready);
             }
         }
         // every arrival of the peer's has come, every product is done, before the pair may end
@@ -581,13 +559,13 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                 tc_fence_after();
                 const uint32_t from = tmem_addr(tmem_base, q * 32, (b * 2 + h) * 128);
                 uint32_t r[2][32];
-                tmem_ask32(from, r[0]);
+                tmem_ask(from, r[0]);
                 ++u;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    tmem_wait32(r[j & 1]);
+                    tmem_wait(r[j & 1]);
                     if (j < 3) {
-                        tmem_ask32(from + (j + 1) * 32, r[(j + 1) & 1]);
+                        tmem_ask(from + (j + 1) * 32, r[(j + 1) & 1]);
                     } else {                               // all of it has been read
                         tc_fence_before();
                         __syncwarp();
