@@ -304,32 +304,27 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     }
                     tc_fence_after();
                     const uint32_t from = tmem_addr(tmem_base, q * 32, u % A * BT + c0);
-                    uint32_t r[W / L > 1 ? 2 : 1][L];
-                    tmem_ask(from, r[0]);
+                    uint32_t r[W / L][L];
 #pragma unroll
-                    for (int j = 0; j < W / L; ++j) {
-                        tmem_wait(r[j & 1]);
-                        if (j + 1 < W / L) {
-                            tmem_ask(from + (j + 1) * L, r[(j + 1) & 1]);
+                    for (int j = 0; j < W / L; ++j) tmem_ask(from + j * L, r[j]);
+#pragma unroll
+                    for (int j = 0; j < W / L; ++j) tmem_wait(r[j]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[u % A]);
+                    ++u;
+                    ready = mbar_test(&acc_full[u % A], (u / A) & 1);
+#pragma unroll
+                    for (int i = 0; i < W; i += 4) {
+                        const uint32_t *p = r[i / L] + i % L;
+                        F2 &lo = acc[i / 2], &hi = acc[i / 2 + 1];
+                        if (kBlock) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + i);
+                            lo = f2_fma(f2_bits(p[0], p[1]), f.x, lo);
+                            hi = f2_fma(f2_bits(p[2], p[3]), f.y, hi);
                         } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&acc_empty[u % A]);
-                            ++u;
-                            ready = mbar_test(&acc_full[u % A], (u / A) & 1);
-                        }
-#pragma unroll
-                        for (int i = 0; i < L; i += 4) {
-                            const uint32_t *p = r[j & 1] + i;
-                            F2 &lo = acc[(j * L + i) / 2], &hi = acc[(j * L + i) / 2 + 1];
-                            if (kBlock) {
-                                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + j * L + i);
-                                lo = f2_fma(f2_bits(p[0], p[1]), f.x, lo);
-                                hi = f2_fma(f2_bits(p[2], p[3]), f.y, hi);
-                            } else {
-                                lo = f2_bits(p[0], p[1]);
-                                hi = f2_bits(p[2], p[3]);
-                            }
+                            lo = f2_bits(p[0], p[1]);
+                            hi = f2_bits(p[2], p[3]);
                         }
                     }
                     ready = __all_sync(0xffffffffu, ready);

@@ -46,8 +46,13 @@ constexpr int kGwThreads = 512, kGwTile = 3, kGwFirstEpi = 4, kGwFirstGather = 1
 constexpr int kGwChunk = 8;              // blocks whose factors are handed over at a time
 constexpr int kGwRows = 256, kGwChannels = 256;
 // Registers of a thread: 128 at launch; the summing warpgroups take what the others
-// give up (64 x 256 + 192 x 256 = 128 x 512).
-constexpr int kGwRegsFew = 64, kGwRegsMany = 192;
+// give up: their sum over the four warpgroups stays 512.  (A spill in any of the loops
+// costs more than it looks: with 48, 64 and 200 bf16 rows gathered took 353 us instead
+// of 268.)
+template <bool kBlock> struct GwRegs {
+    static constexpr int kFew = kBlock ? 56 : 72, kGather = kBlock ? 88 : 72, kMany = 184;
+    static_assert(kFew + kGather + 2 * kMany == 512, "registers that the launch has");
+};
 constexpr uint32_t kGwX = 128 * 128, kGwHalf = 64 * 128, kGwStage = kGwX + 2 * kGwHalf;
 // Staging of a warp: two tiles of 32 rows x 128 bytes in the 128-byte swizzle.
 constexpr uint32_t kGwStaging = 2 * 4096;
@@ -171,13 +176,11 @@ struct WideTiles {
     int row[kGwTiles][128];             // and the rows of x that they take
     uint64_t full[kGwTiles], empty[kGwTiles];
 };
-// The j-th tile of this CTA, for a whole warp.
-__device__ __forceinline__ bool take_tile(WideTiles &w, int j, int4 &a, volatile int *abort, uint32_t *there = nullptr,
-                                          int quarter = 0) {
+// The j-th tile of this CTA, for a whole warp, which then lets go of its place.
+__device__ __forceinline__ bool take_tile(WideTiles &w, int j, int4 &a, volatile int *abort) {
     const int s = j % kGwTiles;
     if (!mbar_wait_all(&w.full[s], (j / kGwTiles) & 1, abort)) return false;
     a = w.at[s];
-    if (there) *there = w.there[s][quarter];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&w.empty[s]);
     return true;
@@ -244,8 +247,8 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     tc_fence_after();
     if (bad && tid == 0 && blockIdx.x == 0) flag_status(GDN_DEVSTAT_BAD_SEQLEN);
 
-    if (warp < kGwFirstEpi || warp >= kGwFirstGather)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGwRegsFew));
+    if (warp < kGwFirstEpi) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GwRegs<kBlock>::kFew));
+    if (warp >= kGwFirstGather) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GwRegs<kBlock>::kGather));
     if (warp == 0) {
         // Half of the weight rows and this CTA's 128 rows of x, counted on the leader's barrier.
         const bool one = elect_lane();
@@ -391,7 +394,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
             const uint32_t to = smem_u32(smem) + sub * 128;
             // the 16 bytes' place in the swizzled rows of even fours, and of odd ones
             const uint32_t even = ((lane & 7) ^ sub) << 4, odd = ((lane & 7) ^ (sub + 4)) << 4;
-            const uint32_t stride16 = (uint32_t)(c.xs * (kBlock ? 1 : 2) / 16);   // a row in pieces (below 2^32: strides < 2^36)
+            const int64_t stride = c.xs * (kBlock ? 1 : 2);
             const int bytes = c.n_in * (kBlock ? 1 : 2) - (lane & 7) * 16;  // of the row from this lane's first on
             const int whole = c.n_in * (kBlock ? 1 : 2) / 128;              // blocks of 128 bytes
             int s = 0, i = 0;
@@ -421,7 +424,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
 #pragma unroll
                             for (int j = 0; j < N; ++j)
                                 copy16_if(row[j] < c.n_x, st + j * kGwGather * 512 + ((first + j * kGwGather) & 1 ? odd : even),
-                                          src + ((uint64_t)row[j] * stride16 << 4));
+                                          src + row[j] * stride);
                         } else {
                             const int n = min(16, max(0, bytes - k * 128));
 #pragma unroll 1
@@ -431,7 +434,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                                 for (int z = 1; z < N; ++z) at = z == j ? row[z] : at;      // no array in memory
                                 if (at < c.n_x)
                                     copy16(st + j * kGwGather * 512 + ((first + j * kGwGather) & 1 ? odd : even),
-                                           n > 0 ? src + ((uint64_t)at * stride16 << 4) : c.x, n);
+                                           n > 0 ? src + at * stride : c.x, n);
                             }
                         }
                         copies_arrive(&gathered[s]);
@@ -516,78 +519,78 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
         }
         if (wrong) flag_status(GDN_DEVSTAT_BAD_INDEX);
     } else if (warp >= kGwFirstEpi && warp < kGwFirstGather) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGwRegsMany));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GwRegs<kBlock>::kMany));
         // Accumulator lane 32 q + l is token row 32 q + l of this CTA's 128; four warps a half.
         const int q = warp & 3, h = (warp - kGwFirstEpi) >> 2, p = kBlock ? h : 0;
         uint8_t *staging = smem + S * kGwStage + (warp - kGwFirstEpi) * kGwStaging;
+        const uint32_t sums = tmem_addr(tmem_base, q * 32, h * 128), release = peer_smem(smem_u32(acc_empty[p]), 0);
         int u = 0, v = 0;                  // accumulators and chunks of factors used so far
+        uint32_t r[2][32];
         bool ok = true, ready = false;     // the next accumulator is known to be there
-        for (int t = pair, tile = 0; t < tiles && ok; t += pairs, ++tile) {
-            int4 a;
-            uint32_t there;
-            if (!take_tile(wide, tile, a, abort, &there, q)) break;
-            const bool mine = !kBlock || h == 0 || a.z + 128 < c.n_out;
+        const int mine_tiles = tiles > pair ? (tiles - pair + pairs - 1) / pairs : 0;
+        for (int tile = 0; tile < mine_tiles; ++tile) {
+            const int slot = tile % kGwTiles;          // held until the tile is out: registers are short here
+            if (!mbar_wait_all(&wide.full[slot], (tile / kGwTiles) & 1, abort)) break;
+            const bool mine = !kBlock || h == 0 || wide.at[slot].z + 128 < c.n_out;
             F2 acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = f2(0.f, 0.f);
-            float f0 = 1.f;
-            const float *from_f = factors;
+            const float *sc = factors + h * kGwChunk * 128 + q * 32 + lane;
 #pragma unroll 1
-            for (int k = 0; k < (kBlock ? nk : 1); ++k) {
-                if (kBlock && k % kGwChunk == 0) {
-                    if (!mbar_wait_all(&sc_full[v & 1], (v >> 1) & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    from_f = factors + (v & 1) * (kGwFactors / 4) + h * kGwChunk * 128 + q * 32 + lane;
-                    f0 = *from_f;
+            for (int k0 = 0; k0 < (kBlock ? nk : 1) && ok; k0 += kGwChunk) {
+                const int n = kBlock ? min(nk - k0, kGwChunk) : 1;
+                const float *f = sc + (v & 1) * (kGwFactors / 4);
+                if (kBlock && !mbar_wait_all(&sc_full[v & 1], (v >> 1) & 1, abort)) {
+                    ok = false;
+                    break;
                 }
-                // a chunk's last factor is read: its block is still to come
-                const bool end = kBlock && (k % kGwChunk == kGwChunk - 1 || k == nk - 1);
-                if (end) {
+                float f0 = kBlock ? *f : 1.f;
+#pragma unroll 1
+                for (int k = 0; mine && k < n; ++k) {
+                    if (!ready) {
+                        if (!mbar_wait_all(&acc_full[p][u & 1], (u >> 1) & 1, abort)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    tc_fence_after();
+                    tmem_ask(sums + (u & 1) * 256, r[0]);
+                    const uint32_t from = sums + (u & 1) * 256;
+                    const F2 f2x = f2(f0, f0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        tmem_wait(r[j & 1]);
+                        if (j < 3) {
+                            tmem_ask(from + (j + 1) * 32, r[(j + 1) & 1]);
+                        } else {                           // all of it has been read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(release + (u & 1) * 8);
+                            ++u;
+                            if (kBlock && k + 1 < n) f0 = f[(k + 1) * 128];
+                            // the next block's first columns, while this one's last are added
+                            ready = mbar_test(&acc_full[p][u & 1], (u >> 1) & 1);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const F2 x = f2_bits(r[j & 1][2 * i], r[j & 1][2 * i + 1]);
+                            acc[j * 16 + i] = kBlock ? f2_fma(x, f2x, acc[j * 16 + i]) : x;
+                        }
+                    }
+                    ready = __all_sync(0xffffffffu, ready);
+                }
+                if (kBlock) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_empty[v & 1]);
                     ++v;
                 }
-                if (!mine) continue;                       // no channels: only the factors pass
-                const F2 f = f2(f0, f0);
-                const int b = u & 1;
-                if (!ready && !mbar_wait_all(&acc_full[p][b], (u >> 1) & 1, abort)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t from = tmem_addr(tmem_base, q * 32, (b * 2 + h) * 128);
-                uint32_t r[2][32];
-                tmem_ask(from, r[0]);
-                ++u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    tmem_wait(r[j & 1]);
-                    if (j < 3) {
-                        tmem_ask(from + (j + 1) * 32, r[(j + 1) & 1]);
-                    } else {                               // all of it has been read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(peer_smem(smem_u32(&acc_empty[p][b]), 0));
-                        // the next block's barrier and factor, while this one's last products are added
-                        ready = mbar_test(&acc_full[p][u & 1], (u >> 1) & 1);
-                        if (kBlock && !end) {
-                            from_f += 128;
-                            f0 = *from_f;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const F2 v2 = f2_bits(r[j & 1][2 * i], r[j & 1][2 * i + 1]);
-                        acc[j * 16 + i] = kBlock ? f2_fma(v2, f, acc[j * 16 + i]) : v2;
-                    }
-                }
-                ready = __all_sync(0xffffffffu, ready);
             }
             if (!ok) break;
-            if (mine)
-                wide_store<O>(acc, staging, &my, c, a.x + rank * 128 + q * 32, a.y, a.z + h * 128, there >> lane & 1, lane);
+            const int4 a = wide.at[slot];
+            const bool there = wide.there[slot][q] >> lane & 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wide.empty[slot]);
+            if (mine) wide_store<O>(acc, staging, &my, c, a.x + rank * 128 + q * 32, a.y, a.z + h * 128, there, lane);
         }
         if (lane == 0) bulk_wait_read_all();       // the staging tiles stay until they are read
         __syncwarp();
