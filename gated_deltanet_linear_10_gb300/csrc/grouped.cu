@@ -1,6 +1,8 @@
 // Products of rows with the weights of their expert, in bf16 or in e4m3 with an
 // fp32 scale for each block of 128 in k, and the product of all rows with one
 // weight in the latter form: argument checks, operand maps and the choice of a kernel.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "grouped.cuh"
@@ -18,20 +20,38 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
     return encode_tmap_operand(map, c.x, c.n_in, c.n_x, c.xs, box_rows, c.e4m3);
 }
 
-// By the rows that an expert has in the mean (the host knows no more): up to 64 go to
-// narrow tiles of twice as many rows, beyond 128 wide tiles pay where there are enough
-// of them for the pairs.
+// The choice of a tile: the shortest by an estimate of waves of tiles, each of as many
+// blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, a block) are
+// fitted to 1 to 4096 rows on products of 512 x 4096 to 4096 x 2048 and to 4 to 800 rows
+// for each of 8, 64 and 256 experts.  Of an expert's rows the host knows the mean: tiles of
+// r rows take mean / r + 1/2 of them, at least one.
 static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     const int64_t ye = c.out_f32 ? 4 : 2;
     c.vec16 = (uintptr_t)c.y % 16 == 0 && c.n_out * ye % 16 == 0 && (c.n_rows == 1 || c.ys * ye % 16 == 0);
     c.sx16 = (uintptr_t)c.sx % 16 == 0 && c.kb % 4 == 0;
-    const int drop = linear_drop();
-    const int mean = (c.n_rows + c.n_experts - 1) / c.n_experts;
-    const int64_t wide = ((int64_t)c.n_rows / 256 + (c.offsets ? std::min(c.n_experts, c.n_rows) : 1)) *
-                         ((c.n_out + 255) / 256);
-    if (mean > 128 && wide >= sm_count() / 2) return launch_grouped_wide(c, drop, s);
-    const int rows = c.offsets ? 2 * mean : mean;
-    return launch_grouped_narrow(c, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, drop, s);
+    struct Tile {
+        int rows, channels, ends, tile, block[2];      // block: bf16, e4m3
+    };
+    constexpr Tile kTiles[] = {{16, 128, 280, 70, {27, 27}}, {32, 128, 250, 80, {30, 30}}, {64, 128, 230, 90, {37, 35}},
+                               {128, 128, 380, 120, {48, 50}}, {256, 256, 450, 90, {42, 50}}};
+    const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
+    const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (const Tile &t : kTiles) {
+        const int64_t halves = c.offsets ? std::max<int64_t>(2 * (int64_t)experts, 2 * (int64_t)c.n_rows / t.rows + experts)
+                                         : 2 * (((int64_t)c.n_rows + t.rows - 1) / t.rows);
+        const int64_t tiles = (halves + 1) / 2 * ((c.n_out + t.channels - 1) / t.channels);
+        const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms;
+        const int64_t cost = t.ends + (tiles + slots - 1) / slots * (t.tile + blocks * t.block[c.e4m3]);
+        // (tiles beyond 31 bits are not launched)
+        if (cost < least && tiles < (1ll << 30)) {
+            least = cost;
+            best = t.rows;
+        }
+    }
+    if (best == 0) return GDN_ERR_UNSUPPORTED;
+    return best == 256 ? launch_grouped_wide(c, linear_drop(), s) : launch_grouped_narrow(c, best, linear_drop(), s);
 }
 
 }  // namespace gdn

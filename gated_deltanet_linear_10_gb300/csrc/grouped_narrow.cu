@@ -4,12 +4,12 @@
 //
 // Persistent CTAs, a warp for each part: loads (tiles by TMA; gathered rows in pieces
 // of 16 bytes, by a warp: a TMA gather of four rows takes 150 cycles and held one
-// token's block at 620), products, scales, and four or eight that sum the blocks.  With block scales
+// token's block at 620), products, scales, and 4 to 16 that sum the blocks.  With block scales
 // every block of 128 in k is a product of its own into one of four accumulators;
 // the summing warps add it, times sx sw of its column, to registers.  A block takes
-// such a warp some 500 cycles of waits and latencies, so two groups of four share the
-// columns of a tile of 64 or 128 rows (256 x 2048 x 8192: with one group 15.9 us, with
-// two 12.7).
+// such a warp some 500 cycles of waits and latencies, so groups of four share the columns
+// of a tile of 64 or 128 rows, 32 columns each (256 x 2048 x 8192 in tiles of 128: with
+// one group 15.9 us, with two 13, with four ...).
 #include <limits.h>
 
 #include <algorithm>
@@ -30,15 +30,15 @@ cudaError_t set_grouped_narrow_limit(uint64_t limit_ns, cudaStream_t s) {
 namespace {
 
 constexpr int kScaleChunk = 8;         // blocks whose scales are handed over at a time
-// Warps: 0 loads by TMA, 1 products, 2 scales, 3 on sums, the last one gathered rows: 12 at
-// most, which leave a thread 168 registers.
+// Warps: 0 loads by TMA, 1 products, 2 scales, 3 on sums, the last one gathered rows: a
+// multiple of four, by which registers are shared out.
 constexpr int kGnScale = 2, kGnFirstSum = 3, kGnGather = 1;
 
 template <int BT> struct GnCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
     static constexpr int kStages = BT == 16 ? 11 : BT == 32 ? 10 : BT == 64 ? 8 : 6;
     static constexpr int kAccs = 4;
-    static constexpr int kSums = BT >= 64 ? 8 : 4;        // summing warps, groups of four share the columns
+    static constexpr int kSums = BT == 128 ? 16 : BT == 64 ? 8 : 4;   // summing warps, groups of four share the columns
     static constexpr int kWidth = BT * 4 / kSums;         // columns of one
     static constexpr int kThreads = 32 * (kGnFirstSum + kSums + kGnGather);
     static constexpr uint32_t kScales = 2 * kScaleChunk * BT * 4;
