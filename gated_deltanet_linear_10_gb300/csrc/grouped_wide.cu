@@ -39,7 +39,7 @@ cudaError_t set_grouped_wide_limit(uint64_t limit_ns, cudaStream_t s) {
 
 namespace {
 
-constexpr int kGwStages = 4, kGwEpiWarps = 8;
+constexpr int kGwEpiWarps = 8;
 // Warps: 0 loads by TMA, 1 and 2 products, 3 looks up tiles and makes the factors, 4 to 11
 // sums, 12 to 14 gathered rows, 15 hands them over.
 constexpr int kGwThreads = 512, kGwTile = 3, kGwFirstEpi = 4, kGwFirstGather = 12, kGwGather = 3, kGwRelay = 15;
@@ -54,10 +54,16 @@ template <bool kBlock> struct GwRegs {
     static_assert(kFew + kGather + 2 * kMany == 512, "registers that the launch has");
 };
 constexpr uint32_t kGwX = 128 * 128, kGwHalf = 64 * 128, kGwStage = kGwX + 2 * kGwHalf;
-// Staging of a warp: two tiles of 32 rows x 128 bytes in the 128-byte swizzle.
-constexpr uint32_t kGwStaging = 2 * 4096;
 constexpr uint32_t kGwFactors = 2 * kGwChunk * 128 * 4;       // [half][block][row], fp32
-constexpr uint32_t kGwSmem = kGwStages * kGwStage + kGwEpiWarps * kGwStaging + 2 * kGwFactors;
+// Shared memory: the ring's stages, a warp's staging tiles of 32 rows x 128 bytes of y in
+// the 128-byte swizzle, the factors.  In bf16 a stage is used up in half the time, and a
+// fifth one gains more than a second staging tile (64 experts of 1300 rows: 261 -> 238
+// us; with block scales 301 -> 327).
+template <bool kBlock> struct GwSmem {
+    static constexpr int kStages = kBlock ? 4 : 5, kHold = kBlock ? 2 : 1;
+    static constexpr uint32_t kStaging = kHold * 4096;
+    static constexpr uint32_t kBytes = kStages * kGwStage + kGwEpiWarps * kStaging + (kBlock ? 2 * kGwFactors : 0);
+};
 
 // Loads into this CTA's shared memory, their bytes counted on a barrier of either CTA.
 __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y) {
@@ -105,7 +111,7 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
 // in pieces of 16 bytes, and where rows are no whole pieces, element by element.
 // (Rows of bulk copies, one a lane, took 5,500 cycles a tile and held up the loads
 // behind them.)
-template <typename O>
+template <typename O, int kHold>
 __device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging, const CUtensorMap *my,
                                            const GroupedCall &c, int row0, int r1, int n0, bool there, int lane) {
     constexpr int COLS = 128 / sizeof(O);              // channels of a staging tile
@@ -116,8 +122,8 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging
     for (int i = 0; i < 128 / COLS; ++i) {
         const int n = n0 + i * COLS, left = c.n_out - n;
         if (left <= 0 || rows <= 0) break;
-        uint8_t *tile = staging + i % 2 * 4096, *row = mine + i % 2 * 4096;
-        if (i % 2 == 0) {                              // the last stores have read the tiles
+        uint8_t *tile = staging + i % kHold * 4096, *row = mine + i % kHold * 4096;
+        if (i % kHold == 0) {                          // the last stores have read the tiles
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
         }
@@ -190,7 +196,8 @@ template <bool kBlock, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGwThreads, 1)
 grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                     const __grid_constant__ CUtensorMap my, const __grid_constant__ GroupedCall c, int keep) {
-    constexpr int S = kGwStages;
+    using M = GwSmem<kBlock>;
+    constexpr int S = M::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GroupTable table;
     __shared__ uint64_t full[S], empty[S], gathered[S], acc_full[2][2], acc_empty[2][2], drained[2], sc_full[2], sc_empty[2];   // [half][accumulator]
@@ -203,7 +210,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     constexpr int kElems = kBlock ? 128 : 64;
     const int nk = (c.n_in + kElems - 1) / kElems, nn = (c.n_out + kGwChannels - 1) / kGwChannels;
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-    float *factors = reinterpret_cast<float *>(smem + S * kGwStage + kGwEpiWarps * kGwStaging);
+    float *factors = reinterpret_cast<float *>(smem + S * kGwStage + kGwEpiWarps * M::kStaging);
     volatile int *abort = &abort_flag;
 
     if (tid == 0) {
@@ -522,7 +529,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GwRegs<kBlock>::kMany));
         // Accumulator lane 32 q + l is token row 32 q + l of this CTA's 128; four warps a half.
         const int q = warp & 3, h = (warp - kGwFirstEpi) >> 2, p = kBlock ? h : 0;
-        uint8_t *staging = smem + S * kGwStage + (warp - kGwFirstEpi) * kGwStaging;
+        uint8_t *staging = smem + S * kGwStage + (warp - kGwFirstEpi) * M::kStaging;
         const uint32_t sums = tmem_addr(tmem_base, q * 32, h * 128), release = peer_smem(smem_u32(acc_empty[p]), 0);
         int u = 0, v = 0;                  // accumulators and chunks of factors used so far
         uint32_t r[2][32];
@@ -590,7 +597,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
             const bool there = wide.there[slot][q] >> lane & 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&wide.empty[slot]);
-            if (mine) wide_store<O>(acc, staging, &my, c, a.x + rank * 128 + q * 32, a.y, a.z + h * 128, there, lane);
+            if (mine) wide_store<O, M::kHold>(acc, staging, &my, c, a.x + rank * 128 + q * 32, a.y, a.z + h * 128, there, lane);
         }
         if (lane == 0) bulk_wait_read_all();       // the staging tiles stay until they are read
         __syncwarp();
@@ -620,12 +627,12 @@ template <bool kBlock, typename O> gdn_status launch(const GroupedCall &c, int d
         return GDN_ERR_CUDA;
     auto kernel = grouped_wide_kernel<kBlock, O>;
     static SmemAllowed allowed;
-    cudaError_t e = allowed.ask(kernel, kGwSmem);
+    cudaError_t e = allowed.ask(kernel, GwSmem<kBlock>::kBytes);
     const int64_t nn = (c.n_out + kGwChannels - 1) / kGwChannels;
     const int64_t tiles = (((int64_t)c.n_rows + kGwRows - 1) / kGwRows + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     if (e == cudaSuccess)
-        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(2 * tiles, sm_count() / 2 * 2)), dim3(kGwThreads), kGwSmem,
+        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(2 * tiles, sm_count() / 2 * 2)), dim3(kGwThreads), GwSmem<kBlock>::kBytes,
                          s, mx, mw, my, c, drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : (c.n_in + (kBlock ? 127 : 63)) / (kBlock ? 128 : 64));
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
