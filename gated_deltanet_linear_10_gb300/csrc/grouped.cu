@@ -23,17 +23,21 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
 // The choice of a tile: the shortest by an estimate of waves of tiles, each of as many
 // blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, a block) are
 // fitted to 1 to 4096 rows on products of 512 x 4096 to 4096 x 2048 and to 4 to 800 rows
-// for each of 8, 64 and 256 experts.  Of an expert's rows the host knows the mean: tiles of
-// r rows take mean / r + 1/2 of them, at least one.
+// for each of 8, 60 and 256 experts, rows in place and gathered.  Of an expert's rows the
+// host knows the mean: tiles of r rows take mean / r + 1/2 of them, at least one.
 static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     const int64_t ye = c.out_f32 ? 4 : 2;
     c.vec16 = (uintptr_t)c.y % 16 == 0 && c.n_out * ye % 16 == 0 && (c.n_rows == 1 || c.ys * ye % 16 == 0);
+    c.vec4 = (uintptr_t)c.y % 4 == 0 && (c.n_rows == 1 || c.ys * ye % 4 == 0);
     c.sx16 = (uintptr_t)c.sx % 16 == 0 && c.kb % 4 == 0;
     struct Tile {
-        int rows, channels, ends, tile, block[2];      // block: bf16, e4m3
+        int rows, channels, ends, tile, block[2][2];   // block: bf16, e4m3; rows in place, gathered
     };
-    constexpr Tile kTiles[] = {{16, 128, 280, 70, {27, 27}}, {32, 128, 250, 80, {30, 30}}, {64, 128, 230, 90, {37, 35}},
-                               {128, 128, 380, 120, {48, 50}}, {256, 256, 450, 90, {42, 50}}};
+    constexpr Tile kTiles[] = {{16, 128, 280, 70, {{26, 27}, {27, 27}}},
+                               {32, 128, 250, 80, {{26, 30}, {29, 31}}},
+                               {64, 128, 230, 90, {{28, 37}, {33, 46}}},
+                               {128, 128, 380, 120, {{30, 63}, {44, 78}}},
+                               {256, 256, 450, 90, {{40, 42}, {50, 53}}}};
     const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
     const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;
     int best = 0;
@@ -43,7 +47,7 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
                                          : 2 * (((int64_t)c.n_rows + t.rows - 1) / t.rows);
         const int64_t tiles = (halves + 1) / 2 * ((c.n_out + t.channels - 1) / t.channels);
         const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms;
-        const int64_t cost = t.ends + (tiles + slots - 1) / slots * (t.tile + blocks * t.block[c.e4m3]);
+        const int64_t cost = t.ends + (tiles + slots - 1) / slots * (t.tile + blocks * t.block[c.e4m3][c.rows != nullptr]);
         // (tiles beyond 31 bits are not launched)
         if (cost < least && tiles < (1ll << 30)) {
             least = cost;

@@ -22,6 +22,7 @@ struct GroupedCall {
     int n_rows, n_x, n_experts, n_in, n_out, kb, nb;
     bool e4m3, out_f32;
     bool vec16;                      // rows of y on 16-byte boundaries, whole 16 bytes of them
+    bool vec4;                       // rows of y on 4-byte boundaries
     bool sx16;                       // rows of sx on 16-byte boundaries
 };
 

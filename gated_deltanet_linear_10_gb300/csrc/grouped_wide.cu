@@ -108,7 +108,7 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
 
 // A warp's 32 rows x 128 channels n0 .. out, through its staging tiles:
 // by a TMA store that goes on behind the call; where the expert ends within the rows,
-// in pieces of 16 bytes, and where rows are no whole pieces, element by element.
+// in pieces of 16 bytes, and where rows are no whole pieces, by words or elements.
 // (Rows of bulk copies, one a lane, took 5,500 cycles a tile and held up the loads
 // behind them.)
 template <typename O, int kHold>
@@ -159,14 +159,27 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging
                         *reinterpret_cast<const uint4 *>(tile + r * 128 + ((piece ^ (r & 7)) << 4));
             }
         } else {
-#pragma unroll 4
-            for (int r = 0; r < min(32, rows); ++r)
+            // words of 4 bytes, or elements; eight rows are read before the first is written
+            constexpr int E = 4 / sizeof(O);               // elements of a word
+#pragma unroll 1
+            for (int r = 0; r < min(32, rows); r += 8) {
+                uint32_t v[8];
 #pragma unroll
-                for (int col = lane; col < COLS; col += 32) {
-                    const uint32_t at = col * (uint32_t)sizeof(O);
-                    if (col < left)
-                        y[r * c.ys + n + col] = *reinterpret_cast<const O *>(tile + r * 128 + ((at >> 4 ^ (r & 7)) << 4) + (at & 15));
+                for (int j = 0; j < 8; ++j)
+                    v[j] = *reinterpret_cast<const uint32_t *>(tile + (r + j) * 128 + ((lane >> 2 ^ (j & 7)) << 4) + (lane & 3) * 4);
+                const int col = lane * E;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (r + j >= rows || col >= left) continue;
+                    O *p = y + (r + j) * c.ys + n + col;
+                    if (E == 1 || (c.vec4 && col + 1 < left)) {
+                        *reinterpret_cast<uint32_t *>(p) = v[j];
+                    } else {
+                        reinterpret_cast<uint16_t *>(p)[0] = (uint16_t)v[j];
+                        if (col + 1 < left) reinterpret_cast<uint16_t *>(p)[1] = (uint16_t)(v[j] >> 16);
+                    }
                 }
+            }
         }
         __syncwarp();
     }
