@@ -5,8 +5,7 @@
 // Router.  One warp a token, the logits as 32-bit keys of the same order (key_of).
 // The top-th largest of the lanes' largest keys is a bound that at least `top`
 // experts reach and few others do; these go to shared memory, and an expert's place
-// among them is the number of larger ones (ties: of lower index).  290 instructions a
-// token of 512 experts instead of 650 for taking the largest ten times.
+// among them is the number of larger ones (ties: of lower index).
 //
 // The sort is a counting sort: a chunk of up to 64 tokens keeps, per expert, a word
 // of 64 bits with the tokens that ask for it, so that a pair's place within its chunk
@@ -28,7 +27,7 @@ constexpr int kMaxExperts = 1024, kMaxTop = 32;
 constexpr int kChunk = 64;                 // the most tokens of a chunk
 constexpr int kRouteThreads = 256;
 // Tokens of a chunk: whole rounds of a CTA's eight warps, and as few as leave the chunks
-// one wave of four CTAs an SM (20668 tokens in chunks of 64, two waves: 31 us, of 40 ...).
+// one wave of four CTAs an SM (20668 tokens in chunks of 64: 31 us, of 40: 26).
 constexpr int kWave = 608;
 static int chunk_of(int64_t n) {
     const int64_t per = (n + kWave - 1) / kWave;
@@ -46,17 +45,49 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu));
 }
 
+// What a lane keeps of an expert, and the word by which experts are ordered: the key,
+// then the index turned round, so that of equal logits the lowest index has the largest
+// word.  A bf16 logit's key has 16 bits, and one word of 32 is both.
+template <typename T> struct Choice;
+template <> struct Choice<float> {
+    using Word = unsigned long long;
+    static __device__ __forceinline__ uint32_t keep(float v, int) { return key_of(v); }
+    static __device__ __forceinline__ Word word(uint32_t kept, int e) { return (Word)kept << 32 | (uint32_t)~e; }
+    static __device__ __forceinline__ float value(uint32_t kept) { return key_value(kept); }
+    static __device__ __forceinline__ float value_of(Word w) { return key_value((uint32_t)(w >> 32)); }
+    static __device__ __forceinline__ int index_of(Word w) { return (int)~(uint32_t)w; }
+    static __device__ __forceinline__ Word warp_max(Word w) {
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(w >> 32));
+        return (Word)hi << 32 | __reduce_max_sync(0xffffffffu, (uint32_t)(w >> 32) == hi ? (uint32_t)w : 0u);
+    }
+};
+template <> struct Choice<__nv_bfloat16> {
+    using Word = uint32_t;
+    static __device__ __forceinline__ uint32_t keep(float v, int e) { return (key_of(v) & 0xffff0000u) | (uint32_t)(0xffff - e); }
+    static __device__ __forceinline__ Word word(uint32_t kept, int) { return kept; }
+    static __device__ __forceinline__ float value(uint32_t kept) {
+        return __uint_as_float(__float_as_uint(key_value(kept)) & 0xffff0000u);
+    }
+    static __device__ __forceinline__ float value_of(Word w) { return value(w); }
+    static __device__ __forceinline__ int index_of(Word w) { return 0xffff - (int)(w & 0xffffu); }
+    static __device__ __forceinline__ Word warp_max(Word w) { return __reduce_max_sync(0xffffffffu, w); }
+};
+constexpr int kCands = 64;                 // candidates of a token that are kept
+
 // A warp's token: its `top` choices to ids and weights, each(expert, place) for every one
-// of them.  PER: experts of a lane, VEC of them neighbours; cands: kCands words of the
+// of them.  PER: experts of a lane, VEC of them neighbours; space: kCands words of the
 // warp's own, for the candidates.
-template <typename T, int PER, int VEC, int kCands, typename F>
-__device__ __forceinline__ void route_token(const T *row, int experts, int top, bool renorm, int lane, uint64_t *cands,
+template <typename T, int PER, int VEC, typename F>
+__device__ __forceinline__ void route_token(const T *row, int experts, int top, bool renorm, int lane, uint64_t *space,
                                             int32_t *ids, float *weights, F each) {
-    uint32_t key[PER];
+    using C = Choice<T>;
+    using Word = typename C::Word;
+    uint32_t kept[PER];
     uint32_t most = 0;
+    auto index = [&](int i) { return i / VEC * VEC * 32 + lane * VEC + i % VEC; };
 #pragma unroll
     for (int i = 0; i < PER; i += VEC) {
-        const int e = i * 32 + lane * VEC;
+        const int e = index(i);
         float v[VEC];
         if constexpr (VEC == 1) {
             v[0] = e < experts ? Io<T>::load(row + e) : 0.f;
@@ -65,12 +96,12 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            key[i + j] = e < experts ? key_of(v[j]) : 0u;
-            most = max(most, key[i + j]);
+            kept[i + j] = e < experts ? C::keep(v[j], e + j) : 0u;
+            most = max(most, kept[i + j]);
         }
     }
     // the bound: each lane's place among the 32, the smallest of those that come first
-    uint32_t *lanes = reinterpret_cast<uint32_t *>(cands);
+    uint32_t *lanes = reinterpret_cast<uint32_t *>(space);
     __syncwarp();                              // the last token's are read
     lanes[lane] = most;
     __syncwarp();
@@ -82,19 +113,18 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
     }
     // (no lane's, where fewer lanes than choices have an expert: all experts)
     const uint32_t bound = max(__reduce_min_sync(0xffffffffu, place < top ? most : 0xffffffffu), 1u);
-    const uint32_t first = __reduce_max_sync(0xffffffffu, most);
-    const float top1 = key_value(first);
+    const float top1 = C::value(__reduce_max_sync(0xffffffffu, most));
     float all = 0.f;
     if (!renorm) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (key[i]) all += expf(key_value(key[i]) - top1);
+            if (kept[i]) all += expf(C::value(kept[i]) - top1);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
     }
     int cnt = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) cnt += key[i] >= bound;
+    for (int i = 0; i < PER; ++i) cnt += kept[i] >= bound;
     int scan = cnt;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -102,33 +132,29 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
         if (lane >= off) scan += o;
     }
     const int total = __shfl_sync(0xffffffffu, scan, 31);
-    // a candidate: its key, then its index turned round, so that the larger word goes first
-    auto word = [&](int i) { return (uint64_t)key[i] << 32 | (uint32_t)~(i / VEC * VEC * 32 + lane * VEC + i % VEC); };
+    Word *cands = reinterpret_cast<Word *>(space);
     __syncwarp();                              // the lanes' largest are read
     if (total <= kCands) {
-        int at = scan - cnt;
+        Word *to = cands + scan - cnt;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (key[i] >= bound) cands[at++] = word(i);
-        __syncwarp();
+            if (kept[i] >= bound) *to++ = C::word(kept[i], index(i));
     } else {                                   // many alike: the largest, one after the other
         for (int j = 0; j < top; ++j) {
-            uint64_t best = 0;
+            Word best = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const uint64_t w = key[i] ? word(i) : 0;
+                const Word w = kept[i] ? C::word(kept[i], index(i)) : 0;
                 best = w > best ? w : best;
             }
-            const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-            const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-            const uint64_t is = (uint64_t)hi << 32 | lo;
+            best = C::warp_max(best);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (word(i) == is) key[i] = 0;
-            if (lane == 0) cands[j] = is;
+                if (C::word(kept[i], index(i)) == best) kept[i] = 0;
+            if (lane == 0) cands[j] = best;
         }
-        __syncwarp();
     }
+    __syncwarp();
     const int n = total <= kCands ? total : top;
     float p[kCands / 32];
     int rank[kCands / 32];
@@ -137,12 +163,12 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
     for (int q = 0; q < kCands / 32; ++q) {
         rank[q] = kCands;
         if (q * 32 >= n) continue;
-        const uint64_t mine = q * 32 + lane < n ? cands[q * 32 + lane] : 0;
+        const Word mine = q * 32 + lane < n ? cands[q * 32 + lane] : 0;
         int r = 0;
 #pragma unroll 4
         for (int j = 0; j < n; ++j) r += cands[j] > mine;
         rank[q] = mine ? r : kCands;
-        p[q] = rank[q] < top ? expf(key_value((uint32_t)(mine >> 32)) - top1) : 0.f;
+        p[q] = rank[q] < top ? expf(C::value_of(mine) - top1) : 0.f;
         sum += p[q];
     }
     if (renorm) {
@@ -153,7 +179,7 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
 #pragma unroll
     for (int q = 0; q < kCands / 32; ++q)
         if (rank[q] < top) {
-            const int id = (int)~(uint32_t)cands[q * 32 + lane];
+            const int id = C::index_of(cands[q * 32 + lane]);
             ids[rank[q]] = id;
             weights[rank[q]] = top1 == -INFINITY ? 0.f : p[q] / all;      // no expert is open to the token
             each(id, rank[q]);
@@ -166,13 +192,13 @@ __global__ void __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 2)
 route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int chunk, int experts, int top, bool renorm,
                  int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ counts) {
     __shared__ int count[kMaxExperts];
-    __shared__ uint64_t cands[kRouteThreads / 32][64];
+    __shared__ uint64_t cands[kRouteThreads / 32][kCands];
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * chunk;
     for (int e = tid; e < experts; e += kRouteThreads) count[e] = 0;
     __syncthreads();
     for (int t = t0 + (tid >> 5); t < min(t0 + chunk, n_tokens); t += kRouteThreads / 32)
-        route_token<T, PER, VEC, 64>(logits + t * ls, experts, top, renorm, lane, cands[tid >> 5], ids + (int64_t)t * top,
+        route_token<T, PER, VEC>(logits + t * ls, experts, top, renorm, lane, cands[tid >> 5], ids + (int64_t)t * top,
                                      weights + (int64_t)t * top, [&](int id, int) { atomicAdd(&count[id], 1); });
     __syncthreads();
     griddep_launch();
@@ -222,7 +248,7 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
                      int32_t *__restrict__ rows, int32_t *__restrict__ slots) {
     __shared__ unsigned long long mask[kMaxExperts];
     __shared__ int base[kMaxExperts], warp_sum[32];
-    __shared__ uint64_t cands[kClusterThreads / 32][64];
+    __shared__ uint64_t cands[kClusterThreads / 32][kCands];
     __shared__ uint16_t pick[kChunk * kMaxTop];
     static_assert(kClusterThreads >= kMaxExperts, "a thread an expert");
     const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x;
@@ -234,7 +260,7 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
     __syncthreads();
     for (int t = tid >> 5; t < n; t += kClusterThreads / 32) {
         int32_t *to = ids + (int64_t)(t0 + t) * top;
-        route_token<T, PER, VEC, 64>(logits + (t0 + t) * ls, experts, top, renorm, lane, cands[tid >> 5], to,
+        route_token<T, PER, VEC>(logits + (t0 + t) * ls, experts, top, renorm, lane, cands[tid >> 5], to,
                                  weights + (int64_t)(t0 + t) * top,
                                  [&](int id, int place) {
                                      atomicOr(&mask[id], 1ull << t);
@@ -273,23 +299,38 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
 }
 
 // Per expert the sum over the chunks in front of each one, in place, and over all
-// of them.  32 experts a CTA, each by 32 threads, a run of chunks for a thread.
+// of them.  8 experts a CTA, each by 128 threads, a run of chunks for a thread.
+constexpr int kScanExperts = 8;
 __global__ void __launch_bounds__(1024)
 route_scan_kernel(int32_t *__restrict__ counts, int chunks, int experts, int32_t *__restrict__ totals) {
-    __shared__ int part[32][33];
+    __shared__ int part[32][kScanExperts];
     griddep_wait();
-    const int x = threadIdx.x & 31, g = threadIdx.x >> 5, e = blockIdx.x * 32 + x;
-    const int a = (int)((int64_t)chunks * g / 32), b = (int)((int64_t)chunks * (g + 1) / 32);
+    griddep_launch();
+    const int x = threadIdx.x % kScanExperts, g = threadIdx.x / kScanExperts, e = blockIdx.x * kScanExperts + x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int a = (int)((int64_t)chunks * g / 128), b = (int)((int64_t)chunks * (g + 1) / 128);
     int sum = 0;
     if (e < experts)
+#pragma unroll 8
         for (int c = a; c < b; ++c) sum += counts[(int64_t)c * experts + e];
-    part[g][x] = sum;
+    // the four runs of a warp, then the warps
+    int scan = sum;
+#pragma unroll
+    for (int off = kScanExperts; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += o;
+    }
+    if (lane >= 32 - kScanExperts) part[warp][x] = scan;
     __syncthreads();
-    griddep_launch();
-    int before = 0;
-    for (int i = 0; i < g; ++i) before += part[i][x];
+    int before = scan - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += part[w][x];
+        all += part[w][x];
+    }
     if (e >= experts) return;
-    if (g == 31) totals[e] = before + sum;
+    if (g == 0) totals[e] = all;
+#pragma unroll 8
     for (int c = a; c < b; ++c) {
         const int n = counts[(int64_t)c * experts + e];
         counts[(int64_t)c * experts + e] = before;
@@ -380,7 +421,7 @@ template <typename T> static cudaError_t launch_route(const RouteCall &c, int32_
     const int chunks = (c.n + c.chunk - 1) / c.chunk;
     cudaError_t e = for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchTop<T>{c});
     if (e == cudaSuccess)
-        e = launch_after(route_scan_kernel, dim3((c.experts + 31) / 32), dim3(1024), 0, c.s, c.counts, chunks, c.experts, totals);
+        e = launch_after(route_scan_kernel, dim3((c.experts + kScanExperts - 1) / kScanExperts), dim3(1024), 0, c.s, c.counts, chunks, c.experts, totals);
     if (e == cudaSuccess)
         e = launch_after(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, c.s, (const int32_t *)c.ids,
                          (const int32_t *)c.counts, (const int32_t *)totals, c.n, c.chunk, c.experts, c.top, c.offsets, c.rows, c.slots);
