@@ -26,12 +26,11 @@ GDN_STATUS_READER(read_status_moe, g_status_moe)
 constexpr int kMaxExperts = 1024, kMaxTop = 32;
 constexpr int kChunk = 64;                 // the most tokens of a chunk
 constexpr int kRouteThreads = 256;
-// Tokens of a chunk: whole rounds of a CTA's eight warps, and as few as leave the chunks
-// one wave of four CTAs an SM (20668 tokens in chunks of 64: 31 us, of 40: 26).
+// Tokens of a chunk: a round of a CTA's eight warps, more once the chunks fill a wave of
+// four CTAs an SM.
 constexpr int kWave = 608;
 static int chunk_of(int64_t n) {
-    const int64_t per = (n + kWave - 1) / kWave;
-    return (int)std::min<int64_t>(kChunk, (per + 7) / 8 * 8);
+    return (int)std::min<int64_t>(kChunk, std::max<int64_t>(kRouteThreads / 32, (n + kWave - 1) / kWave));
 }
 constexpr int kClusterTokens = 512;        // the most of the single launch: eight chunks
 
@@ -51,7 +50,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 template <typename T> struct Choice;
 template <> struct Choice<float> {
     using Word = unsigned long long;
-    static __device__ __forceinline__ uint32_t keep(float v, int) { return key_of(v); }
+    static constexpr uint32_t kLeast = 1;      // no logit keeps less
     static __device__ __forceinline__ Word word(uint32_t kept, int e) { return (Word)kept << 32 | (uint32_t)~e; }
     static __device__ __forceinline__ float value(uint32_t kept) { return key_value(kept); }
     static __device__ __forceinline__ float value_of(Word w) { return key_value((uint32_t)(w >> 32)); }
@@ -63,7 +62,7 @@ template <> struct Choice<float> {
 };
 template <> struct Choice<__nv_bfloat16> {
     using Word = uint32_t;
-    static __device__ __forceinline__ uint32_t keep(float v, int e) { return (key_of(v) & 0xffff0000u) | (uint32_t)(0xffff - e); }
+    static constexpr uint32_t kLeast = 1u << 16;
     static __device__ __forceinline__ Word word(uint32_t kept, int) { return kept; }
     static __device__ __forceinline__ float value(uint32_t kept) {
         return __uint_as_float(__float_as_uint(key_value(kept)) & 0xffff0000u);
@@ -72,53 +71,133 @@ template <> struct Choice<__nv_bfloat16> {
     static __device__ __forceinline__ int index_of(Word w) { return 0xffff - (int)(w & 0xffffu); }
     static __device__ __forceinline__ Word warp_max(Word w) { return __reduce_max_sync(0xffffffffu, w); }
 };
+
+// A lane's logits of a token as they are in memory: PER experts, VEC of them neighbours.
+template <typename T, int PER, int VEC> struct RawLogits {
+    static constexpr int W = (PER * (int)sizeof(T) + 3) / 4;
+    uint32_t w[W];
+    static __device__ __forceinline__ int index(int i, int lane) { return i / VEC * VEC * 32 + lane * VEC + i % VEC; }
+    __device__ __forceinline__ void load(const T *row, int experts, int lane) {
+        if constexpr (VEC > 1) {
+#pragma unroll
+            for (int i = 0; i < PER; i += VEC) {
+                const int e = index(i, lane);
+                const uint4 v = e < experts ? *reinterpret_cast<const uint4 *>(row + e) : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t *to = w + i / VEC * 4;
+                to[0] = v.x;
+                to[1] = v.y;
+                to[2] = v.z;
+                to[3] = v.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                w[i] = index(i, lane) < experts ? *reinterpret_cast<const uint32_t *>(row + index(i, lane)) : 0u;
+        } else {
+            auto half = [&](int i) {
+                return i < PER && index(i, lane) < experts ? *reinterpret_cast<const uint16_t *>(row + index(i, lane)) : (uint16_t)0;
+            };
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = half(2 * i) | (uint32_t)half(2 * i + 1) << 16;
+        }
+    }
+};
+
+// Two bf16 logits at a time, in the halves of a word: what a token takes in instructions
+// is what the router is bound by (one at a time: 20668 x 512 experts 26 us).
+__device__ __forceinline__ uint32_t key_of_two(uint32_t v) {
+    uint32_t b, sign;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v), "r"(0u));
+    asm("prmt.b32 %0, %1, %1, 0xbb99;" : "=r"(sign) : "r"(b));        // each half's sign in all its bits
+    return b ^ (sign | 0x80008000u);
+}
+__device__ __forceinline__ uint32_t max_of_two(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// What a lane keeps of its experts, and of the largest one (of no expert: less than kLeast).
+template <int PER, int VEC>
+__device__ __forceinline__ uint32_t keep_logits(const RawLogits<float, PER, VEC> &raw, int experts, int lane, uint32_t (&kept)[PER]) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        kept[i] = raw.index(i, lane) < experts ? key_of(__uint_as_float(raw.w[i])) : 0u;
+        most = max(most, kept[i]);
+    }
+    return most;
+}
+template <int PER, int VEC>
+__device__ __forceinline__ uint32_t keep_logits(const RawLogits<__nv_bfloat16, PER, VEC> &raw, int experts, int lane, uint32_t (&kept)[PER]) {
+    uint32_t two = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i += 2) {
+        const int e = raw.index(i, lane), f = raw.index(i + 1, lane);
+        uint32_t k = e < experts ? key_of_two(raw.w[i / 2]) : 0u;
+        if ((VEC == 1 && f >= experts) || PER == 1) k &= 0xffffu;
+        two = max_of_two(two, k);
+        kept[i] = __byte_perm(k, 0xffff - e, 0x1054);
+        if constexpr (PER > 1) kept[i + 1] = __byte_perm(k, 0xffff - f, 0x3254);
+    }
+    return max(two << 16, two & 0xffff0000u);
+}
+
+// The top-th largest of the lanes' `most`, or a little less: at least `top` experts keep as
+// much, where there are so many.  space: 128 bytes of the warp's own.
+template <typename T>
+__device__ __forceinline__ uint32_t bound_of(uint32_t most, int top, int lane, void *space) {
+    __syncwarp();                              // the last token's are read
+    if constexpr (sizeof(T) == 4) {
+        uint32_t *lanes = reinterpret_cast<uint32_t *>(space);
+        lanes[lane] = most;
+        __syncwarp();
+        int place = 0;                         // lanes with more
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(lanes + j);
+            place += (q.x > most) + (q.y > most) + (q.z > most) + (q.w > most);
+        }
+        return __reduce_min_sync(0xffffffffu, place < top ? most : 0xffffffffu);
+    } else {
+        // 15 bits of each: the difference's highest bit says which is larger, of two lanes at a time
+        const uint32_t mine = most >> 17, twice = (mine | 0x8000u) * 0x10001u;
+        reinterpret_cast<uint16_t *>(space)[lane] = (uint16_t)mine;
+        __syncwarp();
+        uint32_t less = 0;                     // a bit for each lane that has no more
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 q = reinterpret_cast<const uint4 *>(space)[j];
+            uint32_t a, b;
+            asm("prmt.b32 %0, %1, %2, 0xfdb9;" : "=r"(a) : "r"(twice - q.x), "r"(twice - q.y));
+            asm("prmt.b32 %0, %1, %2, 0xfdb9;" : "=r"(b) : "r"(twice - q.z), "r"(twice - q.w));
+            less |= (a & (0x01010101u << 2 * j)) | (b & (0x02020202u << 2 * j));
+        }
+        const int place = 32 - __popc(less);
+        return __reduce_min_sync(0xffffffffu, place < top ? mine : 0x7fffu) << 17;
+    }
+}
 constexpr int kCands = 64;                 // candidates of a token that are kept
+constexpr int kCandSpace = kCands + 4;     // words, some behind them of zeros
 
 // A warp's token: its `top` choices to ids and weights, each(expert, place) for every one
-// of them.  PER: experts of a lane, VEC of them neighbours; space: kCands words of the
-// warp's own, for the candidates.
+// of them.  space: kCandSpace words of the warp's own, for the candidates.
 template <typename T, int PER, int VEC, typename F>
-__device__ __forceinline__ void route_token(const T *row, int experts, int top, bool renorm, int lane, uint64_t *space,
-                                            int32_t *ids, float *weights, F each) {
+__device__ __forceinline__ void route_token(const RawLogits<T, PER, VEC> &raw, int experts, int top, bool renorm, int lane,
+                                            uint64_t *space, int32_t *ids, float *weights, F each) {
     using C = Choice<T>;
     using Word = typename C::Word;
     uint32_t kept[PER];
-    uint32_t most = 0;
-    auto index = [&](int i) { return i / VEC * VEC * 32 + lane * VEC + i % VEC; };
-#pragma unroll
-    for (int i = 0; i < PER; i += VEC) {
-        const int e = index(i);
-        float v[VEC];
-        if constexpr (VEC == 1) {
-            v[0] = e < experts ? Io<T>::load(row + e) : 0.f;
-        } else if (e < experts) {
-            Vec16<T>::load(row + e, v);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            kept[i + j] = e < experts ? C::keep(v[j], e + j) : 0u;
-            most = max(most, kept[i + j]);
-        }
-    }
-    // the bound: each lane's place among the 32, the smallest of those that come first
-    uint32_t *lanes = reinterpret_cast<uint32_t *>(space);
-    __syncwarp();                              // the last token's are read
-    lanes[lane] = most;
-    __syncwarp();
-    int place = 0;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(lanes + j);
-        place += (q.x > most) + (q.y > most) + (q.z > most) + (q.w > most);
-    }
+    const uint32_t most = keep_logits(raw, experts, lane, kept);
+    auto index = [&](int i) { return raw.index(i, lane); };
     // (no lane's, where fewer lanes than choices have an expert: all experts)
-    const uint32_t bound = max(__reduce_min_sync(0xffffffffu, place < top ? most : 0xffffffffu), 1u);
+    const uint32_t bound = max(bound_of<T>(most, top, lane, space), C::kLeast);
     const float top1 = C::value(__reduce_max_sync(0xffffffffu, most));
     float all = 0.f;
     if (!renorm) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (kept[i]) all += expf(C::value(kept[i]) - top1);
+            if (kept[i] >= C::kLeast) all += expf(C::value(kept[i]) - top1);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
     }
@@ -144,7 +223,7 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
             Word best = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const Word w = kept[i] ? C::word(kept[i], index(i)) : 0;
+                const Word w = kept[i] >= C::kLeast ? C::word(kept[i], index(i)) : 0;
                 best = w > best ? w : best;
             }
             best = C::warp_max(best);
@@ -154,8 +233,9 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
             if (lane == 0) cands[j] = best;
         }
     }
-    __syncwarp();
     const int n = total <= kCands ? total : top;
+    if (lane < 4) cands[n + lane] = 0;
+    __syncwarp();
     float p[kCands / 32];
     int rank[kCands / 32];
     float sum = 0.f;
@@ -165,8 +245,16 @@ __device__ __forceinline__ void route_token(const T *row, int experts, int top, 
         if (q * 32 >= n) continue;
         const Word mine = q * 32 + lane < n ? cands[q * 32 + lane] : 0;
         int r = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) r += cands[j] > mine;
+        for (int j = 0; j < n; j += 4) {
+            Word q[4];
+            if constexpr (sizeof(Word) == 4) {
+                *reinterpret_cast<uint4 *>(q) = *reinterpret_cast<const uint4 *>(cands + j);
+            } else {
+                *reinterpret_cast<ulonglong2 *>(q) = *reinterpret_cast<const ulonglong2 *>(cands + j);
+                *reinterpret_cast<ulonglong2 *>(q + 2) = *reinterpret_cast<const ulonglong2 *>(cands + j + 2);
+            }
+            r += (q[0] > mine) + (q[1] > mine) + (q[2] > mine) + (q[3] > mine);
+        }
         rank[q] = mine ? r : kCands;
         p[q] = rank[q] < top ? expf(C::value_of(mine) - top1) : 0.f;
         sum += p[q];
@@ -192,14 +280,27 @@ __global__ void __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 2)
 route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int chunk, int experts, int top, bool renorm,
                  int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ counts) {
     __shared__ int count[kMaxExperts];
-    __shared__ uint64_t cands[kRouteThreads / 32][kCands];
+    __shared__ __align__(16) uint64_t cands[kRouteThreads / 32][kCandSpace];
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * chunk;
     for (int e = tid; e < experts; e += kRouteThreads) count[e] = 0;
     __syncthreads();
-    for (int t = t0 + (tid >> 5); t < min(t0 + chunk, n_tokens); t += kRouteThreads / 32)
-        route_token<T, PER, VEC>(logits + t * ls, experts, top, renorm, lane, cands[tid >> 5], ids + (int64_t)t * top,
-                                     weights + (int64_t)t * top, [&](int id, int) { atomicAdd(&count[id], 1); });
+    // few registers: the next token's logits are on their way while one is worked on
+    constexpr bool kNext = RawLogits<T, PER, VEC>::W <= 8;
+    const int end = min(t0 + chunk, n_tokens);
+    RawLogits<T, PER, VEC> raw, next;
+    int t = t0 + (tid >> 5);
+    if (kNext && t < end) next.load(logits + t * ls, experts, lane);
+    for (; t < end; t += kRouteThreads / 32) {
+        if (kNext) {
+            raw = next;
+            if (t + kRouteThreads / 32 < end) next.load(logits + (t + kRouteThreads / 32) * ls, experts, lane);
+        } else {
+            raw.load(logits + t * ls, experts, lane);
+        }
+        route_token(raw, experts, top, renorm, lane, cands[tid >> 5], ids + (int64_t)t * top, weights + (int64_t)t * top,
+                    [&](int id, int) { atomicAdd(&count[id], 1); });
+    }
     __syncthreads();
     griddep_launch();
     for (int e = tid; e < experts; e += kRouteThreads) counts[(int64_t)blockIdx.x * experts + e] = count[e];
@@ -248,7 +349,7 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
                      int32_t *__restrict__ rows, int32_t *__restrict__ slots) {
     __shared__ unsigned long long mask[kMaxExperts];
     __shared__ int base[kMaxExperts], warp_sum[32];
-    __shared__ uint64_t cands[kClusterThreads / 32][kCands];
+    __shared__ __align__(16) uint64_t cands[kClusterThreads / 32][kCandSpace];
     __shared__ uint16_t pick[kChunk * kMaxTop];
     static_assert(kClusterThreads >= kMaxExperts, "a thread an expert");
     const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x;
@@ -260,12 +361,13 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
     __syncthreads();
     for (int t = tid >> 5; t < n; t += kClusterThreads / 32) {
         int32_t *to = ids + (int64_t)(t0 + t) * top;
-        route_token<T, PER, VEC>(logits + (t0 + t) * ls, experts, top, renorm, lane, cands[tid >> 5], to,
-                                 weights + (int64_t)(t0 + t) * top,
-                                 [&](int id, int place) {
-                                     atomicOr(&mask[id], 1ull << t);
-                                     pick[t * top + place] = (uint16_t)id;
-                                 });
+        RawLogits<T, PER, VEC> raw;
+        raw.load(logits + (t0 + t) * ls, experts, lane);
+        route_token(raw, experts, top, renorm, lane, cands[tid >> 5], to, weights + (int64_t)(t0 + t) * top,
+                    [&](int id, int place) {
+                        atomicOr(&mask[id], 1ull << t);
+                        pick[t * top + place] = (uint16_t)id;
+                    });
     }
     __syncthreads();
     cluster_arrive();
@@ -421,7 +523,8 @@ template <typename T> static cudaError_t launch_route(const RouteCall &c, int32_
     const int chunks = (c.n + c.chunk - 1) / c.chunk;
     cudaError_t e = for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchTop<T>{c});
     if (e == cudaSuccess)
-        e = launch_after(route_scan_kernel, dim3((c.experts + kScanExperts - 1) / kScanExperts), dim3(1024), 0, c.s, c.counts, chunks, c.experts, totals);
+        e = launch_after(route_scan_kernel, dim3((c.experts + kScanExperts - 1) / kScanExperts), dim3(1024), 0, c.s,
+                         c.counts, chunks, c.experts, totals);
     if (e == cudaSuccess)
         e = launch_after(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, c.s, (const int32_t *)c.ids,
                          (const int32_t *)c.counts, (const int32_t *)totals, c.n, c.chunk, c.experts, c.top, c.offsets, c.rows, c.slots);
