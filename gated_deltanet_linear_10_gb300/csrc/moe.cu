@@ -7,12 +7,13 @@
 // experts reach and few others do; these go to shared memory, and an expert's place
 // among them is the number of larger ones (ties: of lower index).
 //
-// The sort is a counting sort: a chunk of up to 64 tokens keeps, per expert, a word
-// of 64 bits with the tokens that ask for it, so that a pair's place within its chunk
-// is a population count of the bits below it.  That order (by expert, then by token)
-// depends on no timing.  Up to 512 tokens are one launch of one cluster, whose CTAs
-// read each other's words; more are three launches: choices and counts, sums over the
-// chunks, places.
+// The sort is a counting sort in three launches: a CTA has a run of tokens and counts,
+// per expert, who asks for it; sums over the runs in front; places, 64 tokens at a time:
+// per expert a word of 64 bits with those that ask for it, so that a pair's place is a
+// population count of the bits below it.  That order (by expert, then by token) depends
+// on no timing.  Up to 512 tokens are one launch of one cluster, whose CTAs read each
+// other's words.  (With runs in clusters too, that add up their counts, the second
+// launch goes, but 20668 tokens take 28 us instead of 24.)
 #include <algorithm>
 
 #include "linear.cuh"
@@ -24,14 +25,15 @@ GDN_DECLARE_STATUS_WORD(g_status_moe)
 GDN_STATUS_READER(read_status_moe, g_status_moe)
 
 constexpr int kMaxExperts = 1024, kMaxTop = 32;
-constexpr int kChunk = 64;                 // the most tokens of a chunk
+constexpr int kChunk = 64;                 // tokens placed at a time
 constexpr int kRouteThreads = 256;
-// Tokens of a chunk: a round of a CTA's eight warps, more once the chunks fill a wave of
-// four CTAs an SM.
+// Tokens of a run: a round of a CTA's eight warps, more once the CTAs fill a wave of four
+// an SM (20668 tokens in runs of 64, half a wave: 31 us where this took 26).
 constexpr int kWave = 608;
-static int chunk_of(int64_t n) {
-    return (int)std::min<int64_t>(kChunk, std::max<int64_t>(kRouteThreads / 32, (n + kWave - 1) / kWave));
+static int run_of(int64_t n) {
+    return (int)std::max<int64_t>(kRouteThreads / 32, (n + kWave - 1) / kWave);
 }
+static int runs_of(int64_t n) { return (int)((n + run_of(n) - 1) / run_of(n)); }
 constexpr int kClusterTokens = 512;        // the most of the single launch: eight chunks
 
 // Larger logits have larger keys; -0 equals 0 (by the addition, which also makes every
@@ -274,20 +276,20 @@ __device__ __forceinline__ void route_token(const RawLogits<T, PER, VEC> &raw, i
         }
 }
 
-// A chunk's tokens: ids and weights out, and per expert how many ask for it.
+// A run of tokens: ids and weights out, and per expert how many ask for it.
 template <typename T, int PER, int VEC>
 __global__ void __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 2)
-route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int chunk, int experts, int top, bool renorm,
+route_top_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int run, int experts, int top, bool renorm,
                  int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ counts) {
     __shared__ int count[kMaxExperts];
     __shared__ __align__(16) uint64_t cands[kRouteThreads / 32][kCandSpace];
     griddep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * chunk;
+    const int tid = threadIdx.x, lane = tid & 31, t0 = blockIdx.x * run;
     for (int e = tid; e < experts; e += kRouteThreads) count[e] = 0;
     __syncthreads();
     // few registers: the next token's logits are on their way while one is worked on
     constexpr bool kNext = RawLogits<T, PER, VEC>::W <= 8;
-    const int end = min(t0 + chunk, n_tokens);
+    const int end = min(t0 + run, n_tokens);
     RawLogits<T, PER, VEC> raw, next;
     int t = t0 + (tid >> 5);
     if (kNext && t < end) next.load(logits + t * ls, experts, lane);
@@ -400,79 +402,96 @@ route_cluster_kernel(const T *__restrict__ logits, int64_t ls, int n_tokens, int
     cluster_wait();                             // no CTA ends while another one may read its words
 }
 
-// Per expert the sum over the chunks in front of each one, in place, and over all
-// of them.  8 experts a CTA, each by 128 threads, a run of chunks for a thread.
-constexpr int kScanExperts = 8;
+// Per expert the sum over the runs in front of each one, in place, and over all of them.
+// 8 experts a CTA, each by 128 threads, a few runs for a thread.
+constexpr int kScanExperts = 8, kScanParts = 1024 / kScanExperts, kScanRuns = (kWave + kScanParts - 1) / kScanParts;
 __global__ void __launch_bounds__(1024)
-route_scan_kernel(int32_t *__restrict__ counts, int chunks, int experts, int32_t *__restrict__ totals) {
-    __shared__ int part[32][kScanExperts];
+route_scan_kernel(int32_t *__restrict__ counts, int runs, int experts, int32_t *__restrict__ totals) {
+    __shared__ int sums[32][kScanExperts];
     griddep_wait();
     griddep_launch();
-    const int x = threadIdx.x % kScanExperts, g = threadIdx.x / kScanExperts, e = blockIdx.x * kScanExperts + x;
+    const int x = threadIdx.x % kScanExperts, part = threadIdx.x / kScanExperts, e = blockIdx.x * kScanExperts + x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int a = (int)((int64_t)chunks * g / 128), b = (int)((int64_t)chunks * (g + 1) / 128);
-    int sum = 0;
-    if (e < experts)
-#pragma unroll 8
-        for (int c = a; c < b; ++c) sum += counts[(int64_t)c * experts + e];
-    // the four runs of a warp, then the warps
+    const int first = runs * part / kScanParts, end = e < experts ? runs * (part + 1) / kScanParts : 0;
+    int32_t *own = counts + (int64_t)first * experts + e;
+    int n[kScanRuns], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kScanRuns; ++i) {
+        n[i] = first + i < end ? own[(int64_t)i * experts] : 0;
+        sum += n[i];
+    }
+    // the four parts of a warp, then the warps
     int scan = sum;
 #pragma unroll
     for (int off = kScanExperts; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, scan, off);
         if (lane >= off) scan += o;
     }
-    if (lane >= 32 - kScanExperts) part[warp][x] = scan;
+    if (lane >= 32 - kScanExperts) sums[warp][x] = scan;
     __syncthreads();
     int before = scan - sum, all = 0;
 #pragma unroll
     for (int w = 0; w < 32; ++w) {
-        if (w < warp) before += part[w][x];
-        all += part[w][x];
+        if (w < warp) before += sums[w][x];
+        all += sums[w][x];
     }
-    if (e >= experts) return;
-    if (g == 0) totals[e] = all;
-#pragma unroll 8
-    for (int c = a; c < b; ++c) {
-        const int n = counts[(int64_t)c * experts + e];
-        counts[(int64_t)c * experts + e] = before;
-        before += n;
+    if (part == 0 && e < experts) totals[e] = all;
+#pragma unroll
+    for (int i = 0; i < kScanRuns; ++i) {
+        if (first + i < end) own[(int64_t)i * experts] = before;
+        before += n[i];
     }
 }
 
 // Each pair to its place.
 __global__ void __launch_bounds__(kRouteThreads)
 route_place_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
-                   const int32_t *__restrict__ totals, int n_tokens, int chunk, int experts, int top,
+                   const int32_t *__restrict__ totals, int n_tokens, int run, int experts, int top,
                    int32_t *__restrict__ offsets, int32_t *__restrict__ rows, int32_t *__restrict__ slots) {
+    constexpr int Q = kMaxExperts / kRouteThreads;          // experts of a thread
     __shared__ unsigned long long mask[kMaxExperts];
     __shared__ int base[kMaxExperts], warp_sum[kRouteThreads / 32];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < experts; e += kRouteThreads) mask[e] = 0;
     griddep_wait();
     griddep_launch();
-    const int tid = threadIdx.x, t0 = blockIdx.x * chunk;
-    const int n = min(chunk, n_tokens - t0) * top;           // pairs (none: only the offsets)
-    constexpr int Q = kMaxExperts / kRouteThreads;          // experts of a thread
-    int v[Q];
+    int v[Q], before[Q];
 #pragma unroll
-    for (int i = 0; i < Q; ++i) v[i] = tid * Q + i < experts && totals ? totals[tid * Q + i] : 0;
-    for (int e = tid; e < experts; e += kRouteThreads) mask[e] = 0;
+    for (int i = 0; i < Q; ++i) {
+        const int e = tid * Q + i;
+        v[i] = e < experts ? totals[e] : 0;
+        before[i] = e < experts ? counts[(int64_t)blockIdx.x * experts + e] : 0;
+    }
     const int all = scan_experts(v, warp_sum);
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
         const int e = tid * Q + i;
         if (e < experts) {
-            base[e] = v[i] + (n > 0 ? counts[(int64_t)blockIdx.x * experts + e] : 0);
+            base[e] = v[i] + before[i];
             if (blockIdx.x == 0) offsets[e] = v[i];
         }
     }
     if (blockIdx.x == 0 && tid == 0) offsets[experts] = all;
-    for (int i = tid; i < n; i += kRouteThreads) atomicOr(&mask[ids[(int64_t)t0 * top + i]], 1ull << (i / top));
-    __syncthreads();
-    for (int i = tid; i < n; i += kRouteThreads) {
-        const int t = i / top, e = ids[(int64_t)t0 * top + i];
-        const int r = base[e] + __popcll(mask[e] & ((1ull << t) - 1));
-        rows[r] = t0 + t;
-        slots[(int64_t)t0 * top + i] = r;
+    const int end = min((int)(blockIdx.x + 1) * run, n_tokens);
+    for (int t0 = blockIdx.x * run; t0 < end; t0 += kChunk) {
+        const int n = min(kChunk, end - t0) * top;          // pairs
+        const int32_t *from = ids + (int64_t)t0 * top;
+        for (int i = tid; i < n; i += kRouteThreads) atomicOr(&mask[from[i]], 1ull << (i / top));
+        __syncthreads();
+        for (int i = tid; i < n; i += kRouteThreads) {
+            const int t = i / top, e = from[i];
+            const int r = base[e] + __popcll(mask[e] & ((1ull << t) - 1));
+            rows[r] = t0 + t;
+            slots[(int64_t)t0 * top + i] = r;
+        }
+        if (t0 + kChunk < end) {
+            __syncthreads();
+            for (int e = tid; e < experts; e += kRouteThreads) {
+                base[e] += __popcll(mask[e]);
+                mask[e] = 0;
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -495,18 +514,18 @@ template <typename T, typename F> static cudaError_t for_experts(const void *log
 struct RouteCall {
     const void *logits;
     int64_t ls;
-    int n, chunk, experts, top;
+    int n, experts, top;
     bool renorm;
     int32_t *ids;
     float *weights;
-    int32_t *offsets, *rows, *slots, *counts;
+    int32_t *offsets, *rows, *slots, *counts, *totals;
     cudaStream_t s;
 };
 template <typename T> struct LaunchTop {
     const RouteCall &c;
     template <int PER, int VEC> cudaError_t operator()() const {
-        return launch_after(route_top_kernel<T, PER, VEC>, dim3((c.n + c.chunk - 1) / c.chunk), dim3(kRouteThreads), 0, c.s,
-                            (const T *)c.logits, c.ls, c.n, c.chunk, c.experts, c.top, c.renorm, c.ids, c.weights, c.counts);
+        return launch_after(route_top_kernel<T, PER, VEC>, dim3(runs_of(c.n)), dim3(kRouteThreads), 0, c.s,
+                            (const T *)c.logits, c.ls, c.n, run_of(c.n), c.experts, c.top, c.renorm, c.ids, c.weights, c.counts);
     }
 };
 template <typename T> struct LaunchCluster {
@@ -518,16 +537,16 @@ template <typename T> struct LaunchCluster {
                                     c.rows, c.slots);
     }
 };
-template <typename T> static cudaError_t launch_route(const RouteCall &c, int32_t *totals) {
+template <typename T> static cudaError_t launch_route(const RouteCall &c) {
     if (c.n <= kClusterTokens) return for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchCluster<T>{c});
-    const int chunks = (c.n + c.chunk - 1) / c.chunk;
     cudaError_t e = for_experts<T>(c.logits, c.ls, c.n, c.experts, LaunchTop<T>{c});
     if (e == cudaSuccess)
         e = launch_after(route_scan_kernel, dim3((c.experts + kScanExperts - 1) / kScanExperts), dim3(1024), 0, c.s,
-                         c.counts, chunks, c.experts, totals);
+                         c.counts, runs_of(c.n), c.experts, c.totals);
     if (e == cudaSuccess)
-        e = launch_after(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, c.s, (const int32_t *)c.ids,
-                         (const int32_t *)c.counts, (const int32_t *)totals, c.n, c.chunk, c.experts, c.top, c.offsets, c.rows, c.slots);
+        e = launch_after(route_place_kernel, dim3(runs_of(c.n)), dim3(kRouteThreads), 0, c.s, (const int32_t *)c.ids,
+                         (const int32_t *)c.counts, (const int32_t *)c.totals, c.n, run_of(c.n), c.experts, c.top,
+                         c.offsets, c.rows, c.slots);
     return e;
 }
 
@@ -595,7 +614,7 @@ using namespace gdn;
 
 extern "C" size_t gdn_moe_route_workspace_size(int64_t n_tokens, int32_t n_experts) {
     if (n_tokens <= kClusterTokens || n_experts <= 0) return 0;
-    return (size_t)((n_tokens + chunk_of(n_tokens) - 1) / chunk_of(n_tokens) + 1) * n_experts * sizeof(int32_t);
+    return (size_t)(runs_of(n_tokens) + 1) * n_experts * sizeof(int32_t);
 }
 
 extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_stride, int64_t n_tokens, int32_t n_experts,
@@ -604,16 +623,13 @@ extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_strid
                                     size_t workspace_bytes, void *stream) {
     GDN_REQUIRE(dtype == GDN_F32 || dtype == GDN_BF16, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(n_tokens >= 0 && n_experts > 0 && top_k > 0 && top_k <= n_experts, GDN_ERR_INVALID_ARG);
-    GDN_REQUIRE(n_experts <= kMaxExperts && top_k <= kMaxTop && n_tokens * top_k < (1ll << 31) - (1 << 20),
+    GDN_REQUIRE(n_experts <= kMaxExperts && top_k <= kMaxTop && n_tokens < (1ll << 31) &&
+                    n_tokens * top_k < (1ll << 31) - (1 << 20),
                 GDN_ERR_UNSUPPORTED);
     GDN_REQUIRE(offsets && (uintptr_t)offsets % 4 == 0, GDN_ERR_INVALID_ARG);
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    if (n_tokens == 0) {
-        e = launch_after(route_place_kernel, dim3(1), dim3(kRouteThreads), 0, s, (const int32_t *)nullptr,
-                         (const int32_t *)nullptr, (const int32_t *)nullptr, 0, kChunk, n_experts, top_k, offsets, rows, slots);
-    } else {
-        const bool space = n_tokens > kClusterTokens;
+    const bool space = n_tokens > kClusterTokens;
+    if (n_tokens > 0) {                                     // none: only the offsets
         GDN_REQUIRE(logits && ids && weights && rows && slots && (workspace || !space), GDN_ERR_INVALID_ARG);
         GDN_REQUIRE(n_tokens == 1 || logits_row_stride >= n_experts, GDN_ERR_INVALID_ARG);
         GDN_REQUIRE((uintptr_t)logits % (dtype == GDN_F32 ? 4 : 2) == 0 && (uintptr_t)ids % 4 == 0 &&
@@ -622,11 +638,11 @@ extern "C" gdn_status gdn_moe_route(const void *logits, int64_t logits_row_strid
         GDN_REQUIRE(!space || ((uintptr_t)workspace % 16 == 0 &&
                                workspace_bytes >= gdn_moe_route_workspace_size(n_tokens, n_experts)),
                     GDN_ERR_INVALID_ARG);
-        int32_t *totals = (int32_t *)workspace;
-        const RouteCall c = {logits, logits_row_stride, (int)n_tokens, chunk_of(n_tokens), n_experts, top_k, renormalize != 0, ids, weights,
-                             offsets, rows, slots, space ? totals + n_experts : nullptr, s};
-        e = dtype == GDN_F32 ? launch_route<float>(c, totals) : launch_route<__nv_bfloat16>(c, totals);
     }
+    int32_t *counts = (int32_t *)workspace, *totals = space ? counts + (int64_t)runs_of(n_tokens) * n_experts : nullptr;
+    const RouteCall c = {logits, logits_row_stride, (int)n_tokens, n_experts, top_k, renormalize != 0, ids, weights,
+                         offsets, rows, slots, counts, totals, s};
+    const cudaError_t e = dtype == GDN_F32 ? launch_route<float>(c) : launch_route<__nv_bfloat16>(c);
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return GDN_ERR_LAUNCH;
@@ -640,7 +656,8 @@ extern "C" gdn_status gdn_moe_combine(const void *x, int64_t x_row_stride, int64
                                       int32_t dtype, void *stream) {
     GDN_REQUIRE(dtype == GDN_F32 || dtype == GDN_BF16, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(n_tokens >= 0 && n_rows >= 0 && top_k > 0 && hidden > 0, GDN_ERR_INVALID_ARG);
-    GDN_REQUIRE(n_rows < (1ll << 31) && n_tokens * top_k < (1ll << 31) && top_k <= kMaxExperts, GDN_ERR_UNSUPPORTED);
+    GDN_REQUIRE(n_rows < (1ll << 31) && n_tokens < (1ll << 31) && n_tokens * top_k < (1ll << 31) && top_k <= kMaxExperts,
+                GDN_ERR_UNSUPPORTED);
     if (n_tokens == 0) return GDN_OK;
     GDN_REQUIRE(slots && weights && y && (x || n_rows == 0) && y != x, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE((n_rows <= 1 || x_row_stride >= hidden) && (n_tokens == 1 || y_row_stride >= hidden) &&
