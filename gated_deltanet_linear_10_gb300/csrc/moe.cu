@@ -34,7 +34,10 @@ static int run_of(int64_t n) {
     return (int)std::max<int64_t>(kRouteThreads / 32, (n + kWave - 1) / kWave);
 }
 static int runs_of(int64_t n) { return (int)((n + run_of(n) - 1) / run_of(n)); }
-constexpr int kClusterTokens = 512;        // the most of the single launch: eight chunks
+// The most of the single launch, eight chunks.  512 tokens of 512 experts in fp32 take
+// 11.5 us so and 7.9 in three launches, 256 tokens 7.8 and 7.7; but three launches and a
+// workspace are 5 us more on the host, which is what a call outside a graph waits for.
+constexpr int kClusterTokens = 512;
 
 // Larger logits have larger keys; -0 equals 0 (by the addition, which also makes every
 // NaN the same, above everything).  0 is no logit's key.
@@ -194,7 +197,8 @@ __device__ __forceinline__ void route_token(const RawLogits<T, PER, VEC> &raw, i
     auto index = [&](int i) { return raw.index(i, lane); };
     // (no lane's, where fewer lanes than choices have an expert: all experts)
     const uint32_t bound = max(bound_of<T>(most, top, lane, space), C::kLeast);
-    const float top1 = C::value(__reduce_max_sync(0xffffffffu, most));
+    const uint32_t most_of_all = __reduce_max_sync(0xffffffffu, most);
+    const float top1 = C::value(most_of_all);
     float all = 0.f;
     if (!renorm) {
 #pragma unroll
@@ -203,23 +207,46 @@ __device__ __forceinline__ void route_token(const RawLogits<T, PER, VEC> &raw, i
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
     }
-    int cnt = 0;
+    auto count = [&](uint32_t from) {
+        int n = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) cnt += kept[i] >= bound;
-    int scan = cnt;
+        for (int i = 0; i < PER; ++i) n += kept[i] >= from;
+        return n;
+    };
+    auto sum_before = [&](int n) {             // with a lane's own
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, scan, off);
-        if (lane >= off) scan += o;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, n, off);
+            if (lane >= off) n += o;
+        }
+        return n;
+    };
+    uint32_t from = bound;
+    int cnt = count(from), scan = sum_before(cnt), total = __shfl_sync(0xffffffffu, scan, 31);
+    if (total > kCands) {
+        // too many (most of the lanes' largest were needed): between the bound and the largest
+        // (100000 x 1024 top 32: 1657 us one after the other, 238 so)
+        uint32_t past = most_of_all;
+        while (total > kCands && past - from > 1) {
+            const uint32_t mid = from + (past - from) / 2;
+            const int c = count(mid), n = __reduce_add_sync(0xffffffffu, c);
+            if (n >= top) {
+                from = mid;
+                cnt = c;
+                total = n;
+            } else {
+                past = mid;
+            }
+        }
+        scan = sum_before(cnt);
     }
-    const int total = __shfl_sync(0xffffffffu, scan, 31);
     Word *cands = reinterpret_cast<Word *>(space);
     __syncwarp();                              // the lanes' largest are read
     if (total <= kCands) {
         Word *to = cands + scan - cnt;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (kept[i] >= bound) *to++ = C::word(kept[i], index(i));
+            if (kept[i] >= from) *to++ = C::word(kept[i], index(i));
     } else {                                   // many alike: the largest, one after the other
         for (int j = 0; j < top; ++j) {
             Word best = 0;

@@ -39,6 +39,12 @@ def test_tokens(T, E, top):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E,top", [(38912, 24, 3), (38913, 24, 3), (70000, 16, 2), (160001, 9, 1), (40000, 1024, 30)])
+def test_runs_of_more_than_a_word_of_tokens(T, E, top, dtype):
+    _check(_logits(T, T, E, dtype), top)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("E", [1, 2, 3, 8, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 300, 511, 512, 513,
                                777, 1000, 1023, 1024])
 def test_experts(E, dtype):
