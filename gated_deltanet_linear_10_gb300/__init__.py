@@ -1007,9 +1007,7 @@ def gdn_block_quant(x, glu=False, y=None, y_scale=None):
     T, n = shape[0], shape[1] // 2 if glu else shape[1]
     if y is None:
         ys = (n + 15) // 16 * 16
-        y = torch.empty((T, ys), dtype=_E4M3, device=x.device)
-        if n % 16:
-            y = y[:, :n]
+        y = torch.empty_strided((T, n), (ys, 1), dtype=_E4M3, device=x.device)
     elif y.dtype != _E4M3:
         raise GdnError("y: float8_e4m3fn")
     else:
