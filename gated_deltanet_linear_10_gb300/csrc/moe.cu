@@ -578,7 +578,8 @@ template <typename T> static cudaError_t launch_route(const RouteCall &c) {
 }
 
 // y = residual + the weighted rows of a token, one thread a vector of N channels, kAhead
-// rows asked for before the first is added.  `split`: CTAs of a token, or 0 where a CTA
+// rows asked for before the first is added.  Bound by the memory: 20668 x 10 rows of 2048
+// bf16 take 163 us, 0.92 of a copy's rate; 256 x 10 take 3.3, a launch and two trips.  `split`: CTAs of a token, or 0 where a CTA
 // has `per` whole tokens.
 constexpr int kAhead = 5, kCombineThreads = 256;
 template <typename T, int N>
