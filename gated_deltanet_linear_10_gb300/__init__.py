@@ -955,6 +955,8 @@ def gdn_moe_route(logits, top_k, renormalize=True, ids=None, weights=None, offse
     if dtype != _BF16 and dtype != _F32:
         raise GdnError(f"unsupported logits dtype {dtype} (fp32 or bf16)")
     T, E = shape
+    if not 0 < top_k <= E:
+        raise GdnError("top_k: 1 to E")
     empty, lp, ls = torch.empty, logits.data_ptr(), _rows(logits, shape, "logits")
     # outputs made here need no check
     if ids is None:

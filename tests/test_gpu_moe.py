@@ -245,3 +245,9 @@ def test_combine_far_rows():
     near = gdn().gdn_moe_combine(x[-9:].contiguous(), slots - (R - 9), w)
     torch.cuda.synchronize()
     assert bits_equal(y, near)
+
+
+@pytest.mark.parametrize("top", [-1, 0, 9])
+def test_route_refuses_a_number_of_choices(top):
+    with pytest.raises(gdn().GdnError):
+        gdn().gdn_moe_route(torch.zeros(4, 8, device=DEV), top)
