@@ -3,8 +3,10 @@
 // that a tile of few rows costs little more than reading its weights.
 //
 // Persistent CTAs, a warp for each part: loads (tiles by TMA; gathered rows in pieces
-// of 16 bytes, by a warp: a TMA gather of four rows takes 150 cycles and held one
-// token's block at 620), products, scales, and 4 to 16 that sum the blocks.  With block scales
+// of 16 bytes, by a warp or, of 64 and more a tile, five: a TMA gather of four rows takes
+// 150 cycles and held one token's block at 620, one warp 64 rows of a block at 900 and
+// 1237 x 4 rows of 60 experts 1003 x 777 bf16 at 28.5 us), products, scales, and 4 to 16
+// that sum the blocks.  With block scales
 // every block of 128 in k is a product of its own into one of four accumulators;
 // the summing warps add it, times sx sw of its column, to registers.  A block takes
 // such a warp some 500 cycles of waits and latencies, so groups of four share the columns
@@ -30,26 +32,27 @@ cudaError_t set_grouped_narrow_limit(uint64_t limit_ns, cudaStream_t s) {
 namespace {
 
 constexpr int kScaleChunk = 8;         // blocks whose scales are handed over at a time
-// Warps: 0 loads by TMA, 1 products, 2 scales, 3 on sums, the last one gathered rows: a
-// multiple of four, by which registers are shared out.
-constexpr int kGnScale = 2, kGnFirstSum = 3, kGnGather = 1;
+// Warps: 0 loads by TMA, 1 products, 2 scales, 3 on sums, then gathered rows: a multiple
+// of four, by which registers are shared out.
+constexpr int kGnScale = 2, kGnFirstSum = 3;
 
-template <int BT> struct GnCfg {
+template <int BT, bool kBlock> struct GnCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
     static constexpr int kStages = BT == 16 ? 11 : BT == 32 ? 10 : BT == 64 ? 8 : 6;
     static constexpr int kAccs = 4;
-    static constexpr int kSums = BT == 128 ? 16 : BT == 64 ? 8 : 4;   // summing warps, groups of four share the columns
+    static constexpr int kSums = BT == 128 ? (kBlock ? 16 : 8) : BT == 64 ? 8 : 4;   // summing warps, groups of four share the columns
+    static constexpr int kGather = BT == 64 || (BT == 128 && !kBlock) ? 5 : 1;       // warps for gathered rows
     static constexpr int kWidth = BT * 4 / kSums;         // columns of one
-    static constexpr int kThreads = 32 * (kGnFirstSum + kSums + kGnGather);
+    static constexpr int kThreads = 32 * (kGnFirstSum + kSums + kGather);
     static constexpr uint32_t kScales = 2 * kScaleChunk * BT * 4;
     static constexpr uint32_t kSmem = kStages * kStage + kScales;
 };
 
 template <int BT, bool kBlock>
-__global__ void __launch_bounds__(GnCfg<BT>::kThreads)
+__global__ void __launch_bounds__(GnCfg<BT, kBlock>::kThreads)
 grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                       const __grid_constant__ GroupedCall c, int keep) {
-    using C = GnCfg<BT>;
+    using C = GnCfg<BT, kBlock>;
     constexpr int S = C::kStages, A = C::kAccs;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GroupTable table;
@@ -67,7 +70,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         prefetch_tensormap(&mx);
         prefetch_tensormap(&mw);
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], c.rows ? 1 + 32 * kGnGather : 1);
+            mbar_init(&full[i], c.rows ? 1 + 32 * C::kGather : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < A; ++i) {
@@ -173,11 +176,12 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         }
         __syncwarp();
     } else if (warp >= kGnFirstSum + C::kSums) {
-        // A lane copies 16 bytes of a row, the warp four whole rows at a time.  Where there is no row the stage keeps what it holds: a column that is not
-        // written, or written as zeros.
+        // A lane copies 16 bytes of a row, a warp four whole rows at a time and, of more warps,
+        // every so-manieth four.  Where there is no row the stage keeps what it holds: a column
+        // that is not written, or written as zeros.
         if (c.rows) {
-            constexpr int N = BT / 4;
-            const int sub = lane >> 3;                                      // of four rows
+            constexpr int G = C::kGather, N = (BT / 4 + G - 1) / G;
+            const int first = warp - kGnFirstSum - C::kSums, sub = lane >> 3;   // of all fours; row of it
             const uint32_t to = smem_u32(smem) + C::kW + sub * 128;
             // the 16 bytes' place in the swizzled rows of even fours, and of odd ones
             const uint32_t even = ((lane & 7) ^ sub) << 4, odd = ((lane & 7) ^ (sub + 4)) << 4;
@@ -191,7 +195,10 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
                 int row[N];
 #pragma unroll
-                for (int j = 0; j < N; ++j) row[j] = group_x_row(c, a.r0 + sub + j * 4, a.r1);
+                for (int j = 0; j < N; ++j) {
+                    const int four = first + j * G;
+                    row[j] = four < BT / 4 ? group_x_row(c, a.r0 + four * 4 + sub, a.r1) : c.n_x;
+                }
                 const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + (lane & 7) * 16;
 #pragma unroll 1
                 for (int k = 0; k < nk; ++k, ++i, src += 128) {
@@ -200,11 +207,11 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                         break;
                     }
                     if (i < keep) {
-                        const uint32_t st = to + s * C::kStage;
+                        const uint32_t st = to + s * C::kStage + first * 512;
                         if (k < whole) {
 #pragma unroll
                             for (int j = 0; j < N; ++j)
-                                copy16_if(row[j] < c.n_x, st + j * 512 + (j & 1 ? odd : even), src + row[j] * stride);
+                                copy16_if(row[j] < c.n_x, st + j * G * 512 + ((first + j * G) & 1 ? odd : even), src + row[j] * stride);
                         } else {
                             const int n = min(16, max(0, bytes - k * 128));
 #pragma unroll 1
@@ -212,7 +219,8 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                                 int at = row[0];
 #pragma unroll
                                 for (int z = 1; z < N; ++z) at = z == j ? row[z] : at;      // no array in memory
-                                if (at < c.n_x) copy16(st + j * 512 + (j & 1 ? odd : even), n > 0 ? src + at * stride : c.x, n);
+                                if (at < c.n_x)
+                                    copy16(st + j * G * 512 + ((first + j * G) & 1 ? odd : even), n > 0 ? src + at * stride : c.x, n);
                             }
                         }
                         copies_arrive(&full[s]);
@@ -356,7 +364,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
 }
 
 template <int BT, bool kBlock> gdn_status launch(const GroupedCall &c, int drop, cudaStream_t s) {
-    using C = GnCfg<BT>;
+    using C = GnCfg<BT, kBlock>;
     CUtensorMap mx, mw;
     if (!encode_tmap_rows(&mx, c, BT) || !encode_tmap_experts(&mw, c, 128)) return GDN_ERR_CUDA;
     auto kernel = grouped_narrow_kernel<BT, kBlock>;
