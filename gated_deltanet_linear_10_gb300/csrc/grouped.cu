@@ -21,25 +21,27 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
 }
 
 // The choice of a tile: the shortest by an estimate of waves of tiles, each of as many
-// blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, a block) are
-// fitted to 1 to 4096 rows on products of 512 x 4096 to 4096 x 2048 and to 4 to 800 rows
-// for each of 8, 60 and 256 experts, rows in place and gathered.  Of an expert's rows the
-// host knows the mean: tiles of r rows take mean / r + 1/2 of them, at least one.  Over 126
-// gathered sizes its choice takes 1 % longer than the best tile's (the worst 28 %); 256 experts
-// of 82 rows, 1000 x 700 e4m3, take 192, 155, 81, 190 and 104 us in the five.
+// blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, what rows of y
+// off 16 bytes add to that, a block) are fitted to 574 products: 1 to 4096 rows of 512 x
+// 4096 to 4096 x 2048, and 12 to 400 rows for each of 8, 60 and 256 experts, in place and
+// gathered.  There the choice takes 1 % longer than the best tile, 20 % at worst.  Of an
+// expert's rows the host knows the mean: tiles of r rows take mean / r + 1/2 of them, at
+// least one.  (256 experts of 82 rows gathered, 1000 x 700 e4m3, in the five tiles: 193,
+// 154, 81, 84 and 105 us; 256 x 2048 x 8192 in those of 64, 128 and 256: 15.7, 10.5, 13.6.)
 static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     const int64_t ye = c.out_f32 ? 4 : 2;
     c.vec16 = (uintptr_t)c.y % 16 == 0 && c.n_out * ye % 16 == 0 && (c.n_rows == 1 || c.ys * ye % 16 == 0);
     c.vec4 = (uintptr_t)c.y % 4 == 0 && (c.n_rows == 1 || c.ys * ye % 4 == 0);
     c.sx16 = (uintptr_t)c.sx % 16 == 0 && c.kb % 4 == 0;
     struct Tile {
-        int rows, channels, ends, tile, block[2][2];   // block: bf16, e4m3; rows in place, gathered
+        int rows, channels, ends, tile, odd[2], block[2][2];   // odd, block: bf16, e4m3; block: rows in place, gathered
     };
-    constexpr Tile kTiles[] = {{16, 128, 280, 70, {{26, 30}, {27, 27}}},
-                               {32, 128, 250, 80, {{26, 34}, {29, 34}}},
-                               {64, 128, 230, 90, {{28, 32}, {33, 32}}},
-                               {128, 128, 380, 120, {{30, 38}, {44, 78}}},
-                               {256, 256, 450, 90, {{40, 42}, {50, 53}}}};
+    constexpr Tile kTiles[] = {{16, 128, 240, 70, {0, 0}, {{27, 34}, {28, 30}}},
+                               {32, 128, 270, 80, {0, 0}, {{25, 34}, {32, 45}}},
+                               {64, 128, 270, 80, {0, 0}, {{28, 32}, {34, 34}}},
+                               {128, 128, 300, 110, {10, 10}, {{33, 38}, {33, 38}}},
+                               // (pairs write such rows slowly, and with block scales sum nothing meanwhile)
+                               {256, 256, 450, 90, {250, 190}, {{37, 36}, {50, 59}}}};
     const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
     const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;
     int best = 0;
@@ -49,10 +51,8 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
                                          : 2 * (((int64_t)c.n_rows + t.rows - 1) / t.rows);
         const int64_t tiles = (halves + 1) / 2 * ((c.n_out + t.channels - 1) / t.channels);
         const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms;
-        // the summing warps of pairs write rows off 16 bytes themselves, and sum nothing meanwhile
-        // (161 experts of 102 rows, 1408 x 4894 e4m3: 431 us, of 4896 channels 317)
-        const int odd = t.rows == 256 && !c.vec16 && c.e4m3 ? 250 : 0;
-        const int64_t cost = t.ends + (tiles + slots - 1) / slots * (t.tile + odd + blocks * t.block[c.e4m3][c.rows != nullptr]);
+        const int64_t tile = t.tile + (c.vec16 ? 0 : t.odd[c.e4m3]) + blocks * t.block[c.e4m3][c.rows != nullptr];
+        const int64_t cost = t.ends + (tiles + slots - 1) / slots * tile;
         // (tiles beyond 31 bits are not launched)
         if (cost < least && tiles < (1ll << 30)) {
             least = cost;

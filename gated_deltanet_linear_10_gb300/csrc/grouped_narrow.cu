@@ -1,17 +1,18 @@
 // Grouped and block-scaled products, few rows an expert: an expert's 128 weight
 // rows are the lanes of the accumulator and up to BT of its tokens the columns, so
-// that a tile of few rows costs little more than reading its weights.
+// that a tile of few rows costs little more than reading its weights.  Of 128 rows a
+// tile they change places (kTurned): a lane has one token, so that its factor sx sw is
+// one number a block, not one for each column out of shared memory, and its part of a
+// row of y is written in pieces of 16 bytes (256 x 2048 x 8192: 12.1 -> 10.5 us).
 //
 // Persistent CTAs, a warp for each part: loads (tiles by TMA; gathered rows in pieces
 // of 16 bytes, by a warp or, of 64 and more a tile, five: a TMA gather of four rows takes
-// 150 cycles and held one token's block at 620, one warp 64 rows of a block at 900 and
-// 1237 x 4 rows of 60 experts 1003 x 777 bf16 at 28.5 us), products, scales, and 4 to 16
-// that sum the blocks.  With block scales
-// every block of 128 in k is a product of its own into one of four accumulators;
-// the summing warps add it, times sx sw of its column, to registers.  A block takes
-// such a warp some 500 cycles of waits and latencies, so groups of four share the columns
-// of a tile of 64 or 128 rows, 32 columns each (256 x 2048 x 8192 in tiles of 128: with
-// one group 15.9 us, with two 13.2, with four 12.1).
+// 150 cycles and held one token's block at 620, one warp 64 rows of a block at 900),
+// products, scales, and 4 or 8 that sum the blocks.  With block scales every block of 128
+// in k is a product of its own into one of four accumulators; the summing warps add it,
+// times sx sw, to registers.  A block takes such a warp some 500 cycles of waits and
+// latencies, so two groups of four share the columns of a tile of 64 or 128 rows.  (With
+// four groups, 16 warps, 256 x 2048 x 8192 takes 11.0 us.)
 #include <limits.h>
 
 #include <algorithm>
@@ -36,24 +37,75 @@ constexpr int kScaleChunk = 8;         // blocks whose scales are handed over at
 // of four, by which registers are shared out.
 constexpr int kGnScale = 2, kGnFirstSum = 3;
 
-template <int BT, bool kBlock> struct GnCfg {
+template <int BT> struct GnCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
     static constexpr int kStages = BT == 16 ? 11 : BT == 32 ? 10 : BT == 64 ? 8 : 6;
     static constexpr int kAccs = 4;
-    static constexpr int kSums = BT == 128 ? (kBlock ? 16 : 8) : BT == 64 ? 8 : 4;   // summing warps, groups of four share the columns
-    static constexpr int kGather = BT == 64 || (BT == 128 && !kBlock) ? 5 : 1;       // warps for gathered rows
+    static constexpr int kSums = BT >= 64 ? 8 : 4;        // summing warps, groups of four share the columns
+    static constexpr int kGather = BT >= 64 ? 5 : 1;      // warps for gathered rows
     static constexpr int kWidth = BT * 4 / kSums;         // columns of one
     static constexpr int kThreads = 32 * (kGnFirstSum + kSums + kGather);
+    // of 128 rows a tile, the rows are the accumulator's lanes
+    static constexpr bool kTurned = BT == 128;
     static constexpr uint32_t kScales = 2 * kScaleChunk * BT * 4;
-    static constexpr uint32_t kSmem = kStages * kStage + kScales;
+    static constexpr uint32_t kStaging = kTurned ? 1024 : 0;      // of a summing warp: 32 bytes of 32 rows
+    static constexpr uint32_t kSmem = kStages * kStage + kScales + kSums * kStaging;
 };
 
-template <int BT, bool kBlock>
-__global__ void __launch_bounds__(GnCfg<BT, kBlock>::kThreads)
+// A warp's 32 rows from row0 on, a lane each, and W channels from n0 on.  Rows of whole
+// 16 bytes (kPieces) are written by their lanes, others by way of 32 bytes of each in shared
+// memory.
+template <bool kPieces, typename O, int W>
+__device__ __forceinline__ void store_lanes(const F2 (&acc)[W / 2], uint8_t *staging, const GroupedCall &c, int row0, int r1,
+                                            int n0, bool there, int lane) {
+    constexpr int V = 16 / sizeof(O);                  // channels of 16 bytes
+    O *y = reinterpret_cast<O *>(c.y) + (int64_t)row0 * c.ys + n0;
+    const int rows = r1 - row0, left = c.n_out - n0;
+#pragma unroll
+    for (int i = 0; i < W; i += 2 * V) {
+        if (i >= left) break;
+        uint4 v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const F2 *p = acc + (i + j * V) / 2;
+            if constexpr (sizeof(O) == 2) {
+                const float2 a = f2_get(p[0]), b = f2_get(p[1]), d = f2_get(p[2]), e = f2_get(p[3]);
+                v[j] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(d.x, d.y), pack_bf16(e.x, e.y));
+            } else {
+                const float2 a = f2_get(p[0]), b = f2_get(p[1]);
+                v[j] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+            }
+            if (!there) v[j] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (kPieces) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (lane < rows && i + j * V < left) *reinterpret_cast<uint4 *>(y + lane * c.ys + i + j * V) = v[j];
+            continue;
+        }
+        __syncwarp();                                  // the last 32 bytes of each row are read
+#pragma unroll
+        for (int j = 0; j < 2; ++j) reinterpret_cast<uint4 *>(staging)[lane * 2 + j] = v[j];
+        __syncwarp();
+        const int ch = lane % (2 * V), first = lane / (2 * V);
+        O e[2 * V];                                    // all read before the first is written
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) e[j] = reinterpret_cast<const O *>(staging)[j * 32 + lane];
+        O *to = y + first * c.ys + i + ch;
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j)
+            if (j * (16 / V) + first < rows && i + ch < left) to[j * (16 / V) * c.ys] = e[j];
+    }
+    __syncwarp();
+}
+
+template <int BT, bool kBlock, bool kPieces>
+__global__ void __launch_bounds__(GnCfg<BT>::kThreads)
 grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                       const __grid_constant__ GroupedCall c, int keep) {
-    using C = GnCfg<BT, kBlock>;
+    using C = GnCfg<BT>;
     constexpr int S = C::kStages, A = C::kAccs;
+    constexpr bool kTurned = C::kTurned;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GroupTable table;
     __shared__ uint64_t full[S], empty[S], acc_full[A], acc_empty[A], sc_full[2], sc_empty[2], drained;
@@ -151,7 +203,8 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 const bool last = kBlock || k == nk - 1;
                 if (elect_lane()) {
                     const uint32_t st = base + s * (C::kStage >> 4), d = sums + u % A * BT;
-                    const uint64_t da = desc | st, db = desc | (st + (C::kW >> 4));
+                    const uint32_t xt = st + (C::kW >> 4);
+                    const uint64_t da = desc | (kTurned ? xt : st), db = desc | (kTurned ? st : xt);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         linear_mma<kBlock>(d, da + 2 * q, db + 2 * q, idesc, q > 0 || (!kBlock && k > 0));
@@ -253,12 +306,23 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             for (int k0 = 0; k0 < (kBlock ? nk : 1) && ok; k0 += kScaleChunk, ++v, slot ^= 1) {
                 float f[Q][kScaleChunk];
                 if (kBlock) {
+                    const bool pieces = k0 + kScaleChunk <= nk && c.sx16;
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const float *sx = c.sx + (int64_t)row[q] * c.kb + k0;
+                        if (pieces && row[q] < c.n_x) {
+                            *reinterpret_cast<float4 *>(f[q]) = *reinterpret_cast<const float4 *>(sx);
+                            *reinterpret_cast<float4 *>(f[q] + 4) = *reinterpret_cast<const float4 *>(sx + 4);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kScaleChunk; ++i) f[q][i] = k0 + i < nk && row[q] < c.n_x ? sx[i] : 0.f;
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < kScaleChunk; ++i) {
                         const float w = k0 + i < nk ? sw[k0 + i] : 0.f;
 #pragma unroll
-                        for (int q = 0; q < Q; ++q)
-                            f[q][i] = k0 + i < nk && row[q] < c.n_x ? w * c.sx[(int64_t)row[q] * c.kb + k0 + i] : 0.f;
+                        for (int q = 0; q < Q; ++q) f[q][i] *= w;
                     }
                 }
                 if (v >= 2 && !mbar_wait_all(&sc_empty[slot], (v / 2 - 1) & 1, abort)) {
@@ -282,7 +346,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         }
         if (wrong) flag_status(GDN_DEVSTAT_BAD_INDEX);
     } else if (warp >= kGnFirstSum) {
-        // Accumulator lane 32 q + l is channel 32 q + l of the tile.
+        // Accumulator lane 32 q + l is channel 32 q + l of the tile, turned row 32 q + l.
         constexpr int W = C::kWidth, L = W < 32 ? 16 : 32;       // columns, and of a load
         const int q = warp & 3, c0 = ((warp - kGnFirstSum) >> 2) * W;
         int u = 0, v = 0;                  // accumulators and chunks used so far
@@ -293,7 +357,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             F2 acc[W / 2];
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) acc[i] = f2(0.f, 0.f);
-            uint32_t there[(W + 31) / 32];
+            uint32_t there[kTurned ? 1 : (W + 31) / 32];
 #pragma unroll 1
             for (int k0 = 0; k0 < blocks && ok; k0 += kScaleChunk, ++v) {
                 const int slot = v & 1, n = min(blocks - k0, kScaleChunk);
@@ -302,8 +366,8 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < (W + 31) / 32; ++i) there[i] = valid[slot][c0 / 32 + i];
-                const float *sc = scales + slot * kScaleChunk * BT + c0;
+                for (int i = 0; i < (kTurned ? 1 : (W + 31) / 32); ++i) there[i] = valid[slot][kTurned ? q : c0 / 32 + i];
+                const float *sc = scales + slot * kScaleChunk * BT + (kTurned ? q * 32 + lane : c0);
 #pragma unroll 1
                 for (int k = 0; k < n; ++k, sc += BT) {
                     if (!ready && !mbar_wait_all(&acc_full[u % A], (u / A) & 1, abort)) {
@@ -311,6 +375,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                         break;
                     }
                     tc_fence_after();
+                    const float own = kTurned && kBlock ? *sc : 1.f;
                     const uint32_t from = tmem_addr(tmem_base, q * 32, u % A * BT + c0);
                     uint32_t r[W / L][L];
 #pragma unroll
@@ -326,7 +391,10 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     for (int i = 0; i < W; i += 4) {
                         const uint32_t *p = r[i / L] + i % L;
                         F2 &lo = acc[i / 2], &hi = acc[i / 2 + 1];
-                        if (kBlock) {
+                        if (kBlock && kTurned) {
+                            lo = f2_fma(f2_bits(p[0], p[1]), f2(own, own), lo);
+                            hi = f2_fma(f2_bits(p[2], p[3]), f2(own, own), hi);
+                        } else if (kBlock) {
                             const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + i);
                             lo = f2_fma(f2_bits(p[0], p[1]), f.x, lo);
                             hi = f2_fma(f2_bits(p[2], p[3]), f.y, hi);
@@ -341,16 +409,23 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 if (lane == 0) mbar_arrive(&sc_empty[slot]);
             }
             if (!ok) break;
-            const int n = a.n * 128 + q * 32 + lane, cnt = min(W, a.r1 - a.r0 - c0);
-            if (n < c.n_out) {
-                const int64_t at = (int64_t)(a.r0 + c0) * c.ys + n;
+            if constexpr (kTurned) {
+                const bool is = there[0] >> lane & 1;
+                uint8_t *staging = smem + S * C::kStage + C::kScales + (warp - kGnFirstSum) * C::kStaging;
+                if (c.out_f32) store_lanes<kPieces, float, W>(acc, staging, c, a.r0 + q * 32, a.r1, a.n * 128 + c0, is, lane);
+                else store_lanes<kPieces, __nv_bfloat16, W>(acc, staging, c, a.r0 + q * 32, a.r1, a.n * 128 + c0, is, lane);
+            } else {
+                const int n = a.n * 128 + q * 32 + lane, cnt = min(W, a.r1 - a.r0 - c0);
+                if (n < c.n_out) {
+                    const int64_t at = (int64_t)(a.r0 + c0) * c.ys + n;
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const float2 f = f2_get(acc[i / 2]);
-                    const float val = there[i / 32] >> (i % 32) & 1 ? (i & 1 ? f.y : f.x) : 0.f;
-                    if (i < cnt) {
-                        if (c.out_f32) reinterpret_cast<float *>(c.y)[at + i * c.ys] = val;
-                        else reinterpret_cast<__nv_bfloat16 *>(c.y)[at + i * c.ys] = __float2bfloat16_rn(val);
+                    for (int i = 0; i < W; ++i) {
+                        const float2 f = f2_get(acc[i / 2]);
+                        const float val = there[i / 32] >> (i % 32) & 1 ? (i & 1 ? f.y : f.x) : 0.f;
+                        if (i < cnt) {
+                            if (c.out_f32) reinterpret_cast<float *>(c.y)[at + i * c.ys] = val;
+                            else reinterpret_cast<__nv_bfloat16 *>(c.y)[at + i * c.ys] = __float2bfloat16_rn(val);
+                        }
                     }
                 }
             }
@@ -363,11 +438,11 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
-template <int BT, bool kBlock> gdn_status launch(const GroupedCall &c, int drop, cudaStream_t s) {
-    using C = GnCfg<BT, kBlock>;
+template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(const GroupedCall &c, int drop, cudaStream_t s) {
+    using C = GnCfg<BT>;
     CUtensorMap mx, mw;
     if (!encode_tmap_rows(&mx, c, BT) || !encode_tmap_experts(&mw, c, 128)) return GDN_ERR_CUDA;
-    auto kernel = grouped_narrow_kernel<BT, kBlock>;
+    auto kernel = grouped_narrow_kernel<BT, kBlock, kPieces>;
     static SmemAllowed allowed;
     cudaError_t e = allowed.ask(kernel, C::kSmem);
     const int64_t nn = (c.n_out + 127) / 128;
@@ -390,7 +465,9 @@ gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int drop, 
         case 16: return c.e4m3 ? launch<16, true>(c, drop, s) : launch<16, false>(c, drop, s);
         case 32: return c.e4m3 ? launch<32, true>(c, drop, s) : launch<32, false>(c, drop, s);
         case 64: return c.e4m3 ? launch<64, true>(c, drop, s) : launch<64, false>(c, drop, s);
-        default: return c.e4m3 ? launch<128, true>(c, drop, s) : launch<128, false>(c, drop, s);
+        default:
+            if (!c.vec16) return c.e4m3 ? launch<128, true, false>(c, drop, s) : launch<128, false, false>(c, drop, s);
+            return c.e4m3 ? launch<128, true>(c, drop, s) : launch<128, false>(c, drop, s);
     }
 }
 
