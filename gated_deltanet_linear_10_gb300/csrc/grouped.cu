@@ -27,7 +27,7 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
 // gathered.  There the choice takes 1 % longer than the best tile, 20 % at worst.  Of an
 // expert's rows the host knows the mean: tiles of r rows take mean / r + 1/2 of them, at
 // least one.  (256 experts of 82 rows gathered, 1000 x 700 e4m3, in the five tiles: 193,
-// 154, 81, 84 and 105 us; 256 x 2048 x 8192 in those of 64, 128 and 256: 15.7, 10.5, 13.6.)
+// 154, 81, 84 and 105 us; 256 x 2048 x 8192 in those of 64, 128 and 256: 15.8, 9.8, 13.4.)
 static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     const int64_t ye = c.out_f32 ? 4 : 2;
     c.vec16 = (uintptr_t)c.y % 16 == 0 && c.n_out * ye % 16 == 0 && (c.n_rows == 1 || c.ys * ye % 16 == 0);
@@ -36,12 +36,12 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     struct Tile {
         int rows, channels, ends, tile, odd[2], block[2][2];   // odd, block: bf16, e4m3; block: rows in place, gathered
     };
-    constexpr Tile kTiles[] = {{16, 128, 240, 70, {0, 0}, {{27, 34}, {28, 30}}},
-                               {32, 128, 270, 80, {0, 0}, {{25, 34}, {32, 45}}},
-                               {64, 128, 270, 80, {0, 0}, {{28, 32}, {34, 34}}},
-                               {128, 128, 300, 110, {10, 10}, {{33, 38}, {33, 38}}},
+    constexpr Tile kTiles[] = {{16, 128, 240, 70, {0, 0}, {{27, 34}, {28, 33}}},
+                               {32, 128, 290, 80, {0, 0}, {{25, 34}, {31, 44}}},
+                               {64, 128, 270, 90, {0, 0}, {{29, 32}, {36, 36}}},
+                               {128, 128, 290, 90, {60, 60}, {{33, 37}, {31, 41}}},
                                // (pairs write such rows slowly, and with block scales sum nothing meanwhile)
-                               {256, 256, 450, 90, {250, 190}, {{37, 36}, {50, 59}}}};
+                               {256, 256, 450, 90, {180, 170}, {{35, 39}, {46, 61}}}};
     const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
     const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;
     int best = 0;

@@ -2,8 +2,8 @@
 // rows are the lanes of the accumulator and up to BT of its tokens the columns, so
 // that a tile of few rows costs little more than reading its weights.  Of 128 rows a
 // tile they change places (kTurned): a lane has one token, so that its factor sx sw is
-// one number a block, not one for each column out of shared memory, and its part of a
-// row of y is written in pieces of 16 bytes (256 x 2048 x 8192: 12.1 -> 10.5 us).
+// one number a block, not one for each column out of shared memory, and a row's part of
+// y is written in pieces of 16 bytes (256 x 2048 x 8192: 12.1 -> 9.8 us).
 //
 // Persistent CTAs, a warp for each part: loads (tiles by TMA; gathered rows in pieces
 // of 16 bytes, by a warp or, of 64 and more a tile, five: a TMA gather of four rows takes
@@ -12,7 +12,7 @@
 // in k is a product of its own into one of four accumulators; the summing warps add it,
 // times sx sw, to registers.  A block takes such a warp some 500 cycles of waits and
 // latencies, so two groups of four share the columns of a tile of 64 or 128 rows.  (With
-// four groups, 16 warps, 256 x 2048 x 8192 takes 11.0 us.)
+// four groups, 16 warps, that product took half a microsecond longer.)
 #include <limits.h>
 
 #include <algorithm>
@@ -48,53 +48,59 @@ template <int BT> struct GnCfg {
     // of 128 rows a tile, the rows are the accumulator's lanes
     static constexpr bool kTurned = BT == 128;
     static constexpr uint32_t kScales = 2 * kScaleChunk * BT * 4;
-    static constexpr uint32_t kStaging = kTurned ? 1024 : 0;      // of a summing warp: 32 bytes of 32 rows
+    static constexpr uint32_t kStaging = kTurned ? 2048 : 0;      // of a summing warp: 64 bytes of 32 rows
     static constexpr uint32_t kSmem = kStages * kStage + kScales + kSums * kStaging;
 };
 
-// A warp's 32 rows from row0 on, a lane each, and W channels from n0 on.  Rows of whole
-// 16 bytes (kPieces) are written by their lanes, others by way of 32 bytes of each in shared
-// memory.
+// A warp's 32 rows from row0 on, a lane each, and W channels from n0 on, by way of a few
+// bytes of each row in shared memory, so that a row's neighbours go out together: 64, in
+// pieces of 16 (kPieces), or 32, as elements.  (Each lane its own row, 16 bytes at a time,
+// writes half sectors: 18 experts of 3000 rows, 263 x 5392 e4m3, 373 us, so 255.)
 template <bool kPieces, typename O, int W>
 __device__ __forceinline__ void store_lanes(const F2 (&acc)[W / 2], uint8_t *staging, const GroupedCall &c, int row0, int r1,
                                             int n0, bool there, int lane) {
-    constexpr int V = 16 / sizeof(O);                  // channels of 16 bytes
+    constexpr int V = 16 / sizeof(O), P = kPieces ? 4 : 2, N = P * V;    // channels of 16 bytes, of a round
     O *y = reinterpret_cast<O *>(c.y) + (int64_t)row0 * c.ys + n0;
     const int rows = r1 - row0, left = c.n_out - n0;
 #pragma unroll
-    for (int i = 0; i < W; i += 2 * V) {
+    for (int i = 0; i < W; i += N) {
         if (i >= left) break;
-        uint4 v[2];
+        __syncwarp();                                  // the last round's are read
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < P; ++j) {
             const F2 *p = acc + (i + j * V) / 2;
+            uint4 v;
             if constexpr (sizeof(O) == 2) {
                 const float2 a = f2_get(p[0]), b = f2_get(p[1]), d = f2_get(p[2]), e = f2_get(p[3]);
-                v[j] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(d.x, d.y), pack_bf16(e.x, e.y));
+                v = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(d.x, d.y), pack_bf16(e.x, e.y));
             } else {
                 const float2 a = f2_get(p[0]), b = f2_get(p[1]);
-                v[j] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+                v = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
             }
-            if (!there) v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (!there) v = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4 *>(staging)[lane * P + (kPieces ? j ^ (lane >> 1 & 3) : j)] = v;
         }
-        if (kPieces) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (lane < rows && i + j * V < left) *reinterpret_cast<uint4 *>(y + lane * c.ys + i + j * V) = v[j];
-            continue;
-        }
-        __syncwarp();                                  // the last 32 bytes of each row are read
-#pragma unroll
-        for (int j = 0; j < 2; ++j) reinterpret_cast<uint4 *>(staging)[lane * 2 + j] = v[j];
         __syncwarp();
-        const int ch = lane % (2 * V), first = lane / (2 * V);
-        O e[2 * V];                                    // all read before the first is written
+        if (kPieces) {
+            const int first = lane >> 2, piece = lane & 3;                 // eight rows at a time
+            uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 2 * V; ++j) e[j] = reinterpret_cast<const O *>(staging)[j * 32 + lane];
-        O *to = y + first * c.ys + i + ch;
+            for (int j = 0; j < 4; ++j)
+                v[j] = reinterpret_cast<const uint4 *>(staging)[(j * 8 + first) * 4 + (piece ^ (first >> 1 & 3))];
 #pragma unroll
-        for (int j = 0; j < 2 * V; ++j)
-            if (j * (16 / V) + first < rows && i + ch < left) to[j * (16 / V) * c.ys] = e[j];
+            for (int j = 0; j < 4; ++j)
+                if (j * 8 + first < rows && i + piece * V < left)
+                    *reinterpret_cast<uint4 *>(y + (j * 8 + first) * c.ys + i + piece * V) = v[j];
+        } else {
+            const int first = lane / N, ch = lane % N;                     // 32 / N rows at a time
+            O e[N];                                    // all read before the first is written
+#pragma unroll
+            for (int j = 0; j < N; ++j) e[j] = reinterpret_cast<const O *>(staging)[j * 32 + lane];
+            O *to = y + first * c.ys + i + ch;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j * (32 / N) + first < rows && i + ch < left) to[j * (32 / N) * c.ys] = e[j];
+        }
     }
     __syncwarp();
 }

@@ -159,24 +159,38 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging
                         *reinterpret_cast<const uint4 *>(tile + r * 128 + ((piece ^ (r & 7)) << 4));
             }
         } else {
-            // words of 4 bytes, or elements; eight rows are read before the first is written
+            // words of 4 bytes, or elements where rows are not on them; eight of a lane are read
+            // before the first is written
             constexpr int E = 4 / sizeof(O);               // elements of a word
+            if (E == 1 || c.vec4) {
 #pragma unroll 1
-            for (int r = 0; r < min(32, rows); r += 8) {
-                uint32_t v[8];
+                for (int r = 0; r < min(32, rows); r += 8) {
+                    uint32_t v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = *reinterpret_cast<const uint32_t *>(tile + (r + j) * 128 + ((lane >> 2 ^ (j & 7)) << 4) + (lane & 3) * 4);
-                const int col = lane * E;
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = *reinterpret_cast<const uint32_t *>(tile + (r + j) * 128 + ((lane >> 2 ^ (j & 7)) << 4) + (lane & 3) * 4);
+                    const int col = lane * E;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (r + j >= rows || col >= left) continue;
-                    O *p = y + (r + j) * c.ys + n + col;
-                    if (E == 1 || (c.vec4 && col + 1 < left)) {
-                        *reinterpret_cast<uint32_t *>(p) = v[j];
-                    } else {
-                        reinterpret_cast<uint16_t *>(p)[0] = (uint16_t)v[j];
-                        if (col + 1 < left) reinterpret_cast<uint16_t *>(p)[1] = (uint16_t)(v[j] >> 16);
+                    for (int j = 0; j < 8; ++j) {
+                        if (r + j >= rows || col >= left) continue;
+                        O *p = y + (r + j) * c.ys + n + col;
+                        if (E == 1 || col + 1 < left) *reinterpret_cast<uint32_t *>(p) = v[j];
+                        else *reinterpret_cast<uint16_t *>(p) = (uint16_t)v[j];
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < min(32, rows); r += 4) {
+                    uint16_t v[8];                         // 32 neighbours of a row at a time
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = r + (j >> 1), piece = (j & 1) * 4 + (lane >> 3);
+                        v[j] = *reinterpret_cast<const uint16_t *>(tile + row * 128 + ((piece ^ (row & 7)) << 4) + (lane & 7) * 2);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = r + (j >> 1), col = (j & 1) * 32 + lane;
+                        if (row < rows && col < left) reinterpret_cast<uint16_t *>(y + row * c.ys + n)[col] = v[j];
                     }
                 }
             }
