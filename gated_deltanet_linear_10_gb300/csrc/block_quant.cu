@@ -14,17 +14,6 @@ namespace gdn {
 
 constexpr int kQuantBlock = 128;
 
-// Quotients by a number that the host knows, of dividends below 2^31.
-struct QuickDiv {
-    uint32_t mul, shift;
-    explicit QuickDiv(uint32_t d) {
-        shift = 0;
-        while ((1ull << shift) < d) ++shift;
-        mul = (uint32_t)(((1ull << (32 + shift)) + d - 1) / d - (1ull << 32));     // of 33 bits, the highest left out
-    }
-    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
-};
-
 // kVec: rows and blocks on vectors of 8 channels; else lane l holds channels l + 16 i.
 template <typename T, bool kGlu, bool kVec>
 __global__ void __launch_bounds__(256)

@@ -108,6 +108,17 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 }
 
 // Vector of N elements moved as 16 bytes: 8 bf16 or 4 fp32.
+// Quotients by a number that the host knows, of dividends below 2^31.
+struct QuickDiv {
+    uint32_t mul = 0, shift = 0;
+    QuickDiv() = default;
+    explicit QuickDiv(uint32_t d) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((1ull << (32 + shift)) + d - 1) / d - (1ull << 32));     // of 33 bits, the highest left out
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 template <typename T> struct Vec16;
 template <> struct Vec16<float> {
     static constexpr int N = 4;

@@ -9,6 +9,11 @@
 
 namespace gdn {
 
+void GroupedCall::channel_tiles(int64_t nn) {
+    by_channels = QuickDiv((uint32_t)nn);
+    by_raster = QuickDiv((uint32_t)nn * kGroupRaster);
+}
+
 // A single row (or expert) has no stride; a map wants one all the same.
 bool encode_tmap_experts(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows) {
     const int64_t elem = c.e4m3 ? 1 : 2, row = ((int64_t)c.n_in + 15) / 16 * 16;

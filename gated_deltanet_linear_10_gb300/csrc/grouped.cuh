@@ -10,6 +10,7 @@
 namespace gdn {
 
 constexpr int64_t kGroupedRows = 65535 * 256;
+constexpr int kGroupRaster = 8;
 constexpr int kGroupedOut = 1 << 20, kGroupedIn = 1 << 20, kGroupedExperts = 1024;
 
 struct GroupedCall {
@@ -24,6 +25,8 @@ struct GroupedCall {
     bool vec16;                      // rows of y on 16-byte boundaries, whole 16 bytes of them
     bool vec4;                       // rows of y on 4-byte boundaries
     bool sx16;                       // rows of sx on 16-byte boundaries
+    QuickDiv by_channels, by_raster; // by a row of channel tiles, by kGroupRaster of them
+    void channel_tiles(int64_t nn);  // sets these
 };
 
 // grouped_narrow.cu: a tile's weight rows on the accumulator's lanes, its tokens the
@@ -107,17 +110,22 @@ struct GroupTile {
 
 // By a whole warp.  Within an expert groups of kGroupRaster row tiles take the channel
 // tiles one after the other, row tiles fastest: the tiles in flight share weights and rows.
-constexpr int kGroupRaster = 8;
-__device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, int experts, int tile, int nn, int tile_rows) {
-    const int lane = threadIdx.x & 31, rt = tile / nn;
+// (Three quotients by division are most of 900 cycles, which the sums of a tile wait for.)
+__device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, const GroupedCall &c, int tile, int nn, int tile_rows) {
+    const int experts = c.n_experts, lane = threadIdx.x & 31, rt = c.by_channels(tile);
     const int hi = __popc(__ballot_sync(0xffffffffu, g.first[min(32 * (lane + 1), experts)] <= rt));
     const int e = 32 * hi + __popc(__ballot_sync(0xffffffffu, g.first[min(32 * hi + lane + 1, experts)] <= rt));
     GroupTile t;
     t.e = e;
     const int f = g.first[e], tiles = g.first[e + 1] - f, r = tile - f * nn;
-    const int base = r < kGroupRaster * nn ? 0 : r / (kGroupRaster * nn) * kGroupRaster, rr = r - base * nn;
+    const int base = r < kGroupRaster * nn ? 0 : c.by_raster(r) * kGroupRaster, rr = r - base * nn;
     const int rows = min(kGroupRaster, tiles - base);
-    t.n = rows == 1 ? rr : rr / rows;
+    // 2^32 / rows, rounded up: exact below 2^29
+    constexpr uint32_t kInverse[kGroupRaster + 1] = {0, 0, 1u << 31, 1431655766u, 1u << 30, 858993460u, 715827883u, 613566757u, 1u << 29};
+    t.n = rr;
+#pragma unroll
+    for (int i = 2; i <= kGroupRaster; ++i)
+        if (rows == i) t.n = __umulhi((uint32_t)rr, kInverse[i]);
     t.r0 = g.start[e] + (base + rr - t.n * rows) * tile_rows;
     t.r1 = g.start[e + 1];
     return t;

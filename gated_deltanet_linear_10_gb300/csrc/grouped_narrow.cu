@@ -161,7 +161,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         uint32_t phase = 1;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
+            const GroupTile a = find_group_tile(table, c, t, nn, BT);
             const uint32_t bytes = c.rows ? C::kW : C::kStage;
 #pragma unroll 1
             for (int k = 0; k < nk; ++k, ++i) {
@@ -251,7 +251,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             uint32_t phase = 1;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
+                const GroupTile a = find_group_tile(table, c, t, nn, BT);
                 int row[N];
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
@@ -297,7 +297,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         int slot = 0, v = 0;
         bool ok = true, wrong = false;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
+            const GroupTile a = find_group_tile(table, c, t, nn, BT);
             constexpr int Q = (BT + 31) / 32;
             int row[Q];
             uint32_t there[Q];
@@ -359,7 +359,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         bool ok = true, ready = false;     // the next accumulator is known to be there
         const int blocks = kBlock ? nk : 1;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const GroupTile a = find_group_tile(table, c.n_experts, t, nn, BT);
+            const GroupTile a = find_group_tile(table, c, t, nn, BT);
             F2 acc[W / 2];
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) acc[i] = f2(0.f, 0.f);
@@ -444,7 +444,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
-template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(const GroupedCall &c, int drop, cudaStream_t s) {
+template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(GroupedCall c, int drop, cudaStream_t s) {
     using C = GnCfg<BT>;
     CUtensorMap mx, mw;
     if (!encode_tmap_rows(&mx, c, BT) || !encode_tmap_experts(&mw, c, 128)) return GDN_ERR_CUDA;
@@ -454,6 +454,7 @@ template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(const Grou
     const int64_t nn = (c.n_out + 127) / 128;
     const int64_t tiles = (((int64_t)c.n_rows + BT - 1) / BT + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
+    c.channel_tiles(nn);
     if (e == cudaSuccess)
         e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(C::kThreads), C::kSmem, s, mx,
                          mw, c, drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : 1);

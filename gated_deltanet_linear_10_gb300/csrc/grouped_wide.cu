@@ -490,7 +490,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
         const float *sw = nullptr, *next_sw = nullptr;
         auto tell = [&](int t, int j) {
             if (t >= tiles) return true;
-            const GroupTile g = find_group_tile(table, c.n_experts, t, nn, kGwRows);
+            const GroupTile g = find_group_tile(table, c, t, nn, kGwRows);
             const int s = j % kGwTiles, n0 = g.n * kGwChannels;
             uint32_t there[4];
 #pragma unroll
@@ -645,7 +645,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     }
 }
 
-template <bool kBlock, typename O> gdn_status launch(const GroupedCall &c, int drop, cudaStream_t s) {
+template <bool kBlock, typename O> gdn_status launch(GroupedCall c, int drop, cudaStream_t s) {
     CUtensorMap mx, mw, my = {};
     if (!encode_tmap_rows(&mx, c, 128) || !encode_tmap_experts(&mw, c, 64)) return GDN_ERR_CUDA;
     if (c.vec16 && !encode_tmap_2d(&my, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -658,6 +658,7 @@ template <bool kBlock, typename O> gdn_status launch(const GroupedCall &c, int d
     const int64_t nn = (c.n_out + kGwChannels - 1) / kGwChannels;
     const int64_t tiles = (((int64_t)c.n_rows + kGwRows - 1) / kGwRows + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
+    c.channel_tiles(nn);
     if (e == cudaSuccess)
         e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(2 * tiles, sm_count() / 2 * 2)), dim3(kGwThreads), GwSmem<kBlock>::kBytes,
                          s, mx, mw, my, c, drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : (c.n_in + (kBlock ? 127 : 63)) / (kBlock ? 128 : 64));
