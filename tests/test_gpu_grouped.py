@@ -322,3 +322,34 @@ def test_many_tiles(T, k, E, K, N, dtype):
     counts = torch.bincount(torch.randint(0, E, (T * k,), generator=g), minlength=E).tolist()
     _run(T, counts, K, N, dtype, gather=T)
     _run(T, counts, K, N, dtype, F32)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("N", [700, 701, 704, 1022, 129])
+def test_about_a_hundred_rows_an_expert(N, dtype, out):
+    """Tiles of up to 128 rows: full, ragged and nearly empty ones, rows of y on 16 bytes, on words and on neither."""
+    counts = [128, 97, 33, 128, 1, 0, 129, 250, 64, 100, 127, 5]
+    for K in (300, 1152):
+        for gather in (None, 77):
+            _run(N + K, counts, K, N, dtype, out, gather)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("N,off,pad", [(704, 8, 8), (704, 1, 3), (702, 2, 2), (701, 0, 3)])
+def test_about_a_hundred_rows_strided_and_left_out(N, off, pad, dtype, out):
+    counts, K = [128, 97, 33, 128, 1, 0, 129, 250, 64, 100, 127, 5], 520
+    R = sum(counts)
+    x, w, sx, sw = _operands(N + off, 90, len(counts), K, N, dtype)
+    rows = torch.randint(-1, 90, (R,), device=DEV, dtype=torch.int32)
+    rows[::37] = -1
+    go = lambda r, y=None: gdn().gdn_grouped_linear(x, w, _offsets(counts), rows=r, x_scale=sx, weight_scale=sw, y_dtype=out, y=y)  # noqa: E731
+    want = go(rows.clamp_min(0))
+    want[rows < 0] = 0
+    wide = torch.full((R + 1, off + N + pad), 9.0, dtype=out, device=DEV)
+    go(rows, wide[:R, off:off + N])
+    torch.cuda.synchronize()
+    status_clean()
+    assert bits_equal(wide[:R, off:off + N].contiguous(), want)
+    assert torch.all(wide[:R, :off] == 9.0) and torch.all(wide[:R, off + N:] == 9.0) and torch.all(wide[R] == 9.0)
