@@ -47,25 +47,33 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
                                {128, 128, 290, 90, {60, 60}, {{33, 37}, {31, 41}}},
                                // (pairs write such rows slowly, and with block scales sum nothing meanwhile)
                                {256, 256, 450, 90, {180, 170}, {{35, 39}, {46, 61}}}};
+    constexpr int kJoin = 40, kJoinRows = 21;          // k in parts: a call's, 16 rows of a part
     const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
     const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;
-    int best = 0;
+    int best = 0, best_cut = 0;
     int64_t least = INT64_MAX;
     for (const Tile &t : kTiles) {
         const int64_t halves = c.offsets ? std::max<int64_t>(2 * (int64_t)experts, 2 * (int64_t)c.n_rows / t.rows + experts)
                                          : 2 * (((int64_t)c.n_rows + t.rows - 1) / t.rows);
         const int64_t tiles = (halves + 1) / 2 * ((c.n_out + t.channels - 1) / t.channels);
-        const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms;
-        const int64_t tile = t.tile + (c.vec16 ? 0 : t.odd[c.e4m3]) + blocks * t.block[c.e4m3][c.rows != nullptr];
-        const int64_t cost = t.ends + (tiles + slots - 1) / slots * tile;
-        // (tiles beyond 31 bits are not launched)
-        if (cost < least && tiles < (1ll << 30)) {
+        if (tiles >= (1ll << 30)) continue;                // (so many are not launched)
+        const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms, block = t.block[c.e4m3][c.rows != nullptr];
+        const int64_t rest = t.tile + (c.vec16 ? 0 : t.odd[c.e4m3]);
+        for (int cut = 0; cut <= 3; ++cut) {
+            // k in parts: of one group of rows, in one wave, four blocks a CTA at least (16 clusters
+            // of eight, where 15 fit, are two waves: 1 x 4096 x 2048 11.9 us, in clusters of four 6.9)
+            if (cut > 0 && (c.offsets || t.rows == 256 || tiles << cut > sms || blocks >> cut < 4)) break;
+            if (cut == 3 && tiles > grouped_eights()) break;
+            const int64_t cost = t.ends + (tiles + slots - 1) / slots * (rest + ((blocks + (1 << cut) - 1) >> cut) * block) +
+                                 (cut > 0 ? kJoin + (t.rows << cut) * kJoinRows / 16 : 0);
+            if (cost >= least) continue;
             least = cost;
             best = t.rows;
+            best_cut = cut;
         }
     }
     if (best == 0) return GDN_ERR_UNSUPPORTED;
-    return best == 256 ? launch_grouped_wide(c, linear_drop(), s) : launch_grouped_narrow(c, best, linear_drop(), s);
+    return best == 256 ? launch_grouped_wide(c, linear_drop(), s) : launch_grouped_narrow(c, best, best_cut, linear_drop(), s);
 }
 
 }  // namespace gdn

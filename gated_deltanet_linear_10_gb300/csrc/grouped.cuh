@@ -31,7 +31,10 @@ struct GroupedCall {
 
 // grouped_narrow.cu: a tile's weight rows on the accumulator's lanes, its tokens the
 // columns; grouped_wide.cu: tokens on the lanes, a pair of CTAs a tile.
-gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int drop, cudaStream_t s);
+// 2^cut CTAs share a tile, each a part of k: only without offsets, with at least as many
+// blocks, and where that is one wave of CTAs.
+int grouped_eights();                // clusters of eight of its CTAs that the device holds at once
+gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int cut, int drop, cudaStream_t s);
 gdn_status launch_grouped_wide(const GroupedCall &c, int drop, cudaStream_t s);
 cudaError_t set_grouped_narrow_limit(uint64_t limit_ns, cudaStream_t s);
 cudaError_t set_grouped_wide_limit(uint64_t limit_ns, cudaStream_t s);

@@ -11,7 +11,9 @@
 // products, scales, and 4 or 8 that sum the blocks.  With block scales every block of 128
 // in k is a product of its own into one of four accumulators; the summing warps add it,
 // times sx sw, to registers.  A block takes such a warp some 500 cycles of waits and
-// latencies, so two groups of four share the columns of a tile of 64 or 128 rows.  (With
+// latencies, so two groups of four share the columns of a tile of 64 or 128 rows; and where
+// there are few tiles, a cluster's CTAs share the blocks of one (64 x 4096 x 2048: 12.4 ->
+// 8.5 us, 16 x 16384 x 256: 40 -> 10).  (With
 // four groups, 16 warps, that product took half a microsecond longer.)
 #include <limits.h>
 
@@ -108,7 +110,7 @@ __device__ __forceinline__ void store_lanes(const F2 (&acc)[W / 2], uint8_t *sta
 template <int BT, bool kBlock, bool kPieces>
 __global__ void __launch_bounds__(GnCfg<BT>::kThreads)
 grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                      const __grid_constant__ GroupedCall c, int keep) {
+                      const __grid_constant__ GroupedCall c, int cut, int keep) {
     using C = GnCfg<BT>;
     constexpr int S = C::kStages, A = C::kAccs;
     constexpr bool kTurned = C::kTurned;
@@ -120,7 +122,18 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr int kElems = kBlock ? 128 : 64;
-    const int nk = (c.n_in + kElems - 1) / kElems, nn = (c.n_out + 127) / 128;
+    const int nn = (c.n_out + 127) / 128;
+    // Blocks kb0 .. nk - 1 are this CTA's: all, or its part where 2^cut CTAs, a cluster, share
+    // a tile (then one each; of one group of rows, which is always with block scales).
+    const bool shared = kBlock && cut > 0;
+    const int rank = shared ? (int)cta_rank() : 0, split = shared ? 1 << cut : 1;
+    int kb0 = 0, nk = (c.n_in + kElems - 1) / kElems, tile0 = blockIdx.x, tile_step = gridDim.x;
+    if (shared) {
+        kb0 = nk * rank >> cut;
+        nk = nk * (rank + 1) >> cut;
+        tile0 >>= cut;
+        tile_step >>= cut;
+    }
     float *scales = reinterpret_cast<float *>(smem + S * C::kStage);
     volatile int *abort = &abort_flag;
 
@@ -160,11 +173,11 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         int s = 0, i = 0;
         uint32_t phase = 1;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const GroupTile a = find_group_tile(table, c, t, nn, BT);
             const uint32_t bytes = c.rows ? C::kW : C::kStage;
 #pragma unroll 1
-            for (int k = 0; k < nk; ++k, ++i) {
+            for (int k = kb0; k < nk; ++k, ++i) {
                 if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
                     ok = false;
                     break;
@@ -196,12 +209,12 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         int s = 0, u = 0;                  // u: accumulators used so far
         uint32_t phase = 0;
         bool ok = true, ready = false;     // operands and accumulator of the next block are known to be there
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
 #pragma unroll 1
-            for (int k = 0; k < nk; ++k) {
+            for (int k = kb0; k < nk; ++k) {
                 if (!ready) {
                     ok = mbar_wait_all(&full[s], phase, abort);
-                    if (ok && (kBlock || k == 0) && u >= A) ok = mbar_wait_all(&acc_empty[u % A], (u / A - 1) & 1, abort);
+                    if (ok && (kBlock || k == kb0) && u >= A) ok = mbar_wait_all(&acc_empty[u % A], (u / A - 1) & 1, abort);
                     if (!ok) break;
                 }
                 tc_fence_after();
@@ -213,7 +226,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     const uint64_t da = desc | (kTurned ? xt : st), db = desc | (kTurned ? st : xt);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        linear_mma<kBlock>(d, da + 2 * q, db + 2 * q, idesc, q > 0 || (!kBlock && k > 0));
+                        linear_mma<kBlock>(d, da + 2 * q, db + 2 * q, idesc, q > 0 || (!kBlock && k > kb0));
                     mma_commit(&empty[s]);
                     if (last) mma_commit(&acc_full[u % A]);
                 }
@@ -250,7 +263,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             int s = 0, i = 0;
             uint32_t phase = 1;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = tile0; t < tiles && ok; t += tile_step) {
                 const GroupTile a = find_group_tile(table, c, t, nn, BT);
                 int row[N];
 #pragma unroll
@@ -260,7 +273,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 }
                 const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + (lane & 7) * 16;
 #pragma unroll 1
-                for (int k = 0; k < nk; ++k, ++i, src += 128) {
+                for (int k = 0; k < nk; ++k, ++i, src += 128) {     // (never cut)
                     if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
                         ok = false;
                         break;
@@ -296,7 +309,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         // Scales of the next blocks, times the weight's, and which rows there are.
         int slot = 0, v = 0;
         bool ok = true, wrong = false;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const GroupTile a = find_group_tile(table, c, t, nn, BT);
             constexpr int Q = (BT + 31) / 32;
             int row[Q];
@@ -309,10 +322,10 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 there[q] = __ballot_sync(0xffffffffu, row[q] < c.n_x);
             }
             const float *sw = kBlock ? c.sw + ((int64_t)a.e * c.nb + a.n) * c.kb : nullptr;
-            for (int k0 = 0; k0 < (kBlock ? nk : 1) && ok; k0 += kScaleChunk, ++v, slot ^= 1) {
+            for (int k0 = kBlock ? kb0 : 0; k0 < (kBlock ? nk : 1) && ok; k0 += kScaleChunk, ++v, slot ^= 1) {
                 float f[Q][kScaleChunk];
                 if (kBlock) {
-                    const bool pieces = k0 + kScaleChunk <= nk && c.sx16;
+                    const bool pieces = k0 + kScaleChunk <= nk && c.sx16 && k0 % 4 == 0;
 #pragma unroll
                     for (int q = 0; q < Q; ++q) {
                         const float *sx = c.sx + (int64_t)row[q] * c.kb + k0;
@@ -358,14 +371,15 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
         int u = 0, v = 0;                  // accumulators and chunks used so far
         bool ok = true, ready = false;     // the next accumulator is known to be there
         const int blocks = kBlock ? nk : 1;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        bool joined = false;               // the cluster's other parts have been waited for
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const GroupTile a = find_group_tile(table, c, t, nn, BT);
             F2 acc[W / 2];
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) acc[i] = f2(0.f, 0.f);
             uint32_t there[kTurned ? 1 : (W + 31) / 32];
 #pragma unroll 1
-            for (int k0 = 0; k0 < blocks && ok; k0 += kScaleChunk, ++v) {
+            for (int k0 = kBlock ? kb0 : 0; k0 < blocks && ok; k0 += kScaleChunk, ++v) {
                 const int slot = v & 1, n = min(blocks - k0, kScaleChunk);
                 if (!mbar_wait_all(&sc_full[slot], (v >> 1) & 1, abort)) {
                     ok = false;
@@ -415,6 +429,34 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 if (lane == 0) mbar_arrive(&sc_empty[slot]);
             }
             if (!ok) break;
+            if (shared) {
+                // The leader adds the others' sums, in their order, out of their shared memory
+                // (the ring's, which nothing reads or fills any more).
+                joined = true;
+                const uint32_t place = smem_u32(smem) + ((warp - kGnFirstSum) * (W / 2) * 32 + lane) * 8;
+                if (rank != 0) {
+#pragma unroll
+                    for (int i = 0; i < W / 2; ++i)
+                        asm volatile("st.shared.b64 [%0], %1;" ::"r"(place + i * 256), "l"(acc[i]) : "memory");
+                }
+                __syncwarp();
+                cluster_arrive();
+                cluster_wait();
+                if (rank != 0) break;
+                for (int j = 1; j < split; ++j) {
+                    const uint32_t from = peer_smem(place, j);
+                    int gone;
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(gone) : "r"(peer_smem(smem_u32(&abort_flag), j)) : "memory");
+                    if (gone) *abort = 1;                  // what it has is no sum
+#pragma unroll
+                    for (int i = 0; i < W / 2; ++i) {
+                        F2 x;
+                        asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(x) : "r"(from + i * 256) : "memory");
+                        acc[i] = f2_add(acc[i], x);
+                    }
+                }
+                if (*abort) break;
+            }
             if constexpr (kTurned) {
                 const bool is = there[0] >> lane & 1;
                 uint8_t *staging = smem + S * C::kStage + C::kScales + (warp - kGnFirstSum) * C::kStaging;
@@ -436,7 +478,21 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                 }
             }
         }
+        if (shared && !joined) {
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+        }
         tc_fence_before();
+    }
+    if (shared) {
+        __syncwarp();
+        if (warp < kGnFirstSum || warp >= kGnFirstSum + C::kSums) {
+            cluster_arrive();
+            cluster_wait();
+        }
+        cluster_arrive_relaxed();                          // no CTA ends while the leader may read its sums
+        cluster_wait();
     }
     __syncthreads();
     tc_fence_after();
@@ -444,7 +500,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     if (tid == 0 && abort_flag) flag_status(GDN_DEVSTAT_TIMEOUT);
 }
 
-template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(GroupedCall c, int drop, cudaStream_t s) {
+template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(GroupedCall c, int cut, int drop, cudaStream_t s) {
     using C = GnCfg<BT>;
     CUtensorMap mx, mw;
     if (!encode_tmap_rows(&mx, c, BT) || !encode_tmap_experts(&mw, c, 128)) return GDN_ERR_CUDA;
@@ -455,9 +511,12 @@ template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(GroupedCal
     const int64_t tiles = (((int64_t)c.n_rows + BT - 1) / BT + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     c.channel_tiles(nn);
+    const int keep = drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : 1;
     if (e == cudaSuccess)
-        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(C::kThreads), C::kSmem, s, mx,
-                         mw, c, drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : 1);
+        e = cut > 0 ? launch_after_cluster(kernel, 1 << cut, dim3((unsigned)tiles << cut), dim3(C::kThreads), C::kSmem, s, mx,
+                                           mw, c, cut, keep)
+                    : launch_after(kernel, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(C::kThreads), C::kSmem, s,
+                                   mx, mw, c, cut, keep);
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return GDN_ERR_LAUNCH;
@@ -467,14 +526,21 @@ template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(GroupedCal
 
 }  // namespace
 
-gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int drop, cudaStream_t s) {
+int grouped_eights() {
+    static ClustersHeld held;
+    int count = 0;
+    using C = GnCfg<128>;
+    return held.ask(grouped_narrow_kernel<128, true, true>, 8, C::kThreads, C::kSmem, count) == cudaSuccess ? count : 0;
+}
+
+gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int cut, int drop, cudaStream_t s) {
     switch (tile_rows) {
-        case 16: return c.e4m3 ? launch<16, true>(c, drop, s) : launch<16, false>(c, drop, s);
-        case 32: return c.e4m3 ? launch<32, true>(c, drop, s) : launch<32, false>(c, drop, s);
-        case 64: return c.e4m3 ? launch<64, true>(c, drop, s) : launch<64, false>(c, drop, s);
+        case 16: return c.e4m3 ? launch<16, true>(c, cut, drop, s) : launch<16, false>(c, cut, drop, s);
+        case 32: return c.e4m3 ? launch<32, true>(c, cut, drop, s) : launch<32, false>(c, cut, drop, s);
+        case 64: return c.e4m3 ? launch<64, true>(c, cut, drop, s) : launch<64, false>(c, cut, drop, s);
         default:
-            if (!c.vec16) return c.e4m3 ? launch<128, true, false>(c, drop, s) : launch<128, false, false>(c, drop, s);
-            return c.e4m3 ? launch<128, true>(c, drop, s) : launch<128, false>(c, drop, s);
+            if (!c.vec16) return c.e4m3 ? launch<128, true, false>(c, cut, drop, s) : launch<128, false, false>(c, cut, drop, s);
+            return c.e4m3 ? launch<128, true>(c, cut, drop, s) : launch<128, false>(c, cut, drop, s);
     }
 }
 

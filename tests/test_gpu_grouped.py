@@ -353,3 +353,30 @@ def test_about_a_hundred_rows_strided_and_left_out(N, off, pad, dtype, out):
     status_clean()
     assert bits_equal(wide[:R, off:off + N].contiguous(), want)
     assert torch.all(wide[:R, :off] == 9.0) and torch.all(wide[:R, off + N:] == 9.0) and torch.all(wide[R] == 9.0)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 2048), (16, 7168, 512), (5, 16384, 256), (1, 1024, 1), (3, 1025, 130), (70, 5800, 300),
+                                   (40, 3333, 129), (128, 9000, 640), (150, 2100, 1000), (300, 6700, 129), (512, 16384, 256),
+                                   (97, 12289, 8), (64, 4096, 2048), (1000, 8192, 264)])
+def test_k_in_parts(T, K, N, out):
+    """Few tiles and many blocks: clusters share a tile's blocks, in parts that start anywhere; the same bits again,
+    on two streams and in a graph."""
+    y = _block(T + K, T, K, N, out)
+    x, w, sx, sw = _operands(T + K, T, 1, K, N, E4M3)
+    go = lambda t: gdn().gdn_linear_block(x, w[0], sx, sw[0], y=t)  # noqa: E731
+    ys = [torch.zeros_like(y) for _ in range(3)]
+    torch.cuda.synchronize()
+    for t, s in zip(ys, [torch.cuda.Stream(), torch.cuda.Stream()]):
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                go(t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(ys[2])
+    ys[2].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    status_clean()
+    assert all(bits_equal(t, y) for t in ys)
