@@ -25,6 +25,12 @@ bool encode_tmap_rows(CUtensorMap *map, const GroupedCall &c, uint32_t box_rows)
     return encode_tmap_operand(map, c.x, c.n_in, c.n_x, c.xs, box_rows, c.e4m3);
 }
 
+// Of R rows floor(R / r) tiles are full at most, and each expert with rows may have one more.
+int64_t most_row_tiles(const GroupedCall &c, int tile_rows) {
+    const int64_t n = c.n_rows;
+    return c.offsets ? std::min(n, n / tile_rows + std::min<int64_t>(c.n_experts, n)) : (n + tile_rows - 1) / tile_rows;
+}
+
 // The choice of a tile: the shortest by an estimate of waves of tiles, each of as many
 // blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, what rows of y
 // off 16 bytes add to that, a block) are fitted to 574 products: 1 to 4096 rows of 512 x
@@ -57,13 +63,14 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
                                          : 2 * (((int64_t)c.n_rows + t.rows - 1) / t.rows);
         const int64_t tiles = (halves + 1) / 2 * ((c.n_out + t.channels - 1) / t.channels);
         if (tiles >= (1ll << 30)) continue;                // (so many are not launched)
+        const int64_t most = most_row_tiles(c, t.rows) * ((c.n_out + t.channels - 1) / t.channels);
         const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms, block = t.block[c.e4m3][c.rows != nullptr];
         const int64_t rest = t.tile + (c.vec16 ? 0 : t.odd[c.e4m3]);
         for (int cut = 0; cut <= 3; ++cut) {
-            // k in parts: of one group of rows, in one wave, four blocks a CTA at least (16 clusters
-            // of eight, where 15 fit, are two waves: 1 x 4096 x 2048 11.9 us, in clusters of four 6.9)
-            if (cut > 0 && (c.offsets || t.rows == 256 || tiles << cut > sms || blocks >> cut < 4)) break;
-            if (cut == 3 && tiles > grouped_eights()) break;
+            // k in parts: in one wave, four blocks a CTA at least (16 clusters of eight, where 15
+            // fit, are two waves: 1 x 4096 x 2048 11.9 us, in clusters of four 6.9)
+            if (cut > 0 && (t.rows == 256 || most << cut > sms || blocks >> cut < 4)) break;
+            if (cut == 3 && most > grouped_eights()) break;
             const int64_t cost = t.ends + (tiles + slots - 1) / slots * (rest + ((blocks + (1 << cut) - 1) >> cut) * block) +
                                  (cut > 0 ? kJoin + (t.rows << cut) * kJoinRows / 16 : 0);
             if (cost >= least) continue;

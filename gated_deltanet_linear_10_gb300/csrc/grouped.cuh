@@ -31,8 +31,9 @@ struct GroupedCall {
 
 // grouped_narrow.cu: a tile's weight rows on the accumulator's lanes, its tokens the
 // columns; grouped_wide.cu: tokens on the lanes, a pair of CTAs a tile.
-// 2^cut CTAs share a tile, each a part of k: only without offsets, with at least as many
-// blocks, and where that is one wave of CTAs.
+// 2^cut CTAs share a tile, each a part of k: only with at least as many blocks, and where
+// that is one wave of CTAs.
+int64_t most_row_tiles(const GroupedCall &c, int tile_rows);      // that there can be
 int grouped_eights();                // clusters of eight of its CTAs that the device holds at once
 gdn_status launch_grouped_narrow(const GroupedCall &c, int tile_rows, int cut, int drop, cudaStream_t s);
 gdn_status launch_grouped_wide(const GroupedCall &c, int drop, cudaStream_t s);

@@ -124,8 +124,8 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
     constexpr int kElems = kBlock ? 128 : 64;
     const int nn = (c.n_out + 127) / 128;
     // Blocks kb0 .. nk - 1 are this CTA's: all, or its part where 2^cut CTAs, a cluster, share
-    // a tile (then one each; of one group of rows, which is always with block scales).
-    const bool shared = kBlock && cut > 0;
+    // a tile (one each at most).
+    const bool shared = cut > 0;
     const int rank = shared ? (int)cta_rank() : 0, split = shared ? 1 << cut : 1;
     int kb0 = 0, nk = (c.n_in + kElems - 1) / kElems, tile0 = blockIdx.x, tile_step = gridDim.x;
     if (shared) {
@@ -271,9 +271,9 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     const int four = first + j * G;
                     row[j] = four < BT / 4 ? group_x_row(c, a.r0 + four * 4 + sub, a.r1) : c.n_x;
                 }
-                const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + (lane & 7) * 16;
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(c.x) + (lane & 7) * 16 + kb0 * 128;
 #pragma unroll 1
-                for (int k = 0; k < nk; ++k, ++i, src += 128) {     // (never cut)
+                for (int k = kb0; k < nk; ++k, ++i, src += 128) {
                     if (i >= S && !mbar_wait_all(&empty[s], phase, abort)) {
                         ok = false;
                         break;
@@ -508,7 +508,7 @@ template <int BT, bool kBlock, bool kPieces = true> gdn_status launch(GroupedCal
     static SmemAllowed allowed;
     cudaError_t e = allowed.ask(kernel, C::kSmem);
     const int64_t nn = (c.n_out + 127) / 128;
-    const int64_t tiles = (((int64_t)c.n_rows + BT - 1) / BT + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
+    const int64_t tiles = most_row_tiles(c, BT) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     c.channel_tiles(nn);
     const int keep = drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : 1;

@@ -656,7 +656,7 @@ template <bool kBlock, typename O> gdn_status launch(GroupedCall c, int drop, cu
     static SmemAllowed allowed;
     cudaError_t e = allowed.ask(kernel, GwSmem<kBlock>::kBytes);
     const int64_t nn = (c.n_out + kGwChannels - 1) / kGwChannels;
-    const int64_t tiles = (((int64_t)c.n_rows + kGwRows - 1) / kGwRows + (c.offsets ? std::min(c.n_experts, c.n_rows) : 0)) * nn;
+    const int64_t tiles = most_row_tiles(c, kGwRows) * nn;
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     c.channel_tiles(nn);
     if (e == cudaSuccess)

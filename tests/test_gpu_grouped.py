@@ -380,3 +380,23 @@ def test_k_in_parts(T, K, N, out):
     torch.cuda.synchronize()
     status_clean()
     assert all(bits_equal(t, y) for t in ys)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("counts", [[1, 0, 0, 1, 0, 2], [0, 0, 0], [20, 20], [3], [0, 40, 0, 0, 0], [120, 0, 9], [1] * 9])
+def test_few_rows_and_k_in_parts(counts, dtype, out):
+    """Clusters that share a tile's blocks, more of them than there are tiles; rows left out and behind the last."""
+    for K, N in ((2048, 256), (1100, 129), (5000, 250)):
+        for gather in (None, 11):
+            _run(K + N, counts, K, N, dtype, out, gather, behind=3 if sum(counts) else 7)
+    K, N, R = 3000, 264, max(1, sum(counts))
+    x, w, sx, sw = _operands(3, 5, len(counts), K, N, dtype)
+    rows = (torch.arange(R, device=DEV, dtype=torch.int32) % 6 - 1).contiguous()
+    go = lambda r: gdn().gdn_grouped_linear(x, w, _offsets(counts), rows=r, x_scale=sx, weight_scale=sw,  # noqa: E731
+                                            y=torch.full((R, N), 5.0, dtype=out, device=DEV))
+    got, want = go(rows), go(rows.clamp_min(0))
+    want[:sum(counts)][rows[:sum(counts)] < 0] = 0
+    torch.cuda.synchronize()
+    status_clean()
+    assert bits_equal(got, want)
