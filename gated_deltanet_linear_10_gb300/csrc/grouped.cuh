@@ -115,7 +115,8 @@ struct GroupTile {
 // By a whole warp.  Within an expert groups of kGroupRaster row tiles take the channel
 // tiles one after the other, row tiles fastest: the tiles in flight share weights and rows.
 // (Three quotients by division are most of 900 cycles, which the sums of a tile wait for.)
-__device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, const GroupedCall &c, int tile, int nn, int tile_rows) {
+__device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, const GroupedCall &c, int tile, int nn,
+                                                     int tile_rows) {
     const int experts = c.n_experts, lane = threadIdx.x & 31, rt = c.by_channels(tile);
     const int hi = __popc(__ballot_sync(0xffffffffu, g.first[min(32 * (lane + 1), experts)] <= rt));
     const int e = 32 * hi + __popc(__ballot_sync(0xffffffffu, g.first[min(32 * hi + lane + 1, experts)] <= rt));
@@ -125,7 +126,8 @@ __device__ __forceinline__ GroupTile find_group_tile(const GroupTable &g, const 
     const int base = r < kGroupRaster * nn ? 0 : c.by_raster(r) * kGroupRaster, rr = r - base * nn;
     const int rows = min(kGroupRaster, tiles - base);
     // 2^32 / rows, rounded up: exact below 2^29
-    constexpr uint32_t kInverse[kGroupRaster + 1] = {0, 0, 1u << 31, 1431655766u, 1u << 30, 858993460u, 715827883u, 613566757u, 1u << 29};
+    constexpr uint32_t kInverse[kGroupRaster + 1] = {0,       0,          1u << 31,   1431655766u, 1u << 30,
+                                                     858993460u, 715827883u, 613566757u, 1u << 29};
     t.n = rr;
 #pragma unroll
     for (int i = 2; i <= kGroupRaster; ++i)

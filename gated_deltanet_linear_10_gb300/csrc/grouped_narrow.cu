@@ -11,10 +11,10 @@
 // products, scales, and 4 or 8 that sum the blocks.  With block scales every block of 128
 // in k is a product of its own into one of four accumulators; the summing warps add it,
 // times sx sw, to registers.  A block takes such a warp some 500 cycles of waits and
-// latencies, so two groups of four share the columns of a tile of 64 or 128 rows; and where
-// there are few tiles, a cluster's CTAs share the blocks of one (64 x 4096 x 2048: 12.4 ->
-// 8.5 us, 16 x 16384 x 256: 40 -> 10).  (With
-// four groups, 16 warps, that product took half a microsecond longer.)
+// latencies, so two groups of four share the columns of a tile of 64 or 128 rows (with four
+// groups 256 x 2048 x 8192 took half a microsecond longer).  Where there are few tiles, a
+// cluster's CTAs share the blocks of one (64 x 4096 x 2048: 12.4 -> 8.5 us, 16 x 16384 x
+// 256: 40 -> 10).
 #include <limits.h>
 
 #include <algorithm>
@@ -283,7 +283,8 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                         if (k < whole) {
 #pragma unroll
                             for (int j = 0; j < N; ++j)
-                                copy16_if(row[j] < c.n_x, st + j * G * 512 + ((first + j * G) & 1 ? odd : even), src + row[j] * stride);
+                                copy16_if(row[j] < c.n_x, st + j * G * 512 + ((first + j * G) & 1 ? odd : even),
+                                          src + row[j] * stride);
                         } else {
                             const int n = min(16, max(0, bytes - k * 128));
 #pragma unroll 1
@@ -292,7 +293,8 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
 #pragma unroll
                                 for (int z = 1; z < N; ++z) at = z == j ? row[z] : at;      // no array in memory
                                 if (at < c.n_x)
-                                    copy16(st + j * G * 512 + ((first + j * G) & 1 ? odd : even), n > 0 ? src + at * stride : c.x, n);
+                                    copy16(st + j * G * 512 + ((first + j * G) & 1 ? odd : even),
+                                           n > 0 ? src + at * stride : c.x, n);
                             }
                         }
                         copies_arrive(&full[s]);

@@ -168,7 +168,8 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging
                     uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        v[j] = *reinterpret_cast<const uint32_t *>(tile + (r + j) * 128 + ((lane >> 2 ^ (j & 7)) << 4) + (lane & 3) * 4);
+                        v[j] = *reinterpret_cast<const uint32_t *>(tile + (r + j) * 128 + ((lane >> 2 ^ (j & 7)) << 4) +
+                                                                   (lane & 3) * 4);
                     const int col = lane * E;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -185,7 +186,8 @@ __device__ __forceinline__ void wide_store(const F2 (&acc)[64], uint8_t *staging
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int row = r + (j >> 1), piece = (j & 1) * 4 + (lane >> 3);
-                        v[j] = *reinterpret_cast<const uint16_t *>(tile + row * 128 + ((piece ^ (row & 7)) << 4) + (lane & 7) * 2);
+                        v[j] = *reinterpret_cast<const uint16_t *>(tile + row * 128 + ((piece ^ (row & 7)) << 4) +
+                                                                   (lane & 7) * 2);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -227,7 +229,8 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
     constexpr int S = M::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GroupTable table;
-    __shared__ uint64_t full[S], empty[S], gathered[S], acc_full[2][2], acc_empty[2][2], drained[2], sc_full[2], sc_empty[2];   // [half][accumulator]
+    __shared__ uint64_t full[S], empty[S], gathered[S], drained[2], sc_full[2], sc_empty[2];
+    __shared__ uint64_t acc_full[2][2], acc_empty[2][2];   // [half][accumulator]
     constexpr int H = kBlock ? 2 : 1;      // issuing warps; one product makes both halves in bf16
     __shared__ WideTiles wide;
     __shared__ uint32_t tmem_base;
@@ -500,7 +503,9 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                 if (c.rows && r < g.r1) wrong |= c.rows[r] >= c.n_x;
                 there[i] = __ballot_sync(0xffffffffu, next_xr[i] < c.n_x);
             }
-            if (kBlock) next_sw = c.sw + ((int64_t)g.e * c.nb + n0 / 128) * c.kb + (lane < kGwChunk || n0 + 128 >= c.n_out ? 0 : c.kb);
+            if (kBlock)
+                next_sw = c.sw + ((int64_t)g.e * c.nb + n0 / 128) * c.kb +
+                          (lane < kGwChunk || n0 + 128 >= c.n_out ? 0 : c.kb);
             if (j >= kGwTiles && !mbar_wait_warp(&wide.empty[s], (j / kGwTiles - 1) & 1, abort)) return false;
             if (lane == 0) {
                 wide.at[s] = make_int4(g.r0, g.r1, n0, g.e);
@@ -660,8 +665,9 @@ template <bool kBlock, typename O> gdn_status launch(GroupedCall c, int drop, cu
     if (tiles >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     c.channel_tiles(nn);
     if (e == cudaSuccess)
-        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(2 * tiles, sm_count() / 2 * 2)), dim3(kGwThreads), GwSmem<kBlock>::kBytes,
-                         s, mx, mw, my, c, drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : (c.n_in + (kBlock ? 127 : 63)) / (kBlock ? 128 : 64));
+        e = launch_after(kernel, dim3((unsigned)std::min<int64_t>(2 * tiles, sm_count() / 2 * 2)), dim3(kGwThreads),
+                         GwSmem<kBlock>::kBytes, s, mx, mw, my, c,
+                         drop == kDropNone ? INT_MAX : drop & kDropAll ? 0 : (c.n_in + (kBlock ? 127 : 63)) / (kBlock ? 128 : 64));
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return GDN_ERR_LAUNCH;

@@ -100,7 +100,8 @@ template <typename T, int PER, int VEC> struct RawLogits {
                 w[i] = index(i, lane) < experts ? *reinterpret_cast<const uint32_t *>(row + index(i, lane)) : 0u;
         } else {
             auto half = [&](int i) {
-                return i < PER && index(i, lane) < experts ? *reinterpret_cast<const uint16_t *>(row + index(i, lane)) : (uint16_t)0;
+                const int e = index(i, lane);
+                return i < PER && e < experts ? *reinterpret_cast<const uint16_t *>(row + e) : (uint16_t)0;
             };
 #pragma unroll
             for (int i = 0; i < W; ++i) w[i] = half(2 * i) | (uint32_t)half(2 * i + 1) << 16;
@@ -124,7 +125,8 @@ __device__ __forceinline__ uint32_t max_of_two(uint32_t a, uint32_t b) {
 
 // What a lane keeps of its experts, and of the largest one (of no expert: less than kLeast).
 template <int PER, int VEC>
-__device__ __forceinline__ uint32_t keep_logits(const RawLogits<float, PER, VEC> &raw, int experts, int lane, uint32_t (&kept)[PER]) {
+__device__ __forceinline__ uint32_t keep_logits(const RawLogits<float, PER, VEC> &raw, int experts, int lane,
+                                                uint32_t (&kept)[PER]) {
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -134,7 +136,8 @@ __device__ __forceinline__ uint32_t keep_logits(const RawLogits<float, PER, VEC>
     return most;
 }
 template <int PER, int VEC>
-__device__ __forceinline__ uint32_t keep_logits(const RawLogits<__nv_bfloat16, PER, VEC> &raw, int experts, int lane, uint32_t (&kept)[PER]) {
+__device__ __forceinline__ uint32_t keep_logits(const RawLogits<__nv_bfloat16, PER, VEC> &raw, int experts, int lane,
+                                                uint32_t (&kept)[PER]) {
     uint32_t two = 0;
 #pragma unroll
     for (int i = 0; i < PER; i += 2) {
@@ -579,8 +582,8 @@ template <typename T> static cudaError_t launch_route(const RouteCall &c) {
 
 // y = residual + the weighted rows of a token, one thread a vector of N channels, kAhead
 // rows asked for before the first is added.  Bound by the memory: 20668 x 10 rows of 2048
-// bf16 take 163 us, 0.92 of a copy's rate; 256 x 10 take 3.3, a launch and two trips.  `split`: CTAs of a token, or 0 where a CTA
-// has `per` whole tokens.
+// bf16 take 163 us, 0.92 of a copy's rate; 256 x 10 take 3.3, a launch and two trips.
+// `split`: CTAs of a token, or 0 where a CTA has `per` whole tokens.
 constexpr int kAhead = 5, kCombineThreads = 256;
 template <typename T, int N>
 __global__ void __launch_bounds__(kCombineThreads, 4)
