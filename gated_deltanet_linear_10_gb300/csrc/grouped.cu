@@ -35,7 +35,7 @@ int64_t most_row_tiles(const GroupedCall &c, int tile_rows) {
 // blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, what rows of y
 // off 16 bytes add to that, a block) are fitted to 574 products: 1 to 4096 rows of 512 x
 // 4096 to 4096 x 2048, and 12 to 400 rows for each of 8, 60 and 256 experts, in place and
-// gathered.  There the choice takes 1 % longer than the best tile, 20 % at worst.  Of an
+// gathered.  There the choice takes 1 % longer than the best tile, 14 % at worst.  Of an
 // expert's rows the host knows the mean: tiles of r rows take mean / r + 1/2 of them, at
 // least one.  (256 experts of 82 rows gathered, 1000 x 700 e4m3, in the five tiles: 193,
 // 154, 81, 84 and 105 us; 256 x 2048 x 8192 in those of 64, 128 and 256: 15.8, 9.8, 13.4.)
@@ -47,12 +47,12 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     struct Tile {
         int rows, channels, ends, tile, odd[2], block[2][2];   // odd, block: bf16, e4m3; block: rows in place, gathered
     };
-    constexpr Tile kTiles[] = {{16, 128, 240, 70, {0, 0}, {{27, 34}, {28, 33}}},
-                               {32, 128, 290, 80, {0, 0}, {{25, 34}, {31, 44}}},
-                               {64, 128, 270, 90, {0, 0}, {{29, 32}, {36, 36}}},
+    constexpr Tile kTiles[] = {{16, 128, 280, 90, {0, 0}, {{26, 31}, {30, 33}}},
+                               {32, 128, 310, 70, {0, 0}, {{26, 31}, {30, 33}}},
+                               {64, 128, 270, 90, {0, 0}, {{30, 38}, {36, 42}}},
                                {128, 128, 290, 90, {60, 60}, {{33, 37}, {31, 41}}},
                                // (pairs write such rows slowly, and with block scales sum nothing meanwhile)
-                               {256, 256, 450, 90, {180, 170}, {{35, 39}, {46, 61}}}};
+                               {256, 256, 450, 90, {180, 190}, {{39, 39}, {47, 61}}}};
     constexpr int kJoin = 40, kJoinRows = 21;          // k in parts: a call's, 16 rows of a part
     const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
     const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;

@@ -6,12 +6,12 @@
 // y is written in pieces of 16 bytes (256 x 2048 x 8192: 12.1 -> 9.8 us).
 //
 // Persistent CTAs, a warp for each part: loads (tiles by TMA; gathered rows in pieces
-// of 16 bytes, by a warp or, of 64 and more a tile, five: a TMA gather of four rows takes
+// of 16 bytes, by a warp or, of 32 and more a tile, five: a TMA gather of four rows takes
 // 150 cycles and held one token's block at 620, one warp 64 rows of a block at 900),
 // products, scales, and 4 or 8 that sum the blocks.  With block scales every block of 128
 // in k is a product of its own into one of four accumulators; the summing warps add it,
 // times sx sw, to registers.  A block takes such a warp some 500 cycles of waits and
-// latencies, so two groups of four share the columns of a tile of 64 or 128 rows (with four
+// latencies, so two groups of four share the columns of a tile of 32 rows or more (with four
 // groups 256 x 2048 x 8192 took half a microsecond longer).  Where there are few tiles, a
 // cluster's CTAs share the blocks of one (64 x 4096 x 2048: 12.4 -> 8.5 us, 16 x 16384 x
 // 256: 40 -> 10).
@@ -43,8 +43,8 @@ template <int BT> struct GnCfg {
     static constexpr uint32_t kW = 128 * 128, kX = BT * 128, kStage = kW + kX;
     static constexpr int kStages = BT == 16 ? 11 : BT == 32 ? 10 : BT == 64 ? 8 : 6;
     static constexpr int kAccs = 4;
-    static constexpr int kSums = BT >= 64 ? 8 : 4;        // summing warps, groups of four share the columns
-    static constexpr int kGather = BT >= 64 ? 5 : 1;      // warps for gathered rows
+    static constexpr int kSums = BT >= 32 ? 8 : 4;        // summing warps, groups of four share the columns
+    static constexpr int kGather = BT >= 32 ? 5 : 1;      // warps for gathered rows
     static constexpr int kWidth = BT * 4 / kSums;         // columns of one
     static constexpr int kThreads = 32 * (kGnFirstSum + kSums + kGather);
     // of 128 rows a tile, the rows are the accumulator's lanes
@@ -388,7 +388,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < (kTurned ? 1 : (W + 31) / 32); ++i) there[i] = valid[slot][kTurned ? q : c0 / 32 + i];
+                for (int i = 0; i < (kTurned ? 1 : (W + 31) / 32); ++i) there[i] = valid[slot][kTurned ? q : c0 / 32 + i] >> (kTurned ? 0 : c0 % 32);
                 const float *sc = scales + slot * kScaleChunk * BT + (kTurned ? q * 32 + lane : c0);
 #pragma unroll 1
                 for (int k = 0; k < n; ++k, sc += BT) {
