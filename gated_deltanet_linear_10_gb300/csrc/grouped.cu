@@ -48,7 +48,7 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
         int rows, channels, ends, tile, odd[2], block[2][2];   // odd, block: bf16, e4m3; block: rows in place, gathered
     };
     constexpr Tile kTiles[] = {{16, 128, 280, 90, {0, 0}, {{26, 31}, {30, 33}}},
-                               {32, 128, 310, 70, {0, 0}, {{26, 31}, {30, 33}}},
+                               {32, 128, 310, 70, {0, 0}, {{26, 31}, {31, 35}}},
                                {64, 128, 270, 90, {0, 0}, {{30, 38}, {36, 42}}},
                                {128, 128, 290, 90, {60, 60}, {{33, 37}, {31, 41}}},
                                // (pairs write such rows slowly, and with block scales sum nothing meanwhile)
