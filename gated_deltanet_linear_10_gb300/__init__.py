@@ -999,7 +999,8 @@ def gdn_block_quant(x, glu=False, y=None, y_scale=None):
     a free row stride).  Returns y [T, n] float8_e4m3fn, whose rows start on
     16-byte boundaries (a view of a wider buffer where n is no multiple of 16)
     unless it is given, and y_scale [T, ceil(n / 128)]: the x and x_scale of
-    gdn_linear_block and gdn_grouped_linear."""
+    gdn_linear_block and gdn_grouped_linear.  A quotient within fp32's roundings (and,
+    with glu, the fast SiLU's) of the middle between two e4m3 values may go to either."""
     dev = _one_device(x, y, y_scale)
     shape, dtype = x.shape, x.dtype
     if len(shape) != 2 or (glu and shape[1] % 2):

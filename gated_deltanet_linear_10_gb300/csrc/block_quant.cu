@@ -6,6 +6,13 @@
 // the memory and, with SiLU, nearly by instructions (83 % of the slots): 206680 x 512 gate
 // and up in bf16 take 81 us, 0.97 of a copy's rate.  32 registers a thread, so that an SM has
 // 2048 threads whose loads are under way.
+//
+// SiLU takes the fast exponential and division and the quotient is a product with 1 / scale:
+// some 1e-5 of the gated values lie so near to the middle between two steps of e4m3 that
+// they go to the other one than with every operation rounded by itself, which is no nearer to
+// the formula.  That (expf, and one step from the remainder behind each of the two
+// quotients) takes 48 registers and 128 us here, and 28 instead of 25 for 20668 x 2048
+// bf16 without the gate.
 #include <algorithm>
 
 #include "quant.cuh"

@@ -560,6 +560,11 @@ gdn_status gdn_moe_route(const void *logits, int64_t logits_row_stride, int64_t 
  *   y_scale[t][b] = max(max_{j in block b} |v[t][j]| / 448, 2^-126)
  *   y[t][j] = v[t][j] / y_scale[t][j / 128] rounded to e4m3
  * A block with a NaN gets a NaN scale and NaN values; one of zeros gets zeros.
+ * The last step holds to fp32's roundings, not beyond: y is the rounding of a number
+ * within 2^-23 of v / y_scale (v times the scale's rounded reciprocal), v with glu is
+ * within (5 + 1.2 |x[t][j]|) 2^-23 of its formula (the fast exponential and division) or
+ * 0 at gates below -87.3, and y_scale within 2^-23 of the largest v / 448.  A quotient
+ * that lies so near to the middle between two e4m3 values may go to either.
  *   x: rows of n (glu: 2 n, the gate first) elements in `dtype` (GDN_F32 or
  *      GDN_BF16), row stride x_row_stride.
  *   y: rows of n e4m3, row stride y_row_stride (>= n), not over x; with a stride
