@@ -370,6 +370,7 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
                 const bool last = kBlock || k == nk - 1;
                 if (elect_lane()) {
                     if (mine) {
+                        if (c.rows) acquire_smem_of_cluster();         // rows that either CTA's threads have written
                         const uint32_t d = sums + (u & 1) * 256;
                         const uint64_t da = desc | st, db = desc | (st + xh);
 #pragma unroll
@@ -401,9 +402,11 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
         }
         __syncwarp();
     } else if (warp == kGwRelay) {
-        // Gathered rows are in this CTA's shared memory; the fence puts them before the tensor
-        // core's reads there, which the leader's product starts after the arrival: a relaxed one
-        // (with release at the cluster it waited for other copies in flight, 2,000 cycles).
+        // Gathered rows are in this CTA's shared memory; the first fence puts them before the tensor
+        // core's reads there, the second before the arrival that the leader's product waits for
+        // (20668 x 10 rows e4m3 568 us, without the second 565; an arrival with release at the
+        // cluster waits for other copies in flight too, 2,000 cycles, and took 773, in bf16
+        // 20668 x 4 rows 710 us instead of 266).
         if (c.rows) {
             const uint32_t lead = peer_smem(smem_u32(full), 0);
             int s = 0;
@@ -413,7 +416,10 @@ grouped_wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constan
             for (int64_t i = 0; i < min(all, (int64_t)keep); ++i) {
                 if (!mbar_wait_all(&gathered[s], phase, abort)) break;
                 fence_async_smem();
-                if (lane == 0) mbar_arrive_cluster(lead + s * 8);
+                if (lane == 0) {
+                    release_smem_to_cluster();
+                    mbar_arrive_cluster(lead + s * 8);
+                }
                 __syncwarp();
                 if (++s == S) {
                     s = 0;

@@ -114,10 +114,20 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Relaxed: it says that something has been read out.  (With release it first
-// waited for the thread's stores to reach the cluster, 2,000 cycles a tile.)
+// Relaxed: it says that something has been read out, or follows the release below.  (With
+// release of its own it first waited for the thread's stores to reach the cluster, 2,000
+// cycles a tile.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Hands over what is in this CTA's shared memory, with a relaxed arrival behind the one and
+// the other behind the wait for it: a release and an acquire at the cluster that order shared
+// memory alone, and so do not wait for copies and stores elsewhere.
+__device__ __forceinline__ void release_smem_to_cluster() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void acquire_smem_of_cluster() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 // Sets an int of this name in CTA `rank`'s shared memory.
 __device__ __forceinline__ void set_peer_flag(int *flag, uint32_t rank) {
