@@ -35,7 +35,7 @@ EXPORTS = (
     "gdn_decode_step_workspace_size", "gdn_prefill_layer", "gdn_prefill_layer_workspace_size",
     "gdn_prefill_layer_gated", "gdn_add_rmsnorm", "gdn_gated_rmsnorm_quant", "gdn_linear",
     "gdn_linear_block", "gdn_moe_route", "gdn_moe_route_workspace_size", "gdn_block_quant",
-    "gdn_grouped_linear", "gdn_moe_combine",
+    "gdn_grouped_linear", "gdn_moe_combine", "gdn_debug_set_grouped_tile",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -79,6 +79,7 @@ _SIGS = {
     "gdn_grouped_linear": [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32,
                            _i32, _vp, _i64, _i32, _i32, _vp],
     "gdn_moe_combine": [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _i32, _vp],
+    "gdn_debug_set_grouped_tile": [_i32, _i32],
     "gdn_decode_recurrent_gated": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp, _vp, _vp, _i64,
                                    _vp, _f32, _vp, _i32, _vp],
@@ -1126,3 +1127,10 @@ def gdn_debug_set_wait_limit(limit_ns=0, drop_prep_loads=False, device=None, dro
     _need(drop_linear_loads in (0, 1, 2), "drop_linear_loads: 0, 1 or 2")
     _check(_lib.gdn_debug_set_wait_limit(int(limit_ns), int(bool(drop_prep_loads)) + 2 * drop_linear_loads,
                                          _stream(device)), "gdn_debug_set_wait_limit")
+
+
+def gdn_debug_set_grouped_tile(rows=0, cut=-1):
+    """Test control of the products with block scales and of the grouped ones: tiles
+    of 16, 32, 64, 128 or 256 rows in place of the choice by the sizes (0), with the
+    sum over k in 2^cut parts (-1: by the sizes)."""
+    _check(_lib.gdn_debug_set_grouped_tile(rows, cut), "gdn_debug_set_grouped_tile")

@@ -4,6 +4,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "grouped.cuh"
 
@@ -31,6 +32,10 @@ int64_t most_row_tiles(const GroupedCall &c, int tile_rows) {
     return c.offsets ? std::min(n, n / tile_rows + std::min<int64_t>(c.n_experts, n)) : (n + tile_rows - 1) / tile_rows;
 }
 
+// Test control (gdn_debug_set_grouped_tile): the tile's rows, 0 for the estimate's choice,
+// and 16 bits up the cut + 1.
+static std::atomic<int> g_grouped_tile{0};
+
 // The choice of a tile: the shortest by an estimate of waves of tiles, each of as many
 // blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, what rows of y
 // off 16 bytes add to that, a block) are fitted to 574 products: 1 to 4096 rows of 512 x
@@ -56,9 +61,11 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     constexpr int kJoin = 40, kJoinRows = 21;          // k in parts: a call's, 16 rows of a part
     const int sms = sm_count(), experts = c.offsets ? std::min(c.n_experts, c.n_rows) : 1;
     const int64_t blocks = c.e4m3 ? c.kb : (c.n_in + 63) / 64;
+    const int wanted = g_grouped_tile.load(std::memory_order_relaxed), only_rows = wanted & 0xffff, only_cut = (wanted >> 16) - 1;
     int best = 0, best_cut = 0;
     int64_t least = INT64_MAX;
     for (const Tile &t : kTiles) {
+        if (only_rows && t.rows != only_rows) continue;
         const int64_t halves = c.offsets ? std::max<int64_t>(2 * (int64_t)experts, 2 * (int64_t)c.n_rows / t.rows + experts)
                                          : 2 * (((int64_t)c.n_rows + t.rows - 1) / t.rows);
         const int64_t tiles = (halves + 1) / 2 * ((c.n_out + t.channels - 1) / t.channels);
@@ -67,10 +74,13 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
         const int64_t slots = t.rows == 256 ? std::max(1, sms / 2) : sms, block = t.block[c.e4m3][c.rows != nullptr];
         const int64_t rest = t.tile + (c.vec16 ? 0 : t.odd[c.e4m3]);
         for (int cut = 0; cut <= 3; ++cut) {
-            // k in parts: in one wave, four blocks a CTA at least (16 clusters of eight, where 15
+            // k in parts, a block each at least
+            if (cut > 0 && (t.rows == 256 || blocks >> cut < 1 || most << cut >= (1ll << 31))) break;
+            // ... in one wave, four blocks a CTA at least (16 clusters of eight, where 15
             // fit, are two waves: 1 x 4096 x 2048 11.9 us, in clusters of four 6.9)
-            if (cut > 0 && (t.rows == 256 || most << cut > sms || blocks >> cut < 4)) break;
-            if (cut == 3 && most > grouped_eights()) break;
+            if (cut > 0 && only_cut < 0 && (most << cut > sms || blocks >> cut < 4)) break;
+            if (cut == 3 && only_cut < 0 && most > grouped_eights()) break;
+            if (only_cut >= 0 && cut != only_cut) continue;
             const int64_t cost = t.ends + (tiles + slots - 1) / slots * (rest + ((blocks + (1 << cut) - 1) >> cut) * block) +
                                  (cut > 0 ? kJoin + (t.rows << cut) * kJoinRows / 16 : 0);
             if (cost >= least) continue;
@@ -102,6 +112,14 @@ static gdn_status grouped_check(const GroupedCall &c, int64_t n_rows, int64_t n_
                     (uintptr_t)c.offsets % 4 == 0 && (uintptr_t)c.rows % 4 == 0,
                 GDN_ERR_INVALID_ARG);
     GDN_REQUIRE(c.e4m3 ? c.sx && c.sw : !c.sx && !c.sw, GDN_ERR_INVALID_ARG);
+    return GDN_OK;
+}
+
+extern "C" gdn_status gdn_debug_set_grouped_tile(int32_t tile_rows, int32_t cut) {
+    GDN_REQUIRE(tile_rows == 0 || tile_rows == 16 || tile_rows == 32 || tile_rows == 64 || tile_rows == 128 || tile_rows == 256,
+                GDN_ERR_INVALID_ARG);
+    GDN_REQUIRE(cut >= -1 && cut <= (tile_rows == 256 ? 0 : 3) && (tile_rows || cut == -1), GDN_ERR_INVALID_ARG);
+    g_grouped_tile.store(tile_rows | (cut + 1) << 16, std::memory_order_relaxed);
     return GDN_OK;
 }
 

@@ -810,6 +810,16 @@ gdn_status gdn_debug_set_wait_limit(uint64_t limit_ns, int32_t drop_loads,
                                     void *stream);
 
 /*
+ * Test control of the products' tiles (not for production use): the calls of
+ * gdn_linear_block and gdn_grouped_linear (of the process) from here on take tiles of
+ * tile_rows rows, 16, 32, 64, 128 or 256 (pairs of CTAs), and with cut >= 0 share the
+ * sum over k among 2^cut CTAs (up to 3; 256 rows: 0).  A call with fewer blocks of 128
+ * bytes in k than that returns GDN_ERR_UNSUPPORTED.  (0, -1) restores the choice by the
+ * sizes; (rows, -1) leaves the cut to it.  Else GDN_ERR_INVALID_ARG.
+ */
+gdn_status gdn_debug_set_grouped_tile(int32_t tile_rows, int32_t cut);
+
+/*
  * Reads the device status word (bits GDN_DEVSTAT_*) of the current device
  * into *out (a HOST pointer), synchronising `stream` first.  If clear != 0
  * the word is reset to 0 afterwards.
