@@ -917,7 +917,8 @@ def gdn_linear_block(x, weight, x_scale, weight_scale, y_dtype=None, y=None):
     scale for each block of 128 in K: x_scale [T, ceil(K / 128)] (as
     gdn_block_quant gives), weight_scale [ceil(N / 128), ceil(K / 128)].  Unit
     column stride, rows on 16-byte boundaries (K itself may be odd).  y [T, N] bf16
-    (default) or fp32, columns of a wider buffer if wanted.  Returns y."""
+    (default) or fp32, columns of a wider buffer if wanted.  A row's last fp32 bits
+    depend on the call's sizes (T among them), not on the other rows.  Returns y."""
     dev = _one_device(x, weight, x_scale, weight_scale, y)
     shape, wshape = x.shape, weight.shape
     if len(shape) != 2 or len(wshape) != 2 or wshape[1] != shape[1]:
@@ -1032,7 +1033,8 @@ def gdn_grouped_linear(x, weight, offsets, rows=None, x_scale=None, weight_scale
     [n_x, ceil(K / 128)] and weight_scale [E, ceil(N / 128), ceil(K / 128)] fp32;
     unit column stride, rows (and experts) on 16-byte boundaries (K itself may be
     odd).  y [R, N] bf16 (default) or fp32; rows from offsets[E] on are left as
-    they were, so a y that is not given holds anything there.  Returns y."""
+    they were, so a y that is not given holds anything there.  A row's last fp32 bits
+    depend on the call's sizes, not on the other rows.  Returns y."""
     dev = _one_device(x, weight, offsets, rows, x_scale, weight_scale, y)
     shape, wshape, dtype = x.shape, weight.shape, x.dtype
     if len(shape) != 2 or len(wshape) != 3 or wshape[2] != shape[1]:

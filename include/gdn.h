@@ -514,7 +514,9 @@ gdn_status gdn_linear(const void *x, int64_t x_row_stride, const float *x_scale,
  *      writes such x and x_scale.
  *   y: rows of n_out elements, GDN_BF16 or GDN_F32, row stride y_row_stride
  *      (>= n_out: y may be columns of a wider buffer).  It must not overlap an input.
- * The result of a row does not depend on the other rows or on the call's timing.
+ * The result of a row does not depend on the other rows' values or on the call's timing.
+ * It may differ in the last fp32 bits between calls whose sizes differ, n_tokens among
+ * them: these choose the order of the sum over k.
  * Limits: n_tokens <= 16,776,960, n_in and n_out <= 2^20, row strides < 2^36
  * (beyond: GDN_ERR_UNSUPPORTED).
  */
