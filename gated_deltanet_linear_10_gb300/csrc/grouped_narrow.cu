@@ -493,7 +493,10 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             cluster_arrive();
             cluster_wait();
         }
-        cluster_arrive_relaxed();                          // no CTA ends while the leader may read its sums
+        // no CTA ends while the leader may read its sums; one that has given up does not use what
+        // it asked for, and waits for it here
+        if (*abort) cluster_arrive();
+        else cluster_arrive_relaxed();
         cluster_wait();
     }
     __syncthreads();
