@@ -325,7 +325,7 @@ grouped_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_const
             }
             const float *sw = kBlock ? c.sw + ((int64_t)a.e * c.nb + a.n) * c.kb : nullptr;
             for (int k0 = kBlock ? kb0 : 0; k0 < (kBlock ? nk : 1) && ok; k0 += kScaleChunk, ++v, slot ^= 1) {
-                float f[Q][kScaleChunk];
+                __align__(16) float f[Q][kScaleChunk];       // written by vectors
                 if (kBlock) {
                     const bool pieces = k0 + kScaleChunk <= nk && c.sx16 && k0 % 4 == 0;
 #pragma unroll

@@ -278,14 +278,14 @@ __device__ __forceinline__ void route_token(const RawLogits<T, PER, VEC> &raw, i
         const Word mine = q * 32 + lane < n ? cands[q * 32 + lane] : 0;
         int r = 0;
         for (int j = 0; j < n; j += 4) {
-            Word q[4];
+            __align__(16) Word w[4];                     // written by vectors
             if constexpr (sizeof(Word) == 4) {
-                *reinterpret_cast<uint4 *>(q) = *reinterpret_cast<const uint4 *>(cands + j);
+                *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(cands + j);
             } else {
-                *reinterpret_cast<ulonglong2 *>(q) = *reinterpret_cast<const ulonglong2 *>(cands + j);
-                *reinterpret_cast<ulonglong2 *>(q + 2) = *reinterpret_cast<const ulonglong2 *>(cands + j + 2);
+                *reinterpret_cast<ulonglong2 *>(w) = *reinterpret_cast<const ulonglong2 *>(cands + j);
+                *reinterpret_cast<ulonglong2 *>(w + 2) = *reinterpret_cast<const ulonglong2 *>(cands + j + 2);
             }
-            r += (q[0] > mine) + (q[1] > mine) + (q[2] > mine) + (q[3] > mine);
+            r += (w[0] > mine) + (w[1] > mine) + (w[2] > mine) + (w[3] > mine);
         }
         rank[q] = mine ? r : kCands;
         p[q] = rank[q] < top ? expf(C::value_of(mine) - top1) : 0.f;
