@@ -107,7 +107,6 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Vector of N elements moved as 16 bytes: 8 bf16 or 4 fp32.
 // Quotients by a number that the host knows, of dividends below 2^31.
 struct QuickDiv {
     uint32_t mul = 0, shift = 0;
@@ -119,6 +118,7 @@ struct QuickDiv {
     __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
 };
 
+// Vector of N elements moved as 16 bytes: 8 bf16 or 4 fp32.
 template <typename T> struct Vec16;
 template <> struct Vec16<float> {
     static constexpr int N = 4;

@@ -97,7 +97,7 @@ static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
 
 using namespace gdn;
 
-static gdn_status grouped_check(const GroupedCall &c, int64_t n_rows, int64_t n_x, int32_t dtype, int32_t y_dtype) {
+static gdn_status grouped_check(const GroupedCall &c, int64_t n_rows, int64_t n_x) {
     GDN_REQUIRE(c.x && c.w && c.y && c.y != c.x && c.y != c.w, GDN_ERR_INVALID_ARG);
     GDN_REQUIRE((n_x == 1 || c.xs >= c.n_in) && (c.n_out == 1 || c.ws >= c.n_in) && (n_rows == 1 || c.ys >= c.n_out),
                 GDN_ERR_INVALID_ARG);
@@ -133,7 +133,7 @@ extern "C" gdn_status gdn_linear_block(const void *x, int64_t x_row_stride, cons
     const GroupedCall c = {x, w, x_row_stride, w_row_stride, 0, x_scale, w_scale, nullptr, nullptr, y, y_row_stride,
                            (int)n_tokens, (int)n_tokens, 1, n_in, n_out, (n_in + 127) / 128, (n_out + 127) / 128, true,
                            y_dtype == GDN_F32};
-    const gdn_status st = grouped_check(c, n_tokens, n_tokens, GDN_E4M3, y_dtype);
+    const gdn_status st = grouped_check(c, n_tokens, n_tokens);
     return st == GDN_OK ? launch_grouped(c, (cudaStream_t)stream) : st;
 }
 
@@ -154,6 +154,6 @@ extern "C" gdn_status gdn_grouped_linear(const void *x, int64_t x_row_stride, co
     const GroupedCall c = {x, w, x_row_stride, w_row_stride, w_expert_stride, x_scale, w_scale, offsets, rows, y,
                            y_row_stride, (int)n_rows, (int)n_x, n_experts, n_in, n_out, (n_in + 127) / 128,
                            (n_out + 127) / 128, dtype == GDN_E4M3, y_dtype == GDN_F32};
-    const gdn_status st = grouped_check(c, n_rows, n_x, dtype, y_dtype);
+    const gdn_status st = grouped_check(c, n_rows, n_x);
     return st == GDN_OK ? launch_grouped(c, (cudaStream_t)stream) : st;
 }
