@@ -622,7 +622,8 @@ gdn_status gdn_grouped_linear(const void *x, int64_t x_row_stride, const float *
  *      stride) and must not overlap x.
  * Each with its row stride (>= hidden); any alignment of whole elements is taken,
  * rows of 16-byte vectors are faster.
- * Limits: n_rows < 2^31, n_tokens * top_k < 2^31, top_k <= 1024, n_tokens * hidden < 2^39.
+ * Limits: n_rows < 2^31, n_tokens * top_k < 2^31, top_k <= 1024,
+ * n_tokens * ceil(hidden / 256) < 2^31.
  */
 gdn_status gdn_moe_combine(const void *x, int64_t x_row_stride, int64_t n_rows,
                            const int32_t *slots, const float *weights, const void *residual,
@@ -795,8 +796,9 @@ gdn_status gdn_state_snapshot(void *pool, int64_t n_slots, int64_t slot_bytes,
  * Test control of the failure path (not for production use).  Sets the limit
  * of every bounded wait inside the two-kernel tensor-core prefill (the prep
  * and chain kernels of gdn_prefill_chunked with a workspace) and inside the
- * kernels of gdn_linear, gdn_linear_block and gdn_grouped_linear to limit_ns nanoseconds on the current device; 0
- * restores the default of one second.  drop_loads: a sum of
+ * kernels of gdn_linear, gdn_linear_block and gdn_grouped_linear to limit_ns
+ * nanoseconds on the current device; 0 restores the default of one second.
+ * drop_loads: a sum of
  *   1  the prep kernel issues none of its K|Q tile loads,
  *   2  calls of gdn_linear, gdn_linear_block and gdn_grouped_linear (of the
  *      process) issue no loads of x and w,
