@@ -38,11 +38,15 @@ static std::atomic<int> g_grouped_tile{0};
 
 // The choice of a tile: the shortest by an estimate of waves of tiles, each of as many
 // blocks of 128 bytes in k.  The figures (in 10 ns: a call's ends, a tile's, what rows of y
-// off 16 bytes add to that, a block) are fitted to 574 products: 1 to 4096 rows of 512 x
-// 4096 to 4096 x 2048, and 12 to 400 rows for each of 8, 60 and 256 experts, in place and
-// gathered.  There the choice takes 1 % longer than the best tile, 14 % at worst.  Of an
-// expert's rows the host knows the mean: tiles of r rows take mean / r + 1/2 of them, at
-// least one.  (256 experts of 82 rows gathered, 1000 x 700 e4m3, in the five tiles: 193,
+// off 16 bytes add to that, a block) come from a fit, but for the blocks of e4m3 tiles of 32
+// rows, which were raised by hand (256 x 10 rows of 512 experts: 138.4 -> 135.7 us; of 408
+// e4m3 products 19 change, and take 1.9 % longer than their best tile instead of 3.5).
+// Measured with every tile and cut on 626 products (1 to 4096 tokens, 2 to 400 rows for each of
+// 8, 60 and 256 experts, random ones of 64 to 4096 in, 33 to 8192 out), the choice takes
+// 2.2 % longer than the best, more than 15 % for one in twenty (most of them calls under 6 us
+// of one or two blocks), 40 % at worst (6481 x 110 x 4283 to fp32: 53.7 us on pairs, 38.3 in
+// tiles of 128).  Of an expert's rows the host knows the mean: tiles of r rows take mean /
+// r + 1/2 of them, at least one.  (256 experts of 82 rows gathered, 1000 x 700 e4m3, in the five tiles: 193,
 // 154, 81, 84 and 105 us; 256 x 2048 x 8192 in those of 64, 128 and 256: 15.8, 9.8, 13.4.)
 static gdn_status launch_grouped(GroupedCall c, cudaStream_t s) {
     const int64_t ye = c.out_f32 ? 4 : 2;

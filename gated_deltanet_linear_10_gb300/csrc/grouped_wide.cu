@@ -48,7 +48,7 @@ constexpr int kGwRows = 256, kGwChannels = 256;
 // Registers of a thread: 128 at launch; the summing warpgroups take what the others
 // give up: their sum over the four warpgroups stays 512.  (A spill in any of the loops
 // costs more than it looks: with 48, 64 and 200 bf16 rows gathered took 353 us instead
-// of 268.)
+// of 268.  With these, 24 to 34 bytes of a thread are still spilled.)
 template <bool kBlock> struct GwRegs {
     static constexpr int kFew = kBlock ? 56 : 72, kGather = kBlock ? 88 : 72, kMany = 184;
     static_assert(kFew + kGather + 2 * kMany == 512, "registers that the launch has");
